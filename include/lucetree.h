@@ -74,7 +74,8 @@ typedef enum lucetree_status {
 
 typedef enum lucetree_dtype {
     LUCETREE_F16 = 0,  /* IEEE binary16 */
-    LUCETREE_BF16 = 1  /* bfloat16 */
+    LUCETREE_BF16 = 1, /* bfloat16 */
+    LUCETREE_F32 = 2   /* fp32: outputs and logits only, where a call says so */
 } lucetree_dtype;
 
 /* Flags kernels OR into the device status word. */
@@ -140,6 +141,39 @@ LUCETREE_API lucetree_status lucetree_verify_attn_workspace(int B, int N, int Hq
  */
 LUCETREE_API lucetree_status lucetree_verify_attn(const lucetree_attn_args* args, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/* Arguments of lucetree_verify_attn_win. */
+typedef struct lucetree_win_args {
+    lucetree_attn_args attn; /* as for lucetree_verify_attn, except: attn.out is not used (NULL is fine), and
+                                page-table entries of pages that no node sees are not read */
+    int window;              /* >= 1: positions a node sees up to and with its own */
+    int sinks;               /* >= 0: first positions of the sequence that stay visible */
+    int out_dtype;           /* LUCETREE_F32, or attn.dtype */
+    void* out;               /* [B][N][Hq][D] in out_dtype, 16-byte aligned */
+} lucetree_win_args;
+
+/*
+ * lucetree_verify_attn with a sliding window and sinks, for targets (or
+ * drafters) with window layers.  Node i of sequence b is at position
+ * t_i = L_b + depth(i), its depth being the number of its proper ancestors in
+ * anc_mask (bits of nodes before it, as lucetree_build_anc_mask makes them).
+ * It sees
+ *   - committed position p iff p < sinks or t_i - p < window;
+ *   - itself and ancestor j iff t_j < sinks or t_i - t_j < window.
+ * Only the pages of the sinks and of the window of a depth-0 node are read:
+ * table entries between them may be -1 (see lucetree_trim_pages).  K and V of
+ * positions that no node sees may hold anything, NaN included.  N = 1 with
+ * mask 1 is the single-token decode step.  A window of at least L_b + N
+ * positions is the full attention.  Softmax statistics, sums and partial
+ * outputs are fp32; P is rounded to fp16 for the tensor cores as in
+ * lucetree_verify_attn, and a 16-bit output is rounded once from fp32.  A row
+ * that sees no key (its mask lacks the node itself, which raises BAD_NODE)
+ * gives zeros and lse = -infinity.  Workspace as
+ * lucetree_verify_attn_workspace.  Errors as lucetree_verify_attn, plus
+ * INVALID_ARG (window, sinks, out) and UNSUPPORTED (out_dtype).
+ */
+LUCETREE_API lucetree_status lucetree_verify_attn_win(const lucetree_win_args* args, void* workspace,
+                                                      size_t workspace_bytes, void* stream);
 
 /* Size of the device array that backs lucetree_verify_attn_noalloc: 32 MiB. */
 #define LUCETREE_NOALLOC_SCRATCH_BYTES (32u << 20)

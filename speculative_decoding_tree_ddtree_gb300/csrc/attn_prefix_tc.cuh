@@ -130,6 +130,8 @@ struct Misc {
     uint64_t q_ready;  // E4M3 K: the piece's queries split into their two E4M3 parts
     uint32_t tmem_base;
     int abort_flag;
+    int empty_cols;  // windowed: a query row has seen no key of its range so far
+    alignas(8) uint8_t depth[kRowsMax];  // windowed: depth of each query row's node
 };
 static_assert(sizeof(Misc) <= 5632, "misc region");
 static_assert(offsetof(Misc, vexp) == 0 && sizeof(Misc::vexp[0]) % 128 == 0, "128-byte aligned TMA destinations");
@@ -150,14 +152,33 @@ struct VCodes {
 struct Piece {
     int s, L;    // key segment (b * Hkv + g) and its committed length
     int ta, te;  // tile range within the segment
+    WinSpan w;   // windowed: the virtual pages that the tiles are made of
 };
 
+template <bool WIN>
+__device__ __forceinline__ int pages_of(const Piece& pc) {
+    return WIN ? pc.w.vp : (pc.L + kPage - 1) / kPage;
+}
+// The page-table entry of the segment's page number v.
+template <bool WIN>
+__device__ __forceinline__ int table_page(const Piece& pc, int v) {
+    return WIN ? win_page(pc.w, v) : v;
+}
+
+template <bool WIN>
 struct PieceIter {
-    int t0, t1, off, s;
+    int t0, t1, off, s;  // off: flat offset of segment s
     __device__ bool next(const PlanDims& p, const int32_t* ctx_len, Piece& out) {
         while (s < p.S && off < t1) {
             const int L = seq_len_quiet(ctx_len, s / p.Hkv, p.max_pages);
-            const int s0 = off, s1 = off + (int)tiles_of(L);
+            int tiles;
+            if constexpr (WIN) {
+                out.w = win_span(L, p.window, p.sinks);
+                tiles = (out.w.vp + 1) / 2;
+            } else {
+                tiles = (int)tiles_of(L);
+            }
+            const int s0 = off, s1 = off + tiles;
             const int cur = s;
             off = s1;
             ++s;
@@ -173,14 +194,16 @@ struct PieceIter {
 };
 
 // The CTA's tiles in order: piece (key segment) and tile within the segment.
+template <bool WIN>
 struct TileCursor {
-    PieceIter it;
+    PieceIter<WIN> it;
     Piece pc;
     int t;
     int piece_no;
     bool live;
-    __device__ void start(int t0, int t1, const PlanDims& p, const int32_t* ctx_len) {
-        it = PieceIter{t0, t1, 0, 0};
+    // (off, s): a segment at or before the range's first one, and its flat offset
+    __device__ void start(int t0, int t1, const PlanDims& p, const int32_t* ctx_len, int off, int s) {
+        it = PieceIter<WIN>{t0, t1, off, s};
         piece_no = -1;
         t = 0;
         next_piece(p, ctx_len);
@@ -274,7 +297,14 @@ __device__ __forceinline__ bool aborted(Misc* ms) { return *(volatile int*)&ms->
 // runs as two kind::f8f6f4 MMAs per 32-dim step into the same accumulator.
 // The softmax multiplies each key's scores by its exponent and the segment's
 // query scale.
-template <int D, bool BF16, int RGP, int VQ, int KQ>
+//
+// WIN: a sliding window with sinks (16-bit K/V).  A tile is two virtual pages
+// (see WinSpan).  Most tiles are visible to every row; in the one or two that
+// hold the window's edge, a key counts for the rows of the nodes deep enough
+// only (one comparison of the row's depth per score, in warps that need it).
+// V rows that no node sees (past the sinks, before the window) are zeroed like
+// those past L.
+template <int D, bool BF16, int RGP, int VQ, int KQ, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ve,
@@ -284,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChunksK = KQ ? D / 128 : D / 64;        // ring chunks per K operand
     constexpr int kChunksV = D / 64;                       // ring chunks per V operand
     static_assert(!KQ || (D == 256 && BF16), "E4M3 K: head dim 256, bf16 queries");
+    static_assert(!WIN || (VQ == 0 && KQ == 0), "windowed attention: 16-bit K and V");
     constexpr int kNch = Lay::kNch;
     constexpr int kNa = (kNch + kSmGroups - 1) / kSmGroups;  // column chunks per softmax warp (at most)
     constexpr int kNS = Lay::kNS;
@@ -359,13 +390,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // wait, relying on this kernel having waited for their producers first.
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    const long long nT = total_tiles(p, a.ctx_len);
+    long long nT;
+    int off0 = 0, seg0 = 0;
+    if constexpr (WIN) nT = win_total(p, a.ctx_len, 0, &off0);
+    else nT = total_tiles(p, a.ctx_len);
     const int t0 = nT ? (int)cta_begin(cta, nT, p.Cg) : 0, t1 = nT ? (int)cta_begin(cta + 1, nT, p.Cg) : 0;
     if (t0 >= t1) {  // uniform across the CTA: nothing to do but give TMEM back
         if (warp == 1) tmem_dealloc(tmem, kTmemCols);
         return;
     }
     const uint32_t n_tiles = (uint32_t)(t1 - t0);
+    if constexpr (WIN) {  // every role starts at the sequence of the range's first tile
+        win_find(p, a.ctx_len, t0, &seg0, &off0);
+        seg0 *= p.Hkv;
+    }
 
     if (warp < 4) {
     regs_dec<kRegsIssue>();
@@ -417,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         };
-        TileCursor cur;
-        cur.start(t0, t1, p, a.ctx_len);
+        TileCursor<WIN> cur;
+        cur.start(t0, t1, p, a.ctx_len, off0, seg0);
         int npages = 0;
         const int32_t* pt = a.page_table;
         // page ids of the current piece, 16 tiles (32 pages) per warp-wide load, one batch ahead
@@ -426,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pg = 2 * tb + lane;
             int pid = -1;
             if (pg < npages && pg < 2 * cur.pc.te) {
-                const int v = pt[pg];
+                const int v = pt[table_page<WIN>(cur.pc, pg)];
                 if (v >= 0 && v < a.num_pages) pid = v;
                 else atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
             }
@@ -459,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++q_loads;
-                npages = (cur.pc.L + kPage - 1) / kPage;
+                npages = pages_of<WIN>(cur.pc);
                 pt = a.page_table + (size_t)(cur.pc.s / p.Hkv) * p.max_pages;
                 pid_cur = load_batch(cur.pc.ta);
                 pid_next = load_batch(cur.pc.ta + 16);
@@ -507,9 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t aQ = smem_u32(sQ), aP = smem_u32(sP), aS = smem_u32(sSlots);
             uint32_t chunk = 0, jq = 0, j = 0;
             bool ok = true;
-            TileCursor qk, pv;
-            qk.start(t0, t1, p, a.ctx_len);
-            pv.start(t0, t1, p, a.ctx_len);
+            TileCursor<WIN> qk, pv;
+            qk.start(t0, t1, p, a.ctx_len, off0, seg0);
+            pv.start(t0, t1, p, a.ctx_len, off0, seg0);
             // S^T(jq) = K(jq) . Q^T; S^T is free once the softmax has read tile jq-1
             auto issue_qk = [&]() -> bool {
                 if (jq > 0) {
@@ -617,8 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 64 * (c & 1) + (u % 512) / 8 (each 8 KB box is [64 keys][128 B]; the
         // swizzle permutes units only within a key's row).
         const int ct = threadIdx.x - 64;  // 0 .. 63
-        TileCursor cur;
-        cur.start(t0, t1, p, a.ctx_len);
+        TileCursor<WIN> cur;
+        cur.start(t0, t1, p, a.ctx_len, off0, seg0);
         uint32_t j = 0;
         bool ok = true;
         while (ok && cur.live) {
@@ -636,10 +674,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
-                const int nv = nvalid - 64 * (c & 1);  // valid keys of this chunk's page
+                int nv = nvalid - 64 * (c & 1);  // valid keys of this chunk's page
+                // windowed: of those, the first ns (sinks) and those from nl on (window) count
+                int ns = 64, nl = 0;
+                if constexpr (WIN) {
+                    const int v = 2 * cur.t + (c & 1), p0 = win_page(cur.pc.w, v) * kPage;
+                    nv = v < cur.pc.w.vp ? cur.pc.L - p0 : 0;
+                    ns = p.sinks - p0;
+                    nl = cur.pc.w.lo - p0;
+                }
+                const bool whole = nv >= 64 && (!WIN || ns >= 64 || nl <= 0);
                 constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
                 constexpr int kBatch = 4;                                      // loads in flight
-                if (BF16 && nv >= 64) {
+                if (BF16 && whole) {
                     // a full page (every chunk but a segment's last few): no per-key test
 #pragma unroll 1
                     for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
@@ -655,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             base[ct + 32 * kConvWarps * (i0 + k)] = x[k];
                         }
                     }
-                } else if (BF16 || nv < 64) {
+                } else if (BF16 || !whole) {
 #pragma unroll 1
                     for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
                         uint4 x[kBatch];
@@ -663,7 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) {
                             const int u = ct + 32 * kConvWarps * (i0 + k);
-                            kv[k] = ((u & 511) >> 3) < nv;
+                            const int key = (u & 511) >> 3;
+                            kv[k] = key < nv && (!WIN || key < ns || key >= nl);
                             x[k] = kv[k] ? base[u] : make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
@@ -718,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // previous tile still reads the shared P^T buffer; store_p writes it
         // once that PV has completed.
         auto exp_pass = [&](float (&lpart)[kNa * 16], bool valid, float sign, bool keep_p, float& ex,
-                            uint32_t (&ph)[kNa * 8]) {
+                            uint32_t (&ph)[kNa * 8], bool part, int dmax) {
             // 16-column chunks, each in two 8-column blocks b = 2*cc + hb; the
             // TMEM load of chunk cc+1 is in flight while chunk cc is computed.
             // An invalid key's exponents are -inf, and so are a padding
@@ -741,9 +789,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float4 ma = m4[0], mb = m4[1];
                     const float mv[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
                     float pv[8];
+                    float xw[8];  // windowed: exponents with the rows whose window does not reach my key masked
+                    if constexpr (WIN) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            xw[k] = valid ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY;
+                        if (part) {
+                            const uint2 dd = *reinterpret_cast<const uint2*>(ms->depth + 16 * c + 8 * hb);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if ((int)(((k < 4 ? dd.x : dd.y) >> (8 * (k & 3))) & 0xFFu) > dmax) xw[k] = -INFINITY;
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float x = valid ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY;
+                        const float x =
+                            WIN ? xw[k] : (valid ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY);
                         ex = fmaxf(ex, x);
                         pv[k] = ex2(x);
                         float& acc = lpart[cc * 16 + 8 * hb + k];
@@ -767,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
 
-        TileCursor cur;
-        cur.start(t0, t1, p, a.ctx_len);
+        TileCursor<WIN> cur;
+        cur.start(t0, t1, p, a.ctx_len, off0, seg0);
 
         while (cur.live) {
             const int piece_no = cur.piece_no;
@@ -776,6 +837,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_sync(1, kSoftmaxThreads);
             // padding columns keep a shift of +inf, so their exponents are -inf and P = 0
             for (int col = st; col < RGP; col += kSoftmaxThreads) ms->m_ref[col] = col < R_seg ? -INFINITY : INFINITY;
+            if constexpr (WIN) {
+                // (a node's depth is the number of its proper ancestors)
+                for (int col = st; col < RGP; col += kSoftmaxThreads) {
+                    int d = 0;
+                    if (col < R_seg)
+                        d = max(__popcll(a.anc_mask[(size_t)(seg / p.Hkv) * p.N + i0 + col / p.G] &
+                                         (~0ull >> (64 - p.N))) - 1, 0);
+                    ms->depth[col] = (uint8_t)d;
+                }
+                if (st == 0) ms->empty_cols = 0;
+            }
             bar_sync(1, kSoftmaxThreads);
             float lpart[kNa * 16];
 #pragma unroll
@@ -784,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int pid_lane = -1;  // E4M3 K: page id of my key's page for tile (batch start + lane)
             // E4M3 K: my key's exponent byte, loaded one tile ahead; the segment's query scale
             auto page_of = [&](int tile) -> int {
-                const int pg = 2 * tile + my_half;
+                const int pg = 2 * tile + my_half;  // (E4M3 K is never windowed)
                 return pg < (cur.pc.L + kPage - 1) / kPage ? a.page_table[(size_t)(seg / p.Hkv) * p.max_pages + pg] : -1;
             };
             auto k_exp_of = [&](int pid) -> uint32_t {
@@ -888,8 +960,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int pg = 2 * tt + my_half;
                     bool okp = false;
                     pid_lane = -1;
-                    if (tt < cur.pc.te && pg < (cur.pc.L + kPage - 1) / kPage) {
-                        const int pid = a.page_table[(size_t)(seg / p.Hkv) * p.max_pages + pg];
+                    if (tt < cur.pc.te && pg < pages_of<WIN>(cur.pc)) {
+                        const int pid =
+                            a.page_table[(size_t)(seg / p.Hkv) * p.max_pages + table_page<WIN>(cur.pc, pg)];
                         okp = pid >= 0 && pid < a.num_pages;
                         pid_lane = pid;
                     }
@@ -897,8 +970,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int nvalid = min(kTileKeys, cur.pc.L - t * kTileKeys);
                 const bool page_ok = (page_bits >> tb) & 1u;
-                const bool valid = kl < nvalid && page_ok;
+                bool valid = kl < nvalid && page_ok;
                 const bool first = cur.first();
+                // windowed: my key counts for rows of depth <= dmax; part: some lane's key not for all
+                int dmax = 64;
+                bool part = false;
+                if constexpr (WIN) {
+                    const int v = 2 * t + my_half, pos = win_page(cur.pc.w, v) * kPage + (kl & (kPage - 1));
+                    if (pos >= p.sinks) dmax = min(pos - max(cur.pc.L - p.window + 1, -64), 64);
+                    valid = v < cur.pc.w.vp && pos < cur.pc.L && page_ok && dmax >= 0;
+                    part = __any_sync(0xffffffffu, valid && dmax < p.N - 1);
+                }
+                // no shifts to go by: the range's first tile, or a row that has seen no key yet
+                const bool fresh = first || (WIN && ms->empty_cols != 0);
                 if constexpr (KQ) {
                     // this tile's exponent was loaded during the previous tile; load the next one's
                     const uint32_t ek = valid ? ek_next : 0u;
@@ -923,19 +1007,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The first tile of a range has no shifts yet and starts at pass 2.
                 float ex = -INFINITY;
                 uint32_t ph[kNa * 8];
-                if (!bad && !first) {
-                    exp_pass(lpart, valid, 1.f, true, ex, ph);
+                if (!bad && !fresh) {
+                    exp_pass(lpart, valid, 1.f, true, ex, ph, part, dmax);
                 }
                 // one barrier decides the path; a second one only when it says
                 // "slow", to tell a timeout (somewhere) from a shift update
                 const bool bad_now = bad || aborted(ms);
-                const bool slow = bar_sync_or(1, kSoftmaxThreads, bad_now || first || ex > kTau);
+                const bool slow = bar_sync_or(1, kSoftmaxThreads, bad_now || fresh || ex > kTau);
                 if (slow && bar_sync_or(1, kSoftmaxThreads, bad_now)) {
                     bad = true;
                     break;
                 }
                 if (slow) {
-                    if (!first) exp_pass(lpart, valid, -1.f, false, ex, ph);  // pass 1
+                    if (!fresh) exp_pass(lpart, valid, -1.f, false, ex, ph, part, dmax);  // pass 1
+                    if (WIN && st == 0) ms->empty_cols = 0;
                     // pass 2: exact column maxima of this tile, then move the shifts
 #pragma unroll 1
                     for (int cc = 0; cc < nch; ++cc) {
@@ -946,7 +1031,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int lim = valid ? R_seg - 16 * c : 0;
                         float v[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = k < lim ? __uint_as_float(r[k]) * sl2 : -INFINITY;
+                        for (int k = 0; k < 16; ++k) {
+                            v[k] = k < lim ? __uint_as_float(r[k]) * sl2 : -INFINITY;
+                            if (WIN && part && (int)ms->depth[16 * c + k] > dmax) v[k] = -INFINITY;
+                        }
                         // maxima of the 16 columns over the warp's 32 key lanes
                         const float cm = col_max16(v, lane);
                         if ((lane & 1) == 0) ms->col_red[quarter][16 * c + (lane >> 1)] = cm;
@@ -959,6 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float mn = fmaxf(mo, cm);
                         ms->alpha[col] = mn > mo ? ex2(mo - mn) : 1.f;
                         ms->m_ref[col] = mn;
+                        if (WIN && mn == -INFINITY) ms->empty_cols = 1;
                     }
                     bar_sync(1, kSoftmaxThreads);
 #pragma unroll
@@ -995,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!bad) tmem_wait_st();
                     }
-                    if (!bad) exp_pass(lpart, valid, 1.f, true, ex, ph);
+                    if (!bad) exp_pass(lpart, valid, 1.f, true, ex, ph, part, dmax);
                 }
                 // S^T is no longer read: the next tile's QK may overwrite it
                 tc_fence_before();
@@ -1212,11 +1301,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool BF16, int RGP, int VQ, int KQ>
+template <int D, bool BF16, int RGP, int VQ, int KQ, bool WIN>
 cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, const CUtensorMap& tve,
                        const CUtensorMap& tq2, const AttnLaunch& L, cudaStream_t stream) {
     using Lay = Layout<D, RGP>;
-    auto kern = prefix_tc_kernel<D, BF16, RGP, VQ, KQ>;
+    auto kern = prefix_tc_kernel<D, BF16, RGP, VQ, KQ, WIN>;
     static SmemLimitSeen seen;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Lay::kBytes, seen);
     if (e != cudaSuccess) return e;
@@ -1225,20 +1314,20 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
 
 // tve: the per-token exponents of quantised V (VQ != 0); tq2: the low query
 // parts of E4M3 K (KQ != 0); unused otherwise
-template <int D, bool BF16, int VQ = 0, int KQ = 0>
+template <int D, bool BF16, int VQ = 0, int KQ = 0, bool WIN = false>
 cudaError_t launch_rgp(int rgp, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                        const CUtensorMap& tve, const CUtensorMap& tq2, const AttnLaunch& L, cudaStream_t stream) {
     static_assert(kRowsMax == 144, "one instantiation per padded row count up to kRowsMax");
     switch (rgp) {
-        case 16: return launch_one<D, BF16, 16, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 32: return launch_one<D, BF16, 32, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 48: return launch_one<D, BF16, 48, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 64: return launch_one<D, BF16, 64, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 80: return launch_one<D, BF16, 80, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 96: return launch_one<D, BF16, 96, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 112: return launch_one<D, BF16, 112, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 128: return launch_one<D, BF16, 128, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
-        case 144: return launch_one<D, BF16, 144, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 16: return launch_one<D, BF16, 16, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 32: return launch_one<D, BF16, 32, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 48: return launch_one<D, BF16, 48, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 64: return launch_one<D, BF16, 64, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 80: return launch_one<D, BF16, 80, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 96: return launch_one<D, BF16, 96, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 112: return launch_one<D, BF16, 112, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 128: return launch_one<D, BF16, 128, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 144: return launch_one<D, BF16, 144, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -1257,6 +1346,11 @@ cudaError_t launch_prefix_tc_bf16_128(int rgp, const CUtensorMap&, const CUtenso
 cudaError_t launch_prefix_tc_f16_256(int rgp, int vq, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                      const CUtensorMap&, const AttnLaunch&, cudaStream_t);
 cudaError_t launch_prefix_tc_f16_128(int rgp, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                     const AttnLaunch&, cudaStream_t);
+// windowed (L.plan.window > 0), 16-bit K and V
+cudaError_t launch_prefix_tc_bf16_win(int rgp, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                      const AttnLaunch&, cudaStream_t);
+cudaError_t launch_prefix_tc_f16_win(int rgp, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                      const AttnLaunch&, cudaStream_t);
 
 }  // namespace lucetree

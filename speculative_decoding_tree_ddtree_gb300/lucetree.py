@@ -20,6 +20,7 @@ LUCETREE_V_SAME, LUCETREE_V_INT8, LUCETREE_V_INT4 = 0, 1, 2
 LUCETREE_K_SAME, LUCETREE_K_E4M3 = 0, 1
 LUCETREE_F16 = 0
 LUCETREE_BF16 = 1
+LUCETREE_F32 = 2
 PAGE_SIZE = 64
 MAX_NODES = 64
 
@@ -54,6 +55,7 @@ EXPORTED = (
     "lucetree_verify_attn_kq_workspace",
     "lucetree_verify_attn_kq",
     "lucetree_commit_kq",
+    "lucetree_verify_attn_win",
 )
 
 
@@ -70,6 +72,13 @@ class AttnArgs(ctypes.Structure):
         ("ctx_len", ctypes.c_void_p), ("k_tree", ctypes.c_void_p), ("v_tree", ctypes.c_void_p),
         ("anc_mask", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("status", ctypes.c_void_p),
+    ]
+
+
+class WinArgs(ctypes.Structure):
+    _fields_ = [
+        ("attn", AttnArgs), ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("out_dtype", ctypes.c_int),
+        ("out", ctypes.c_void_p),
     ]
 
 
@@ -158,6 +167,7 @@ def load(path: str | None = None):
     lib.lucetree_verify_attn_kq_workspace.argtypes = [I, I, I, I, I, ctypes.POINTER(SZ)]
     lib.lucetree_verify_attn_kq.argtypes = [ctypes.POINTER(AttnArgs), P, I, P, P, SZ, P]
     lib.lucetree_commit_kq.argtypes = [ctypes.POINTER(CommitArgs), P, P]
+    lib.lucetree_verify_attn_win.argtypes = [ctypes.POINTER(WinArgs), P, SZ, P]
     for name in EXPORTED:
         if name not in ("lucetree_status_string", "lucetree_abi_version"):
             getattr(lib, name).restype = I
@@ -231,6 +241,25 @@ def _expect_16bit(t, name: str, shape: tuple):
         raise LucetreeError(f"{name}: expected shape {tuple(shape)} of a 16-bit type, got {tuple(t.shape)} of {t.dtype}")
 
 
+def _expect_here(*tensors):
+    """Refuse tensors of several devices, or of a device that is not current:
+    a call acts on the current device and takes plain pointers."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise LucetreeError(f"tensors on several devices: {', '.join(sorted(str(d) for d in devices))}")
+    for d in devices:
+        if d.type == "cuda" and d.index != torch.cuda.current_device():
+            raise LucetreeError(f"tensors on {d}, but cuda:{torch.cuda.current_device()} is current")
+
+
+def _i32(v, name: str, lo: int = 0) -> int:
+    """A host integer that the C struct holds in an int."""
+    v = int(v)
+    if not lo <= v <= 0x7FFFFFFF:
+        raise LucetreeError(f"{name}: expected an integer in [{lo}, 2^31), got {v}")
+    return v
+
+
 def dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return LUCETREE_BF16
@@ -248,10 +277,11 @@ def lucetree_verify_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) ->
 
 
 def _check_attn(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse,
-                v_format=None, v_exp=None, k_exp=None):
+                v_format=None, v_exp=None, k_exp=None, out_types=_F32):
     """Shapes and element types of one tree-verify attention call (layouts as
     lucetree_verify_attn documents them); v_format selects the quantised V
-    pool, k_exp the E4M3 K pool (k_pool then holds the codes)."""
+    pool, k_exp the E4M3 K pool (k_pool then holds the codes), out_types the
+    element types the output may have."""
     B, N, Hq, D = _dims(q, "q", 4)
     if q.dtype not in _H16:
         raise LucetreeError(f"q: unsupported dtype {q.dtype}")
@@ -271,16 +301,16 @@ def _check_attn(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask
     _expect(page_table, "page_table", (B, _dims(page_table, "page_table", 2)[1]), _I32)
     _expect(ctx_len, "ctx_len", (B,), _I32)
     _expect(anc_mask, "anc_mask", (B, N), _W64)
-    _expect(out, "out", (B, N, Hq, D), _F32)
+    _expect(out, "out", (B, N, Hq, D), out_types)
     if lse is not None:
         _expect(lse, "lse", (B, N, Hq), _F32)
     _expect_status(status)
 
 
 def _attn_args(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse, scale,
-               v_format=None, v_exp=None, k_exp=None):
+               v_format=None, v_exp=None, k_exp=None, out_types=_F32):
     _check_attn(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse, v_format, v_exp,
-                k_exp)
+                k_exp, out_types)
     B, N, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     a = AttnArgs()
@@ -319,6 +349,23 @@ def lucetree_verify_attn_vq(q, k_pool, v_codes, v_exp, v_format, page_table, ctx
                    v_format=v_format, v_exp=v_exp)
     _check(load().lucetree_verify_attn_vq(ctypes.byref(a), int(v_format), _ptr(v_exp), _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def lucetree_verify_attn_win(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, window: int, sinks: int,
+                             out, status, workspace, lse=None, scale: float | None = None, stream=None):
+    """As lucetree_verify_attn with a sliding window and sinks: node i, at
+    position t_i = ctx_len + its depth, sees committed and tree positions p
+    with p < sinks or t_i - p < window.  out fp32 or in q's dtype."""
+    a = _attn_args(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse, scale,
+                   out_types=_F32 + ((q.dtype,) if q is not None else ()))
+    _expect_here(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, workspace, lse)
+    w = WinArgs()
+    w.attn = a
+    w.window, w.sinks = _i32(window, "window", 1), _i32(sinks, "sinks")
+    w.out_dtype = LUCETREE_F32 if out.dtype == torch.float32 else a.dtype
+    w.out = a.out
+    _check(load().lucetree_verify_attn_win(ctypes.byref(w), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def lucetree_verify_attn_kq_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
