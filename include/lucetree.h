@@ -88,6 +88,9 @@ typedef enum lucetree_dtype {
 #define LUCETREE_DEV_NONFINITE 0x40u /* an attention output is inf or NaN: non-finite inputs, or a bf16 V value
                                         of magnitude >= 65536 (beyond the fp16 range of the on-chip PV product) */
 
+#define LUCETREE_DEV_BAD_ROW 0x80u   /* source row outside [-1, rows) */
+#define LUCETREE_DEV_NO_PAGE 0x100u  /* the pool has no free page left */
+
 #define LUCETREE_PAGE_SIZE 64 /* tokens per KV page */
 #define LUCETREE_MAX_NODES 64 /* tree budget limit (one 64-bit ancestor mask per node) */
 
@@ -426,6 +429,48 @@ LUCETREE_API lucetree_status lucetree_lmhead_argmax_workspace(int rows, size_t* 
 LUCETREE_API lucetree_status lucetree_lmhead_argmax(const lucetree_lmhead_args* args, void* workspace,
                                                     size_t workspace_bytes, void* stream);
 
+#define LUCETREE_MAX_BEAMS 32 /* beams of one request */
+
+/* Arguments of lucetree_beam_select. */
+typedef struct lucetree_beam_args {
+    int dtype;               /* of the logits: LUCETREE_F32, LUCETREE_F16 or LUCETREE_BF16 */
+    int batch;               /* requests; batch * beams_in <= 65535 */
+    int beams_in, beams_out; /* beams of each request before and after, 1..LUCETREE_MAX_BEAMS,
+                                beams_out <= beams_in * vocab */
+    int vocab;
+    long long row_stride;    /* elements from one row of logits to the next, >= vocab */
+    const void* logits;      /* [batch][beams_in] rows of vocab, aligned to their type */
+    const float* cum;        /* [batch][beams_in] log-probability of each beam so far; -inf = a dead beam */
+    const int32_t* finished; /* [batch][beams_in] non-zero: the beam has ended, or NULL: none has */
+    int eos;                 /* token that ends a beam; outside [0, vocab) = none */
+    float* out_score;        /* [batch][beams_out], best first */
+    int32_t* out_token;      /* [batch][beams_out] */
+    int32_t* out_row;        /* [batch][beams_out]: row b * beams_in + beam that it continues */
+    int32_t* out_finished;   /* [batch][beams_out] 0 / 1, or NULL */
+} lucetree_beam_args;
+
+/* Workspace bytes of lucetree_beam_select on the CURRENT device (256-byte aligned, no initialisation). */
+LUCETREE_API lucetree_status lucetree_beam_select_workspace(int batch, int beams_in, int beams_out, int vocab,
+                                                            size_t* bytes);
+
+/*
+ * Beam selection over beams and vocabulary: the beams_out best of a request's
+ * candidates (beam k, token t), scored
+ *     cum_k + logit_kt - log sum_t' exp logit_kt'
+ * or, for a beam that has ended, cum_k for t = eos and -inf otherwise.  A
+ * masked logit (-inf), a beam with cum = -inf and a row of masked logits alone
+ * score -inf.  Ties go to the lower beam, then the lower token, -inf among
+ * them, so there are always beams_out candidates.  With beams_in = 1 this
+ * opens a search, or grows a node of a draft tree into its best children;
+ * out_row is the `src` of lucetree_reorder_pages and lucetree_reorder_states.
+ * The order within a row is that of the logits; sums are fp32 per thread and
+ * fp64 across chunks, scores fp64 and rounded once to fp32, so candidates of
+ * different beams closer than that may come in either order.  NaN and +inf
+ * logits are outside the contract.  The logits are read once.
+ */
+LUCETREE_API lucetree_status lucetree_beam_select(const lucetree_beam_args* args, void* workspace,
+                                                  size_t workspace_bytes, void* stream);
+
 /* Arguments of lucetree_delta_tree and lucetree_delta_commit. */
 typedef struct lucetree_delta_args {
     int dtype;               /* LUCETREE_F16 / LUCETREE_BF16: q, k, v */
@@ -500,6 +545,158 @@ typedef struct lucetree_stage_args {
  * that page is skipped).
  */
 LUCETREE_API lucetree_status lucetree_stage_pages(const lucetree_stage_args* args, void* stream);
+
+/*
+ * Page tables of sequences that share, take over and give back pages.  The
+ * pages describe the pool's 64-token chunks and a block table per sequence
+ * ("Lucebox Hub", sections "KVFlash" and "Paged attention + continuous
+ * batching"); the bookkeeping below is this library's.  The caller keeps, for
+ * one pool (or several of the same page numbering, one per layer),
+ *   - ref [num_pages]: how many table entries name each page, 0 = free;
+ *   - tables [rows][max_pages_per_seq]: -1 where a row maps nothing.
+ * The calls below change tables and counts together and say which pages' data
+ * has to move; lucetree_copy_pages then moves it in each layer's pools.  Where
+ * several choices are possible the lowest page and row numbers go first, so
+ * results depend on the inputs alone.
+ */
+
+#define LUCETREE_MAX_RESERVE 4032 /* positions past the committed length that lucetree_reorder_pages maps at most */
+
+/* Arguments of lucetree_reorder_pages. */
+typedef struct lucetree_reorder_args {
+    const int32_t* table_in;   /* [rows_in][max_pages_per_seq] */
+    const int32_t* ctx_in;     /* [rows_in] committed lengths */
+    int rows_in;
+    const int32_t* src;        /* [rows_out]: the old row that each new row continues, -1 = the new row is empty */
+    int rows_out;
+    int max_pages_per_seq;
+    int reserve;               /* positions [L, L + reserve) that every new row must map, 0..LUCETREE_MAX_RESERVE */
+    const int32_t* ref_in;     /* [num_pages] */
+    int num_pages;
+    int32_t* table_out;        /* [rows_out][max_pages_per_seq]; must not overlap table_in */
+    int32_t* ctx_out;          /* [rows_out]; must not overlap ctx_in */
+    int32_t* ref_out;          /* [num_pages]; may be ref_in */
+    int32_t* copy_src;         /* [rows_out]: page whose data goes ... */
+    int32_t* copy_dst;         /* [rows_out]: ... to this page for the new row, or -1 in both */
+    uint32_t* status;
+} lucetree_reorder_args;
+
+/* Workspace bytes of lucetree_reorder_pages (256-byte aligned, no initialisation). */
+LUCETREE_API lucetree_status lucetree_reorder_pages_workspace(int rows_in, int rows_out, int num_pages, size_t* bytes);
+
+/*
+ * All rows at once: new row r continues old row src[r].  One old row may be
+ * continued by several new ones (a fork; the beams of a search that descend
+ * from one), by one (a permutation) or by none (it ends and gives its pages
+ * back).  With L the old row's length:
+ *   - pages [0, L / 64) are shared: every new row names the old page;
+ *   - pages [L / 64, ceil((L + reserve) / 64)), into which the new row will
+ *     commit, are its own.  The lowest new row keeps those that no other row
+ *     held (count 1); every other one, and what was not mapped, is a free page
+ *     (free before the call; the lowest first, in the order of rows and
+ *     positions).  When L is not a multiple of 64 and the first of them is new,
+ *     (copy_src[r], copy_dst[r]) asks for its committed part to be copied;
+ *   - entries past that range are given back.
+ * ctx_out[r] = L (0 for an empty row).  Entries of -1 stay -1 in the shared range.
+ * Device checks: BAD_ROW (src out of range: the new row is empty), BAD_CTX (a
+ * length outside the table: that row keeps its pages and its new rows are
+ * empty; or L + reserve past the table: mapped as far as it goes), BAD_PAGE (an
+ * entry out of range, or a count that would fall below zero), NO_PAGE (no free
+ * page left: the entry is -1).
+ */
+LUCETREE_API lucetree_status lucetree_reorder_pages(const lucetree_reorder_args* args, void* workspace,
+                                                    size_t workspace_bytes, void* stream);
+
+/* Arguments of lucetree_trim_pages. */
+typedef struct lucetree_trim_args {
+    const int32_t* table_in;   /* [rows][max_pages_per_seq] */
+    const int32_t* ctx_len;    /* [rows] */
+    int rows;
+    int max_pages_per_seq;
+    int window, sinks;         /* of lucetree_verify_attn_win: window >= 1, sinks >= 0 */
+    const int32_t* ref_in;     /* [num_pages] */
+    int num_pages;
+    int32_t* table_out;        /* may be table_in */
+    int32_t* ref_out;          /* may be ref_in */
+    uint32_t* status;
+} lucetree_trim_args;
+
+/*
+ * Gives back the pages that lie wholly behind the window: those without a
+ * position below `sinks` or at or past L - window + 1.  Their entries become
+ * -1 and their counts drop by one; lucetree_verify_attn_win with the same
+ * window and sinks reads none of them, now or at any greater length.
+ * Device checks: BAD_CTX (the row is left as it is), BAD_PAGE (such an entry
+ * out of range, or a count that would fall below zero).
+ */
+LUCETREE_API lucetree_status lucetree_trim_pages(const lucetree_trim_args* args, void* stream);
+
+/* Arguments of lucetree_compact_pages. */
+typedef struct lucetree_compact_args {
+    const int32_t* table_in;   /* [rows][max_pages_per_seq]: every table that names pages of the pool */
+    int rows;
+    int max_pages_per_seq;
+    const int32_t* ref_in;     /* [num_pages] */
+    int num_pages;
+    int32_t* table_out;        /* may be table_in */
+    int32_t* ref_out;          /* may be ref_in */
+    int32_t* copy_src;         /* [num_pages / 2]: pages that move ... */
+    int32_t* copy_dst;         /* [num_pages / 2]: ... and where to; -1 in both past copy_n */
+    int32_t* copy_n;           /* [1] */
+    int32_t* live;             /* [1] pages in use: they are [0, live) afterwards */
+    uint32_t* status;
+} lucetree_compact_args;
+
+/* Workspace bytes of lucetree_compact_pages (256-byte aligned, no initialisation). */
+LUCETREE_API lucetree_status lucetree_compact_pages_workspace(int num_pages, size_t* bytes);
+
+/*
+ * Closes the pool up: with `live` pages in use (count > 0), the k-th used page
+ * at or past `live` moves to the k-th free page before it.  Tables and counts
+ * take the new numbers; no page that moves is a target, so the copies may run
+ * in any order.  Device check: BAD_PAGE (an entry out of range, or one that
+ * names a free page at or past `live`: it becomes -1).
+ */
+LUCETREE_API lucetree_status lucetree_compact_pages(const lucetree_compact_args* args, void* workspace,
+                                                    size_t workspace_bytes, void* stream);
+
+/* Arguments of lucetree_copy_pages. */
+typedef struct lucetree_copy_pages_args {
+    const int32_t* src;        /* [n] pages */
+    const int32_t* dst;        /* [n] distinct pages, none of them in src; (-1, -1) is no copy */
+    int n;
+    const int32_t* count;      /* device [1]: only the first *count pairs, or NULL */
+    void* k_pool;              /* [num_pages][k_page_bytes], 16-byte aligned */
+    void* v_pool;              /* [num_pages][v_page_bytes], 16-byte aligned, or NULL */
+    long long k_page_bytes;    /* positive multiples of 16 */
+    long long v_page_bytes;
+    int num_pages;
+    uint32_t* status;
+} lucetree_copy_pages_args;
+
+/*
+ * Copies pages src[i] to dst[i] within both pools, byte for byte (any element
+ * types: the pools of quantised caches and their exponents too).  Device
+ * check: BAD_PAGE (a page out of range: that pair is skipped).
+ */
+LUCETREE_API lucetree_status lucetree_copy_pages(const lucetree_copy_pages_args* args, void* stream);
+
+/* Arguments of lucetree_reorder_states. */
+typedef struct lucetree_reorder_states_args {
+    const void* state_in;      /* [rows_in][row_bytes], 16-byte aligned */
+    void* state_out;           /* [rows_out][row_bytes]; must not overlap state_in */
+    const int32_t* src;        /* [rows_out], as for lucetree_reorder_pages */
+    int rows_in, rows_out;
+    long long row_bytes;       /* a positive multiple of 16 */
+    uint32_t* status;
+} lucetree_reorder_states_args;
+
+/*
+ * state_out[r] = state_in[src[r]] for the recurrent states (or any per-row
+ * data) of sequences that lucetree_reorder_pages rearranges; rows with src
+ * -1 are left as they were.  Device check: BAD_ROW (that row is left).
+ */
+LUCETREE_API lucetree_status lucetree_reorder_states(const lucetree_reorder_states_args* args, void* stream);
 
 /*
  * Self-test of the failure path shared by every kernel wait: one block waits

@@ -1,0 +1,452 @@
+// beam.cu -- lucetree_beam_select: the best continuations of a request's beams
+// over the whole vocabulary.
+//
+// score(k, t) = cum_k + x_kt - log sum_t' exp x_kt'.  Within a row the order is
+// that of the logits, so one pass over a row finds both its softmax sum and its
+// best Kout tokens; only those can be among the request's best Kout.
+//
+// Launch 1 cuts the rows into chunks (about four CTAs per SM over all rows).
+// Each thread keeps a running maximum and sum of its elements; each warp keeps
+// a sorted list of its 32 best (logit, token) keys, one in each lane, as 64-bit
+// integers whose order is (logit descending, token ascending).  A list changes
+// seldom: elements are compared with its Kout-th key, those that pass go to
+// a 64-entry buffer in shared memory, and 32 of them at a time are sorted and
+// merged in (bitonic networks of shuffles).  The first batch's lane maxima give
+// the starting threshold.
+// Launch 2, one CTA per request, merges the chunks' lists and sums row by row,
+// turns the rows' lists into scores in 64 bits (neighbouring candidates of
+// different rows are closer than fp32 keeps beside a long sum) and merges those.
+// Bound by reading the logits once.
+#include "beam.h"
+#include "internal.cuh"
+
+namespace lucetree {
+
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kU = 8;  // 16-byte loads in flight per thread
+constexpr int kMergeThreads = 1024;
+constexpr int kMergeWarps = kMergeThreads / 32;
+
+struct BeamLaunch {
+    lucetree_beam_args a;
+    int chunks;
+    u64* keys;     // [rows][chunks][32]
+    float2* sums;  // [rows][chunks] (maximum, sum of exp(x - maximum))
+};
+
+// Order of (x, index) as an integer: larger x first, then the lower index;
+// -0.0 ties +0.0.  0 is below every element.
+__device__ inline u64 pack_key(float x, unsigned idx) {
+    if (x == 0.f) x = 0.f;
+    unsigned u = __float_as_uint(x);
+    u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return ((u64)u << 32) | (u64)(~idx);
+}
+__device__ inline float key_value(u64 k) {
+    const unsigned u = (unsigned)(k >> 32);
+    return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
+}
+__device__ inline unsigned key_index(u64 k) { return ~(unsigned)k; }
+
+// Keys across the warp's lanes, descending by lane.
+__device__ inline u64 exchange(u64 k, int stride, bool keep_max) {
+    const u64 o = __shfl_xor_sync(0xffffffffu, k, stride);
+    return (k > o) == keep_max ? k : o;
+}
+__device__ inline u64 sort32(u64 k) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1)
+            k = exchange(k, stride, ((lane & stride) == 0) == ((lane & size) == 0));
+    return k;
+}
+// The 32 best of two descending lists.
+__device__ inline u64 merge32(u64 a, u64 b) {
+    const int lane = threadIdx.x & 31;
+    const u64 r = __shfl_sync(0xffffffffu, b, 31 - lane);
+    u64 k = a > r ? a : r;
+#pragma unroll
+    for (int stride = 16; stride > 0; stride >>= 1) k = exchange(k, stride, (lane & stride) == 0);
+    return k;
+}
+
+// A warp's list with its buffer of candidates.
+struct TopList {
+    u64 list;   // this lane's key
+    u64 limit;  // the Kout-th key: only larger ones matter
+    float low;  // its logit
+    int count;  // candidates in the buffer
+    u64* buf;   // 64 keys of shared memory
+
+    __device__ void set_limit(u64 k) {
+        if (k > limit) {
+            limit = k;
+            low = key_value(k);
+        }
+    }
+    __device__ void flush(int kout) {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        list = merge32(list, sort32(lane < count ? buf[lane] : 0));
+        const u64 rest = lane + 32 < count ? buf[lane + 32] : 0;
+        __syncwarp();
+        buf[lane] = rest;
+        count = max(count - 32, 0);
+        set_limit(__shfl_sync(0xffffffffu, list, kout - 1));
+    }
+    // One element of each lane; `in`: it is one.
+    __device__ void offer(float x, unsigned idx, bool in, int kout) {
+        const u64 key = in && x >= low ? pack_key(x, idx) : 0;
+        const bool pass = key > limit;
+        const unsigned who = __ballot_sync(0xffffffffu, pass);
+        if (!who) return;
+        if (pass) buf[count + __popc(who & ((1u << (threadIdx.x & 31)) - 1u))] = key;
+        count += __popc(who);
+        if (count >= 32) flush(kout);
+    }
+};
+
+template <typename T>
+struct Vec {
+    static constexpr int kE = 16 / sizeof(T);
+};
+
+template <typename T>
+__device__ inline void unpack(const uint4& u, float (&x)[Vec<T>::kE]) {
+    if constexpr (sizeof(T) == 4) {
+        x[0] = __uint_as_float(u.x);
+        x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z);
+        x[3] = __uint_as_float(u.w);
+    } else {
+        load8_f32<T>(reinterpret_cast<const T*>(&u), x);
+    }
+}
+
+__device__ inline float scalar(const float* p) { return *p; }
+__device__ inline float scalar(const __half* p) { return __half2float(*p); }
+__device__ inline float scalar(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+__device__ inline float exp_diff(float x, float m) { return exp2f((x - m) * kLog2e); }
+
+// (m, s) += (m2, s2): sums of exponentials relative to their maxima; a maximum of -inf has sum 0.
+__device__ inline void add_sums(float& m, float& s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    if (top == -INFINITY) return;
+    s = (m == -INFINITY ? 0.f : s * exp_diff(m, top)) + (m2 == -INFINITY ? 0.f : s2 * exp_diff(m2, top));
+    m = top;
+}
+
+__device__ inline bool row_ended(const lucetree_beam_args& a, int row) {
+    return a.finished && a.finished[row] != 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamLaunch L) {
+    constexpr int kE = Vec<T>::kE;
+    __shared__ u64 s_buf[kWarps][64];
+    __shared__ float2 s_sum[kWarps];
+    const lucetree_beam_args& a = L.a;
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    const int row = blockIdx.y, chunk = blockIdx.x;
+    // rows that ended or are dead need no logits (launch 2 knows their candidates)
+    if (row_ended(a, row) || a.cum[row] == -INFINITY) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kout = a.beams_out;
+    const T* x = reinterpret_cast<const T*>(a.logits) + (long long)row * a.row_stride;
+    // 16-byte vectors from the first aligned element on; the elements before
+    // and behind them (fewer than 2 kE) belong to the row's last chunk
+    const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)), a.vocab);
+    const int nv = (a.vocab - head) / kE;
+    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+    const int v0 = (int)((long long)nv * chunk / L.chunks), v1 = (int)((long long)nv * (chunk + 1) / L.chunks);
+
+    TopList top{0, 0, -INFINITY, 0, s_buf[warp]};
+    float m = -INFINITY, s = 0.f;
+    for (int base = v0; base < v1; base += kU * kThreads) {
+        uint4 u[kU];
+        bool in[kU];
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            const int v = base + k * kThreads + threadIdx.x;
+            in[k] = v < v1;
+            if (in[k]) u[k] = __ldcs(xv + v);
+        }
+        float mb = -INFINITY;
+        u64 best = 0;
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            float f[kE];
+            unpack<T>(u[k], f);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) mb = in[k] ? fmaxf(mb, f[e]) : mb;
+        }
+        if (base == v0) {
+            // lane maxima are elements: the Kout-th of them bounds the Kout-th element from below (a key
+            // with the highest index of its value, so that no tie is lost)
+            best = sort32(pack_key(mb, 0xffffffffu));
+            top.set_limit(__shfl_sync(0xffffffffu, best, kout - 1));
+        }
+        if (mb > m) {
+            s = m == -INFINITY ? 0.f : s * exp_diff(m, mb);
+            m = mb;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            float f[kE];
+            unpack<T>(u[k], f);
+            float vm = -INFINITY;
+            float part = 0.f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                part += exp_diff(f[e], mm);
+                vm = fmaxf(vm, f[e]);
+            }
+            if (in[k]) s += part;
+            if (__any_sync(0xffffffffu, in[k] && vm >= top.low)) {
+                const unsigned idx = (unsigned)(head + (base + k * kThreads + (int)threadIdx.x) * kE);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) top.offer(f[e], idx + e, in[k], kout);
+            }
+        }
+    }
+    if (chunk == L.chunks - 1 && warp == 0) {
+        const int tail = head + nv * kE;  // first element behind the vectors
+        const int t = lane < head ? lane : tail + lane - head;
+        const bool in = t < a.vocab && (lane < head || t >= tail);
+        const float f = in ? scalar(x + t) : -INFINITY;
+        if (in) add_sums(m, s, f, f == -INFINITY ? 0.f : 1.f);
+        top.offer(f, (unsigned)t, in, kout);
+    }
+    if (top.count > 0) top.flush(kout);
+    // the CTA's sum and list
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        add_sums(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+    __syncwarp();
+    s_buf[warp][lane] = top.list;
+    if (lane == 0) s_sum[warp] = make_float2(m, s);
+#pragma unroll
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        if (warp < half) {
+            const u64 k = merge32(s_buf[warp][lane], s_buf[warp + half][lane]);
+            s_buf[warp][lane] = k;
+        }
+    }
+    if (warp == 0) {
+        const size_t at = (size_t)row * L.chunks + chunk;
+        L.keys[at * 32 + lane] = s_buf[0][lane];
+        if (lane == 0) {
+            for (int w = 1; w < kWarps; ++w) add_sums(m, s, s_sum[w].x, s_sum[w].y);
+            L.sums[at] = make_float2(m, s);
+        }
+    }
+}
+
+// A candidate of the request: score as an ordered integer, then beam * vocab + token.
+struct Cand {
+    u64 score, index;
+};
+__device__ inline bool better(const Cand& p, const Cand& q) {
+    return p.score > q.score || (p.score == q.score && p.index < q.index);
+}
+__device__ inline Cand shfl_xor(const Cand& c, int stride) {
+    return Cand{__shfl_xor_sync(0xffffffffu, c.score, stride), __shfl_xor_sync(0xffffffffu, c.index, stride)};
+}
+__device__ inline Cand exchange(const Cand& c, int stride, bool keep_best) {
+    const Cand o = shfl_xor(c, stride);
+    return better(c, o) == keep_best ? c : o;
+}
+__device__ inline Cand sort32(Cand c) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1)
+            c = exchange(c, stride, ((lane & stride) == 0) == ((lane & size) == 0));
+    return c;
+}
+__device__ inline Cand merge32(const Cand& a, const Cand& b) {
+    const int lane = threadIdx.x & 31;
+    const Cand r{__shfl_sync(0xffffffffu, b.score, 31 - lane), __shfl_sync(0xffffffffu, b.index, 31 - lane)};
+    Cand c = better(a, r) ? a : r;
+#pragma unroll
+    for (int stride = 16; stride > 0; stride >>= 1) c = exchange(c, stride, (lane & stride) == 0);
+    return c;
+}
+
+__device__ inline u64 order_double(double x) {
+    if (x == 0.0) x = 0.0;
+    const u64 u = (u64)__double_as_longlong(x);
+    return (u >> 63) ? ~u : (u | (1ull << 63));
+}
+__device__ inline double order_value(u64 u) {
+    return __longlong_as_double((long long)((u >> 63) ? u & ~(1ull << 63) : ~u));
+}
+
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L) {
+    __shared__ u64 s_keys[kMergeWarps][32];
+    __shared__ Cand s_cand[kMergeWarps][32];
+    const lucetree_beam_args& a = L.a;
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int K = a.beams_in;
+    // `per` warps to a row merge its chunks' lists
+    const int per = kMergeWarps / K;
+    const int k = warp / per, w = warp % per;
+    const int row = b * K + k;
+    const bool mine = k < K;
+    const bool ended = mine && row_ended(a, row);
+    const bool dead = mine && !ended && a.cum[row] == -INFINITY;
+    u64 list = 0;
+    if (mine && !ended && !dead) {
+        const u64* keys = L.keys + (size_t)row * L.chunks * 32;
+        for (int c = w; c < L.chunks; c += per) list = merge32(list, keys[(size_t)c * 32 + lane]);
+    }
+    s_keys[warp][lane] = list;
+    __syncthreads();
+    Cand cand{0, ~0ull};  // none: behind every candidate
+    if (mine && w == 0) {
+        for (int o = 1; o < per; ++o) list = merge32(list, s_keys[warp + o][lane]);
+        const float cum = a.cum[row];
+        int token = lane;
+        double score = -INFINITY;
+        bool have = lane < a.vocab;
+        if (ended) {
+            // one candidate, then the other tokens in order at -inf
+            const bool eos = a.eos >= 0 && a.eos < a.vocab;
+            if (eos) token = lane == 0 ? a.eos : (lane - 1 < a.eos ? lane - 1 : lane);
+            if (eos && lane == 0) score = cum;
+        } else if (!dead) {
+            // log-sum-exp of the row from its chunks
+            float m = -INFINITY;
+            for (int c = lane; c < L.chunks; c += 32) m = fmaxf(m, L.sums[(size_t)row * L.chunks + c].x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (m > -INFINITY) {
+                double s = 0.0;
+                for (int c = lane; c < L.chunks; c += 32) {
+                    const float2 p = L.sums[(size_t)row * L.chunks + c];
+                    if (p.x > -INFINITY) s += (double)p.y * exp((double)p.x - (double)m);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                const double lse = (double)m + log(s);
+                have = list != 0;
+                token = have ? (int)key_index(list) : 0;
+                const float x = key_value(list);
+                if (have && x > -INFINITY) score = (double)cum + ((double)x - lse);
+                if (!(score == score)) score = -INFINITY;
+            }
+        }
+        if (have) cand = Cand{order_double(score), (u64)k * (u64)a.vocab + (u64)token};
+        // scores follow the logits' order, but ties of rounded scores and -inf follow the index
+        cand = sort32(cand);
+    }
+    if (mine && w == 0) s_cand[k][lane] = cand;
+    for (int half = 16; half > 0; half >>= 1) {
+        __syncthreads();
+        if (warp < half && warp + half < K) s_cand[warp][lane] = merge32(s_cand[warp][lane], s_cand[warp + half][lane]);
+    }
+    if (warp == 0 && lane < a.beams_out) {
+        const Cand c = s_cand[0][lane];
+        const int beam = (int)(c.index / (u64)a.vocab), token = (int)(c.index % (u64)a.vocab);
+        const size_t at = (size_t)b * a.beams_out + lane;
+        a.out_score[at] = (float)order_value(c.score);
+        a.out_token[at] = token;
+        a.out_row[at] = b * K + beam;
+        if (a.out_finished) a.out_finished[at] = (row_ended(a, b * K + beam) || token == a.eos) ? 1 : 0;
+    }
+}
+
+// About four CTAs per SM over all rows, and no chunk shorter than a round of loads of half the CTA's threads.
+int beam_chunks(int rows, int vocab, int sms) {
+    int chunks = (4 * sms + rows - 1) / rows;
+    const int most = (vocab + 4 * kThreads - 1) / (4 * kThreads);
+    if (chunks > most) chunks = most;
+    return chunks < 1 ? 1 : chunks;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t beam_workspace_bytes(int batch, int beams, int vocab, int device) {
+    const size_t lists = (size_t)batch * beams * beam_chunks(batch * beams, vocab, device_sm_count(device));
+    return align256(lists * 32 * sizeof(u64)) + align256(lists * sizeof(float2));
+}
+
+cudaError_t launch_beam_select(const lucetree_beam_args& a, void* workspace, int device, cudaStream_t stream) {
+    BeamLaunch L;
+    L.a = a;
+    const int rows = a.batch * a.beams_in;
+    L.chunks = beam_chunks(rows, a.vocab, device_sm_count(device));
+    L.keys = reinterpret_cast<u64*>(workspace);
+    L.sums = reinterpret_cast<float2*>(reinterpret_cast<char*>(workspace) +
+                                       align256((size_t)rows * L.chunks * 32 * sizeof(u64)));
+    const dim3 grid(L.chunks, rows), block(kThreads);
+    cudaError_t e;
+    if (a.dtype == LUCETREE_F32) e = launch_pdl(beam_scan_kernel<float>, grid, block, 0, stream, L);
+    else if (a.dtype == LUCETREE_BF16) e = launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, block, 0, stream, L);
+    else e = launch_pdl(beam_scan_kernel<__half>, grid, block, 0, stream, L);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(beam_merge_kernel, dim3(a.batch), dim3(kMergeThreads), 0, stream, L);
+}
+
+}  // namespace lucetree
+
+using namespace lucetree;
+
+extern "C" {
+
+static lucetree_status beam_sizes(int batch, int beams_in, int beams_out, int vocab) {
+    if (batch < 1 || beams_in < 1 || beams_out < 1 || vocab < 1) return LUCETREE_ERR_INVALID_ARG;
+    if (beams_in > LUCETREE_MAX_BEAMS || beams_out > LUCETREE_MAX_BEAMS || (long long)batch * beams_in > 65535)
+        return LUCETREE_ERR_UNSUPPORTED;
+    if (beams_out > (long long)beams_in * vocab) return LUCETREE_ERR_INVALID_ARG;  // fewer candidates than beams
+    return LUCETREE_OK;
+}
+
+lucetree_status lucetree_beam_select_workspace(int batch, int beams_in, int beams_out, int vocab, size_t* bytes) {
+    if (!bytes) return LUCETREE_ERR_INVALID_ARG;
+    const lucetree_status st = beam_sizes(batch, beams_in, beams_out, vocab);
+    if (st != LUCETREE_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    *bytes = beam_workspace_bytes(batch, beams_in, vocab, dev);
+    return LUCETREE_OK;
+}
+
+lucetree_status lucetree_beam_select(const lucetree_beam_args* a, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    if (!a) return LUCETREE_ERR_INVALID_ARG;
+    if (a->dtype != LUCETREE_F16 && a->dtype != LUCETREE_BF16 && a->dtype != LUCETREE_F32)
+        return LUCETREE_ERR_UNSUPPORTED;
+    const lucetree_status st = beam_sizes(a->batch, a->beams_in, a->beams_out, a->vocab);
+    if (st != LUCETREE_OK) return st;
+    const uintptr_t elem = a->dtype == LUCETREE_F32 ? 4 : 2;
+    if (!a->logits || !a->cum || !a->out_score || !a->out_token || !a->out_row || a->row_stride < a->vocab ||
+        (reinterpret_cast<uintptr_t>(a->logits) & (elem - 1)) != 0)
+        return LUCETREE_ERR_INVALID_ARG;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    if (!workspace || workspace_bytes < beam_workspace_bytes(a->batch, a->beams_in, a->vocab, dev) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return LUCETREE_ERR_WORKSPACE;
+    if (launch_beam_select(*a, workspace, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return LUCETREE_ERR_CUDA;
+    return LUCETREE_OK;
+}
+
+}  // extern "C"

@@ -31,6 +31,10 @@ DEV_BAD_TOKEN = 0x8
 DEV_BAD_NODE = 0x10
 DEV_TIMEOUT = 0x20
 DEV_NONFINITE = 0x40
+DEV_BAD_ROW = 0x80
+DEV_NO_PAGE = 0x100
+MAX_BEAMS = 32  # LUCETREE_MAX_BEAMS
+MAX_RESERVE = 4032  # LUCETREE_MAX_RESERVE of include/lucetree.h
 
 EXPORTED = (
     "lucetree_verify_attn_workspace",
@@ -56,6 +60,15 @@ EXPORTED = (
     "lucetree_verify_attn_kq",
     "lucetree_commit_kq",
     "lucetree_verify_attn_win",
+    "lucetree_reorder_pages_workspace",
+    "lucetree_reorder_pages",
+    "lucetree_trim_pages",
+    "lucetree_compact_pages_workspace",
+    "lucetree_compact_pages",
+    "lucetree_copy_pages",
+    "lucetree_reorder_states",
+    "lucetree_beam_select_workspace",
+    "lucetree_beam_select",
 )
 
 
@@ -131,6 +144,60 @@ class StageArgs(ctypes.Structure):
     ]
 
 
+class BeamArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("batch", ctypes.c_int), ("beams_in", ctypes.c_int), ("beams_out", ctypes.c_int),
+        ("vocab", ctypes.c_int), ("row_stride", ctypes.c_longlong), ("logits", ctypes.c_void_p),
+        ("cum", ctypes.c_void_p), ("finished", ctypes.c_void_p), ("eos", ctypes.c_int),
+        ("out_score", ctypes.c_void_p), ("out_token", ctypes.c_void_p), ("out_row", ctypes.c_void_p),
+        ("out_finished", ctypes.c_void_p),
+    ]
+
+
+class ReorderArgs(ctypes.Structure):
+    _fields_ = [
+        ("table_in", ctypes.c_void_p), ("ctx_in", ctypes.c_void_p), ("rows_in", ctypes.c_int),
+        ("src", ctypes.c_void_p), ("rows_out", ctypes.c_int), ("max_pages_per_seq", ctypes.c_int),
+        ("reserve", ctypes.c_int), ("ref_in", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+        ("table_out", ctypes.c_void_p), ("ctx_out", ctypes.c_void_p), ("ref_out", ctypes.c_void_p),
+        ("copy_src", ctypes.c_void_p), ("copy_dst", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class TrimArgs(ctypes.Structure):
+    _fields_ = [
+        ("table_in", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("rows", ctypes.c_int),
+        ("max_pages_per_seq", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int),
+        ("ref_in", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("table_out", ctypes.c_void_p),
+        ("ref_out", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class CompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("table_in", ctypes.c_void_p), ("rows", ctypes.c_int), ("max_pages_per_seq", ctypes.c_int),
+        ("ref_in", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("table_out", ctypes.c_void_p),
+        ("ref_out", ctypes.c_void_p), ("copy_src", ctypes.c_void_p), ("copy_dst", ctypes.c_void_p),
+        ("copy_n", ctypes.c_void_p), ("live", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class CopyPagesArgs(ctypes.Structure):
+    _fields_ = [
+        ("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int), ("count", ctypes.c_void_p),
+        ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_page_bytes", ctypes.c_longlong),
+        ("v_page_bytes", ctypes.c_longlong), ("num_pages", ctypes.c_int), ("status", ctypes.c_void_p),
+    ]
+
+
+class ReorderStatesArgs(ctypes.Structure):
+    _fields_ = [
+        ("state_in", ctypes.c_void_p), ("state_out", ctypes.c_void_p), ("src", ctypes.c_void_p),
+        ("rows_in", ctypes.c_int), ("rows_out", ctypes.c_int), ("row_bytes", ctypes.c_longlong),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -168,6 +235,15 @@ def load(path: str | None = None):
     lib.lucetree_verify_attn_kq.argtypes = [ctypes.POINTER(AttnArgs), P, I, P, P, SZ, P]
     lib.lucetree_commit_kq.argtypes = [ctypes.POINTER(CommitArgs), P, P]
     lib.lucetree_verify_attn_win.argtypes = [ctypes.POINTER(WinArgs), P, SZ, P]
+    lib.lucetree_reorder_pages_workspace.argtypes = [I, I, I, ctypes.POINTER(SZ)]
+    lib.lucetree_reorder_pages.argtypes = [ctypes.POINTER(ReorderArgs), P, SZ, P]
+    lib.lucetree_trim_pages.argtypes = [ctypes.POINTER(TrimArgs), P]
+    lib.lucetree_compact_pages_workspace.argtypes = [I, ctypes.POINTER(SZ)]
+    lib.lucetree_compact_pages.argtypes = [ctypes.POINTER(CompactArgs), P, SZ, P]
+    lib.lucetree_copy_pages.argtypes = [ctypes.POINTER(CopyPagesArgs), P]
+    lib.lucetree_beam_select_workspace.argtypes = [I, I, I, I, ctypes.POINTER(SZ)]
+    lib.lucetree_beam_select.argtypes = [ctypes.POINTER(BeamArgs), P, SZ, P]
+    lib.lucetree_reorder_states.argtypes = [ctypes.POINTER(ReorderStatesArgs), P]
     for name in EXPORTED:
         if name not in ("lucetree_status_string", "lucetree_abi_version"):
             getattr(lib, name).restype = I
@@ -719,6 +795,180 @@ def lucetree_stage_pages(host_k, host_v, src, dst, k_pool, v_pool, status, table
     a.k_pool, a.v_pool, a.num_pages = _ptr(k_pool), _ptr(v_pool), k_pool.shape[0]
     a.status = _ptr(status)
     _check(load().lucetree_stage_pages(ctypes.byref(a), _stream(stream)))
+
+
+# ---------------------------------------------------------------- beam selection
+
+def lucetree_beam_select_workspace(batch: int, beams_in: int, beams_out: int, vocab: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().lucetree_beam_select_workspace(_i32(batch, "batch", 1), _i32(beams_in, "beams_in", 1),
+                                                 _i32(beams_out, "beams_out", 1), _i32(vocab, "vocab", 1),
+                                                 ctypes.byref(n)))
+    return int(n.value)
+
+
+def lucetree_beam_select(logits, cum, finished, eos: int, out_score, out_token, out_row, out_finished, workspace,
+                         stream=None):
+    """The best continuations of each request's beams: logits [B][K][V] (fp32 or
+    16-bit; rows may be further apart than V), cum fp32 [B][K], finished int32
+    [B][K] or None -> out_score fp32, out_token, out_row (b * K + beam), out_finished
+    (or None) int32, all [B][Kout], best first."""
+    B, K, V = _dims(logits, "logits", 3)
+    if logits.dtype not in _H16 + _F32:
+        raise LucetreeError(f"logits: unsupported dtype {logits.dtype}")
+    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or stride < V or (B > 1 and logits.stride(0) != K * stride):
+        raise LucetreeError(f"logits: rows must be contiguous and evenly spaced, got strides {logits.stride()}")
+    if not -0x80000000 <= int(eos) <= 0x7FFFFFFF:
+        raise LucetreeError(f"eos: expected a 32-bit integer, got {eos}")
+    Kout = _dims(out_score, "out_score", 2)[1]
+    for t, name, shape, types in ((cum, "cum", (B, K), _F32), (out_score, "out_score", (B, Kout), _F32),
+                                  (out_token, "out_token", (B, Kout), _I32), (out_row, "out_row", (B, Kout), _I32)):
+        _expect(t, name, shape, types)
+    if finished is not None:
+        _expect(finished, "finished", (B, K), _I32)
+    if out_finished is not None:
+        _expect(out_finished, "out_finished", (B, Kout), _I32)
+    _expect_here(logits, cum, finished, out_score, out_token, out_row, out_finished, workspace)
+    a = BeamArgs()
+    a.dtype = LUCETREE_F32 if logits.dtype == torch.float32 else dtype_code(logits)
+    a.batch, a.beams_in, a.beams_out, a.vocab, a.row_stride = B, K, Kout, V, stride
+    a.logits, a.cum, a.finished, a.eos = logits.data_ptr(), _ptr(cum), _ptr(finished), int(eos)
+    a.out_score, a.out_token, a.out_row = _ptr(out_score), _ptr(out_token), _ptr(out_row)
+    a.out_finished = _ptr(out_finished)
+    _check(load().lucetree_beam_select(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream(stream)))
+
+
+# ---------------------------------------------------------------- page tables, counts and copies
+
+def lucetree_reorder_pages_workspace(rows_in: int, rows_out: int, num_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().lucetree_reorder_pages_workspace(_i32(rows_in, "rows_in", 1), _i32(rows_out, "rows_out", 1),
+                                                   _i32(num_pages, "num_pages", 1), ctypes.byref(n)))
+    return int(n.value)
+
+
+def lucetree_reorder_pages(table_in, ctx_in, src, reserve: int, ref_in, table_out, ctx_out, ref_out, copy_src, copy_dst,
+                           status, workspace, stream=None):
+    """New row r continues old row src[r] (-1: it is empty): table_in [rows_in][P],
+    ctx_in [rows_in], src [rows_out] -> table_out [rows_out][P], ctx_out
+    [rows_out], with ref_in / ref_out [num_pages] (may be one tensor) the
+    pages' counts.  Every new row has its own pages for the positions
+    [L, L + reserve); (copy_src, copy_dst) [rows_out] are the page copies that
+    this takes, for lucetree_copy_pages.  All int32."""
+    rows_in, P = _dims(table_in, "table_in", 2)
+    rows = _dims(src, "src", 1)[0]
+    pages = _dims(ref_in, "ref_in", 1)[0]
+    for t, name, shape in ((table_in, "table_in", (rows_in, P)), (ctx_in, "ctx_in", (rows_in,)), (src, "src", (rows,)),
+                           (ref_in, "ref_in", (pages,)), (table_out, "table_out", (rows, P)),
+                           (ctx_out, "ctx_out", (rows,)), (ref_out, "ref_out", (pages,)),
+                           (copy_src, "copy_src", (rows,)), (copy_dst, "copy_dst", (rows,))):
+        _expect(t, name, shape, _I32)
+    _expect_status(status)
+    _expect_here(table_in, ctx_in, src, ref_in, table_out, ctx_out, ref_out, copy_src, copy_dst, status, workspace)
+    a = ReorderArgs()
+    a.table_in, a.ctx_in, a.rows_in = _ptr(table_in), _ptr(ctx_in), rows_in
+    a.src, a.rows_out, a.max_pages_per_seq = _ptr(src), rows, P
+    a.reserve = _i32(reserve, "reserve")
+    a.ref_in, a.num_pages = _ptr(ref_in), pages
+    a.table_out, a.ctx_out, a.ref_out = _ptr(table_out), _ptr(ctx_out), _ptr(ref_out)
+    a.copy_src, a.copy_dst, a.status = _ptr(copy_src), _ptr(copy_dst), _ptr(status)
+    _check(load().lucetree_reorder_pages(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         _stream(stream)))
+
+
+def lucetree_trim_pages(table_in, ctx_len, window: int, sinks: int, ref_in, table_out, ref_out, status, stream=None):
+    """Give back the pages wholly behind the window of lucetree_verify_attn_win:
+    their entries of table_in [rows][P] are -1 in table_out, their counts one
+    less in ref_out (outputs may be the inputs).  All int32."""
+    rows, P = _dims(table_in, "table_in", 2)
+    pages = _dims(ref_in, "ref_in", 1)[0]
+    for t, name, shape in ((table_in, "table_in", (rows, P)), (ctx_len, "ctx_len", (rows,)), (ref_in, "ref_in", (pages,)),
+                           (table_out, "table_out", (rows, P)), (ref_out, "ref_out", (pages,))):
+        _expect(t, name, shape, _I32)
+    _expect_status(status)
+    _expect_here(table_in, ctx_len, ref_in, table_out, ref_out, status)
+    a = TrimArgs()
+    a.table_in, a.ctx_len, a.rows, a.max_pages_per_seq = _ptr(table_in), _ptr(ctx_len), rows, P
+    a.window, a.sinks = _i32(window, "window", 1), _i32(sinks, "sinks")
+    a.ref_in, a.num_pages = _ptr(ref_in), pages
+    a.table_out, a.ref_out, a.status = _ptr(table_out), _ptr(ref_out), _ptr(status)
+    _check(load().lucetree_trim_pages(ctypes.byref(a), _stream(stream)))
+
+
+def lucetree_compact_pages_workspace(num_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().lucetree_compact_pages_workspace(_i32(num_pages, "num_pages", 1), ctypes.byref(n)))
+    return int(n.value)
+
+
+def lucetree_compact_pages(table_in, ref_in, table_out, ref_out, copy_src, copy_dst, copy_n, live, status, workspace,
+                           stream=None):
+    """Close the pool up: the pages in use become [0, live), in table_in [rows][P]
+    and ref_in [num_pages] (outputs may be the inputs).  (copy_src, copy_dst)
+    [num_pages // 2] with copy_n [1] are the copies this takes, for
+    lucetree_copy_pages.  All int32."""
+    rows, P = _dims(table_in, "table_in", 2)
+    pages = _dims(ref_in, "ref_in", 1)[0]
+    for t, name, shape in ((table_in, "table_in", (rows, P)), (ref_in, "ref_in", (pages,)),
+                           (table_out, "table_out", (rows, P)), (ref_out, "ref_out", (pages,)),
+                           (copy_src, "copy_src", (pages // 2,)), (copy_dst, "copy_dst", (pages // 2,)),
+                           (copy_n, "copy_n", (1,)), (live, "live", (1,))):
+        _expect(t, name, shape, _I32)
+    _expect_status(status)
+    _expect_here(table_in, ref_in, table_out, ref_out, copy_src, copy_dst, copy_n, live, status, workspace)
+    a = CompactArgs()
+    a.table_in, a.rows, a.max_pages_per_seq = _ptr(table_in), rows, P
+    a.ref_in, a.num_pages = _ptr(ref_in), pages
+    a.table_out, a.ref_out = _ptr(table_out), _ptr(ref_out)
+    a.copy_src, a.copy_dst, a.copy_n, a.live = _ptr(copy_src), _ptr(copy_dst), _ptr(copy_n), _ptr(live)
+    a.status = _ptr(status)
+    _check(load().lucetree_compact_pages(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         _stream(stream)))
+
+
+def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=None):
+    """Copy pages src[i] to dst[i] (int32 [n]; -1 in both: no copy) of the pools,
+    whose first dimension is the page, byte for byte; v_pool may be None.
+    count (int32 [1] on the device): only the first count pairs."""
+    n = _dims(src, "src", 1)[0]
+    _expect(src, "src", (n,), _I32)
+    _expect(dst, "dst", (n,), _I32)
+    if count is not None:
+        _expect(count, "count", (1,), _I32)
+    if k_pool is None or k_pool.dim() < 2 or k_pool.shape[0] < 1:
+        raise LucetreeError("k_pool: expected a pool [pages][...]")
+    pages = k_pool.shape[0]
+    if v_pool is not None and (v_pool.dim() < 2 or v_pool.shape[0] != pages):
+        raise LucetreeError(f"v_pool: expected a pool of {pages} pages, got shape {tuple(v_pool.shape)}")
+    _expect_status(status)
+    _expect_here(src, dst, k_pool, v_pool, status, count)
+    a = CopyPagesArgs()
+    a.src, a.dst, a.n, a.count = _ptr(src), _ptr(dst), n, _ptr(count)
+    a.k_pool, a.v_pool = _ptr(k_pool), _ptr(v_pool)
+    a.k_page_bytes = k_pool.numel() // pages * k_pool.element_size()
+    a.v_page_bytes = v_pool.numel() // pages * v_pool.element_size() if v_pool is not None else 0
+    a.num_pages, a.status = pages, _ptr(status)
+    _check(load().lucetree_copy_pages(ctypes.byref(a), _stream(stream)))
+
+
+def lucetree_reorder_states(state_in, src, state_out, status, stream=None):
+    """state_out[r] = state_in[src[r]] (rows are the first dimension; src int32
+    [rows_out], -1: state_out[r] stays as it is), byte for byte."""
+    rows = _dims(src, "src", 1)[0]
+    _expect(src, "src", (rows,), _I32)
+    if state_in is None or state_in.dim() < 2 or state_in.shape[0] < 1:
+        raise LucetreeError("state_in: expected states [rows][...]")
+    _expect(state_out, "state_out", (rows, *state_in.shape[1:]), (state_in.dtype,))
+    _expect_status(status)
+    _expect_here(state_in, src, state_out, status)
+    a = ReorderStatesArgs()
+    a.state_in, a.state_out, a.src = _ptr(state_in), _ptr(state_out), _ptr(src)
+    a.rows_in, a.rows_out = state_in.shape[0], rows
+    a.row_bytes = state_in.numel() // state_in.shape[0] * state_in.element_size()
+    a.status = _ptr(status)
+    _check(load().lucetree_reorder_states(ctypes.byref(a), _stream(stream)))
 
 
 # ---------------------------------------------------------------- failure path self-test

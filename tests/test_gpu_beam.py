@@ -1,0 +1,178 @@
+"""Beam selection against its definition in 64 bits: exact whole numbers, ties
+to the lower beam and token, finished and dead beams, masked vocabularies, odd
+sizes, alignments and strides."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _lt():
+    from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
+    return LT
+
+
+def reference(logits, cum, finished, eos, Kout):
+    x, cum = logits.double().numpy(), cum.double().numpy()
+    B, K, V = x.shape
+    out = [np.zeros((B, Kout)), *(np.zeros((B, Kout), np.int64) for _ in range(3))]
+    for b in range(B):
+        score = np.full((K, V), -np.inf)
+        for k in range(K):
+            if finished is not None and finished[b, k]:
+                if 0 <= eos < V:
+                    score[k, eos] = cum[b, k]
+            elif np.isfinite(x[b, k]).any() and np.isfinite(cum[b, k]):
+                m = x[b, k].max()
+                score[k] = x[b, k] - (m + np.log(np.exp(x[b, k] - m).sum())) + cum[b, k]
+        order = np.argsort(-score.reshape(-1), kind="stable")[:Kout]
+        out[0][b] = score.reshape(-1)[order]
+        out[1][b], out[2][b] = order % V, b * K + order // V
+        for j, i in enumerate(order):
+            ended = finished is not None and bool(finished[b, i // V])
+            out[3][b, j] = int(ended or i % V == eos)
+    return out
+
+
+def call(logits, cum, finished, eos, Kout, done=True, ws=None):
+    LT = _lt()
+    B, K, V = logits.shape
+    i32 = lambda: torch.full((B, Kout), -7, dtype=torch.int32, device="cuda")  # noqa: E731
+    score, token, row, fin = torch.full((B, Kout), float("nan"), device="cuda"), i32(), i32(), i32()
+    if ws is None:
+        ws = torch.empty(LT.lucetree_beam_select_workspace(B, K, Kout, V), dtype=torch.uint8, device="cuda")
+        ws.fill_(0xFF)
+    LT.lucetree_beam_select(logits, cum.cuda(), None if finished is None else finished.cuda(), eos, score, token, row,
+                            fin if done else None, ws)
+    torch.cuda.synchronize()
+    return score.cpu(), token.cpu(), row.cpu(), fin.cpu()
+
+
+def check(logits, cum, finished, eos, Kout, dev=None):
+    """dev: the device logits, where their layout differs from the host's."""
+    got = call(logits.cuda() if dev is None else dev, cum, finished, eos, Kout)
+    want = reference(logits, cum, finished, eos, Kout)
+    for g, w in zip(got[1:], want[1:]):
+        assert np.array_equal(g.numpy(), w)
+    g, w = got[0].double().numpy(), want[0]
+    assert np.array_equal(np.isneginf(g), np.isneginf(w))
+    fine = ~np.isneginf(w)
+    # the sum's fp32 terms are off by a few 2^-24 each (difference, product, exponential of 2 ulp) and so is its
+    # logarithm; one more rounding of the score
+    assert np.all(np.abs(g - w)[fine] <= 16 * 2.0 ** -24 + 2.0 ** -24 * np.abs(w[fine]))
+
+
+def draw(B, K, V, dtype, seed, spread=3.0):
+    g = torch.Generator().manual_seed(seed)
+    return (spread * torch.randn(B, K, V, generator=g)).to(TYPES[dtype]), -10 * torch.rand(B, K, generator=g)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B,K,Kout,V", [(1, 1, 1, 1), (1, 1, 3, 3), (2, 3, 5, 7), (1, 4, 4, 100), (3, 2, 32, 33),
+                                        (1, 32, 32, 1000), (2, 5, 7, 4097), (5, 8, 8, 30011), (1, 1, 8, 151936),
+                                        (2, 31, 17, 20001)])
+def test_matches_the_definition(cuda_dev, dtype, B, K, Kout, V):
+    logits, cum = draw(B, K, V, dtype, seed=B + K + V)
+    check(logits, cum, None, -1, Kout)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_finished_dead_and_masked(cuda_dev, dtype):
+    logits, cum = draw(6, 5, 2051, dtype, seed=3)
+    g = torch.Generator().manual_seed(4)
+    logits.masked_fill_(torch.rand(6, 5, 2051, generator=g) < 0.97, float("-inf"))
+    logits[1, 2] = float("-inf")                       # no token left
+    logits[5] = float("-inf")
+    finished = (torch.rand(6, 5, generator=g) < 0.4).int()
+    finished[2] = torch.tensor([0, -3, 1 << 30, 0, 1], dtype=torch.int32)  # any non-zero value
+    cum[0, 1:] = float("-inf")                         # the first step of a search
+    cum[3] = float("-inf")
+    finished[4] = 1
+    for eos in (0, 17, 2050, -1, 2051):
+        check(logits, cum, finished, eos, 8)
+        check(logits, cum, finished, eos, 32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ties_go_to_the_lower_beam_and_token(cuda_dev, dtype):
+    for V in (64, 5003):
+        logits = torch.zeros(2, 4, V, dtype=TYPES[dtype])
+        logits[0, :, 5::7] = 2.0                       # many equal best tokens, equal rows
+        logits[0, 2, 6] = -0.0
+        logits[1] = torch.randint(0, 3, (4, V), generator=torch.Generator().manual_seed(1)).to(TYPES[dtype])
+        logits[1, 1:] = logits[1, 0]                   # the same sums in every row
+        check(logits, torch.full((2, 4), -1.5), None, 3, 32)
+
+
+def test_large_and_far_logits(cuda_dev):
+    logits, cum = draw(2, 3, 9001, "f32", seed=8, spread=1e3)
+    check(logits + 5e4, cum, None, -1, 8)
+    logits = torch.linspace(-3e38, 3e38, 4099, dtype=torch.float64).float().expand(1, 2, 4099).contiguous()
+    check(logits, torch.tensor([[-1.0, -2.0]]), None, -1, 2)
+
+
+def test_sorted_rows_change_the_list_most(cuda_dev):
+    up = torch.arange(20000, dtype=torch.float32)[None, None] * 1e-3
+    check(up.contiguous(), torch.zeros(1, 1), None, -1, 32)
+    check(up.flip(-1).contiguous(), torch.zeros(1, 1), None, -1, 32)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("offset,stride", [(0, 1003), (1, 1003), (3, 1024), (5, 1001), (7, 1011)])
+def test_rows_of_any_alignment_and_stride(cuda_dev, dtype, offset, stride):
+    B, K, V = 2, 3, 1001
+    logits, cum = draw(B, K, V, dtype, seed=offset)
+    flat = torch.full((offset + B * K * stride,), 1e4, device="cuda").to(TYPES[dtype])  # larger than any logit
+    dev = flat[offset:].view(B * K, stride)[:, :V].unflatten(0, (B, K))
+    dev.copy_(logits)
+    check(logits, cum, None, -1, 6, dev=dev)
+
+
+def test_short_rows_of_any_alignment(cuda_dev):
+    for V in range(1, 24):
+        flat = torch.full((8 + 4 * 25,), 1e4, dtype=torch.float16, device="cuda")
+        logits, cum = draw(1, 3, V, "f16", seed=V)
+        for offset in range(8):
+            dev = flat[offset:offset + 75].view(3, 25)[:, :V][None]
+            dev.copy_(logits)
+            check(logits, cum, None, 1, min(9, 3 * V), dev=dev)
+
+
+def test_without_the_optional_outputs(cuda_dev):
+    logits, cum = draw(2, 2, 500, "f32", seed=1)
+    got = call(logits.cuda(), cum, None, 4, 3, done=False)
+    want = reference(logits, cum, None, 4, 3)
+    assert np.array_equal(got[1].numpy(), want[1]) and (got[3] == -7).all()
+
+
+def test_captured_replayed_and_two_streams_at_once(cuda_dev):
+    LT = _lt()
+    B, K, V = 2, 4, 33333
+    sets = [draw(B, K, V, "bf16", seed=s) for s in (1, 2)]
+    want = [reference(x, c, None, 5, 4) for x, c in sets]
+    dev = [(x.cuda(), c.cuda()) for x, c in sets]
+    outs = [[torch.empty(B, 4, dtype=t, device="cuda") for t in (torch.float32,) + (torch.int32,) * 3] for _ in sets]
+    ws = [torch.empty(LT.lucetree_beam_select_workspace(B, K, 4, V), dtype=torch.uint8, device="cuda") for _ in sets]
+    go = lambda i: LT.lucetree_beam_select(*dev[i], None, 5, *outs[i], ws[i])  # noqa: E731
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                go(i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(outs[i][1].cpu().numpy(), want[i][1])
+        assert np.array_equal(outs[i][2].cpu().numpy(), want[i][2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(0)
+    for i in (1, 0):
+        dev[0][0].copy_(sets[i][0])
+        dev[0][1].copy_(sets[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(outs[0][1].cpu().numpy(), want[i][1])
