@@ -437,7 +437,7 @@ typedef struct lucetree_beam_args {
     int batch;               /* requests; batch * beams_in <= 65535 */
     int beams_in, beams_out; /* beams of each request before and after, 1..LUCETREE_MAX_BEAMS,
                                 beams_out <= beams_in * vocab */
-    int vocab;
+    int vocab;               /* beams_in * vocab < 2^32 - 1 */
     long long row_stride;    /* elements from one row of logits to the next, >= vocab */
     const void* logits;      /* [batch][beams_in] rows of vocab, aligned to their type */
     const float* cum;        /* [batch][beams_in] log-probability of each beam so far; -inf = a dead beam */

@@ -67,6 +67,22 @@ __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// DPL consecutive outputs of a lane, 4 or 8 of fp32 or 16 bits
+template <int DPL, typename TO>
+__device__ __forceinline__ void store_slice(TO* p, const float (&v)[DPL]) {
+    if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+        for (int x = 0; x < DPL; x += 4)
+            *reinterpret_cast<float4*>(p + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+    } else {
+        alignas(16) TO t[DPL];
+#pragma unroll
+        for (int x = 0; x < DPL; ++x) store_out(t + x, v[x]);
+        if constexpr (DPL == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+        else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
+    }
+}
+
 // One output row (b, node i, head h) by a group of W warps starting at warp
 // wbase of the CTA, which synchronise on named barrier bar_id (so several
 // groups of a CTA can each merge a row).  anc: the node's ancestor-or-self
@@ -253,6 +269,21 @@ __device__ __forceinline__ void merge_row(const AttnLaunch& L, long long row, ui
             }
             m_w = mr;
         }
+    }
+
+    if constexpr (W == 1) {
+        // one warp has the whole row: no exchange, and its slice goes out in one store
+        const float inv1 = l_w > 0.f || !WIN ? 1.f / l_w : 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < DPL; ++x) {
+            o[x] *= inv1;
+            bad |= !isfinite(o[x]);
+        }
+        store_slice<DPL>(reinterpret_cast<TO*>(a.out) + (size_t)row * D + lane * DPL, o);
+        if (bad) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
+        if (a.lse && lane == 0) a.lse[row] = l_w > 0.f || !WIN ? (m_w + log2f(l_w)) * kLn2 : -INFINITY;
+        return;
     }
 
     // ---- the warps' parts on the common shift

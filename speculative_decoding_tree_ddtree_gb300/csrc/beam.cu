@@ -9,14 +9,17 @@
 // Each thread keeps a running maximum and sum of its elements; each warp keeps
 // a sorted list of its 32 best (logit, token) keys, one in each lane, as 64-bit
 // integers whose order is (logit descending, token ascending).  A list changes
-// seldom: elements are compared with its Kout-th key, those that pass go to
-// a 64-entry buffer in shared memory, and 32 of them at a time are sorted and
-// merged in (bitonic networks of shuffles).  The first batch's lane maxima give
-// the starting threshold.
+// seldom: the largest element of each 16-byte vector is compared with its Kout-th
+// key, the few vectors that may hold a better one are gone through again, and
+// their keys wait in shared memory until 32 of them are sorted and merged in
+// (bitonic networks of shuffles).  The first batch's lane maxima give the
+// starting threshold.
 // Launch 2, one CTA per request, merges the chunks' lists and sums row by row,
 // turns the rows' lists into scores in 64 bits (neighbouring candidates of
 // different rows are closer than fp32 keeps beside a long sum) and merges those.
 // Bound by reading the logits once.
+#include <type_traits>
+
 #include "beam.h"
 #include "internal.cuh"
 
@@ -78,12 +81,14 @@ __device__ inline u64 merge32(u64 a, u64 b) {
 }
 
 // A warp's list with its buffer of candidates.
+constexpr int kBuf = 32 * 8 + 32;  // what one vector of every lane may add to 31 waiting keys
+
 struct TopList {
     u64 list;   // this lane's key
     u64 limit;  // the Kout-th key: only larger ones matter
     float low;  // its logit
-    int count;  // candidates in the buffer
-    u64* buf;   // 64 keys of shared memory
+    int count;  // keys in the buffer
+    u64* buf;   // kBuf keys of shared memory
 
     __device__ void set_limit(u64 k) {
         if (k > limit) {
@@ -91,25 +96,41 @@ struct TopList {
             low = key_value(k);
         }
     }
-    __device__ void flush(int kout) {
+    // Merges waiting keys, 32 at a time, while at least `least` of them wait.
+    __device__ __noinline__ void flush(int least, int kout) {
         const int lane = threadIdx.x & 31;
         __syncwarp();
-        list = merge32(list, sort32(lane < count ? buf[lane] : 0));
-        const u64 rest = lane + 32 < count ? buf[lane + 32] : 0;
+        for (; count >= least; count -= 32) {  // from the back of the buffer: the rest stays where it is
+            const int at = count - 32 + lane;
+            list = merge32(list, sort32(at >= 0 ? buf[at] : 0));
+        }
+        count = max(count, 0);
         __syncwarp();
-        buf[lane] = rest;
-        count = max(count - 32, 0);
         set_limit(__shfl_sync(0xffffffffu, list, kout - 1));
     }
-    // One element of each lane; `in`: it is one.
-    __device__ void offer(float x, unsigned idx, bool in, int kout) {
-        const u64 key = in && x >= low ? pack_key(x, idx) : 0;
-        const bool pass = key > limit;
-        const unsigned who = __ballot_sync(0xffffffffu, pass);
-        if (!who) return;
-        if (pass) buf[count + __popc(who & ((1u << (threadIdx.x & 31)) - 1u))] = key;
-        count += __popc(who);
-        if (count >= 32) flush(kout);
+    // n elements of each lane with consecutive indices.
+    template <int n>
+    __device__ void offer(const float (&x)[n], unsigned idx, bool in, int kout) {
+        const int lane = threadIdx.x & 31;
+        u64 key[n];
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+            key[e] = in && x[e] >= low ? pack_key(x[e], idx + e) : 0;
+            mine += key[e] > limit;
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        int at = count + upto - mine;
+#pragma unroll
+        for (int e = 0; e < n; ++e)
+            if (key[e] > limit) buf[at++] = key[e];
+        count += __shfl_sync(0xffffffffu, upto, 31);
+        if (count >= 32) flush(32, kout);
     }
 };
 
@@ -130,11 +151,32 @@ __device__ inline void unpack(const uint4& u, float (&x)[Vec<T>::kE]) {
     }
 }
 
+// Largest element (of 16-bit ones in their own type: no conversions to keep in registers).
+template <typename T>
+__device__ inline float vector_max(const uint4& u) {
+    if constexpr (sizeof(T) == 4) {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    } else if constexpr (std::is_same<T, __half>::value) {
+        const __half2* h = reinterpret_cast<const __half2*>(&u);
+        const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    } else {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+}
+
 __device__ inline float scalar(const float* p) { return *p; }
 __device__ inline float scalar(const __half* p) { return __half2float(*p); }
 __device__ inline float scalar(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-__device__ inline float exp_diff(float x, float m) { return exp2f((x - m) * kLog2e); }
+// exp(x - m) by the hardware's base-2 exponential (2 ulp)
+__device__ inline float exp_diff(float x, float m) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - m) * kLog2e));
+    return y;
+}
 
 // (m, s) += (m2, s2): sums of exponentials relative to their maxima; a maximum of -inf has sum 0.
 __device__ inline void add_sums(float& m, float& s, float m2, float s2) {
@@ -149,9 +191,9 @@ __device__ inline bool row_ended(const lucetree_beam_args& a, int row) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamLaunch L) {
+__global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(BeamLaunch L) {
     constexpr int kE = Vec<T>::kE;
-    __shared__ u64 s_buf[kWarps][64];
+    __shared__ u64 s_buf[kWarps][kBuf];
     __shared__ float2 s_sum[kWarps];
     const lucetree_beam_args& a = L.a;
     pdl_wait();
@@ -173,69 +215,70 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamLaunch L) {
     float m = -INFINITY, s = 0.f;
     for (int base = v0; base < v1; base += kU * kThreads) {
         uint4 u[kU];
-        bool in[kU];
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
             const int v = base + k * kThreads + threadIdx.x;
-            in[k] = v < v1;
-            if (in[k]) u[k] = __ldcs(xv + v);
+            if (v < v1) u[k] = __ldg(xv + v);
         }
-        float mb = -INFINITY;
-        u64 best = 0;
+        // largest element of each vector, of the batch
+        float vm[kU], mb = -INFINITY;
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-            float f[kE];
-            unpack<T>(u[k], f);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) mb = in[k] ? fmaxf(mb, f[e]) : mb;
+            vm[k] = vector_max<T>(u[k]);
+            if (base + k * kThreads + (int)threadIdx.x >= v1) vm[k] = -INFINITY;
+            mb = fmaxf(mb, vm[k]);
         }
         if (base == v0) {
             // lane maxima are elements: the Kout-th of them bounds the Kout-th element from below (a key
             // with the highest index of its value, so that no tie is lost)
-            best = sort32(pack_key(mb, 0xffffffffu));
-            top.set_limit(__shfl_sync(0xffffffffu, best, kout - 1));
+            top.set_limit(__shfl_sync(0xffffffffu, sort32(pack_key(mb, 0xffffffffu)), kout - 1));
         }
         if (mb > m) {
             s = m == -INFINITY ? 0.f : s * exp_diff(m, mb);
             m = mb;
         }
         const float mm = m == -INFINITY ? 0.f : m;
+        unsigned may = 0;  // vectors with an element that may pass
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
             float f[kE];
             unpack<T>(u[k], f);
-            float vm = -INFINITY;
             float part = 0.f;
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                part += exp_diff(f[e], mm);
-                vm = fmaxf(vm, f[e]);
+            for (int e = 0; e < kE; ++e) part += exp_diff(f[e], mm);
+            if (base + k * kThreads + (int)threadIdx.x < v1) {
+                s += part;
+                may |= vm[k] >= top.low ? 1u << k : 0u;
             }
-            if (in[k]) s += part;
-            if (__any_sync(0xffffffffu, in[k] && vm >= top.low)) {
-                const unsigned idx = (unsigned)(head + (base + k * kThreads + (int)threadIdx.x) * kE);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) top.offer(f[e], idx + e, in[k], kout);
-            }
+        }
+        // those vectors once more (few, and still in the cache), with one copy of the list's code
+        may = __reduce_or_sync(0xffffffffu, may);
+        while (may) {
+            const int k = __ffs(may) - 1;
+            may &= may - 1;
+            const int v = base + k * kThreads + threadIdx.x;
+            float f[kE];
+            const bool in = v < v1;
+            unpack<T>(in ? __ldg(xv + v) : make_uint4(0, 0, 0, 0), f);
+            top.offer<kE>(f, (unsigned)(head + v * kE), in, kout);
         }
     }
     if (chunk == L.chunks - 1 && warp == 0) {
         const int tail = head + nv * kE;  // first element behind the vectors
         const int t = lane < head ? lane : tail + lane - head;
         const bool in = t < a.vocab && (lane < head || t >= tail);
-        const float f = in ? scalar(x + t) : -INFINITY;
-        if (in) add_sums(m, s, f, f == -INFINITY ? 0.f : 1.f);
-        top.offer(f, (unsigned)t, in, kout);
+        const float f[1] = {in ? scalar(x + t) : -INFINITY};
+        if (in) add_sums(m, s, f[0], f[0] == -INFINITY ? 0.f : 1.f);
+        top.offer<1>(f, (unsigned)t, in, kout);
     }
-    if (top.count > 0) top.flush(kout);
+    top.flush(1, kout);
     // the CTA's sum and list
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         add_sums(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-    __syncwarp();
     s_buf[warp][lane] = top.list;
     if (lane == 0) s_sum[warp] = make_float2(m, s);
-#pragma unroll
+#pragma unroll 1
     for (int half = kWarps / 2; half > 0; half >>= 1) {
         __syncthreads();
         if (warp < half) {
@@ -255,7 +298,8 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamLaunch L) {
 
 // A candidate of the request: score as an ordered integer, then beam * vocab + token.
 struct Cand {
-    u64 score, index;
+    u64 score;
+    unsigned index;
 };
 __device__ inline bool better(const Cand& p, const Cand& q) {
     return p.score > q.score || (p.score == q.score && p.index < q.index);
@@ -316,7 +360,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
     }
     s_keys[warp][lane] = list;
     __syncthreads();
-    Cand cand{0, ~0ull};  // none: behind every candidate
+    Cand cand{0, ~0u};  // none: behind every candidate
     if (mine && w == 0) {
         for (int o = 1; o < per; ++o) list = merge32(list, s_keys[warp + o][lane]);
         const float cum = a.cum[row];
@@ -338,7 +382,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
                 double s = 0.0;
                 for (int c = lane; c < L.chunks; c += 32) {
                     const float2 p = L.sums[(size_t)row * L.chunks + c];
-                    if (p.x > -INFINITY) s += (double)p.y * exp((double)p.x - (double)m);
+                    if (p.x > -INFINITY) s += (double)(p.y * exp_diff(p.x, m));
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -350,9 +394,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
                 if (!(score == score)) score = -INFINITY;
             }
         }
-        if (have) cand = Cand{order_double(score), (u64)k * (u64)a.vocab + (u64)token};
+        if (have) cand = Cand{order_double(score), (unsigned)k * (unsigned)a.vocab + (unsigned)token};
         // scores follow the logits' order, but ties of rounded scores and -inf follow the index
-        cand = sort32(cand);
+        const Cand next{__shfl_down_sync(0xffffffffu, cand.score, 1), __shfl_down_sync(0xffffffffu, cand.index, 1)};
+        if (__any_sync(0xffffffffu, lane < 31 && better(next, cand))) cand = sort32(cand);
     }
     if (mine && w == 0) s_cand[k][lane] = cand;
     for (int half = 16; half > 0; half >>= 1) {
@@ -361,7 +406,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
     }
     if (warp == 0 && lane < a.beams_out) {
         const Cand c = s_cand[0][lane];
-        const int beam = (int)(c.index / (u64)a.vocab), token = (int)(c.index % (u64)a.vocab);
+        const int beam = (int)(c.index / (unsigned)a.vocab), token = (int)(c.index % (unsigned)a.vocab);
         const size_t at = (size_t)b * a.beams_out + lane;
         a.out_score[at] = (float)order_value(c.score);
         a.out_token[at] = token;
@@ -414,6 +459,7 @@ static lucetree_status beam_sizes(int batch, int beams_in, int beams_out, int vo
     if (batch < 1 || beams_in < 1 || beams_out < 1 || vocab < 1) return LUCETREE_ERR_INVALID_ARG;
     if (beams_in > LUCETREE_MAX_BEAMS || beams_out > LUCETREE_MAX_BEAMS || (long long)batch * beams_in > 65535)
         return LUCETREE_ERR_UNSUPPORTED;
+    if ((long long)beams_in * vocab > 0xfffffffell) return LUCETREE_ERR_UNSUPPORTED;  // candidates by a 32-bit index
     if (beams_out > (long long)beams_in * vocab) return LUCETREE_ERR_INVALID_ARG;  // fewer candidates than beams
     return LUCETREE_OK;
 }

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -198,6 +199,21 @@ class ReorderStatesArgs(ctypes.Structure):
     ]
 
 
+# The same layouts for struct.pack, which fills a whole argument struct at once
+# (the calls of small steps are bound by the host).
+_WIN_ARGS = struct.Struct("@7if3PiPi7P3iP")
+_BEAM_ARGS = struct.Struct("@5iq3Pi4P")
+_REORDER_ARGS = struct.Struct("@2PiP3iPi6P")
+_TRIM_ARGS = struct.Struct("@2P4iPi3P")
+_COMPACT_ARGS = struct.Struct("@P2iPi7P")
+_COPY_PAGES_ARGS = struct.Struct("@2Pi3P2qiP")
+_REORDER_STATES_ARGS = struct.Struct("@3P2iqP")
+for _packer, _kind in ((_WIN_ARGS, WinArgs), (_BEAM_ARGS, BeamArgs), (_REORDER_ARGS, ReorderArgs), (_TRIM_ARGS, TrimArgs),
+                       (_COMPACT_ARGS, CompactArgs), (_COPY_PAGES_ARGS, CopyPagesArgs),
+                       (_REORDER_STATES_ARGS, ReorderStatesArgs)):
+    assert _packer.size == ctypes.sizeof(_kind), _kind.__name__
+
+
 _lib = None
 
 
@@ -234,16 +250,17 @@ def load(path: str | None = None):
     lib.lucetree_verify_attn_kq_workspace.argtypes = [I, I, I, I, I, ctypes.POINTER(SZ)]
     lib.lucetree_verify_attn_kq.argtypes = [ctypes.POINTER(AttnArgs), P, I, P, P, SZ, P]
     lib.lucetree_commit_kq.argtypes = [ctypes.POINTER(CommitArgs), P, P]
-    lib.lucetree_verify_attn_win.argtypes = [ctypes.POINTER(WinArgs), P, SZ, P]
+    # (argument structs as P: packed bytes, or byref of the ctypes Structure)
+    lib.lucetree_verify_attn_win.argtypes = [P, P, SZ, P]
     lib.lucetree_reorder_pages_workspace.argtypes = [I, I, I, ctypes.POINTER(SZ)]
-    lib.lucetree_reorder_pages.argtypes = [ctypes.POINTER(ReorderArgs), P, SZ, P]
-    lib.lucetree_trim_pages.argtypes = [ctypes.POINTER(TrimArgs), P]
+    lib.lucetree_reorder_pages.argtypes = [P, P, SZ, P]
+    lib.lucetree_trim_pages.argtypes = [P, P]
     lib.lucetree_compact_pages_workspace.argtypes = [I, ctypes.POINTER(SZ)]
-    lib.lucetree_compact_pages.argtypes = [ctypes.POINTER(CompactArgs), P, SZ, P]
-    lib.lucetree_copy_pages.argtypes = [ctypes.POINTER(CopyPagesArgs), P]
+    lib.lucetree_compact_pages.argtypes = [P, P, SZ, P]
+    lib.lucetree_copy_pages.argtypes = [P, P]
     lib.lucetree_beam_select_workspace.argtypes = [I, I, I, I, ctypes.POINTER(SZ)]
-    lib.lucetree_beam_select.argtypes = [ctypes.POINTER(BeamArgs), P, SZ, P]
-    lib.lucetree_reorder_states.argtypes = [ctypes.POINTER(ReorderStatesArgs), P]
+    lib.lucetree_beam_select.argtypes = [P, P, SZ, P]
+    lib.lucetree_reorder_states.argtypes = [P, P]
     for name in EXPORTED:
         if name not in ("lucetree_status_string", "lucetree_abi_version"):
             getattr(lib, name).restype = I
@@ -317,15 +334,42 @@ def _expect_16bit(t, name: str, shape: tuple):
         raise LucetreeError(f"{name}: expected shape {tuple(shape)} of a 16-bit type, got {tuple(t.shape)} of {t.dtype}")
 
 
-def _expect_here(*tensors):
-    """Refuse tensors of several devices, or of a device that is not current:
-    a call acts on the current device and takes plain pointers."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise LucetreeError(f"tensors on several devices: {', '.join(sorted(str(d) for d in devices))}")
-    for d in devices:
-        if d.type == "cuda" and d.index != torch.cuda.current_device():
-            raise LucetreeError(f"tensors on {d}, but cuda:{torch.cuda.current_device()} is current")
+def _device() -> int:
+    """The current device, which a call acts on."""
+    return torch.cuda.current_device()
+
+
+def _arg(t, name: str, shape, dtypes: tuple, dev: int) -> int:
+    """Address of a required tensor of this shape and element type (None: any),
+    contiguous and on device dev."""
+    if t is None:
+        raise LucetreeError(f"{name} is required")
+    if (dtypes is not None and t.dtype not in dtypes) or (shape is not None and t.shape != shape):
+        _expect(t, name, t.shape if shape is None else shape, (t.dtype,) if dtypes is None else dtypes)
+    if t.get_device() != dev:
+        raise LucetreeError(f"{name}: lucetree takes tensors of the current device, cuda:{dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise LucetreeError(f"{name}: lucetree takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _status_arg(t, dev: int) -> int:
+    _expect_status(t)
+    return _arg(t, "status", None, None, dev)
+
+
+def _workspace(t, dev: int):
+    """Address and size of a workspace."""
+    return _arg(t, "workspace", None, None, dev), t.numel() * t.element_size()
+
+
+# the raw handle of a device's current stream, without the Stream object around it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _i32(v, name: str, lo: int = 0) -> int:
@@ -353,11 +397,10 @@ def lucetree_verify_attn_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) ->
 
 
 def _check_attn(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse,
-                v_format=None, v_exp=None, k_exp=None, out_types=_F32):
+                v_format=None, v_exp=None, k_exp=None):
     """Shapes and element types of one tree-verify attention call (layouts as
     lucetree_verify_attn documents them); v_format selects the quantised V
-    pool, k_exp the E4M3 K pool (k_pool then holds the codes), out_types the
-    element types the output may have."""
+    pool, k_exp the E4M3 K pool (k_pool then holds the codes)."""
     B, N, Hq, D = _dims(q, "q", 4)
     if q.dtype not in _H16:
         raise LucetreeError(f"q: unsupported dtype {q.dtype}")
@@ -377,16 +420,16 @@ def _check_attn(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask
     _expect(page_table, "page_table", (B, _dims(page_table, "page_table", 2)[1]), _I32)
     _expect(ctx_len, "ctx_len", (B,), _I32)
     _expect(anc_mask, "anc_mask", (B, N), _W64)
-    _expect(out, "out", (B, N, Hq, D), out_types)
+    _expect(out, "out", (B, N, Hq, D), _F32)
     if lse is not None:
         _expect(lse, "lse", (B, N, Hq), _F32)
     _expect_status(status)
 
 
 def _attn_args(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse, scale,
-               v_format=None, v_exp=None, k_exp=None, out_types=_F32):
+               v_format=None, v_exp=None, k_exp=None):
     _check_attn(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse, v_format, v_exp,
-                k_exp, out_types)
+                k_exp)
     B, N, Hq, D = q.shape
     Hkv = k_pool.shape[1]
     a = AttnArgs()
@@ -432,16 +475,24 @@ def lucetree_verify_attn_win(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_t
     """As lucetree_verify_attn with a sliding window and sinks: node i, at
     position t_i = ctx_len + its depth, sees committed and tree positions p
     with p < sinks or t_i - p < window.  out fp32 or in q's dtype."""
-    a = _attn_args(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, lse, scale,
-                   out_types=_F32 + ((q.dtype,) if q is not None else ()))
-    _expect_here(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, out, status, workspace, lse)
-    w = WinArgs()
-    w.attn = a
-    w.window, w.sinks = _i32(window, "window", 1), _i32(sinks, "sinks")
-    w.out_dtype = LUCETREE_F32 if out.dtype == torch.float32 else a.dtype
-    w.out = a.out
-    _check(load().lucetree_verify_attn_win(ctypes.byref(w), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _device()
+    B, N, Hq, D = _dims(q, "q", 4)
+    P, Hkv, page, _ = _dims(k_pool, "k_pool", 4)
+    maxp = _dims(page_table, "page_table", 2)[1]
+    kind = (q.dtype,)
+    code = dtype_code(q)
+    pool, tree = (P, Hkv, page, D), (B, N, Hkv, D)
+    out_at = _arg(out, "out", (B, N, Hq, D), _F32 + kind, dev)
+    args = _WIN_ARGS.pack(
+        code, B, N, Hq, Hkv, D, page, float(D) ** -0.5 if scale is None else float(scale),
+        _arg(q, "q", None, None, dev), _arg(k_pool, "k_pool", pool, kind, dev), _arg(v_pool, "v_pool", pool, kind, dev), P,
+        _arg(page_table, "page_table", (B, maxp), _I32, dev), maxp, _arg(ctx_len, "ctx_len", (B,), _I32, dev),
+        _arg(k_tree, "k_tree", tree, kind, dev), _arg(v_tree, "v_tree", tree, kind, dev),
+        _arg(anc_mask, "anc_mask", (B, N), _W64, dev), 0,
+        0 if lse is None else _arg(lse, "lse", (B, N, Hq), _F32, dev), _status_arg(status, dev),
+        _i32(window, "window", 1), _i32(sinks, "sinks"), LUCETREE_F32 if out.dtype == torch.float32 else code, out_at)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().lucetree_verify_attn_win(args, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def lucetree_verify_attn_kq_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
@@ -822,22 +873,18 @@ def lucetree_beam_select(logits, cum, finished, eos: int, out_score, out_token, 
     if not -0x80000000 <= int(eos) <= 0x7FFFFFFF:
         raise LucetreeError(f"eos: expected a 32-bit integer, got {eos}")
     Kout = _dims(out_score, "out_score", 2)[1]
-    for t, name, shape, types in ((cum, "cum", (B, K), _F32), (out_score, "out_score", (B, Kout), _F32),
-                                  (out_token, "out_token", (B, Kout), _I32), (out_row, "out_row", (B, Kout), _I32)):
-        _expect(t, name, shape, types)
-    if finished is not None:
-        _expect(finished, "finished", (B, K), _I32)
-    if out_finished is not None:
-        _expect(out_finished, "out_finished", (B, Kout), _I32)
-    _expect_here(logits, cum, finished, out_score, out_token, out_row, out_finished, workspace)
-    a = BeamArgs()
-    a.dtype = LUCETREE_F32 if logits.dtype == torch.float32 else dtype_code(logits)
-    a.batch, a.beams_in, a.beams_out, a.vocab, a.row_stride = B, K, Kout, V, stride
-    a.logits, a.cum, a.finished, a.eos = logits.data_ptr(), _ptr(cum), _ptr(finished), int(eos)
-    a.out_score, a.out_token, a.out_row = _ptr(out_score), _ptr(out_token), _ptr(out_row)
-    a.out_finished = _ptr(out_finished)
-    _check(load().lucetree_beam_select(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _stream(stream)))
+    dev = _device()
+    if logits.get_device() != dev:
+        raise LucetreeError(f"logits: lucetree takes tensors of the current device, cuda:{dev}, got {logits.device}")
+    old, new = (B, K), (B, Kout)
+    args = _BEAM_ARGS.pack(
+        LUCETREE_F32 if logits.dtype == torch.float32 else dtype_code(logits), B, K, Kout, V, stride, logits.data_ptr(),
+        _arg(cum, "cum", old, _F32, dev), 0 if finished is None else _arg(finished, "finished", old, _I32, dev), int(eos),
+        _arg(out_score, "out_score", new, _F32, dev), _arg(out_token, "out_token", new, _I32, dev),
+        _arg(out_row, "out_row", new, _I32, dev),
+        0 if out_finished is None else _arg(out_finished, "out_finished", new, _I32, dev))
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().lucetree_beam_select(args, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- page tables, counts and copies
@@ -860,22 +907,16 @@ def lucetree_reorder_pages(table_in, ctx_in, src, reserve: int, ref_in, table_ou
     rows_in, P = _dims(table_in, "table_in", 2)
     rows = _dims(src, "src", 1)[0]
     pages = _dims(ref_in, "ref_in", 1)[0]
-    for t, name, shape in ((table_in, "table_in", (rows_in, P)), (ctx_in, "ctx_in", (rows_in,)), (src, "src", (rows,)),
-                           (ref_in, "ref_in", (pages,)), (table_out, "table_out", (rows, P)),
-                           (ctx_out, "ctx_out", (rows,)), (ref_out, "ref_out", (pages,)),
-                           (copy_src, "copy_src", (rows,)), (copy_dst, "copy_dst", (rows,))):
-        _expect(t, name, shape, _I32)
-    _expect_status(status)
-    _expect_here(table_in, ctx_in, src, ref_in, table_out, ctx_out, ref_out, copy_src, copy_dst, status, workspace)
-    a = ReorderArgs()
-    a.table_in, a.ctx_in, a.rows_in = _ptr(table_in), _ptr(ctx_in), rows_in
-    a.src, a.rows_out, a.max_pages_per_seq = _ptr(src), rows, P
-    a.reserve = _i32(reserve, "reserve")
-    a.ref_in, a.num_pages = _ptr(ref_in), pages
-    a.table_out, a.ctx_out, a.ref_out = _ptr(table_out), _ptr(ctx_out), _ptr(ref_out)
-    a.copy_src, a.copy_dst, a.status = _ptr(copy_src), _ptr(copy_dst), _ptr(status)
-    _check(load().lucetree_reorder_pages(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                         _stream(stream)))
+    dev = _device()
+    args = _REORDER_ARGS.pack(
+        _arg(table_in, "table_in", (rows_in, P), _I32, dev), _arg(ctx_in, "ctx_in", (rows_in,), _I32, dev), rows_in,
+        _arg(src, "src", (rows,), _I32, dev), rows, P, _i32(reserve, "reserve"),
+        _arg(ref_in, "ref_in", (pages,), _I32, dev), pages, _arg(table_out, "table_out", (rows, P), _I32, dev),
+        _arg(ctx_out, "ctx_out", (rows,), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
+        _arg(copy_src, "copy_src", (rows,), _I32, dev), _arg(copy_dst, "copy_dst", (rows,), _I32, dev),
+        _status_arg(status, dev))
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().lucetree_reorder_pages(args, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def lucetree_trim_pages(table_in, ctx_len, window: int, sinks: int, ref_in, table_out, ref_out, status, stream=None):
@@ -884,17 +925,13 @@ def lucetree_trim_pages(table_in, ctx_len, window: int, sinks: int, ref_in, tabl
     less in ref_out (outputs may be the inputs).  All int32."""
     rows, P = _dims(table_in, "table_in", 2)
     pages = _dims(ref_in, "ref_in", 1)[0]
-    for t, name, shape in ((table_in, "table_in", (rows, P)), (ctx_len, "ctx_len", (rows,)), (ref_in, "ref_in", (pages,)),
-                           (table_out, "table_out", (rows, P)), (ref_out, "ref_out", (pages,))):
-        _expect(t, name, shape, _I32)
-    _expect_status(status)
-    _expect_here(table_in, ctx_len, ref_in, table_out, ref_out, status)
-    a = TrimArgs()
-    a.table_in, a.ctx_len, a.rows, a.max_pages_per_seq = _ptr(table_in), _ptr(ctx_len), rows, P
-    a.window, a.sinks = _i32(window, "window", 1), _i32(sinks, "sinks")
-    a.ref_in, a.num_pages = _ptr(ref_in), pages
-    a.table_out, a.ref_out, a.status = _ptr(table_out), _ptr(ref_out), _ptr(status)
-    _check(load().lucetree_trim_pages(ctypes.byref(a), _stream(stream)))
+    dev = _device()
+    args = _TRIM_ARGS.pack(
+        _arg(table_in, "table_in", (rows, P), _I32, dev), _arg(ctx_len, "ctx_len", (rows,), _I32, dev), rows, P,
+        _i32(window, "window", 1), _i32(sinks, "sinks"), _arg(ref_in, "ref_in", (pages,), _I32, dev), pages,
+        _arg(table_out, "table_out", (rows, P), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
+        _status_arg(status, dev))
+    _check(load().lucetree_trim_pages(args, _raw_stream(stream, dev)))
 
 
 def lucetree_compact_pages_workspace(num_pages: int) -> int:
@@ -911,21 +948,15 @@ def lucetree_compact_pages(table_in, ref_in, table_out, ref_out, copy_src, copy_
     lucetree_copy_pages.  All int32."""
     rows, P = _dims(table_in, "table_in", 2)
     pages = _dims(ref_in, "ref_in", 1)[0]
-    for t, name, shape in ((table_in, "table_in", (rows, P)), (ref_in, "ref_in", (pages,)),
-                           (table_out, "table_out", (rows, P)), (ref_out, "ref_out", (pages,)),
-                           (copy_src, "copy_src", (pages // 2,)), (copy_dst, "copy_dst", (pages // 2,)),
-                           (copy_n, "copy_n", (1,)), (live, "live", (1,))):
-        _expect(t, name, shape, _I32)
-    _expect_status(status)
-    _expect_here(table_in, ref_in, table_out, ref_out, copy_src, copy_dst, copy_n, live, status, workspace)
-    a = CompactArgs()
-    a.table_in, a.rows, a.max_pages_per_seq = _ptr(table_in), rows, P
-    a.ref_in, a.num_pages = _ptr(ref_in), pages
-    a.table_out, a.ref_out = _ptr(table_out), _ptr(ref_out)
-    a.copy_src, a.copy_dst, a.copy_n, a.live = _ptr(copy_src), _ptr(copy_dst), _ptr(copy_n), _ptr(live)
-    a.status = _ptr(status)
-    _check(load().lucetree_compact_pages(ctypes.byref(a), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                         _stream(stream)))
+    dev = _device()
+    half = (pages // 2,)
+    args = _COMPACT_ARGS.pack(
+        _arg(table_in, "table_in", (rows, P), _I32, dev), rows, P, _arg(ref_in, "ref_in", (pages,), _I32, dev), pages,
+        _arg(table_out, "table_out", (rows, P), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
+        _arg(copy_src, "copy_src", half, _I32, dev), _arg(copy_dst, "copy_dst", half, _I32, dev),
+        _arg(copy_n, "copy_n", (1,), _I32, dev), _arg(live, "live", (1,), _I32, dev), _status_arg(status, dev))
+    ws, ws_bytes = _workspace(workspace, dev)
+    _check(load().lucetree_compact_pages(args, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=None):
@@ -933,42 +964,33 @@ def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=Non
     whose first dimension is the page, byte for byte; v_pool may be None.
     count (int32 [1] on the device): only the first count pairs."""
     n = _dims(src, "src", 1)[0]
-    _expect(src, "src", (n,), _I32)
-    _expect(dst, "dst", (n,), _I32)
-    if count is not None:
-        _expect(count, "count", (1,), _I32)
     if k_pool is None or k_pool.dim() < 2 or k_pool.shape[0] < 1:
         raise LucetreeError("k_pool: expected a pool [pages][...]")
     pages = k_pool.shape[0]
     if v_pool is not None and (v_pool.dim() < 2 or v_pool.shape[0] != pages):
         raise LucetreeError(f"v_pool: expected a pool of {pages} pages, got shape {tuple(v_pool.shape)}")
-    _expect_status(status)
-    _expect_here(src, dst, k_pool, v_pool, status, count)
-    a = CopyPagesArgs()
-    a.src, a.dst, a.n, a.count = _ptr(src), _ptr(dst), n, _ptr(count)
-    a.k_pool, a.v_pool = _ptr(k_pool), _ptr(v_pool)
-    a.k_page_bytes = k_pool.numel() // pages * k_pool.element_size()
-    a.v_page_bytes = v_pool.numel() // pages * v_pool.element_size() if v_pool is not None else 0
-    a.num_pages, a.status = pages, _ptr(status)
-    _check(load().lucetree_copy_pages(ctypes.byref(a), _stream(stream)))
+    dev = _device()
+    args = _COPY_PAGES_ARGS.pack(
+        _arg(src, "src", (n,), _I32, dev), _arg(dst, "dst", (n,), _I32, dev), n,
+        0 if count is None else _arg(count, "count", (1,), _I32, dev), _arg(k_pool, "k_pool", None, None, dev),
+        0 if v_pool is None else _arg(v_pool, "v_pool", None, None, dev), k_pool.numel() // pages * k_pool.element_size(),
+        0 if v_pool is None else v_pool.numel() // pages * v_pool.element_size(), pages, _status_arg(status, dev))
+    _check(load().lucetree_copy_pages(args, _raw_stream(stream, dev)))
 
 
 def lucetree_reorder_states(state_in, src, state_out, status, stream=None):
     """state_out[r] = state_in[src[r]] (rows are the first dimension; src int32
     [rows_out], -1: state_out[r] stays as it is), byte for byte."""
     rows = _dims(src, "src", 1)[0]
-    _expect(src, "src", (rows,), _I32)
     if state_in is None or state_in.dim() < 2 or state_in.shape[0] < 1:
         raise LucetreeError("state_in: expected states [rows][...]")
-    _expect(state_out, "state_out", (rows, *state_in.shape[1:]), (state_in.dtype,))
-    _expect_status(status)
-    _expect_here(state_in, src, state_out, status)
-    a = ReorderStatesArgs()
-    a.state_in, a.state_out, a.src = _ptr(state_in), _ptr(state_out), _ptr(src)
-    a.rows_in, a.rows_out = state_in.shape[0], rows
-    a.row_bytes = state_in.numel() // state_in.shape[0] * state_in.element_size()
-    a.status = _ptr(status)
-    _check(load().lucetree_reorder_states(ctypes.byref(a), _stream(stream)))
+    shape, kind = state_in.shape, (state_in.dtype,)
+    dev = _device()
+    args = _REORDER_STATES_ARGS.pack(
+        _arg(state_in, "state_in", None, None, dev), _arg(state_out, "state_out", (rows, *shape[1:]), kind, dev),
+        _arg(src, "src", (rows,), _I32, dev), shape[0], rows, state_in.numel() // shape[0] * state_in.element_size(),
+        _status_arg(status, dev))
+    _check(load().lucetree_reorder_states(args, _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- failure path self-test

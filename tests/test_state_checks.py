@@ -6,7 +6,17 @@ import pytest
 import torch
 
 from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
-from tests.test_binding_checks import _StubLib, stub  # noqa: F401
+from tests.test_binding_checks import _StubLib
+
+
+@pytest.fixture
+def stub(monkeypatch):
+    """The binding on host tensors, with entry points that only record the call."""
+    lib = _StubLib()
+    monkeypatch.setattr(LT, "load", lambda path=None: lib)
+    monkeypatch.setattr(LT, "_device", lambda: -1)  # where host tensors are
+    monkeypatch.setattr(LT, "_raw_stream", lambda stream, dev: 0)
+    return lib
 
 I32 = torch.int32
 FAKE = 1 << 20  # never dereferenced: every call below is refused first
@@ -58,12 +68,12 @@ def states(**over):
 
 
 @pytest.mark.parametrize("go", [beam, reorder, trim, compact, copy, states])
-def test_accepts(stub, go):  # noqa: F811
+def test_accepts(stub, go):
     go()
     assert len(stub.calls) == 1
 
 
-def test_accepts_what_is_optional(stub):  # noqa: F811
+def test_accepts_what_is_optional(stub):
     beam(finished=None, out_finished=None)
     beam(logits=torch.zeros(2, 3, 64)[:, :, :50])
     beam(logits=torch.zeros(2, 3, 50, dtype=torch.bfloat16), eos=-1)
@@ -84,7 +94,7 @@ def test_accepts_what_is_optional(stub):  # noqa: F811
     (reorder, dict(table_out=i32(5, 3))), (reorder, dict(table_in=torch.zeros(3, 4, dtype=torch.int64))),
     (reorder, dict(ctx_in=i32(2))), (reorder, dict(ref_out=i32(8))), (reorder, dict(copy_src=i32(4))),
     (reorder, dict(reserve=-1)), (reorder, dict(reserve=1 << 32)), (reorder, dict(src=None)),
-    (reorder, dict(ref_in=i32(9).to("meta"))),
+    (reorder, dict(table_in=i32(4, 3).T)),
     (trim, dict(window=0)), (trim, dict(sinks=-1)), (trim, dict(table_out=i32(3, 3))), (trim, dict(ref_out=i32(8))),
     (trim, dict(window=1 << 31)),
     (compact, dict(copy_src=i32(3))), (compact, dict(copy_n=i32(2))), (compact, dict(live=None)),
@@ -95,9 +105,17 @@ def test_accepts_what_is_optional(stub):  # noqa: F811
     (states, dict(state_out=torch.zeros(4, 2, 8, dtype=torch.float16))), (states, dict(state_in=torch.zeros(3))),
     (states, dict(status=None)),
 ])
-def test_refuses(stub, go, bad):  # noqa: F811
+def test_refuses(stub, go, bad):
     with pytest.raises(LT.LucetreeError):
         go(**bad)
+    assert stub.calls == []
+
+
+@pytest.mark.parametrize("go", [beam, reorder, trim, compact, copy, states])
+def test_refuses_tensors_of_another_device(stub, monkeypatch, go):
+    monkeypatch.setattr(LT, "_device", lambda: 0)
+    with pytest.raises(LT.LucetreeError, match="cuda:0"):
+        go()
     assert stub.calls == []
 
 

@@ -6,7 +6,17 @@ import pytest
 import torch
 
 from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
-from tests.test_binding_checks import _StubLib, stub  # noqa: F401
+from tests.test_binding_checks import _StubLib
+
+
+@pytest.fixture
+def stub(monkeypatch):
+    """The binding on host tensors, with entry points that only record the call."""
+    lib = _StubLib()
+    monkeypatch.setattr(LT, "load", lambda path=None: lib)
+    monkeypatch.setattr(LT, "_device", lambda: -1)  # where host tensors are
+    monkeypatch.setattr(LT, "_raw_stream", lambda stream, dev: 0)
+    return lib
 
 
 def _call(**over):
@@ -22,7 +32,7 @@ def _call(**over):
     LT.lucetree_verify_attn_win(**a)
 
 
-def test_accepts_both_output_types(stub):  # noqa: F811
+def test_accepts_both_output_types(stub):
     _call()
     _call(out=torch.zeros(2, 3, 4, 128), lse=torch.zeros(2, 3, 4))
     assert stub.calls == ["lucetree_verify_attn_win"] * 2
@@ -33,11 +43,18 @@ def test_accepts_both_output_types(stub):  # noqa: F811
     dict(sinks=1 << 31), dict(out=torch.zeros(2, 3, 4, 128, dtype=torch.bfloat16)),
     dict(out=torch.zeros(2, 3, 4, 128, dtype=torch.float64)), dict(out=torch.zeros(2, 3, 4, 64)),
     dict(lse=torch.zeros(2, 3, 3)), dict(anc_mask=torch.zeros(2, 3, dtype=torch.int32)),
-    dict(status=torch.zeros(1, dtype=torch.int32, device="meta")),
+    dict(k_pool=torch.zeros(5, 64, 2, 128, dtype=torch.float16).transpose(1, 2)),
 ], ids=str)
-def test_refuses(stub, bad):  # noqa: F811
+def test_refuses(stub, bad):
     with pytest.raises(LT.LucetreeError):
         _call(**bad)
+    assert stub.calls == []
+
+
+def test_refuses_tensors_of_another_device(stub, monkeypatch):
+    monkeypatch.setattr(LT, "_device", lambda: 0)
+    with pytest.raises(LT.LucetreeError, match="cuda:0"):
+        _call()
     assert stub.calls == []
 
 
