@@ -5,15 +5,14 @@
 // that of the logits, so one pass over a row finds both its softmax sum and its
 // best Kout tokens; only those can be among the request's best Kout.
 //
-// Launch 1 cuts the rows into chunks (about four CTAs per SM over all rows).
-// Each thread keeps a running maximum and sum of its elements; each warp keeps
-// a sorted list of its 32 best (logit, token) keys, one in each lane, as 64-bit
-// integers whose order is (logit descending, token ascending).  A list changes
-// seldom: the largest element of each 16-byte vector is compared with its Kout-th
-// key, the few vectors that may hold a better one are gone through again, and
-// their keys wait in shared memory until 32 of them are sorted and merged in
-// (bitonic networks of shuffles).  The first batch's lane maxima give the
-// starting threshold.
+// Launch 1 cuts the rows into chunks (no more CTAs than run at once).  While
+// streaming, a thread only keeps a running maximum, the vector it lies in, and
+// the sum: the Kout best elements of a chunk can only be in the Kout threads
+// with the best maxima.  Those threads are found by sorting 256 (maximum,
+// vector) keys, and their vectors are gone through once more for the elements.
+// Keys are 64-bit integers whose order is (logit descending, index ascending),
+// lists of 32 lie across a warp's lanes, and sorts and merges are bitonic
+// networks of shuffles.
 // Launch 2, one CTA per request, merges the chunks' lists and sums row by row,
 // turns the rows' lists into scores in 64 bits (neighbouring candidates of
 // different rows are closer than fp32 keeps beside a long sum) and merges those.
@@ -80,60 +79,6 @@ __device__ inline u64 merge32(u64 a, u64 b) {
     return k;
 }
 
-// A warp's list with its buffer of candidates.
-constexpr int kBuf = 32 * 8 + 32;  // what one vector of every lane may add to 31 waiting keys
-
-struct TopList {
-    u64 list;   // this lane's key
-    u64 limit;  // the Kout-th key: only larger ones matter
-    float low;  // its logit
-    int count;  // keys in the buffer
-    u64* buf;   // kBuf keys of shared memory
-
-    __device__ void set_limit(u64 k) {
-        if (k > limit) {
-            limit = k;
-            low = key_value(k);
-        }
-    }
-    // Merges waiting keys, 32 at a time, while at least `least` of them wait.
-    __device__ __noinline__ void flush(int least, int kout) {
-        const int lane = threadIdx.x & 31;
-        __syncwarp();
-        for (; count >= least; count -= 32) {  // from the back of the buffer: the rest stays where it is
-            const int at = count - 32 + lane;
-            list = merge32(list, sort32(at >= 0 ? buf[at] : 0));
-        }
-        count = max(count, 0);
-        __syncwarp();
-        set_limit(__shfl_sync(0xffffffffu, list, kout - 1));
-    }
-    // n elements of each lane with consecutive indices.
-    template <int n>
-    __device__ void offer(const float (&x)[n], unsigned idx, bool in, int kout) {
-        const int lane = threadIdx.x & 31;
-        u64 key[n];
-        int mine = 0;
-#pragma unroll
-        for (int e = 0; e < n; ++e) {
-            key[e] = in && x[e] >= low ? pack_key(x[e], idx + e) : 0;
-            mine += key[e] > limit;
-        }
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        int at = count + upto - mine;
-#pragma unroll
-        for (int e = 0; e < n; ++e)
-            if (key[e] > limit) buf[at++] = key[e];
-        count += __shfl_sync(0xffffffffu, upto, 31);
-        if (count >= 32) flush(32, kout);
-    }
-};
-
 template <typename T>
 struct Vec {
     static constexpr int kE = 16 / sizeof(T);
@@ -190,19 +135,29 @@ __device__ inline bool row_ended(const lucetree_beam_args& a, int row) {
     return a.finished && a.finished[row] != 0;
 }
 
+// The best keys of all warps' sorted lists in s_list[0] (kWarps lists of 32).
+__device__ inline void merge_warps(u64 (*s_list)[32], u64 mine) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    s_list[warp][lane] = mine;
+#pragma unroll
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        if (warp < half) s_list[warp][lane] = mine = merge32(mine, s_list[warp + half][lane]);
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(BeamLaunch L) {
     constexpr int kE = Vec<T>::kE;
-    __shared__ u64 s_buf[kWarps][kBuf];
+    __shared__ u64 s_list[kWarps][32];
     __shared__ float2 s_sum[kWarps];
     const lucetree_beam_args& a = L.a;
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    const int row = blockIdx.y, chunk = blockIdx.x;
+    const int row = blockIdx.y, chunk = blockIdx.x, t = threadIdx.x;
     // rows that ended or are dead need no logits (launch 2 knows their candidates)
     if (row_ended(a, row) || a.cum[row] == -INFINITY) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kout = a.beams_out;
+    const int warp = t >> 5, lane = t & 31;
     const T* x = reinterpret_cast<const T*>(a.logits) + (long long)row * a.row_stride;
     // 16-byte vectors from the first aligned element on; the elements before
     // and behind them (fewer than 2 kE) belong to the row's last chunk
@@ -211,34 +166,28 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(BeamLaunch L) {
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
     const int v0 = (int)((long long)nv * chunk / L.chunks), v1 = (int)((long long)nv * (chunk + 1) / L.chunks);
 
-    TopList top{0, 0, -INFINITY, 0, s_buf[warp]};
+    // thread t's vectors are v0 + t, v0 + t + kThreads, ..
     float m = -INFINITY, s = 0.f;
-    for (int base = v0; base < v1; base += kU * kThreads) {
+    int best = v0 + t;
+    for (int base = v0 + t; base < v1; base += kU * kThreads) {
         uint4 u[kU];
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
-            const int v = base + k * kThreads + threadIdx.x;
-            if (v < v1) u[k] = __ldg(xv + v);
-        }
-        // largest element of each vector, of the batch
-        float vm[kU], mb = -INFINITY;
+        for (int k = 0; k < kU; ++k)
+            if (base + k * kThreads < v1) u[k] = __ldg(xv + base + k * kThreads);
+        float mb = m;
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-            vm[k] = vector_max<T>(u[k]);
-            if (base + k * kThreads + (int)threadIdx.x >= v1) vm[k] = -INFINITY;
-            mb = fmaxf(mb, vm[k]);
-        }
-        if (base == v0) {
-            // lane maxima are elements: the Kout-th of them bounds the Kout-th element from below (a key
-            // with the highest index of its value, so that no tie is lost)
-            top.set_limit(__shfl_sync(0xffffffffu, sort32(pack_key(mb, 0xffffffffu)), kout - 1));
+            const float vm = vector_max<T>(u[k]);
+            if (base + k * kThreads < v1 && vm > mb) {
+                mb = vm;
+                best = base + k * kThreads;
+            }
         }
         if (mb > m) {
             s = m == -INFINITY ? 0.f : s * exp_diff(m, mb);
             m = mb;
         }
         const float mm = m == -INFINITY ? 0.f : m;
-        unsigned may = 0;  // vectors with an element that may pass
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
             float f[kE];
@@ -246,49 +195,51 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(BeamLaunch L) {
             float part = 0.f;
 #pragma unroll
             for (int e = 0; e < kE; ++e) part += exp_diff(f[e], mm);
-            if (base + k * kThreads + (int)threadIdx.x < v1) {
-                s += part;
-                may |= vm[k] >= top.low ? 1u << k : 0u;
-            }
+            if (base + k * kThreads < v1) s += part;
         }
-        // those vectors once more (few, and still in the cache), with one copy of the list's code
-        may = __reduce_or_sync(0xffffffffu, may);
-        while (may) {
-            const int k = __ffs(may) - 1;
-            may &= may - 1;
-            const int v = base + k * kThreads + threadIdx.x;
+    }
+    // the threads with the best maxima
+    merge_warps(s_list, sort32(v0 + t < v1 ? pack_key(m, (unsigned)best) : 0));
+    __syncthreads();
+    const u64 threads = s_list[0][lane];
+    const u64 limit = __shfl_sync(0xffffffffu, threads, a.beams_out - 1);  // 0: fewer threads than that have a vector
+    // a warp goes through one thread's vectors at a time
+    u64 list = 0;
+    for (int i = warp; i < a.beams_out; i += kWarps) {
+        const u64 key = __shfl_sync(0xffffffffu, threads, i);
+        if (key == 0) break;
+        const int first = v0 + (int)((key_index(key) - (unsigned)v0) % kThreads);
+        for (int v = first + lane * kThreads; __any_sync(0xffffffffu, v < v1); v += 32 * kThreads) {
+            u64 keys[kE];
             float f[kE];
-            const bool in = v < v1;
-            unpack<T>(in ? __ldg(xv + v) : make_uint4(0, 0, 0, 0), f);
-            top.offer<kE>(f, (unsigned)(head + v * kE), in, kout);
+            unpack<T>(v < v1 ? __ldg(xv + v) : make_uint4(0, 0, 0, 0), f);
+            // no element of a vector below the limit is among the best (keys of vectors order as their elements' do)
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+                keys[e] = v < v1 && pack_key(f[e], (unsigned)v) >= limit ? pack_key(f[e], (unsigned)(head + v * kE + e)) : 0;
+#pragma unroll
+            for (int e = 0; e < kE; ++e)
+                if (__any_sync(0xffffffffu, keys[e] != 0)) list = merge32(list, sort32(keys[e]));
         }
     }
     if (chunk == L.chunks - 1 && warp == 0) {
         const int tail = head + nv * kE;  // first element behind the vectors
-        const int t = lane < head ? lane : tail + lane - head;
-        const bool in = t < a.vocab && (lane < head || t >= tail);
-        const float f[1] = {in ? scalar(x + t) : -INFINITY};
-        if (in) add_sums(m, s, f[0], f[0] == -INFINITY ? 0.f : 1.f);
-        top.offer<1>(f, (unsigned)t, in, kout);
+        const int i = lane < head ? lane : tail + lane - head;
+        const bool in = i < a.vocab;
+        const float f = in ? scalar(x + i) : -INFINITY;
+        if (in) add_sums(m, s, f, f == -INFINITY ? 0.f : 1.f);
+        list = merge32(list, sort32(in ? pack_key(f, (unsigned)i) : 0));
     }
-    top.flush(1, kout);
     // the CTA's sum and list
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         add_sums(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-    s_buf[warp][lane] = top.list;
     if (lane == 0) s_sum[warp] = make_float2(m, s);
-#pragma unroll 1
-    for (int half = kWarps / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        if (warp < half) {
-            const u64 k = merge32(s_buf[warp][lane], s_buf[warp + half][lane]);
-            s_buf[warp][lane] = k;
-        }
-    }
+    __syncthreads();  // every warp has read the threads' list
+    merge_warps(s_list, list);
     if (warp == 0) {
         const size_t at = (size_t)row * L.chunks + chunk;
-        L.keys[at * 32 + lane] = s_buf[0][lane];
+        L.keys[at * 32 + lane] = s_list[0][lane];
         if (lane == 0) {
             for (int w = 1; w < kWarps; ++w) add_sums(m, s, s_sum[w].x, s_sum[w].y);
             L.sums[at] = make_float2(m, s);
@@ -341,6 +292,7 @@ __device__ inline double order_value(u64 u) {
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L) {
     __shared__ u64 s_keys[kMergeWarps][32];
     __shared__ Cand s_cand[kMergeWarps][32];
+    __shared__ double s_lse[kMergeWarps];
     const lucetree_beam_args& a = L.a;
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
@@ -359,6 +311,20 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
         for (int c = w; c < L.chunks; c += per) list = merge32(list, keys[(size_t)c * 32 + lane]);
     }
     s_keys[warp][lane] = list;
+    if (mine && !ended && !dead && w == per - 1) {
+        // log-sum-exp of the row from its chunks
+        const float2* sums = L.sums + (size_t)row * L.chunks;
+        float m = -INFINITY;
+        for (int c = lane; c < L.chunks; c += 32) m = fmaxf(m, sums[c].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        double s = 0.0;
+        for (int c = lane; c < L.chunks; c += 32)
+            if (sums[c].x > -INFINITY) s += (double)(sums[c].y * exp_diff(sums[c].x, m));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) s_lse[k] = m > -INFINITY ? (double)m + log(s) : -INFINITY;
+    }
     __syncthreads();
     Cand cand{0, ~0u};  // none: behind every candidate
     if (mine && w == 0) {
@@ -373,20 +339,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
             if (eos) token = lane == 0 ? a.eos : (lane - 1 < a.eos ? lane - 1 : lane);
             if (eos && lane == 0) score = cum;
         } else if (!dead) {
-            // log-sum-exp of the row from its chunks
-            float m = -INFINITY;
-            for (int c = lane; c < L.chunks; c += 32) m = fmaxf(m, L.sums[(size_t)row * L.chunks + c].x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (m > -INFINITY) {
-                double s = 0.0;
-                for (int c = lane; c < L.chunks; c += 32) {
-                    const float2 p = L.sums[(size_t)row * L.chunks + c];
-                    if (p.x > -INFINITY) s += (double)(p.y * exp_diff(p.x, m));
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                const double lse = (double)m + log(s);
+            const double lse = s_lse[k];
+            if (lse > -INFINITY) {
                 have = list != 0;
                 token = have ? (int)key_index(list) : 0;
                 const float x = key_value(list);
@@ -415,9 +369,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
     }
 }
 
-// About four CTAs per SM over all rows, and no chunk shorter than a round of loads of half the CTA's threads.
+// No more CTAs than run at once (four per SM), as long as there are no more rows
+// than that, and no chunk of fewer than four elements a thread.
 int beam_chunks(int rows, int vocab, int sms) {
-    int chunks = (4 * sms + rows - 1) / rows;
+    int chunks = 4 * sms / rows;
     const int most = (vocab + 4 * kThreads - 1) / (4 * kThreads);
     if (chunks > most) chunks = most;
     return chunks < 1 ? 1 : chunks;
