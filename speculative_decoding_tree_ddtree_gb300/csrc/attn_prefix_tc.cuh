@@ -57,6 +57,8 @@
 // copies and MMAs and returns.
 #pragma once
 
+#include <type_traits>
+
 #include "e4m3.cuh"
 #include "internal.cuh"
 #include "tc_ptx.cuh"
@@ -131,7 +133,7 @@ struct Misc {
     uint32_t tmem_base;
     int abort_flag;
     int empty_cols;  // windowed: a query row has seen no key of its range so far
-    alignas(8) uint8_t depth[kRowsMax];  // windowed: depth of each query row's node
+    alignas(16) uint8_t depth[kRowsMax];  // windowed: depth of each query row's node
 };
 static_assert(sizeof(Misc) <= 5632, "misc region");
 static_assert(offsetof(Misc, vexp) == 0 && sizeof(Misc::vexp[0]) % 128 == 0, "128-byte aligned TMA destinations");
@@ -155,30 +157,23 @@ struct Piece {
     WinSpan w;   // windowed: the virtual pages that the tiles are made of
 };
 
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ int pages_of(const Piece& pc) {
     return WIN ? pc.w.vp : (pc.L + kPage - 1) / kPage;
 }
 // The page-table entry of the segment's page number v.
-template <bool WIN>
+template <int WIN>
 __device__ __forceinline__ int table_page(const Piece& pc, int v) {
     return WIN ? win_page(pc.w, v) : v;
 }
 
-template <bool WIN>
+template <int WIN>
 struct PieceIter {
     int t0, t1, off, s;  // off: flat offset of segment s
     __device__ bool next(const PlanDims& p, const int32_t* ctx_len, Piece& out) {
         while (s < p.S && off < t1) {
             const int L = seq_len_quiet(ctx_len, s / p.Hkv, p.max_pages);
-            int tiles;
-            if constexpr (WIN) {
-                out.w = win_span(L, p.window, p.sinks);
-                tiles = (out.w.vp + 1) / 2;
-            } else {
-                tiles = (int)tiles_of(L);
-            }
-            const int s0 = off, s1 = off + tiles;
+            const int s0 = off, s1 = off + (int)tiles_of(L);
             const int cur = s;
             off = s1;
             ++s;
@@ -192,18 +187,41 @@ struct PieceIter {
         return false;
     }
 };
+// Windowed: starts at the range's first segment, and reads a length only when a
+// sequence begins.
+struct WinPieceIter {
+    int t0, t1, off, b, g, L;
+    __device__ bool next(const PlanDims& p, const int32_t* ctx_len, Piece& out) {
+        while (b < p.B && off < t1) {
+            out.w = win_span(L, p.window, p.sinks);
+            const int s0 = off, s1 = off + (out.w.vp + 1) / 2;
+            out.s = b * p.Hkv + g;
+            out.L = L;
+            off = s1;
+            if (++g == p.Hkv) {
+                g = 0;
+                if (++b < p.B) L = seq_len_quiet(ctx_len, b, p.max_pages);
+            }
+            if (s1 == s0) continue;
+            out.ta = (t0 > s0 ? t0 : s0) - s0;
+            out.te = (t1 < s1 ? t1 : s1) - s0;
+            return true;
+        }
+        return false;
+    }
+};
 
 // The CTA's tiles in order: piece (key segment) and tile within the segment.
-template <bool WIN>
+template <int WIN>
 struct TileCursor {
-    PieceIter<WIN> it;
+    typename std::conditional<WIN != 0, WinPieceIter, PieceIter<WIN>>::type it;
     Piece pc;
     int t;
     int piece_no;
     bool live;
-    // (off, s): a segment at or before the range's first one, and its flat offset
-    __device__ void start(int t0, int t1, const PlanDims& p, const int32_t* ctx_len, int off, int s) {
-        it = PieceIter<WIN>{t0, t1, off, s};
+    __device__ void start(const WinStart& st, const PlanDims& p, const int32_t* ctx_len) {
+        if constexpr (WIN != 0) it = {st.t0, st.t1, st.off, st.b, st.g, st.L};
+        else it = {st.t0, st.t1, 0, 0};
         piece_no = -1;
         t = 0;
         next_piece(p, ctx_len);
@@ -238,6 +256,20 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// Bit k: byte k of eight node depths is at most dmax (0 .. 127; depths are below 64).
+__device__ __forceinline__ uint32_t depths_up_to(uint2 d, int dmax) {
+    // dmax - d in every byte at once, its sign bit kept out of the neighbours by the 128 added
+    const uint32_t base = (uint32_t)(128 + dmax) * 0x01010101u;
+    const uint32_t lo = ((base - d.x) >> 7) & 0x01010101u, hi = ((base - d.y) >> 7) & 0x01010101u;
+    // bytes 0, 1, 2, 3 -> bits 0, 1, 2, 3
+    return ((lo * 0x01020408u) >> 24 & 0xFu) | ((hi * 0x01020408u) >> 20 & 0xF0u);
+}
+// Maximum over the warp in one instruction.
+__device__ __forceinline__ float redux_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
 
 // Column maxima of a warp's 16 x 32 values (v[k] = column k in this lane):
 // recursive halving over the lane bits 16, 8, 4, 2 (a lane keeps the upper or
@@ -266,6 +298,11 @@ __device__ __forceinline__ float col_sum16(float (&v)[16], int lane) { return co
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
@@ -303,8 +340,12 @@ __device__ __forceinline__ bool aborted(Misc* ms) { return *(volatile int*)&ms->
 // hold the window's edge, a key counts for the rows of the nodes deep enough
 // only (one comparison of the row's depth per score, in warps that need it).
 // V rows that no node sees (past the sinks, before the window) are zeroed like
-// those past L.
-template <int D, bool BF16, int RGP, int VQ, int KQ, bool WIN>
+// those past L.  WIN = 2: bf16 with a bf16 output.  P is then rounded to bf16
+// (half a step is 2^-8 of a term, as much as the output's own rounding; terms'
+// roundings are independent and average out in the sum) and V is multiplied as it
+// lands, so its conversion's two passes through shared memory and the wait for it
+// fall away.
+template <int D, bool BF16, int RGP, int VQ, int KQ, int WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ve,
@@ -315,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChunksV = D / 64;                       // ring chunks per V operand
     static_assert(!KQ || (D == 256 && BF16), "E4M3 K: head dim 256, bf16 queries");
     static_assert(!WIN || (VQ == 0 && KQ == 0), "windowed attention: 16-bit K and V");
+    static_assert(WIN != 2 || BF16, "P in bf16: bf16 operands");
+    constexpr bool kConvert = BF16 && WIN != 2;  // V converted to fp16 on chip
     constexpr int kNch = Lay::kNch;
     constexpr int kNa = (kNch + kSmGroups - 1) / kSmGroups;  // column chunks per softmax warp (at most)
     constexpr int kNS = Lay::kNS;
@@ -390,20 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // wait, relying on this kernel having waited for their producers first.
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    long long nT;
-    int off0 = 0, seg0 = 0;
-    if constexpr (WIN) nT = win_total(p, a.ctx_len, 0, &off0);
-    else nT = total_tiles(p, a.ctx_len);
-    const int t0 = nT ? (int)cta_begin(cta, nT, p.Cg) : 0, t1 = nT ? (int)cta_begin(cta + 1, nT, p.Cg) : 0;
+    WinStart ws0 = {0, 0, 0, 0, 0, 0};
+    if constexpr (WIN != 0) {
+        ws0 = win_start(p, a.ctx_len, cta);
+    } else {
+        const long long nT = total_tiles(p, a.ctx_len);
+        ws0.t0 = nT ? (int)cta_begin(cta, nT, p.Cg) : 0;
+        ws0.t1 = nT ? (int)cta_begin(cta + 1, nT, p.Cg) : 0;
+    }
+    const int t0 = ws0.t0, t1 = ws0.t1;
     if (t0 >= t1) {  // uniform across the CTA: nothing to do but give TMEM back
         if (warp == 1) tmem_dealloc(tmem, kTmemCols);
         return;
     }
     const uint32_t n_tiles = (uint32_t)(t1 - t0);
-    if constexpr (WIN) {  // every role starts at the sequence of the range's first tile
-        win_find(p, a.ctx_len, t0, &seg0, &off0);
-        seg0 *= p.Hkv;
-    }
 
     if (warp < 4) {
     regs_dec<kRegsIssue>();
@@ -456,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         TileCursor<WIN> cur;
-        cur.start(t0, t1, p, a.ctx_len, off0, seg0);
+        cur.start(ws0, p, a.ctx_len);
         int npages = 0;
         const int32_t* pt = a.page_table;
         // page ids of the current piece, 16 tiles (32 pages) per warp-wide load, one batch ahead
@@ -538,16 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             // (for E4M3 K the same descriptor bits read as E4M3 x E4M3 under kind::f8f6f4)
             const uint32_t id_qk = idesc_f16(128, RGP, KQ ? 0u : kAB, 0, 0);
-            const uint32_t id_pv = idesc_f16(128, RGP, 0u, 1, 1);  // fp16 V and P
+            const uint32_t id_pv = idesc_f16(128, RGP, WIN == 2 ? 1u : 0u, 1, 1);  // V and P: fp16 (WIN = 2: bf16)
             constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
             constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
             constexpr uint64_t hi_p = desc_hi(128, 2048, kLayoutInterleave);
             const uint32_t aQ = smem_u32(sQ), aP = smem_u32(sP), aS = smem_u32(sSlots);
             uint32_t chunk = 0, jq = 0, j = 0;
             bool ok = true;
+            // windowed: one cursor (qk); PV's first-tile flags follow from QK's, kept in
+            // first_bits (bit 0: the last QK issued), which spares this warp's registers
             TileCursor<WIN> qk, pv;
-            qk.start(t0, t1, p, a.ctx_len, off0, seg0);
-            pv.start(t0, t1, p, a.ctx_len, off0, seg0);
+            uint32_t first_bits = 0;
+            qk.start(ws0, p, a.ctx_len);
+            if constexpr (WIN == 0) pv.start(ws0, p, a.ctx_len);
             // S^T(jq) = K(jq) . Q^T; S^T is free once the softmax has read tile jq-1
             auto issue_qk = [&]() -> bool {
                 if (jq > 0) {
@@ -585,12 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mma_commit(&ms->s_full);
                 if (qk.last()) mma_commit(&ms->q_empty);
+                first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
                 ++jq;
                 qk.step(p, a.ctx_len);
                 return true;
             };
             if (qk.live) ok = issue_qk();
-            while (ok && pv.live) {
+            while (ok && (WIN ? j < n_tiles : pv.live)) {
                 if (aborted(ms)) {
                     ok = false;
                     break;
@@ -609,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // O^T += V^T . P^T once the softmax has written P^T(j)
                     if (!(ok = mbar_wait(&ms->p_full, j & 1))) break;
                     tc_fence_after();
-                    const bool first = pv.first();
+                    const bool first = WIN ? (first_bits >> (jq - 1 - j)) & 1u : pv.first();
                     // output dims 128h..128h+127: chunk 2h holds keys 0..63, chunk
                     // 2h+1 keys 64..127 (four 16-key steps each)
                     for (int h = 0; h < kChunksV / 2 && ok; ++h) {
@@ -633,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     mma_commit(&ms->pv_done);
                     ++j;
-                    pv.step(p, a.ctx_len);
+                    if constexpr (WIN == 0) pv.step(p, a.ctx_len);
                 }
             }
             if (!ok || aborted(ms)) {
@@ -656,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // swizzle permutes units only within a key's row).
         const int ct = threadIdx.x - 64;  // 0 .. 63
         TileCursor<WIN> cur;
-        cur.start(t0, t1, p, a.ctx_len, off0, seg0);
+        cur.start(ws0, p, a.ctx_len);
         uint32_t j = 0;
         bool ok = true;
         while (ok && cur.live) {
@@ -686,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool whole = nv >= 64 && (!WIN || ns >= 64 || nl <= 0);
                 constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
                 constexpr int kBatch = 4;                                      // loads in flight
-                if (BF16 && whole) {
+                if (kConvert && whole) {
                     // a full page (every chunk but a segment's last few): no per-key test
 #pragma unroll 1
                     for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
@@ -702,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             base[ct + 32 * kConvWarps * (i0 + k)] = x[k];
                         }
                     }
-                } else if (BF16 || !whole) {
+                } else if (kConvert || !whole) {
 #pragma unroll 1
                     for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
                         uint4 x[kBatch];
@@ -717,13 +764,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) {
                             const int u = ct + 32 * kConvWarps * (i0 + k);
-                            if constexpr (BF16) {
+                            if constexpr (kConvert) {
                                 x[k].x = bf16x2_to_f16x2(x[k].x);
                                 x[k].y = bf16x2_to_f16x2(x[k].y);
                                 x[k].z = bf16x2_to_f16x2(x[k].z);
                                 x[k].w = bf16x2_to_f16x2(x[k].w);
                             }
-                            if (BF16 || !kv[k]) base[u] = x[k];
+                            if (kConvert || !kv[k]) base[u] = x[k];
                         }
                     }
                 }
@@ -789,22 +836,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float4 ma = m4[0], mb = m4[1];
                     const float mv[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
                     float pv[8];
-                    float xw[8];  // windowed: exponents with the rows whose window does not reach my key masked
-                    if constexpr (WIN) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            xw[k] = valid ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY;
-                        if (part) {
-                            const uint2 dd = *reinterpret_cast<const uint2*>(ms->depth + 16 * c + 8 * hb);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if ((int)(((k < 4 ? dd.x : dd.y) >> (8 * (k & 3))) & 0xFFu) > dmax) xw[k] = -INFINITY;
-                        }
+                    uint32_t vis = 0;  // windowed: bit k: column k's row sees my key
+                    if constexpr (WIN != 0) {
+                        vis = valid ? 0xFFu : 0u;
+                        if (part)
+                            vis &= depths_up_to(*reinterpret_cast<const uint2*>(ms->depth + 16 * c + 8 * hb), dmax);
                     }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float x =
-                            WIN ? xw[k] : (valid ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY);
+                        const bool sees = WIN ? ((vis >> k) & 1u) != 0 : valid;
+                        const float x = sees ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY;
                         ex = fmaxf(ex, x);
                         pv[k] = ex2(x);
                         float& acc = lpart[cc * 16 + 8 * hb + k];
@@ -812,7 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (keep_p) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) ph[4 * bi + k] = pack_half2(pv[2 * k], pv[2 * k + 1]);
+                        for (int k = 0; k < 4; ++k)
+                            ph[4 * bi + k] = WIN == 2 ? pack_bf162(pv[2 * k], pv[2 * k + 1])
+                                                      : pack_half2(pv[2 * k], pv[2 * k + 1]);
                     }
                 }
             }
@@ -829,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
 
         TileCursor<WIN> cur;
-        cur.start(t0, t1, p, a.ctx_len, off0, seg0);
+        cur.start(ws0, p, a.ctx_len);
 
         while (cur.live) {
             const int piece_no = cur.piece_no;
@@ -1029,13 +1072,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld16(tl + 16 * c, r);
                         tmem_wait_ld_regs16(r);
                         const int lim = valid ? R_seg - 16 * c : 0;
+                        // maxima of the 16 columns over the warp's 32 key lanes
+                        if constexpr (WIN != 0) {
+                            uint32_t vis = lim >= 16 ? 0xFFFFu : lim > 0 ? (1u << lim) - 1u : 0u;
+                            if (part) {
+                                const uint4 dd = *reinterpret_cast<const uint4*>(ms->depth + 16 * c);
+                                vis &= depths_up_to(make_uint2(dd.x, dd.y), dmax) |
+                                       depths_up_to(make_uint2(dd.z, dd.w), dmax) << 8;
+                            }
+                            float mine = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float cm =
+                                    redux_max((vis >> k) & 1u ? __uint_as_float(r[k]) * sl2 : -INFINITY);
+                                if (lane == k) mine = cm;
+                            }
+                            if (lane < 16) ms->col_red[quarter][16 * c + lane] = mine;
+                            continue;
+                        }
                         float v[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            v[k] = k < lim ? __uint_as_float(r[k]) * sl2 : -INFINITY;
-                            if (WIN && part && (int)ms->depth[16 * c + k] > dmax) v[k] = -INFINITY;
-                        }
-                        // maxima of the 16 columns over the warp's 32 key lanes
+                        for (int k = 0; k < 16; ++k) v[k] = k < lim ? __uint_as_float(r[k]) * sl2 : -INFINITY;
                         const float cm = col_max16(v, lane);
                         if ((lane & 1) == 0) ms->col_red[quarter][16 * c + (lane >> 1)] = cm;
                     }
@@ -1301,7 +1358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool BF16, int RGP, int VQ, int KQ, bool WIN>
+template <int D, bool BF16, int RGP, int VQ, int KQ, int WIN>
 cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, const CUtensorMap& tve,
                        const CUtensorMap& tq2, const AttnLaunch& L, cudaStream_t stream) {
     using Lay = Layout<D, RGP>;
@@ -1314,7 +1371,7 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
 
 // tve: the per-token exponents of quantised V (VQ != 0); tq2: the low query
 // parts of E4M3 K (KQ != 0); unused otherwise
-template <int D, bool BF16, int VQ = 0, int KQ = 0, bool WIN = false>
+template <int D, bool BF16, int VQ = 0, int KQ = 0, int WIN = 0>
 cudaError_t launch_rgp(int rgp, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                        const CUtensorMap& tve, const CUtensorMap& tq2, const AttnLaunch& L, cudaStream_t stream) {
     static_assert(kRowsMax == 144, "one instantiation per padded row count up to kRowsMax");

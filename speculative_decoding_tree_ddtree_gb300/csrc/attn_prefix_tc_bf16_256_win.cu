@@ -1,5 +1,5 @@
 // Instantiations of the tensor-core prefix kernel with a sliding window and sinks, bf16 operands, head
-// dim 256; dispatch over the head dim.
+// dim 256; dispatch over the head dim and the output type.
 #include "attn_prefix_tc.cuh"
 
 namespace lucetree {
@@ -7,10 +7,14 @@ namespace lucetree {
 cudaError_t launch_prefix_tc_bf16_128_win(int rgp, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                           const AttnLaunch& L, cudaStream_t stream);
 
+cudaError_t launch_prefix_tc_bf16_256_win16(int rgp, const CUtensorMap& tk, const CUtensorMap& tv,
+                                            const CUtensorMap& tq, const AttnLaunch& L, cudaStream_t stream);
+
 cudaError_t launch_prefix_tc_bf16_win(int rgp, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                       const AttnLaunch& L, cudaStream_t stream) {
     if (L.a.D == 128) return launch_prefix_tc_bf16_128_win(rgp, tk, tv, tq, L, stream);
-    return prefix_tc::launch_rgp<256, true, 0, 0, true>(rgp, tk, tv, tq, tv, tv, L, stream);
+    if (L.out_dtype == LUCETREE_BF16) return launch_prefix_tc_bf16_256_win16(rgp, tk, tv, tq, L, stream);
+    return prefix_tc::launch_rgp<256, true, 0, 0, 1>(rgp, tk, tv, tq, tv, tv, L, stream);
 }
 
 }  // namespace lucetree

@@ -6,7 +6,7 @@ namespace lucetree {
 
 cudaError_t launch_prefix_tc_f16_128_win(int rgp, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                           const AttnLaunch& L, cudaStream_t stream) {
-    return prefix_tc::launch_rgp<128, false, 0, 0, true>(rgp, tk, tv, tq, tv, tv, L, stream);
+    return prefix_tc::launch_rgp<128, false, 0, 0, 1>(rgp, tk, tv, tq, tv, tv, L, stream);
 }
 
 }  // namespace lucetree

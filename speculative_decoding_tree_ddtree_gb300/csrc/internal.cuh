@@ -183,30 +183,49 @@ __device__ inline int win_total(const PlanDims& p, const int32_t* ctx_len, int b
     return all * p.Hkv;
 }
 
-// The sequence that flat tile t belongs to and the flat offset of its first
-// tile, by the whole warp.
-__device__ inline void win_find(const PlanDims& p, const int32_t* ctx_len, int t, int* b_of, int* off_of) {
+// Where a CTA of the prefix kernel starts: its tile range and the key segment of
+// its first tile, found by the whole warp from one read of the lengths.
+struct WinStart {
+    int t0, t1;  // tile range, empty when t0 == t1
+    int b, g;    // sequence and KV head of tile t0
+    int off;     // flat offset of that segment's first tile
+    int L;       // committed length of sequence b
+};
+
+__device__ inline WinStart win_start(const PlanDims& p, const int32_t* ctx_len, int cta) {
     const int lane = threadIdx.x & 31;
-    int off = 0;
+    WinStart s = {0, 0, 0, 0, 0, 0};
+    int before, nT = p.B > 32 ? win_total(p, ctx_len, 0, &before) : 0, off = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int mine = b0 + lane < p.B ? win_tiles(p, ctx_len, b0 + lane) * p.Hkv : 0;
+        const int L = b0 + lane < p.B ? seq_len_quiet(ctx_len, b0 + lane, p.max_pages) : 0;
+        const int tiles = (win_span(L, p.window, p.sinks).vp + 1) / 2, mine = tiles * p.Hkv;
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
         }
-        const unsigned in = __ballot_sync(0xffffffffu, t < off + incl);
-        if (in) {
-            const int l = __ffs(in) - 1;
-            *b_of = b0 + l;
-            *off_of = off + __shfl_sync(0xffffffffu, incl - mine, l);
-            return;
+        const int all = __shfl_sync(0xffffffffu, incl, 31);
+        if (b0 == 0) {
+            if (p.B <= 32) nT = all;
+            if (nT == 0) return s;
+            s.t0 = (int)cta_begin(cta, nT, p.Cg);
+            s.t1 = (int)cta_begin(cta + 1, nT, p.Cg);
+            if (s.t0 == s.t1) return s;
         }
-        off += __shfl_sync(0xffffffffu, incl, 31);
+        const unsigned in = __ballot_sync(0xffffffffu, s.t0 < off + incl);
+        if (in) {
+            const int l = __ffs(in) - 1, per = __shfl_sync(0xffffffffu, tiles, l);
+            s.b = b0 + l;
+            s.off = off + __shfl_sync(0xffffffffu, incl - mine, l);
+            s.L = __shfl_sync(0xffffffffu, L, l);
+            s.g = (s.t0 - s.off) / per;
+            s.off += s.g * per;
+            return s;
+        }
+        off += all;
     }
-    *b_of = p.B;
-    *off_of = off;
+    return s;
 }
 
 // ---------------------------------------------------------------------------

@@ -60,13 +60,13 @@ def make(ctx, N, Hq, Hkv, D, dtype, window, sinks, tree="random", seed=0, spare=
                 anc_mask=torch.from_numpy(anc.view(np.int64)), paths=paths, window=window, sinks=sinks)
 
 
-def reference(s, scale=None):
+def reference(s, scale=None, p_step=2.0 ** -11):
     """(out, lse, bound): the formula in 64 bits, row by row, and how far a
     correct kernel's output may be from it.
 
-    P is rounded to fp16 (half a step: 2^-11 of each term) relative to a shift
-    that lies within the factor 2^8 of the row's largest term, so a term below
-    2^-24 of it is off by at most 2^-25.  A score is a sum of D exact products
+    P is rounded to fp16 (half a step: 2^-11 of each term; with a bf16 output to
+    bf16: 2^-8) relative to a shift that lies within the factor 2^8 of the row's
+    largest term, so a term below 2^-24 of it is off by at most 2^-25.  A score is a sum of D exact products
     in fp32: off by at most D 2^-24 sum|q k| scale, which moves each term by
     that fraction; 2^-20 more covers the exponential, the sums and the shifts."""
     q, (B, N, Hq, D) = s["q"].double(), s["q"].shape
@@ -92,10 +92,13 @@ def reference(s, scale=None):
                 p = torch.exp(x - lse[b, i, hs, None])
                 out[b, i, hs] = p @ v
                 err = (D * 2.0 ** -24 * abs(scale) * (q[b, i, hs].abs() @ k.abs().T)).amax(-1, keepdim=True) + 2.0 ** -20
-                bound[b, i, hs] = (2.0 ** -11 + 2 * err) * (p @ v.abs()) + \
+                bound[b, i, hs] = (p_step + 2 * err) * (p @ v.abs()) + \
                     2.0 ** -25 * p.amax(-1, keepdim=True) * v.abs().sum(0)
                 lse_bound[b, i, hs] = err[:, 0] + 2.0 ** -24 * lse[b, i, hs].abs()
     return out, lse, bound, lse_bound
+
+
+P_STEP = {torch.float32: 2.0 ** -11, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
 
 
 def call(s, out_dtype, lse=True, scale=None, stream=None):
@@ -117,7 +120,7 @@ def call(s, out_dtype, lse=True, scale=None, stream=None):
 
 def check(s, out_dtype, **kw):
     out, lse, status = call(s, out_dtype, **kw)
-    ref, ref_lse, bound, lse_bound = reference(s, kw.get("scale"))
+    ref, ref_lse, bound, lse_bound = reference(s, kw.get("scale"), P_STEP[out_dtype])
     assert status == 0
     bound = bound + (0 if out_dtype == torch.float32 else torch.finfo(out_dtype).eps / 2) * (ref.abs() + bound)
     assert torch.isfinite(out).all()
@@ -242,6 +245,6 @@ def test_captured_and_replayed_on_another_stream(cuda_dev):
             side.wait_stream(torch.cuda.default_stream())
             graph.replay()
         torch.cuda.synchronize()
-        ref, _, bound, _ = reference(s)
+        ref, _, bound, _ = reference(s, p_step=P_STEP[out.dtype])
         assert ((out.cpu().double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
     assert int(st.item()) == 0
