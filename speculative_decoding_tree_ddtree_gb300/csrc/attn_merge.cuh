@@ -63,38 +63,13 @@ __device__ __forceinline__ void group_sync(int bar_id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(bar_id), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__half* p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// DPL consecutive outputs of a lane, 4 or 8 of fp32 or 16 bits
-template <int DPL, typename TO>
-__device__ __forceinline__ void store_slice(TO* p, const float (&v)[DPL]) {
-    if constexpr (sizeof(TO) == 4) {
-#pragma unroll
-        for (int x = 0; x < DPL; x += 4)
-            *reinterpret_cast<float4*>(p + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
-    } else {
-        alignas(16) TO t[DPL];
-#pragma unroll
-        for (int x = 0; x < DPL; ++x) store_out(t + x, v[x]);
-        if constexpr (DPL == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
-        else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
-    }
-}
-
 // One output row (b, node i, head h) by a group of W warps starting at warp
 // wbase of the CTA, which synchronise on named barrier bar_id (so several
 // groups of a CTA can each merge a row).  anc: the node's ancestor-or-self
 // mask.  s_o: W x D floats and s_red: W floats of shared memory (the
 // group's own).  Runs the tree block, then pdl_wait(), then the log-sum-exp
 // merge of the prefix partials.  The arithmetic depends only on W.
-//
-// WIN: ancestors outside the node's window (and not among the sinks) are left
-// out, the split follows the window's key list, a row that sees no key at all
-// (a mask without the node itself) gives zeros and lse = -inf, and the output
-// is stored as TO (rounded once from fp32).
-template <typename T, int D, int W, int kBar = 1, bool WIN = false, typename TO = float>
+template <typename T, int D, int W, int kBar = 1>
 __device__ __forceinline__ void merge_row(const AttnLaunch& L, long long row, uint64_t anc, float (*s_o)[D],
                                           float* s_red, int wbase = 0) {
     constexpr int bar_id = kBar;
@@ -125,17 +100,6 @@ __device__ __forceinline__ void merge_row(const AttnLaunch& L, long long row, ui
         load_slice<T, D>(reinterpret_cast<const T*>(a.q) + (size_t)row * D + lane * DPL, qf);
         if (p.N < 64) anc &= (1ull << p.N) - 1ull;
         if (!((anc >> i) & 1ull) && gt == 0) atomicOr(a.status, LUCETREE_DEV_BAD_NODE);
-        if constexpr (WIN) {
-            // the k-th ancestor in node order is at depth k, the node itself at the last
-            const int d = __popcll(anc) - 1;
-            const long long L0 = seq_len_quiet(a.ctx_len, b, p.max_pages);
-            uint64_t rest = anc;
-            for (int k = 0; rest && d - k >= p.window; ++k) {
-                const uint64_t low = rest & (0ull - rest);
-                rest ^= low;
-                if (L0 + k >= p.sinks) anc ^= low;
-            }
-        }
         // this warp's keys: every W-th set bit of anc, starting at rank `warp`
         uint64_t mine = 0;
         {
@@ -202,16 +166,7 @@ __device__ __forceinline__ void merge_row(const AttnLaunch& L, long long row, ui
     const int Lb = seq_len(a.ctx_len, b, p.max_pages, (i == 0 && h == 0 && gt == 0) ? a.status : nullptr);
     int count = 0, c_lo = 0;
     long long nT = 0;
-    if constexpr (WIN) {
-        int before = 0;
-        nT = win_total(p, a.ctx_len, b, &before);
-        const int tiles = (win_span(Lb, p.window, p.sinks).vp + 1) / 2;
-        if (tiles > 0) {
-            const long long first = before + (long long)g * tiles;
-            c_lo = cta_of_tile(first, nT, p.Cg);
-            count = cta_of_tile(first + tiles - 1, nT, p.Cg) - c_lo + 1;
-        }
-    } else if (Lb > 0) {
+    if (Lb > 0) {
         nT = total_tiles(p, a.ctx_len);
         const long long first = segment_offset(p, a.ctx_len, s);
         const long long last = first + tiles_of(Lb) - 1;
@@ -271,21 +226,6 @@ __device__ __forceinline__ void merge_row(const AttnLaunch& L, long long row, ui
         }
     }
 
-    if constexpr (W == 1) {
-        // one warp has the whole row: no exchange, and its slice goes out in one store
-        const float inv1 = l_w > 0.f || !WIN ? 1.f / l_w : 0.f;
-        bool bad = false;
-#pragma unroll
-        for (int x = 0; x < DPL; ++x) {
-            o[x] *= inv1;
-            bad |= !isfinite(o[x]);
-        }
-        store_slice<DPL>(reinterpret_cast<TO*>(a.out) + (size_t)row * D + lane * DPL, o);
-        if (bad) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
-        if (a.lse && lane == 0) a.lse[row] = l_w > 0.f || !WIN ? (m_w + log2f(l_w)) * kLn2 : -INFINITY;
-        return;
-    }
-
     // ---- the warps' parts on the common shift
     if (lane == 0) s_red[warp] = m_w;
     group_sync(bar_id, 32 * W);
@@ -304,17 +244,17 @@ __device__ __forceinline__ void merge_row(const AttnLaunch& L, long long row, ui
     float l = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) l += s_red[w];
-    const float inv = WIN && l == 0.f ? 0.f : 1.f / l;
-    TO* orow = reinterpret_cast<TO*>(a.out) + (size_t)row * D;
+    const float inv = 1.f / l;
+    float* orow = a.out + (size_t)row * D;
     for (int d = gt; d < D; d += 32 * W) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) v += s_o[w][d];
         v *= inv;
-        store_out(orow + d, v);
+        orow[d] = v;
         if (!isfinite(v)) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
     }
-    if (a.lse && gt == 0) a.lse[row] = WIN && l == 0.f ? -INFINITY : (mmax + log2f(l)) * kLn2;
+    if (a.lse && gt == 0) a.lse[row] = (mmax + log2f(l)) * kLn2;
 }
 
 }  // namespace merge

@@ -78,9 +78,6 @@ cudaError_t launch_attn_prefix(const AttnLaunch& L, cudaStream_t stream) {
     }
 
     const int rgp = (p.rg.RG + 15) / 16 * 16;
-    if (p.window > 0)
-        return a.dtype == LUCETREE_BF16 ? launch_prefix_tc_bf16_win(rgp, tk, tv, tq, L, stream)
-                                        : launch_prefix_tc_f16_win(rgp, tk, tv, tq, L, stream);
     if (kq) return launch_prefix_tc_bf16_256_kq(rgp, vq, tk, tv, tq, tve, tq2, L, stream);
     if (a.dtype == LUCETREE_BF16)
         return a.D == 256 ? launch_prefix_tc_bf16_256(rgp, vq, tk, tv, tq, tve, L, stream)

@@ -57,8 +57,6 @@
 // copies and MMAs and returns.
 #pragma once
 
-#include <type_traits>
-
 #include "e4m3.cuh"
 #include "internal.cuh"
 #include "tc_ptx.cuh"
@@ -132,8 +130,6 @@ struct Misc {
     uint64_t q_ready;  // E4M3 K: the piece's queries split into their two E4M3 parts
     uint32_t tmem_base;
     int abort_flag;
-    int empty_cols;  // windowed: a query row has seen no key of its range so far
-    alignas(16) uint8_t depth[kRowsMax];  // windowed: depth of each query row's node
 };
 static_assert(sizeof(Misc) <= 5632, "misc region");
 static_assert(offsetof(Misc, vexp) == 0 && sizeof(Misc::vexp[0]) % 128 == 0, "128-byte aligned TMA destinations");
@@ -154,22 +150,10 @@ struct VCodes {
 struct Piece {
     int s, L;    // key segment (b * Hkv + g) and its committed length
     int ta, te;  // tile range within the segment
-    WinSpan w;   // windowed: the virtual pages that the tiles are made of
 };
 
-template <int WIN>
-__device__ __forceinline__ int pages_of(const Piece& pc) {
-    return WIN ? pc.w.vp : (pc.L + kPage - 1) / kPage;
-}
-// The page-table entry of the segment's page number v.
-template <int WIN>
-__device__ __forceinline__ int table_page(const Piece& pc, int v) {
-    return WIN ? win_page(pc.w, v) : v;
-}
-
-template <int WIN>
 struct PieceIter {
-    int t0, t1, off, s;  // off: flat offset of segment s
+    int t0, t1, off, s;
     __device__ bool next(const PlanDims& p, const int32_t* ctx_len, Piece& out) {
         while (s < p.S && off < t1) {
             const int L = seq_len_quiet(ctx_len, s / p.Hkv, p.max_pages);
@@ -187,41 +171,16 @@ struct PieceIter {
         return false;
     }
 };
-// Windowed: starts at the range's first segment, and reads a length only when a
-// sequence begins.
-struct WinPieceIter {
-    int t0, t1, off, b, g, L;
-    __device__ bool next(const PlanDims& p, const int32_t* ctx_len, Piece& out) {
-        while (b < p.B && off < t1) {
-            out.w = win_span(L, p.window, p.sinks);
-            const int s0 = off, s1 = off + (out.w.vp + 1) / 2;
-            out.s = b * p.Hkv + g;
-            out.L = L;
-            off = s1;
-            if (++g == p.Hkv) {
-                g = 0;
-                if (++b < p.B) L = seq_len_quiet(ctx_len, b, p.max_pages);
-            }
-            if (s1 == s0) continue;
-            out.ta = (t0 > s0 ? t0 : s0) - s0;
-            out.te = (t1 < s1 ? t1 : s1) - s0;
-            return true;
-        }
-        return false;
-    }
-};
 
 // The CTA's tiles in order: piece (key segment) and tile within the segment.
-template <int WIN>
 struct TileCursor {
-    typename std::conditional<WIN != 0, WinPieceIter, PieceIter<WIN>>::type it;
+    PieceIter it;
     Piece pc;
     int t;
     int piece_no;
     bool live;
-    __device__ void start(const WinStart& st, const PlanDims& p, const int32_t* ctx_len) {
-        if constexpr (WIN != 0) it = {st.t0, st.t1, st.off, st.b, st.g, st.L};
-        else it = {st.t0, st.t1, 0, 0};
+    __device__ void start(int t0, int t1, const PlanDims& p, const int32_t* ctx_len) {
+        it = PieceIter{t0, t1, 0, 0};
         piece_no = -1;
         t = 0;
         next_piece(p, ctx_len);
@@ -256,20 +215,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// Bit k: byte k of eight node depths is at most dmax (0 .. 127; depths are below 64).
-__device__ __forceinline__ uint32_t depths_up_to(uint2 d, int dmax) {
-    // dmax - d in every byte at once, its sign bit kept out of the neighbours by the 128 added
-    const uint32_t base = (uint32_t)(128 + dmax) * 0x01010101u;
-    const uint32_t lo = ((base - d.x) >> 7) & 0x01010101u, hi = ((base - d.y) >> 7) & 0x01010101u;
-    // bytes 0, 1, 2, 3 -> bits 0, 1, 2, 3
-    return ((lo * 0x01020408u) >> 24 & 0xFu) | ((hi * 0x01020408u) >> 20 & 0xF0u);
-}
-// Maximum over the warp in one instruction.
-__device__ __forceinline__ float redux_max(float v) {
-    float m;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-    return m;
-}
 
 // Column maxima of a warp's 16 x 32 values (v[k] = column k in this lane):
 // recursive halving over the lane bits 16, 8, 4, 2 (a lane keeps the upper or
@@ -301,11 +246,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // Two bf16 (one 32-bit word) -> two fp16 (round to nearest), exact for
 // magnitudes below 65536; larger magnitudes become inf.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -334,18 +274,7 @@ __device__ __forceinline__ bool aborted(Misc* ms) { return *(volatile int*)&ms->
 // runs as two kind::f8f6f4 MMAs per 32-dim step into the same accumulator.
 // The softmax multiplies each key's scores by its exponent and the segment's
 // query scale.
-//
-// WIN: a sliding window with sinks (16-bit K/V).  A tile is two virtual pages
-// (see WinSpan).  Most tiles are visible to every row; in the one or two that
-// hold the window's edge, a key counts for the rows of the nodes deep enough
-// only (one comparison of the row's depth per score, in warps that need it).
-// V rows that no node sees (past the sinks, before the window) are zeroed like
-// those past L.  WIN = 2: bf16 with a bf16 output.  P is then rounded to bf16
-// (half a step is 2^-8 of a term, as much as the output's own rounding; terms'
-// roundings are independent and average out in the sum) and V is multiplied as it
-// lands, so its conversion's two passes through shared memory and the wait for it
-// fall away.
-template <int D, bool BF16, int RGP, int VQ, int KQ, int WIN>
+template <int D, bool BF16, int RGP, int VQ, int KQ>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ve,
@@ -355,9 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChunksK = KQ ? D / 128 : D / 64;        // ring chunks per K operand
     constexpr int kChunksV = D / 64;                       // ring chunks per V operand
     static_assert(!KQ || (D == 256 && BF16), "E4M3 K: head dim 256, bf16 queries");
-    static_assert(!WIN || (VQ == 0 && KQ == 0), "windowed attention: 16-bit K and V");
-    static_assert(WIN != 2 || BF16, "P in bf16: bf16 operands");
-    constexpr bool kConvert = BF16 && WIN != 2;  // V converted to fp16 on chip
     constexpr int kNch = Lay::kNch;
     constexpr int kNa = (kNch + kSmGroups - 1) / kSmGroups;  // column chunks per softmax warp (at most)
     constexpr int kNS = Lay::kNS;
@@ -433,15 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // wait, relying on this kernel having waited for their producers first.
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    WinStart ws0 = {0, 0, 0, 0, 0, 0};
-    if constexpr (WIN != 0) {
-        ws0 = win_start(p, a.ctx_len, cta);
-    } else {
-        const long long nT = total_tiles(p, a.ctx_len);
-        ws0.t0 = nT ? (int)cta_begin(cta, nT, p.Cg) : 0;
-        ws0.t1 = nT ? (int)cta_begin(cta + 1, nT, p.Cg) : 0;
-    }
-    const int t0 = ws0.t0, t1 = ws0.t1;
+    const long long nT = total_tiles(p, a.ctx_len);
+    const int t0 = nT ? (int)cta_begin(cta, nT, p.Cg) : 0, t1 = nT ? (int)cta_begin(cta + 1, nT, p.Cg) : 0;
     if (t0 >= t1) {  // uniform across the CTA: nothing to do but give TMEM back
         if (warp == 1) tmem_dealloc(tmem, kTmemCols);
         return;
@@ -498,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         };
-        TileCursor<WIN> cur;
-        cur.start(ws0, p, a.ctx_len);
+        TileCursor cur;
+        cur.start(t0, t1, p, a.ctx_len);
         int npages = 0;
         const int32_t* pt = a.page_table;
         // page ids of the current piece, 16 tiles (32 pages) per warp-wide load, one batch ahead
@@ -507,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pg = 2 * tb + lane;
             int pid = -1;
             if (pg < npages && pg < 2 * cur.pc.te) {
-                const int v = pt[table_page<WIN>(cur.pc, pg)];
+                const int v = pt[pg];
                 if (v >= 0 && v < a.num_pages) pid = v;
                 else atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
             }
@@ -540,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++q_loads;
-                npages = pages_of<WIN>(cur.pc);
+                npages = (cur.pc.L + kPage - 1) / kPage;
                 pt = a.page_table + (size_t)(cur.pc.s / p.Hkv) * p.max_pages;
                 pid_cur = load_batch(cur.pc.ta);
                 pid_next = load_batch(cur.pc.ta + 16);
@@ -581,19 +500,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             // (for E4M3 K the same descriptor bits read as E4M3 x E4M3 under kind::f8f6f4)
             const uint32_t id_qk = idesc_f16(128, RGP, KQ ? 0u : kAB, 0, 0);
-            const uint32_t id_pv = idesc_f16(128, RGP, WIN == 2 ? 1u : 0u, 1, 1);  // V and P: fp16 (WIN = 2: bf16)
+            const uint32_t id_pv = idesc_f16(128, RGP, 0u, 1, 1);  // fp16 V and P
             constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
             constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
             constexpr uint64_t hi_p = desc_hi(128, 2048, kLayoutInterleave);
             const uint32_t aQ = smem_u32(sQ), aP = smem_u32(sP), aS = smem_u32(sSlots);
             uint32_t chunk = 0, jq = 0, j = 0;
             bool ok = true;
-            // windowed: one cursor (qk); PV's first-tile flags follow from QK's, kept in
-            // first_bits (bit 0: the last QK issued), which spares this warp's registers
-            TileCursor<WIN> qk, pv;
-            uint32_t first_bits = 0;
-            qk.start(ws0, p, a.ctx_len);
-            if constexpr (WIN == 0) pv.start(ws0, p, a.ctx_len);
+            TileCursor qk, pv;
+            qk.start(t0, t1, p, a.ctx_len);
+            pv.start(t0, t1, p, a.ctx_len);
             // S^T(jq) = K(jq) . Q^T; S^T is free once the softmax has read tile jq-1
             auto issue_qk = [&]() -> bool {
                 if (jq > 0) {
@@ -631,13 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mma_commit(&ms->s_full);
                 if (qk.last()) mma_commit(&ms->q_empty);
-                first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
                 ++jq;
                 qk.step(p, a.ctx_len);
                 return true;
             };
             if (qk.live) ok = issue_qk();
-            while (ok && (WIN ? j < n_tiles : pv.live)) {
+            while (ok && pv.live) {
                 if (aborted(ms)) {
                     ok = false;
                     break;
@@ -656,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // O^T += V^T . P^T once the softmax has written P^T(j)
                     if (!(ok = mbar_wait(&ms->p_full, j & 1))) break;
                     tc_fence_after();
-                    const bool first = WIN ? (first_bits >> (jq - 1 - j)) & 1u : pv.first();
+                    const bool first = pv.first();
                     // output dims 128h..128h+127: chunk 2h holds keys 0..63, chunk
                     // 2h+1 keys 64..127 (four 16-key steps each)
                     for (int h = 0; h < kChunksV / 2 && ok; ++h) {
@@ -680,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     mma_commit(&ms->pv_done);
                     ++j;
-                    if constexpr (WIN == 0) pv.step(p, a.ctx_len);
+                    pv.step(p, a.ctx_len);
                 }
             }
             if (!ok || aborted(ms)) {
@@ -702,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 64 * (c & 1) + (u % 512) / 8 (each 8 KB box is [64 keys][128 B]; the
         // swizzle permutes units only within a key's row).
         const int ct = threadIdx.x - 64;  // 0 .. 63
-        TileCursor<WIN> cur;
-        cur.start(ws0, p, a.ctx_len);
+        TileCursor cur;
+        cur.start(t0, t1, p, a.ctx_len);
         uint32_t j = 0;
         bool ok = true;
         while (ok && cur.live) {
@@ -721,19 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
-                int nv = nvalid - 64 * (c & 1);  // valid keys of this chunk's page
-                // windowed: of those, the first ns (sinks) and those from nl on (window) count
-                int ns = 64, nl = 0;
-                if constexpr (WIN) {
-                    const int v = 2 * cur.t + (c & 1), p0 = win_page(cur.pc.w, v) * kPage;
-                    nv = v < cur.pc.w.vp ? cur.pc.L - p0 : 0;
-                    ns = p.sinks - p0;
-                    nl = cur.pc.w.lo - p0;
-                }
-                const bool whole = nv >= 64 && (!WIN || ns >= 64 || nl <= 0);
+                const int nv = nvalid - 64 * (c & 1);  // valid keys of this chunk's page
                 constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
                 constexpr int kBatch = 4;                                      // loads in flight
-                if (kConvert && whole) {
+                if (BF16 && nv >= 64) {
                     // a full page (every chunk but a segment's last few): no per-key test
 #pragma unroll 1
                     for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
@@ -749,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             base[ct + 32 * kConvWarps * (i0 + k)] = x[k];
                         }
                     }
-                } else if (kConvert || !whole) {
+                } else if (BF16 || nv < 64) {
 #pragma unroll 1
                     for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
                         uint4 x[kBatch];
@@ -757,20 +663,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) {
                             const int u = ct + 32 * kConvWarps * (i0 + k);
-                            const int key = (u & 511) >> 3;
-                            kv[k] = key < nv && (!WIN || key < ns || key >= nl);
+                            kv[k] = ((u & 511) >> 3) < nv;
                             x[k] = kv[k] ? base[u] : make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) {
                             const int u = ct + 32 * kConvWarps * (i0 + k);
-                            if constexpr (kConvert) {
+                            if constexpr (BF16) {
                                 x[k].x = bf16x2_to_f16x2(x[k].x);
                                 x[k].y = bf16x2_to_f16x2(x[k].y);
                                 x[k].z = bf16x2_to_f16x2(x[k].z);
                                 x[k].w = bf16x2_to_f16x2(x[k].w);
                             }
-                            if (kConvert || !kv[k]) base[u] = x[k];
+                            if (BF16 || !kv[k]) base[u] = x[k];
                         }
                     }
                 }
@@ -813,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // previous tile still reads the shared P^T buffer; store_p writes it
         // once that PV has completed.
         auto exp_pass = [&](float (&lpart)[kNa * 16], bool valid, float sign, bool keep_p, float& ex,
-                            uint32_t (&ph)[kNa * 8], bool part, int dmax) {
+                            uint32_t (&ph)[kNa * 8]) {
             // 16-column chunks, each in two 8-column blocks b = 2*cc + hb; the
             // TMEM load of chunk cc+1 is in flight while chunk cc is computed.
             // An invalid key's exponents are -inf, and so are a padding
@@ -836,16 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float4 ma = m4[0], mb = m4[1];
                     const float mv[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
                     float pv[8];
-                    uint32_t vis = 0;  // windowed: bit k: column k's row sees my key
-                    if constexpr (WIN != 0) {
-                        vis = valid ? 0xFFu : 0u;
-                        if (part)
-                            vis &= depths_up_to(*reinterpret_cast<const uint2*>(ms->depth + 16 * c + 8 * hb), dmax);
-                    }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const bool sees = WIN ? ((vis >> k) & 1u) != 0 : valid;
-                        const float x = sees ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY;
+                        const float x = valid ? fmaf(__uint_as_float(r[8 * hb + k]), sl2, -mv[k]) : -INFINITY;
                         ex = fmaxf(ex, x);
                         pv[k] = ex2(x);
                         float& acc = lpart[cc * 16 + 8 * hb + k];
@@ -853,9 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (keep_p) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ph[4 * bi + k] = WIN == 2 ? pack_bf162(pv[2 * k], pv[2 * k + 1])
-                                                      : pack_half2(pv[2 * k], pv[2 * k + 1]);
+                        for (int k = 0; k < 4; ++k) ph[4 * bi + k] = pack_half2(pv[2 * k], pv[2 * k + 1]);
                     }
                 }
             }
@@ -871,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
 
-        TileCursor<WIN> cur;
-        cur.start(ws0, p, a.ctx_len);
+        TileCursor cur;
+        cur.start(t0, t1, p, a.ctx_len);
 
         while (cur.live) {
             const int piece_no = cur.piece_no;
@@ -880,17 +776,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_sync(1, kSoftmaxThreads);
             // padding columns keep a shift of +inf, so their exponents are -inf and P = 0
             for (int col = st; col < RGP; col += kSoftmaxThreads) ms->m_ref[col] = col < R_seg ? -INFINITY : INFINITY;
-            if constexpr (WIN) {
-                // (a node's depth is the number of its proper ancestors)
-                for (int col = st; col < RGP; col += kSoftmaxThreads) {
-                    int d = 0;
-                    if (col < R_seg)
-                        d = max(__popcll(a.anc_mask[(size_t)(seg / p.Hkv) * p.N + i0 + col / p.G] &
-                                         (~0ull >> (64 - p.N))) - 1, 0);
-                    ms->depth[col] = (uint8_t)d;
-                }
-                if (st == 0) ms->empty_cols = 0;
-            }
             bar_sync(1, kSoftmaxThreads);
             float lpart[kNa * 16];
 #pragma unroll
@@ -899,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int pid_lane = -1;  // E4M3 K: page id of my key's page for tile (batch start + lane)
             // E4M3 K: my key's exponent byte, loaded one tile ahead; the segment's query scale
             auto page_of = [&](int tile) -> int {
-                const int pg = 2 * tile + my_half;  // (E4M3 K is never windowed)
+                const int pg = 2 * tile + my_half;
                 return pg < (cur.pc.L + kPage - 1) / kPage ? a.page_table[(size_t)(seg / p.Hkv) * p.max_pages + pg] : -1;
             };
             auto k_exp_of = [&](int pid) -> uint32_t {
@@ -1003,9 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int pg = 2 * tt + my_half;
                     bool okp = false;
                     pid_lane = -1;
-                    if (tt < cur.pc.te && pg < pages_of<WIN>(cur.pc)) {
-                        const int pid =
-                            a.page_table[(size_t)(seg / p.Hkv) * p.max_pages + table_page<WIN>(cur.pc, pg)];
+                    if (tt < cur.pc.te && pg < (cur.pc.L + kPage - 1) / kPage) {
+                        const int pid = a.page_table[(size_t)(seg / p.Hkv) * p.max_pages + pg];
                         okp = pid >= 0 && pid < a.num_pages;
                         pid_lane = pid;
                     }
@@ -1013,19 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int nvalid = min(kTileKeys, cur.pc.L - t * kTileKeys);
                 const bool page_ok = (page_bits >> tb) & 1u;
-                bool valid = kl < nvalid && page_ok;
+                const bool valid = kl < nvalid && page_ok;
                 const bool first = cur.first();
-                // windowed: my key counts for rows of depth <= dmax; part: some lane's key not for all
-                int dmax = 64;
-                bool part = false;
-                if constexpr (WIN) {
-                    const int v = 2 * t + my_half, pos = win_page(cur.pc.w, v) * kPage + (kl & (kPage - 1));
-                    if (pos >= p.sinks) dmax = min(pos - max(cur.pc.L - p.window + 1, -64), 64);
-                    valid = v < cur.pc.w.vp && pos < cur.pc.L && page_ok && dmax >= 0;
-                    part = __any_sync(0xffffffffu, valid && dmax < p.N - 1);
-                }
-                // no shifts to go by: the range's first tile, or a row that has seen no key yet
-                const bool fresh = first || (WIN && ms->empty_cols != 0);
                 if constexpr (KQ) {
                     // this tile's exponent was loaded during the previous tile; load the next one's
                     const uint32_t ek = valid ? ek_next : 0u;
@@ -1050,20 +923,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // The first tile of a range has no shifts yet and starts at pass 2.
                 float ex = -INFINITY;
                 uint32_t ph[kNa * 8];
-                if (!bad && !fresh) {
-                    exp_pass(lpart, valid, 1.f, true, ex, ph, part, dmax);
+                if (!bad && !first) {
+                    exp_pass(lpart, valid, 1.f, true, ex, ph);
                 }
                 // one barrier decides the path; a second one only when it says
                 // "slow", to tell a timeout (somewhere) from a shift update
                 const bool bad_now = bad || aborted(ms);
-                const bool slow = bar_sync_or(1, kSoftmaxThreads, bad_now || fresh || ex > kTau);
+                const bool slow = bar_sync_or(1, kSoftmaxThreads, bad_now || first || ex > kTau);
                 if (slow && bar_sync_or(1, kSoftmaxThreads, bad_now)) {
                     bad = true;
                     break;
                 }
                 if (slow) {
-                    if (!fresh) exp_pass(lpart, valid, -1.f, false, ex, ph, part, dmax);  // pass 1
-                    if (WIN && st == 0) ms->empty_cols = 0;
+                    if (!first) exp_pass(lpart, valid, -1.f, false, ex, ph);  // pass 1
                     // pass 2: exact column maxima of this tile, then move the shifts
 #pragma unroll 1
                     for (int cc = 0; cc < nch; ++cc) {
@@ -1072,27 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld16(tl + 16 * c, r);
                         tmem_wait_ld_regs16(r);
                         const int lim = valid ? R_seg - 16 * c : 0;
-                        // maxima of the 16 columns over the warp's 32 key lanes
-                        if constexpr (WIN != 0) {
-                            uint32_t vis = lim >= 16 ? 0xFFFFu : lim > 0 ? (1u << lim) - 1u : 0u;
-                            if (part) {
-                                const uint4 dd = *reinterpret_cast<const uint4*>(ms->depth + 16 * c);
-                                vis &= depths_up_to(make_uint2(dd.x, dd.y), dmax) |
-                                       depths_up_to(make_uint2(dd.z, dd.w), dmax) << 8;
-                            }
-                            float mine = 0.f;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float cm =
-                                    redux_max((vis >> k) & 1u ? __uint_as_float(r[k]) * sl2 : -INFINITY);
-                                if (lane == k) mine = cm;
-                            }
-                            if (lane < 16) ms->col_red[quarter][16 * c + lane] = mine;
-                            continue;
-                        }
                         float v[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) v[k] = k < lim ? __uint_as_float(r[k]) * sl2 : -INFINITY;
+                        // maxima of the 16 columns over the warp's 32 key lanes
                         const float cm = col_max16(v, lane);
                         if ((lane & 1) == 0) ms->col_red[quarter][16 * c + (lane >> 1)] = cm;
                     }
@@ -1104,7 +959,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float mn = fmaxf(mo, cm);
                         ms->alpha[col] = mn > mo ? ex2(mo - mn) : 1.f;
                         ms->m_ref[col] = mn;
-                        if (WIN && mn == -INFINITY) ms->empty_cols = 1;
                     }
                     bar_sync(1, kSoftmaxThreads);
 #pragma unroll
@@ -1141,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (!bad) tmem_wait_st();
                     }
-                    if (!bad) exp_pass(lpart, valid, 1.f, true, ex, ph, part, dmax);
+                    if (!bad) exp_pass(lpart, valid, 1.f, true, ex, ph);
                 }
                 // S^T is no longer read: the next tile's QK may overwrite it
                 tc_fence_before();
@@ -1358,11 +1212,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool BF16, int RGP, int VQ, int KQ, int WIN>
+template <int D, bool BF16, int RGP, int VQ, int KQ>
 cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, const CUtensorMap& tve,
                        const CUtensorMap& tq2, const AttnLaunch& L, cudaStream_t stream) {
     using Lay = Layout<D, RGP>;
-    auto kern = prefix_tc_kernel<D, BF16, RGP, VQ, KQ, WIN>;
+    auto kern = prefix_tc_kernel<D, BF16, RGP, VQ, KQ>;
     static SmemLimitSeen seen;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Lay::kBytes, seen);
     if (e != cudaSuccess) return e;
@@ -1371,20 +1225,20 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUten
 
 // tve: the per-token exponents of quantised V (VQ != 0); tq2: the low query
 // parts of E4M3 K (KQ != 0); unused otherwise
-template <int D, bool BF16, int VQ = 0, int KQ = 0, int WIN = 0>
+template <int D, bool BF16, int VQ = 0, int KQ = 0>
 cudaError_t launch_rgp(int rgp, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                        const CUtensorMap& tve, const CUtensorMap& tq2, const AttnLaunch& L, cudaStream_t stream) {
     static_assert(kRowsMax == 144, "one instantiation per padded row count up to kRowsMax");
     switch (rgp) {
-        case 16: return launch_one<D, BF16, 16, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 32: return launch_one<D, BF16, 32, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 48: return launch_one<D, BF16, 48, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 64: return launch_one<D, BF16, 64, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 80: return launch_one<D, BF16, 80, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 96: return launch_one<D, BF16, 96, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 112: return launch_one<D, BF16, 112, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 128: return launch_one<D, BF16, 128, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
-        case 144: return launch_one<D, BF16, 144, VQ, KQ, WIN>(tk, tv, tq, tve, tq2, L, stream);
+        case 16: return launch_one<D, BF16, 16, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 32: return launch_one<D, BF16, 32, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 48: return launch_one<D, BF16, 48, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 64: return launch_one<D, BF16, 64, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 80: return launch_one<D, BF16, 80, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 96: return launch_one<D, BF16, 96, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 112: return launch_one<D, BF16, 112, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 128: return launch_one<D, BF16, 128, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
+        case 144: return launch_one<D, BF16, 144, VQ, KQ>(tk, tv, tq, tve, tq2, L, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -1403,11 +1257,6 @@ cudaError_t launch_prefix_tc_bf16_128(int rgp, const CUtensorMap&, const CUtenso
 cudaError_t launch_prefix_tc_f16_256(int rgp, int vq, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                      const CUtensorMap&, const AttnLaunch&, cudaStream_t);
 cudaError_t launch_prefix_tc_f16_128(int rgp, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                     const AttnLaunch&, cudaStream_t);
-// windowed (L.plan.window > 0), 16-bit K and V
-cudaError_t launch_prefix_tc_bf16_win(int rgp, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                                      const AttnLaunch&, cudaStream_t);
-cudaError_t launch_prefix_tc_f16_win(int rgp, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                      const AttnLaunch&, cudaStream_t);
 
 }  // namespace lucetree

@@ -58,8 +58,6 @@ struct PlanDims {
     int S;          // key segments = B * Hkv
     int Cg;         // CTAs per row group
     int max_pages;  // page-table row length
-    int window;     // sliding window in positions (0: full attention)
-    int sinks;      // first positions that stay visible behind the window
 };
 
 __host__ __device__ inline PlanDims make_plan(int B, int N, int Hq, int Hkv, int D, int ctas, int max_pages) {
@@ -70,7 +68,6 @@ __host__ __device__ inline PlanDims make_plan(int B, int N, int Hq, int Hkv, int
     p.Cg = ctas / p.rg.NG;
     if (p.Cg < 1) p.Cg = 1;
     p.max_pages = max_pages;
-    p.window = p.sinks = 0;
     return p;
 }
 
@@ -128,104 +125,6 @@ __device__ inline long long cta_begin(long long c, long long T, int C) { return 
 // The CTA whose range holds flat tile t (largest c with cta_begin(c) <= t).
 __device__ inline int cta_of_tile(long long t, long long T, int C) {
     return (int)(((t + 1) * (long long)C - 1) / T);
-}
-
-// ---------------------------------------------------------------------------
-// Sliding window with sinks.  A node at depth d of the tree is at position
-// L + d and sees the committed positions p with p < sinks or L + d - p <
-// window.  A sequence's key list is then made of the pages that some node can
-// see: its sink pages, and the pages from the window of a depth-0 node on
-// (deeper nodes see less).  These "virtual" pages are numbered without the gap
-// between them, and two consecutive ones make a key tile, so the split plan
-// above works on them as it does on whole prefixes.
-// ---------------------------------------------------------------------------
-struct WinSpan {
-    int lo;    // first position that the window of a depth-0 node reaches
-    int sp;    // sink pages
-    int skip;  // pages between the last sink page and the window's first
-    int vp;    // virtual pages
-};
-
-__host__ __device__ inline WinSpan win_span(int L, int window, int sinks) {
-    WinSpan w;
-    const int n = L / kPage + (L % kPage != 0);
-    const int sp = sinks / kPage + (sinks % kPage != 0);
-    w.lo = L - window + 1 > 0 ? L - window + 1 : 0;  // window >= 1: no overflow
-    w.sp = sp < n ? sp : n;
-    const int wp = w.lo >= L ? n : w.lo / kPage;
-    w.skip = wp > w.sp ? wp - w.sp : 0;
-    w.vp = n - w.skip;
-    return w;
-}
-
-// The page of the sequence that virtual page v stands for.
-__host__ __device__ inline int win_page(const WinSpan& w, int v) { return v < w.sp ? v : v + w.skip; }
-
-__device__ inline int win_tiles(const PlanDims& p, const int32_t* ctx_len, int b) {
-    return (win_span(seq_len_quiet(ctx_len, b, p.max_pages), p.window, p.sinks).vp + 1) / 2;
-}
-
-// Flat tiles of all key segments, and of those before sequence b, by the whole
-// warp (the host refuses shapes whose flat tile count reaches 2^31).
-__device__ inline int win_total(const PlanDims& p, const int32_t* ctx_len, int b, int* before) {
-    int all = 0, pre = 0;
-    for (int i = threadIdx.x & 31; i < p.B; i += 32) {
-        const int t = win_tiles(p, ctx_len, i);
-        all += t;
-        pre += i < b ? t : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        pre += __shfl_xor_sync(0xffffffffu, pre, o);
-    }
-    *before = pre * p.Hkv;
-    return all * p.Hkv;
-}
-
-// Where a CTA of the prefix kernel starts: its tile range and the key segment of
-// its first tile, found by the whole warp from one read of the lengths.
-struct WinStart {
-    int t0, t1;  // tile range, empty when t0 == t1
-    int b, g;    // sequence and KV head of tile t0
-    int off;     // flat offset of that segment's first tile
-    int L;       // committed length of sequence b
-};
-
-__device__ inline WinStart win_start(const PlanDims& p, const int32_t* ctx_len, int cta) {
-    const int lane = threadIdx.x & 31;
-    WinStart s = {0, 0, 0, 0, 0, 0};
-    int before, nT = p.B > 32 ? win_total(p, ctx_len, 0, &before) : 0, off = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int L = b0 + lane < p.B ? seq_len_quiet(ctx_len, b0 + lane, p.max_pages) : 0;
-        const int tiles = (win_span(L, p.window, p.sinks).vp + 1) / 2, mine = tiles * p.Hkv;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
-        const int all = __shfl_sync(0xffffffffu, incl, 31);
-        if (b0 == 0) {
-            if (p.B <= 32) nT = all;
-            if (nT == 0) return s;
-            s.t0 = (int)cta_begin(cta, nT, p.Cg);
-            s.t1 = (int)cta_begin(cta + 1, nT, p.Cg);
-            if (s.t0 == s.t1) return s;
-        }
-        const unsigned in = __ballot_sync(0xffffffffu, s.t0 < off + incl);
-        if (in) {
-            const int l = __ffs(in) - 1, per = __shfl_sync(0xffffffffu, tiles, l);
-            s.b = b0 + l;
-            s.off = off + __shfl_sync(0xffffffffu, incl - mine, l);
-            s.L = __shfl_sync(0xffffffffu, L, l);
-            s.g = (s.t0 - s.off) / per;
-            s.off += s.g * per;
-            return s;
-        }
-        off += all;
-    }
-    return s;
 }
 
 // ---------------------------------------------------------------------------
@@ -287,14 +186,12 @@ struct AttnLaunch {
     const uint8_t* v_exp;  // per-token exponents of quantised V [num_pages][Hkv][64]
     int k_format;          // LUCETREE_K_SAME, or LUCETREE_K_E4M3 (k_pool holds E4M3 codes)
     const uint8_t* k_exp;  // per-token exponents of E4M3 K [num_pages][Hkv][64]
-    int out_dtype;         // windowed attention: lucetree_dtype of the output (a.out holds its address)
 };
 
 int prefix_grid_ctas(int device);  // persistent grid size of the prefix kernel
 bool prefix_shape_supported(const lucetree_attn_args& a);
 cudaError_t launch_attn_prefix(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_attn_merge(const AttnLaunch& L, cudaStream_t stream);
-cudaError_t launch_attn_merge_win(const AttnLaunch& L, cudaStream_t stream);
 cudaError_t launch_build_anc(const int32_t* parent, int B, int N, uint64_t* anc, uint32_t* status,
                              cudaStream_t stream);
 cudaError_t launch_accept(const int32_t* parent, const int32_t* draft, const int32_t* argmax, int B, int N,
