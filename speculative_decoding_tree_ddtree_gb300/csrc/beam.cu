@@ -30,6 +30,7 @@ typedef unsigned long long u64;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;
 constexpr int kU = 8;  // 16-byte loads in flight per thread
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeWarps = kMergeThreads / 32;
@@ -112,6 +113,21 @@ __device__ inline float vector_max(const uint4& u) {
     }
 }
 
+// Vec<T>::kE elements from p on: one load where p is aligned to 16 bytes.
+template <typename T, bool ALIGNED>
+__device__ inline uint4 load_vector(const T* p) {
+    if constexpr (ALIGNED) {
+        return __ldg(reinterpret_cast<const uint4*>(p));
+    } else if constexpr (sizeof(T) == 4) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+        return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+    } else {
+        const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+        auto two = [&](int e) { return (uint32_t)__ldg(h + e) | (uint32_t)__ldg(h + e + 1) << 16; };
+        return make_uint4(two(0), two(2), two(4), two(6));
+    }
+}
+
 __device__ inline float scalar(const float* p) { return *p; }
 __device__ inline float scalar(const __half* p) { return __half2float(*p); }
 __device__ inline float scalar(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -121,6 +137,32 @@ __device__ inline float exp_diff(float x, float m) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - m) * kLog2e));
     return y;
+}
+
+// Two fp32 in one register pair: one instruction for two additions or products.
+__device__ inline uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ inline float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ inline float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ inline uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ inline uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ inline uint64_t exp_diff2(float x, float y, uint64_t minus_m) {
+    const uint64_t r = mul2(add2(pack2(x, y), minus_m), pack2(kLog2e, kLog2e));
+    float p, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(low(r)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(high(r)));
+    return pack2(p, q);
 }
 
 // (m, s) += (m2, s2): sums of exponentials relative to their maxima; a maximum of -inf has sum 0.
@@ -146,10 +188,12 @@ __device__ inline void merge_warps(u64 (*s_list)[32], u64 mine) {
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(BeamLaunch L) {
+// ALIGNED: every row starts on a 16-byte boundary.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLaunch L) {
     constexpr int kE = Vec<T>::kE;
     __shared__ u64 s_list[kWarps][32];
+    __shared__ u64 s_buf[kWarps][32 + 32 * kE];  // what one vector of every lane may add to 31 waiting keys
     __shared__ float2 s_sum[kWarps];
     const lucetree_beam_args& a = L.a;
     pdl_wait();
@@ -159,72 +203,89 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(BeamLaunch L) {
     if (row_ended(a, row) || a.cum[row] == -INFINITY) return;
     const int warp = t >> 5, lane = t & 31;
     const T* x = reinterpret_cast<const T*>(a.logits) + (long long)row * a.row_stride;
-    // 16-byte vectors from the first aligned element on; the elements before
-    // and behind them (fewer than 2 kE) belong to the row's last chunk
-    const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)), a.vocab);
-    const int nv = (a.vocab - head) / kE;
-    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+    // vectors of kE elements by index, so that a row's sum does not depend on where
+    // it lies (equal rows tie exactly); the last vocab % kE belong to the last chunk
+    const int nv = a.vocab / kE;
+    auto fetch = [&](int v) { return load_vector<T, ALIGNED>(x + (long long)v * kE); };
     const int v0 = (int)((long long)nv * chunk / L.chunks), v1 = (int)((long long)nv * (chunk + 1) / L.chunks);
 
     // thread t's vectors are v0 + t, v0 + t + kThreads, ..
-    float m = -INFINITY, s = 0.f;
+    float m = -INFINITY;
+    uint64_t s2 = 0;  // two sums of exp(x - m)
     int best = v0 + t;
-    for (int base = v0 + t; base < v1; base += kU * kThreads) {
-        uint4 u[kU];
+    // n vectors, kThreads apart, the first of them v
+    auto batch = [&](auto n, int v) {
+        uint4 u[n.value];
 #pragma unroll
-        for (int k = 0; k < kU; ++k)
-            if (base + k * kThreads < v1) u[k] = __ldg(xv + base + k * kThreads);
+        for (int k = 0; k < n.value; ++k) u[k] = fetch(v + k * kThreads);
         float mb = m;
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
+        for (int k = 0; k < n.value; ++k) {
             const float vm = vector_max<T>(u[k]);
-            if (base + k * kThreads < v1 && vm > mb) {
+            if (vm > mb) {
                 mb = vm;
-                best = base + k * kThreads;
+                best = v + k * kThreads;
             }
         }
         if (mb > m) {
-            s = m == -INFINITY ? 0.f : s * exp_diff(m, mb);
+            const float f = exp_diff(m, mb);  // 0 for the first
+            s2 = mul2(s2, pack2(f, f));
             m = mb;
         }
         const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t minus_m = pack2(-mm, -mm);
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
+        for (int k = 0; k < n.value; ++k) {
             float f[kE];
             unpack<T>(u[k], f);
-            float part = 0.f;
 #pragma unroll
-            for (int e = 0; e < kE; ++e) part += exp_diff(f[e], mm);
-            if (base + k * kThreads < v1) s += part;
+            for (int e = 0; e < kE; e += 2) s2 = add2(s2, exp_diff2(f[e], f[e + 1], minus_m));
         }
-    }
+    };
+    int base = v0;
+    for (; base + kU * kThreads <= v1; base += kU * kThreads) batch(std::integral_constant<int, kU>{}, base + t);
+    for (int v = base + t; v < v1; v += kThreads) batch(std::integral_constant<int, 1>{}, v);
+    float s = low(s2) + high(s2);
     // the threads with the best maxima
     merge_warps(s_list, sort32(v0 + t < v1 ? pack_key(m, (unsigned)best) : 0));
     __syncthreads();
     const u64 threads = s_list[0][lane];
     const u64 limit = __shfl_sync(0xffffffffu, threads, a.beams_out - 1);  // 0: fewer threads than that have a vector
-    // a warp goes through one thread's vectors at a time
+    // a warp goes through one thread's vectors at a time; the few keys that count
+    // wait in shared memory until 32 of them are sorted and merged in
     u64 list = 0;
+    int waiting = 0;
     for (int i = warp; i < a.beams_out; i += kWarps) {
         const u64 key = __shfl_sync(0xffffffffu, threads, i);
         if (key == 0) break;
         const int first = v0 + (int)((key_index(key) - (unsigned)v0) % kThreads);
         for (int v = first + lane * kThreads; __any_sync(0xffffffffu, v < v1); v += 32 * kThreads) {
-            u64 keys[kE];
             float f[kE];
-            unpack<T>(v < v1 ? __ldg(xv + v) : make_uint4(0, 0, 0, 0), f);
+            unpack<T>(v < v1 ? fetch(v) : make_uint4(0, 0, 0, 0), f);
             // no element of a vector below the limit is among the best (keys of vectors order as their elements' do)
+            unsigned pass = 0;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) pass |= v < v1 && pack_key(f[e], (unsigned)v) >= limit ? 1u << e : 0u;
+            int upto = __popc(pass);
+            const int mine = upto;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            int at = waiting + upto - mine;
 #pragma unroll
             for (int e = 0; e < kE; ++e)
-                keys[e] = v < v1 && pack_key(f[e], (unsigned)v) >= limit ? pack_key(f[e], (unsigned)(head + v * kE + e)) : 0;
-#pragma unroll
-            for (int e = 0; e < kE; ++e)
-                if (__any_sync(0xffffffffu, keys[e] != 0)) list = merge32(list, sort32(keys[e]));
+                if ((pass >> e) & 1u) s_buf[warp][at++] = pack_key(f[e], (unsigned)(v * kE + e));
+            waiting += __shfl_sync(0xffffffffu, upto, 31);
+            __syncwarp();
+            for (; waiting >= 32; waiting -= 32) list = merge32(list, sort32(s_buf[warp][waiting - 32 + lane]));
+            __syncwarp();
         }
     }
+    if (waiting > 0) list = merge32(list, sort32(lane < waiting ? s_buf[warp][lane] : 0));
     if (chunk == L.chunks - 1 && warp == 0) {
-        const int tail = head + nv * kE;  // first element behind the vectors
-        const int i = lane < head ? lane : tail + lane - head;
+        const int i = nv * kE + lane;
         const bool in = i < a.vocab;
         const float f = in ? scalar(x + i) : -INFINITY;
         if (in) add_sums(m, s, f, f == -INFINITY ? 0.f : 1.f);
@@ -308,7 +369,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
     u64 list = 0;
     if (mine && !ended && !dead) {
         const u64* keys = L.keys + (size_t)row * L.chunks * 32;
-        for (int c = w; c < L.chunks; c += per) list = merge32(list, keys[(size_t)c * 32 + lane]);
+        for (int c = w; c < L.chunks; c += 4 * per) {
+            u64 next[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) next[x] = c + x * per < L.chunks ? keys[(size_t)(c + x * per) * 32 + lane] : 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (c + x * per < L.chunks) list = merge32(list, next[x]);
+        }
     }
     s_keys[warp][lane] = list;
     if (mine && !ended && !dead && w == per - 1) {
@@ -372,10 +440,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
 // No more CTAs than run at once (four per SM), as long as there are no more rows
 // than that, and no chunk of fewer than four elements a thread.
 int beam_chunks(int rows, int vocab, int sms) {
-    int chunks = 4 * sms / rows;
+    int chunks = kCtasPerSm * sms / rows;
     const int most = (vocab + 4 * kThreads - 1) / (4 * kThreads);
     if (chunks > most) chunks = most;
     return chunks < 1 ? 1 : chunks;
+}
+
+template <typename T>
+cudaError_t launch_scan(const BeamLaunch& L, bool aligned, dim3 grid, cudaStream_t stream) {
+    if (aligned) return launch_pdl(beam_scan_kernel<T, true>, grid, dim3(kThreads), 0, stream, L);
+    return launch_pdl(beam_scan_kernel<T, false>, grid, dim3(kThreads), 0, stream, L);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -395,11 +469,13 @@ cudaError_t launch_beam_select(const lucetree_beam_args& a, void* workspace, int
     L.keys = reinterpret_cast<u64*>(workspace);
     L.sums = reinterpret_cast<float2*>(reinterpret_cast<char*>(workspace) +
                                        align256((size_t)rows * L.chunks * 32 * sizeof(u64)));
-    const dim3 grid(L.chunks, rows), block(kThreads);
+    const dim3 grid(L.chunks, rows);
+    const int size = a.dtype == LUCETREE_F32 ? 4 : 2;
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (rows == 1 || a.row_stride * size % 16 == 0);
     cudaError_t e;
-    if (a.dtype == LUCETREE_F32) e = launch_pdl(beam_scan_kernel<float>, grid, block, 0, stream, L);
-    else if (a.dtype == LUCETREE_BF16) e = launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, block, 0, stream, L);
-    else e = launch_pdl(beam_scan_kernel<__half>, grid, block, 0, stream, L);
+    if (a.dtype == LUCETREE_F32) e = launch_scan<float>(L, aligned, grid, stream);
+    else if (a.dtype == LUCETREE_BF16) e = launch_scan<__nv_bfloat16>(L, aligned, grid, stream);
+    else e = launch_scan<__half>(L, aligned, grid, stream);
     if (e != cudaSuccess) return e;
     return launch_pdl(beam_merge_kernel, dim3(a.batch), dim3(kMergeThreads), 0, stream, L);
 }

@@ -340,27 +340,38 @@ def _device() -> int:
 
 
 def _arg(t, name: str, shape, dtypes: tuple, dev: int) -> int:
-    """Address of a required tensor of this shape and element type (None: any),
+    """Address of a required tensor of this shape (None: any) and element type,
     contiguous and on device dev."""
     if t is None:
         raise LucetreeError(f"{name} is required")
-    if (dtypes is not None and t.dtype not in dtypes) or (shape is not None and t.shape != shape):
-        _expect(t, name, t.shape if shape is None else shape, (t.dtype,) if dtypes is None else dtypes)
+    if t.dtype not in dtypes or (shape is not None and t.shape != shape):
+        _expect(t, name, t.shape if shape is None else shape, dtypes)
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dev)
+    return t.data_ptr()
+
+
+def _refuse(t, name: str, dev: int):
     if t.get_device() != dev:
         raise LucetreeError(f"{name}: lucetree takes tensors of the current device, cuda:{dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise LucetreeError(f"{name}: lucetree takes contiguous tensors")
+    raise LucetreeError(f"{name}: lucetree takes contiguous tensors")
+
+
+def _any(t, name: str, dev: int) -> int:
+    """Address of a contiguous tensor of any shape and type on device dev."""
+    if t is None:
+        raise LucetreeError(f"{name} is required")
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dev)
     return t.data_ptr()
 
 
 def _status_arg(t, dev: int) -> int:
-    _expect_status(t)
-    return _arg(t, "status", None, None, dev)
-
-
-def _workspace(t, dev: int):
-    """Address and size of a workspace."""
-    return _arg(t, "workspace", None, None, dev), t.numel() * t.element_size()
+    if t is None or t.dtype not in _W32 or t.numel() < 1:
+        _expect_status(t)
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "status", dev)
+    return t.data_ptr()
 
 
 # the raw handle of a device's current stream, without the Stream object around it
@@ -485,14 +496,14 @@ def lucetree_verify_attn_win(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_t
     out_at = _arg(out, "out", (B, N, Hq, D), _F32 + kind, dev)
     args = _WIN_ARGS.pack(
         code, B, N, Hq, Hkv, D, page, float(D) ** -0.5 if scale is None else float(scale),
-        _arg(q, "q", None, None, dev), _arg(k_pool, "k_pool", pool, kind, dev), _arg(v_pool, "v_pool", pool, kind, dev), P,
+        _any(q, "q", dev), _arg(k_pool, "k_pool", pool, kind, dev), _arg(v_pool, "v_pool", pool, kind, dev), P,
         _arg(page_table, "page_table", (B, maxp), _I32, dev), maxp, _arg(ctx_len, "ctx_len", (B,), _I32, dev),
         _arg(k_tree, "k_tree", tree, kind, dev), _arg(v_tree, "v_tree", tree, kind, dev),
         _arg(anc_mask, "anc_mask", (B, N), _W64, dev), 0,
         0 if lse is None else _arg(lse, "lse", (B, N, Hq), _F32, dev), _status_arg(status, dev),
         _i32(window, "window", 1), _i32(sinks, "sinks"), LUCETREE_F32 if out.dtype == torch.float32 else code, out_at)
-    ws, ws_bytes = _workspace(workspace, dev)
-    _check(load().lucetree_verify_attn_win(args, ws, ws_bytes, _raw_stream(stream, dev)))
+    ws = _any(workspace, "workspace", dev)
+    _check(load().lucetree_verify_attn_win(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
 
 
 def lucetree_verify_attn_kq_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
@@ -883,8 +894,8 @@ def lucetree_beam_select(logits, cum, finished, eos: int, out_score, out_token, 
         _arg(out_score, "out_score", new, _F32, dev), _arg(out_token, "out_token", new, _I32, dev),
         _arg(out_row, "out_row", new, _I32, dev),
         0 if out_finished is None else _arg(out_finished, "out_finished", new, _I32, dev))
-    ws, ws_bytes = _workspace(workspace, dev)
-    _check(load().lucetree_beam_select(args, ws, ws_bytes, _raw_stream(stream, dev)))
+    ws = _any(workspace, "workspace", dev)
+    _check(load().lucetree_beam_select(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- page tables, counts and copies
@@ -915,8 +926,8 @@ def lucetree_reorder_pages(table_in, ctx_in, src, reserve: int, ref_in, table_ou
         _arg(ctx_out, "ctx_out", (rows,), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
         _arg(copy_src, "copy_src", (rows,), _I32, dev), _arg(copy_dst, "copy_dst", (rows,), _I32, dev),
         _status_arg(status, dev))
-    ws, ws_bytes = _workspace(workspace, dev)
-    _check(load().lucetree_reorder_pages(args, ws, ws_bytes, _raw_stream(stream, dev)))
+    ws = _any(workspace, "workspace", dev)
+    _check(load().lucetree_reorder_pages(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
 
 
 def lucetree_trim_pages(table_in, ctx_len, window: int, sinks: int, ref_in, table_out, ref_out, status, stream=None):
@@ -955,8 +966,8 @@ def lucetree_compact_pages(table_in, ref_in, table_out, ref_out, copy_src, copy_
         _arg(table_out, "table_out", (rows, P), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
         _arg(copy_src, "copy_src", half, _I32, dev), _arg(copy_dst, "copy_dst", half, _I32, dev),
         _arg(copy_n, "copy_n", (1,), _I32, dev), _arg(live, "live", (1,), _I32, dev), _status_arg(status, dev))
-    ws, ws_bytes = _workspace(workspace, dev)
-    _check(load().lucetree_compact_pages(args, ws, ws_bytes, _raw_stream(stream, dev)))
+    ws = _any(workspace, "workspace", dev)
+    _check(load().lucetree_compact_pages(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
 
 
 def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=None):
@@ -972,8 +983,8 @@ def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=Non
     dev = _device()
     args = _COPY_PAGES_ARGS.pack(
         _arg(src, "src", (n,), _I32, dev), _arg(dst, "dst", (n,), _I32, dev), n,
-        0 if count is None else _arg(count, "count", (1,), _I32, dev), _arg(k_pool, "k_pool", None, None, dev),
-        0 if v_pool is None else _arg(v_pool, "v_pool", None, None, dev), k_pool.numel() // pages * k_pool.element_size(),
+        0 if count is None else _arg(count, "count", (1,), _I32, dev), _any(k_pool, "k_pool", dev),
+        0 if v_pool is None else _any(v_pool, "v_pool", dev), k_pool.numel() // pages * k_pool.element_size(),
         0 if v_pool is None else v_pool.numel() // pages * v_pool.element_size(), pages, _status_arg(status, dev))
     _check(load().lucetree_copy_pages(args, _raw_stream(stream, dev)))
 
@@ -987,7 +998,7 @@ def lucetree_reorder_states(state_in, src, state_out, status, stream=None):
     shape, kind = state_in.shape, (state_in.dtype,)
     dev = _device()
     args = _REORDER_STATES_ARGS.pack(
-        _arg(state_in, "state_in", None, None, dev), _arg(state_out, "state_out", (rows, *shape[1:]), kind, dev),
+        _any(state_in, "state_in", dev), _arg(state_out, "state_out", (rows, *shape[1:]), kind, dev),
         _arg(src, "src", (rows,), _I32, dev), shape[0], rows, state_in.numel() // shape[0] * state_in.element_size(),
         _status_arg(status, dev))
     _check(load().lucetree_reorder_states(args, _raw_stream(stream, dev)))
