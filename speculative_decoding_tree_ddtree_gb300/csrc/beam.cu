@@ -213,14 +213,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     float m = -INFINITY;
     uint64_t s2 = 0;  // two sums of exp(x - m)
     int best = v0 + t;
-    // n vectors, kThreads apart, the first of them v
-    auto batch = [&](auto n, int v) {
-        uint4 u[n.value];
+    // kU vectors, kThreads apart, the first of them v; `all`: they all lie in the chunk
+    // (those that do not count as vectors of -inf)
+    auto batch = [&](auto all, int v) {
+        constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+        uint4 u[kU];
 #pragma unroll
-        for (int k = 0; k < n.value; ++k) u[k] = fetch(v + k * kThreads);
+        for (int k = 0; k < kU; ++k)
+            u[k] = all.value || v + k * kThreads < v1 ? fetch(v + k * kThreads) : make_uint4(kNone, kNone, kNone, kNone);
         float mb = m;
 #pragma unroll
-        for (int k = 0; k < n.value; ++k) {
+        for (int k = 0; k < kU; ++k) {
             const float vm = vector_max<T>(u[k]);
             if (vm > mb) {
                 mb = vm;
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
         const float mm = m == -INFINITY ? 0.f : m;
         const uint64_t minus_m = pack2(-mm, -mm);
 #pragma unroll
-        for (int k = 0; k < n.value; ++k) {
+        for (int k = 0; k < kU; ++k) {
             float f[kE];
             unpack<T>(u[k], f);
 #pragma unroll
@@ -243,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
         }
     };
     int base = v0;
-    for (; base + kU * kThreads <= v1; base += kU * kThreads) batch(std::integral_constant<int, kU>{}, base + t);
-    for (int v = base + t; v < v1; v += kThreads) batch(std::integral_constant<int, 1>{}, v);
+    for (; base + kU * kThreads <= v1; base += kU * kThreads) batch(std::true_type{}, base + t);
+    if (base < v1) batch(std::false_type{}, base + t);
     float s = low(s2) + high(s2);
     // the threads with the best maxima
     merge_warps(s_list, sort32(v0 + t < v1 ? pack_key(m, (unsigned)best) : 0));
