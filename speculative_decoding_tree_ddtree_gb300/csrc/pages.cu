@@ -21,6 +21,11 @@ constexpr int kChunk = 1024;            // pages per chunk: one thread each, 32 
 constexpr int kCols = 1024;             // table columns per CTA
 constexpr int kThreads = 256;
 constexpr int kMaxTail = 64;            // tail pages of a row (one 64-bit mask)
+// Up to these sizes one CTA does the whole of a call: a launch costs as much as its
+// pass over a thousand entries.  Measured (reorder + copies + states; trim + compact +
+// copies): 80 entries 9.2 us against 11.7 us in several launches, 63 entries 8.9 against
+// 11.7; but 25,000 entries 93 against 73, and 6,000 entries 120 against 111.
+constexpr int kSmallPages = 8192, kSmallRows = 512, kSmallEntries = 2048;
 constexpr int kMaxPages = 1 << 30;      // chunk and page numbers stay within an int
 
 int chunks_of(int num_pages) { return (num_pages + kChunk - 1) / kChunk; }
@@ -98,32 +103,34 @@ __device__ inline int block_scan(int v, int* s_warp, int* total) {
     return v + before;
 }
 
-// CTA 0 plans the rows; CTA 1 + i takes pages [i kChunk, (i + 1) kChunk): free
-// mask, count, and the copy of the reference counts.
-__global__ void __launch_bounds__(kChunk) reorder_plan_kernel(ReorderLaunch R) {
+// Pages [chunk kChunk, (chunk + 1) kChunk): free mask, count, and the copy of the
+// reference counts (kChunk threads).
+__device__ inline void scan_pages(const ReorderLaunch& R, int chunk, int* s_warp) {
     const lucetree_reorder_args& a = R.a;
-    __shared__ int s_warp[kChunk / 32];
-    pdl_wait();
-    if (threadIdx.x == 0) pdl_trigger();
-    const int t = threadIdx.x;
-    if (blockIdx.x > 0) {
-        const int chunk = blockIdx.x - 1;
-        const int page = chunk * kChunk + t;
-        const int ref = page < a.num_pages ? a.ref_in[page] : -1;
-        if (page < a.num_pages && a.ref_out != a.ref_in) a.ref_out[page] = ref;
-        const unsigned free = __ballot_sync(0xffffffffu, ref == 0);
-        if ((t & 31) == 0) {
-            R.w.free_bits[chunk * 32 + (t >> 5)] = free;
-            s_warp[t >> 5] = __popc(free);
-        }
-        __syncthreads();
-        if (t == 0) {
-            int n = 0;
-            for (int w = 0; w < 32; ++w) n += s_warp[w];
-            R.w.free_count[chunk] = n;
-        }
-        return;
+    const int t = threadIdx.x, page = chunk * kChunk + t;
+    const int ref = page < a.num_pages ? a.ref_in[page] : -1;
+    if (page < a.num_pages && a.ref_out != a.ref_in) a.ref_out[page] = ref;
+    const unsigned free = __ballot_sync(0xffffffffu, ref == 0);
+    if ((t & 31) == 0) {
+        R.w.free_bits[chunk * 32 + (t >> 5)] = free;
+        s_warp[t >> 5] = __popc(free);
     }
+    __syncthreads();
+    if (t == 0) {
+        int n = 0;
+        for (int w = 0; w < 32; ++w) n += s_warp[w];
+        R.w.free_count[chunk] = n;
+    }
+    __syncthreads();
+}
+
+// (the plan's counters are updated by atomics: read past the L1 cache, or from shared memory)
+__device__ inline int now(const int32_t* p) { return *(const volatile int32_t*)p; }
+
+// Who takes which row, what stays with it, and where its new pages start (kChunk threads).
+__device__ inline void plan_rows(const ReorderLaunch& R, int* s_warp) {
+    const lucetree_reorder_args& a = R.a;
+    const int t = threadIdx.x;
     for (int b = t; b < a.rows_in; b += kChunk) {
         R.w.children[b] = 0;
         R.w.first[b] = 0x7fffffff;
@@ -140,7 +147,7 @@ __global__ void __launch_bounds__(kChunk) reorder_plan_kernel(ReorderLaunch R) {
     for (int b = t; b < a.rows_in; b += kChunk) {
         uint64_t kept = 0;
         const RowSpan s = row_span(a, b, a.status);
-        if (__ldcg(&R.w.children[b]) > 0)
+        if (now(&R.w.children[b]) > 0)
             for (int c = s.full; c < s.end; ++c) {
                 const int page = a.table_in[(size_t)b * a.max_pages_per_seq + c];
                 if (page_ok(page, a.num_pages) && a.ref_in[page] == 1) kept |= 1ull << (c - s.full);
@@ -158,7 +165,7 @@ __global__ void __launch_bounds__(kChunk) reorder_plan_kernel(ReorderLaunch R) {
             if (b >= 0) {
                 const RowSpan s = row_span(a, b, nullptr);
                 need = s.end - s.full;
-                if (__ldcg(&R.w.first[b]) == r) need -= __popcll(R.w.kept[b]);
+                if (now(&R.w.first[b]) == r) need -= __popcll(R.w.kept[b]);
             }
         }
         int all;
@@ -202,108 +209,161 @@ __device__ inline int free_page(const ReorderPlan& w, int chunks, int k) {
     return -1;
 }
 
-// blockIdx.y < rows_out: the new rows; behind them the old ones, whose pages
-// gain a holder for each row that takes them and lose the old one.
-__global__ void __launch_bounds__(kThreads) reorder_apply_kernel(ReorderLaunch R) {
+// Columns [c0, c1) of row y: y < rows_out: the new rows; behind them the old ones, whose
+// pages gain a holder for each row that takes them and lose the old one.  The
+// thread is number t of n, whole warps.
+__device__ inline void apply_row(const ReorderLaunch& R, int y, int c0, int c1, int t, int n) {
     const lucetree_reorder_args& a = R.a;
-    pdl_wait();
-    if (threadIdx.x == 0) pdl_trigger();
     const int P = a.max_pages_per_seq;
-    const int c0 = blockIdx.x * kCols, c1 = min(P, c0 + kCols);
-    for (int y = blockIdx.y; y < a.rows_in + a.rows_out; y += gridDim.y) {
-        if (y >= a.rows_out) {
-            const int b = y - a.rows_out;
-            const RowSpan s = row_span(a, b, nullptr);
-            if (!s.ok) continue;  // a row of unknown length keeps its pages
-            const int children = R.w.children[b];
-            const uint64_t kept = R.w.kept[b];
-            for (int c = c0 + threadIdx.x; c < c1; c += kThreads) {
-                const int page = a.table_in[(size_t)b * P + c];
-                if (page == -1) continue;
-                if (!page_ok(page, a.num_pages)) {
-                    atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
-                    continue;
-                }
-                int delta = -1;
-                if (c < s.full) delta = children - 1;
-                else if (c < s.end && ((kept >> (c - s.full)) & 1)) delta = 0;
-                if (delta != 0 && atomicAdd(a.ref_out + page, delta) + delta < 0)
-                    atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
-            }
-            continue;
-        }
-        const int r = y;
-        int b = source_row(a, r, nullptr);
-        RowSpan s{0, 0, 0, false};
-        if (b >= 0) s = row_span(a, b, nullptr);
-        if (!s.ok) b = -1;
-        int32_t* out = a.table_out + (size_t)r * P;
-        const int32_t* in = a.table_in + (size_t)(b < 0 ? 0 : b) * P;
-        for (int c = c0 + threadIdx.x; c < c1; c += kThreads) {
-            if (c >= s.full && c < s.end) continue;
-            int page = -1;
-            if (b >= 0 && c < s.full) {
-                page = in[c];
-                if (!page_ok(page, a.num_pages)) page = -1;
-            }
-            out[c] = page;
-        }
-        if (blockIdx.x > 0) continue;
-        // the tail, a warp to a page
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const uint64_t kept = b >= 0 && R.w.first[b] == r ? R.w.kept[b] : 0;
-        for (int c = s.full + warp; c < s.end; c += kThreads / 32) {
-            const int k = c - s.full, old = in[c];
-            if ((kept >> k) & 1) {
-                if (lane == 0) out[c] = old;
+    if (y >= a.rows_out) {
+        const int b = y - a.rows_out;
+        const RowSpan s = row_span(a, b, nullptr);
+        if (!s.ok) return;  // a row of unknown length keeps its pages
+        const int children = now(&R.w.children[b]);
+        const uint64_t kept = R.w.kept[b];
+        for (int c = c0 + t; c < c1; c += n) {
+            const int page = a.table_in[(size_t)b * P + c];
+            if (page == -1) continue;
+            if (!page_ok(page, a.num_pages)) {
+                atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
                 continue;
             }
-            const int rank = R.w.base[r] + k - __popcll(kept & ((1ull << k) - 1));
-            const int page = free_page(R.w, R.chunks, rank);
-            if (lane == 0) {
-                out[c] = page;
-                if (page < 0) atomicOr(a.status, LUCETREE_DEV_NO_PAGE);
-                else a.ref_out[page] = 1;
-                if (k == 0) {
-                    const bool copy = s.L % kPage != 0 && page >= 0 && page_ok(old, a.num_pages);
-                    a.copy_src[r] = copy ? old : -1;
-                    a.copy_dst[r] = copy ? page : -1;
-                }
+            int delta = -1;
+            if (c < s.full) delta = children - 1;
+            else if (c < s.end && ((kept >> (c - s.full)) & 1)) delta = 0;
+            if (delta != 0 && atomicAdd(a.ref_out + page, delta) + delta < 0) atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
+        }
+        return;
+    }
+    const int r = y;
+    int b = source_row(a, r, nullptr);
+    RowSpan s{0, 0, 0, false};
+    if (b >= 0) s = row_span(a, b, nullptr);
+    if (!s.ok) b = -1;
+    int32_t* out = a.table_out + (size_t)r * P;
+    const int32_t* in = a.table_in + (size_t)(b < 0 ? 0 : b) * P;
+    for (int c = c0 + t; c < c1; c += n) {
+        if (c >= s.full && c < s.end) continue;
+        int page = -1;
+        if (b >= 0 && c < s.full) {
+            page = in[c];
+            if (!page_ok(page, a.num_pages)) page = -1;
+        }
+        out[c] = page;
+    }
+    if (c0 > 0) return;
+    // the tail, a warp to a page
+    const int warp = t >> 5, lane = t & 31;
+    const uint64_t kept = b >= 0 && now(&R.w.first[b]) == r ? R.w.kept[b] : 0;
+    for (int c = s.full + warp; c < s.end; c += n / 32) {
+        const int k = c - s.full, old = in[c];
+        if ((kept >> k) & 1) {
+            if (lane == 0) out[c] = old;
+            continue;
+        }
+        const int rank = R.w.base[r] + k - __popcll(kept & ((1ull << k) - 1));
+        const int page = free_page(R.w, R.chunks, rank);
+        if (lane == 0) {
+            out[c] = page;
+            if (page < 0) atomicOr(a.status, LUCETREE_DEV_NO_PAGE);
+            else a.ref_out[page] = 1;
+            if (k == 0) {
+                const bool copy = s.L % kPage != 0 && page >= 0 && page_ok(old, a.num_pages);
+                a.copy_src[r] = copy ? old : -1;
+                a.copy_dst[r] = copy ? page : -1;
             }
         }
-        if (threadIdx.x == 0) {
-            a.ctx_out[r] = s.L;
-            if (s.full >= s.end || (kept & 1)) a.copy_src[r] = a.copy_dst[r] = -1;
-        }
     }
+    if (t == 0) {
+        a.ctx_out[r] = s.L;
+        if (s.full >= s.end || (kept & 1)) a.copy_src[r] = a.copy_dst[r] = -1;
+    }
+}
+
+// CTA 0 plans the rows, CTA 1 + i takes chunk i of the pages.
+__global__ void __launch_bounds__(kChunk) reorder_plan_kernel(ReorderLaunch R) {
+    __shared__ int s_warp[kChunk / 32];
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    if (blockIdx.x == 0) plan_rows(R, s_warp);
+    else scan_pages(R, blockIdx.x - 1, s_warp);
+}
+
+__global__ void __launch_bounds__(kThreads) reorder_apply_kernel(ReorderLaunch R) {
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    const int c0 = blockIdx.x * kCols, c1 = min(R.a.max_pages_per_seq, c0 + kCols);
+    for (int y = blockIdx.y; y < R.a.rows_in + R.a.rows_out; y += gridDim.y) apply_row(R, y, c0, c1, threadIdx.x, kThreads);
+}
+
+// Both in one CTA, with the plan in shared memory: a warp to a row.
+__global__ void __launch_bounds__(kChunk) reorder_small_kernel(ReorderLaunch R) {
+    __shared__ int s_warp[kChunk / 32];
+    __shared__ int32_t s_children[kSmallRows], s_first[kSmallRows], s_base[kSmallRows];
+    __shared__ uint64_t s_kept[kSmallRows];
+    __shared__ uint32_t s_bits[kSmallPages / 32];
+    __shared__ int32_t s_count[kSmallPages / kChunk];
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    R.w = ReorderPlan{s_children, s_first, s_kept, s_base, s_bits, s_count};
+    for (int c = 0; c < R.chunks; ++c) scan_pages(R, c, s_warp);
+    plan_rows(R, s_warp);
+    __syncthreads();
+    for (int y = threadIdx.x >> 5; y < R.a.rows_in + R.a.rows_out; y += kChunk / 32)
+        apply_row(R, y, 0, R.a.max_pages_per_seq, threadIdx.x & 31, 32);
 }
 
 // ---------------------------------------------------------------- trim
 
+// Columns [c0, c1) of row b, by thread t of n.
+__device__ inline void trim_row(const lucetree_trim_args& a, int b, int c0, int c1, int t, int n) {
+    const int P = a.max_pages_per_seq;
+    int L = a.ctx_len[b];
+    if (L < 0 || (long long)L > (long long)P * kPage) {
+        if (t == 0 && c0 == 0) atomicOr(a.status, LUCETREE_DEV_BAD_CTX);
+        L = 0;  // nothing of it is known to lie behind the window
+    }
+    // pages [sp, wp) hold no sink and nothing that the window of the next token reaches
+    const int lo = max(L - a.window + 1, 0);
+    const int sp = a.sinks / kPage + (a.sinks % kPage != 0), wp = lo / kPage;
+    for (int c = c0 + t; c < c1; c += n) {
+        const int page = a.table_in[(size_t)b * P + c];
+        const bool gone = c >= sp && c < wp;
+        if (gone && page != -1) {
+            if (!page_ok(page, a.num_pages) || atomicSub(a.ref_out + page, 1) <= 0)
+                atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
+        }
+        if (gone || a.table_out != a.table_in) a.table_out[(size_t)b * P + c] = gone ? -1 : page;
+    }
+}
+
 __global__ void __launch_bounds__(kThreads) trim_kernel(lucetree_trim_args a) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    const int P = a.max_pages_per_seq;
-    const int c0 = blockIdx.x * kCols, c1 = min(P, c0 + kCols);
-    for (int b = blockIdx.y; b < a.rows; b += gridDim.y) {
-        int L = a.ctx_len[b];
-        if (L < 0 || (long long)L > (long long)P * kPage) {
-            if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(a.status, LUCETREE_DEV_BAD_CTX);
-            L = 0;  // nothing of it is known to lie behind the window
-        }
-        // pages [sp, wp) hold no sink and nothing that the window of the next token reaches
-        const int lo = max(L - a.window + 1, 0);
-        const int sp = a.sinks / kPage + (a.sinks % kPage != 0), wp = lo / kPage;
-        for (int c = c0 + threadIdx.x; c < c1; c += kThreads) {
-            const int page = a.table_in[(size_t)b * P + c];
-            const bool gone = c >= sp && c < wp;
-            if (gone && page != -1) {
-                if (!page_ok(page, a.num_pages) || atomicSub(a.ref_out + page, 1) <= 0)
-                    atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
-            }
-            if (gone || a.table_out != a.table_in) a.table_out[(size_t)b * P + c] = gone ? -1 : page;
-        }
+    const int c0 = blockIdx.x * kCols, c1 = min(a.max_pages_per_seq, c0 + kCols);
+    for (int b = blockIdx.y; b < a.rows; b += gridDim.y) trim_row(a, b, c0, c1, threadIdx.x, kThreads);
+}
+
+__global__ void __launch_bounds__(kThreads) copy_counts_kernel(const int32_t* from, int32_t* to, int n) {
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const long long i = ((long long)blockIdx.x * 4 + k) * kThreads + threadIdx.x;
+        if (i < n) to[i] = from[i];
     }
+}
+
+// The same in one CTA, counts copied first.
+__global__ void __launch_bounds__(kChunk) trim_small_kernel(lucetree_trim_args a) {
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    if (a.ref_out != a.ref_in) {
+        for (int p = threadIdx.x; p < a.num_pages; p += kChunk) a.ref_out[p] = a.ref_in[p];
+        __syncthreads();
+    }
+    for (int b = threadIdx.x >> 5; b < a.rows; b += kChunk / 32)
+        trim_row(a, b, 0, a.max_pages_per_seq, threadIdx.x & 31, 32);
 }
 
 // ---------------------------------------------------------------- compact
@@ -416,6 +476,77 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(CompactLaunch C
     }
 }
 
+// All of it in one CTA: each thread keeps the counts of its pages, and the new names
+// stay in shared memory.
+__global__ void __launch_bounds__(kChunk) compact_small_kernel(CompactLaunch C) {
+    constexpr int kMine = kSmallPages / kChunk;
+    const lucetree_compact_args& a = C.a;
+    __shared__ int s_warp[kChunk / 32];
+    __shared__ int16_t s_name[kSmallPages];      // new number of a page at or past the live count, -1 if free
+    __shared__ int16_t s_hole[kSmallPages / 2];  // free pages before it
+    static_assert(kSmallPages <= 32767 + 1, "page numbers in 16 bits");
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+    const int t = threadIdx.x;
+    int ref[kMine], used_before[kMine], live = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int p = i * kChunk + t;
+        ref[i] = p < a.num_pages ? a.ref_in[p] : 0;
+        used_before[i] = 0;
+        if (i >= C.chunks) continue;  // the same for all threads
+        int n;
+        used_before[i] = live + block_scan(ref[i] > 0 ? 1 : 0, s_warp, &n) - (ref[i] > 0 ? 1 : 0);
+        live += n;
+    }
+    int low = 0, low_used;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int p = i * kChunk + t;
+        low += p < live && ref[i] > 0;
+        if (p < live && ref[i] <= 0) s_hole[p - used_before[i]] = (int16_t)p;
+    }
+    block_scan(low, s_warp, &low_used);  // (and every hole is written)
+    const int movers = live - low_used;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int p = i * kChunk + t;
+        if (p >= a.num_pages) continue;
+        if (p < live) {
+            if (ref[i] > 0 && a.ref_out != a.ref_in) a.ref_out[p] = ref[i];
+        } else if (ref[i] > 0) {
+            const int k = used_before[i] - low_used, to = s_hole[k];
+            s_name[p] = (int16_t)to;
+            a.copy_src[k] = p;
+            a.copy_dst[k] = to;
+            a.ref_out[to] = ref[i];
+            a.ref_out[p] = 0;
+        } else {
+            s_name[p] = -1;
+            a.ref_out[p] = ref[i];
+        }
+    }
+    for (int i = movers + t; i < a.num_pages / 2; i += kChunk) a.copy_src[i] = a.copy_dst[i] = -1;
+    if (t == 0) {
+        *a.live = live;
+        *a.copy_n = movers;
+    }
+    __syncthreads();
+    const int n = a.rows * a.max_pages_per_seq;
+    for (int e = t; e < n; e += kChunk) {
+        int page = a.table_in[e];
+        if (page != -1) {
+            if (!page_ok(page, a.num_pages) || (page >= live && s_name[page] < 0)) {
+                atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
+                page = -1;
+            } else if (page >= live) {
+                page = s_name[page];
+            }
+        }
+        a.table_out[e] = page;
+    }
+}
+
 // ---------------------------------------------------------------- copies
 
 // Copies of rows of 16-byte units: pair i copies row src[i] of `from` to row
@@ -456,9 +587,9 @@ __global__ void __launch_bounds__(kThreads) copy_rows_kernel(CopyLaunch C) {
             if (s == 0 && threadIdx.x == 0) atomicOr(C.status, C.bad);
             continue;
         }
-        const long long units = C.units[which];
-        const uint4* x = C.from[which] + (long long)from * units;
-        uint4* y = C.to[which] + (long long)to * units;
+        const long long units = which ? C.units[1] : C.units[0];
+        const uint4* x = (which ? C.from[1] : C.from[0]) + (long long)from * units;
+        uint4* y = (which ? C.to[1] : C.to[0]) + (long long)to * units;
         uint4 v[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
@@ -506,15 +637,22 @@ cudaError_t launch_reorder_pages(const lucetree_reorder_args& a, void* workspace
     R.w.base = reinterpret_cast<int32_t*>(take(4 * (size_t)a.rows_out));
     R.w.free_bits = reinterpret_cast<uint32_t*>(take((size_t)R.chunks * 128));
     R.w.free_count = reinterpret_cast<int32_t*>(take((size_t)R.chunks * 4));
+    const long long all = (long long)a.rows_in + a.rows_out;
+    if (a.num_pages <= kSmallPages && a.rows_in <= kSmallRows && a.rows_out <= kSmallRows &&
+        all * a.max_pages_per_seq <= kSmallEntries)
+        return launch_pdl(reorder_small_kernel, dim3(1), dim3(kChunk), 0, stream, R);
     cudaError_t e = launch_pdl(reorder_plan_kernel, dim3(1 + R.chunks), dim3(kChunk), 0, stream, R);
     if (e != cudaSuccess) return e;
-    return launch_pdl(reorder_apply_kernel, table_grid(a.max_pages_per_seq, (long long)a.rows_in + a.rows_out),
+    return launch_pdl(reorder_apply_kernel, table_grid(a.max_pages_per_seq, all),
                       dim3(kThreads), 0, stream, R);
 }
 
 cudaError_t launch_trim_pages(const lucetree_trim_args& a, cudaStream_t stream) {
+    if (a.num_pages <= kSmallPages && (long long)a.rows * a.max_pages_per_seq <= kSmallEntries)
+        return launch_pdl(trim_small_kernel, dim3(1), dim3(kChunk), 0, stream, a);
     if (a.ref_out != a.ref_in) {
-        cudaError_t e = cudaMemcpyAsync(a.ref_out, a.ref_in, 4 * (size_t)a.num_pages, cudaMemcpyDeviceToDevice, stream);
+        const unsigned ctas = (unsigned)((a.num_pages + 4 * kThreads - 1) / (4 * kThreads));
+        cudaError_t e = launch_pdl(copy_counts_kernel, dim3(ctas), dim3(kThreads), 0, stream, a.ref_in, a.ref_out, a.num_pages);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(trim_kernel, table_grid(a.max_pages_per_seq, a.rows), dim3(kThreads), 0, stream, a);
@@ -530,6 +668,8 @@ cudaError_t launch_compact_pages(const lucetree_compact_args& a, void* workspace
     C.chunks = chunks_of(a.num_pages);
     C.used_count = reinterpret_cast<int32_t*>(workspace);
     C.rank = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(workspace) + align256(4 * (size_t)C.chunks));
+    if (a.num_pages <= kSmallPages && (long long)a.rows * a.max_pages_per_seq <= kSmallEntries)
+        return launch_pdl(compact_small_kernel, dim3(1), dim3(kChunk), 0, stream, C);
     cudaError_t e = launch_pdl(compact_count_kernel, dim3(C.chunks), dim3(kChunk), 0, stream, C);
     if (e != cudaSuccess) return e;
     e = launch_pdl(compact_rank_kernel, dim3(C.chunks), dim3(kChunk), 0, stream, C);

@@ -95,6 +95,7 @@ def run_reorder(table, L, ref, src, reserve, in_place=False):
 @pytest.mark.parametrize("rows,rows_out,P,reserve,spare", [
     (1, 1, 1, 0, 4), (1, 4, 17, 22, 20), (3, 2, 5, 64, 9), (8, 8, 40, 1, 30), (8, 20, 9, 200, 120), (40, 64, 33, 22, 200),
     (5, 5, 1500, 8, 30), (2, 3, 70, 4032, 300), (1100, 1200, 3, 22, 2500), (6, 6, 12, 0, 9000),
+    (30, 40, 700, 10, 300),
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_reorder(cuda_dev, rows, rows_out, P, reserve, spare, in_place):
@@ -156,7 +157,7 @@ def ref_trim(table, L, window, sinks, ref):
 
 
 @pytest.mark.parametrize("rows,P,window,sinks", [(1, 1, 1, 0), (3, 20, 100, 4), (7, 1100, 4096, 64), (5, 9, 64, 65),
-                                                 (4, 30, 5000, 0), (300, 4, 1, 0), (2, 6, 2 ** 31 - 1, 2 ** 31 - 1)])
+                                                 (4, 30, 5000, 0), (300, 4, 1, 0), (40, 1100, 500, 4), (2, 6, 2 ** 31 - 1, 2 ** 31 - 1)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_trim(cuda_dev, rows, P, window, sinks, in_place):
     LT = _lt()
@@ -193,7 +194,8 @@ def ref_compact(table, ref):
 
 
 @pytest.mark.parametrize("rows,P,spare,used", [(1, 1, 0, 1.0), (1, 1, 1, 0.0), (3, 7, 5, 0.5), (20, 60, 3000, 0.3),
-                                               (9, 40, 1024, 0.9), (2, 3, 5000, 0.5), (30, 90, 0, 0.6), (4, 600, 0, 1.0)])
+                                               (9, 40, 1024, 0.9), (2, 3, 5000, 0.5), (30, 90, 0, 0.6), (4, 600, 0, 1.0),
+                                               (30, 90, 9000, 0.6), (60, 600, 100, 0.5)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compact(cuda_dev, rows, P, spare, used, in_place):
     LT = _lt()
