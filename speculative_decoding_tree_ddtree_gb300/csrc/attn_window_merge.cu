@@ -60,12 +60,13 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
     __shared__ float2 s_ml[kMergeWarps];
     const lucetree_attn_args& a = W.L.a;
     const PlanDims& p = W.L.plan;
-    pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     int before;
     const Cut cut(flat_tiles(W, 0, &before), p.Cg);
-    // ---- segments with a CTA boundary inside, by the sequences' tile offsets
+    // ---- segments with a CTA boundary inside, by the sequences' tile offsets.  This
+    // reads the lengths before the wait below: the attention kernel lets this
+    // one start only after its own wait, so its inputs are final.
     int base = 0, n_split = 0;
     for (int b0 = 0; b0 < p.B; b0 += kSeqs) {
         const int nb = min(p.B - b0, kSeqs);
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
         base = run;
     }
     __syncthreads();
+    pdl_wait();  // the partial sums
     const size_t sf = slot_floats(p);
     const int R = p.N * p.G;  // rows of a segment
     const long long rows = (long long)n_split * R, warps = (long long)gridDim.x * kMergeWarps;
@@ -145,9 +147,23 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
         // this warp's partials are member, member + G, ..
         const int mine = has_row ? (sp.count - member + G - 1) / G : 0;
         for (int k0 = 0; k0 < mine; k0 += 32) {
-            const int k = member + (k0 + lane) * G;
+            const int n = min(32, mine - k0), k = member + (k0 + lane) * G;
+            // rows u0 .. u0 + kU - 1 of this round
+            float v[kU][kV];
+            auto load = [&](int u0) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    if (u0 + u < n) {
+                        load_row<kV>(parts + (size_t)(member + (k0 + u0 + u) * G) * sf, v[u]);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < kV; ++y) v[u][y] = 0.f;
+                    }
+                }
+            };
+            load(0);  // with the maxima and sums, not after them
             float mk = -INFINITY, lk = 0.f;
-            if (k0 + lane < mine) {
+            if (lane < n) {
                 const float* s = ws + (size_t)k * sf + (size_t)p.rg.RG * D + rl;
                 mk = s[0];
                 lk = s[p.rg.RG];
@@ -155,7 +171,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
             float top = fmaxf(m, mk);
 #pragma unroll
             for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
-            const float w = mk > -INFINITY ? exp2f(mk - top) : 0.f;
+            const float w = mk > -INFINITY ? exp2f(mk - top) : 0.f;  // (0 past n)
             float sum = w * lk;
 #pragma unroll
             for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
@@ -164,23 +180,14 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
             m = top;
 #pragma unroll
             for (int y = 0; y < kV; ++y) o[y] *= keep;
-            const int n = min(32, mine - k0);
             for (int u0 = 0; u0 < n; u0 += kU) {
-                float v[kU][kV], wu[kU];
+                if (u0 > 0) load(u0);
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
-                    wu[u] = __shfl_sync(0xffffffffu, w, u0 + u);  // 0 past n
-                    if (u0 + u < n) {
-                        load_row<kV>(parts + (size_t)(member + (k0 + u0 + u) * G) * sf, v[u]);
-                    } else {
+                    const float wu = __shfl_sync(0xffffffffu, w, u0 + u);
 #pragma unroll
-                        for (int y = 0; y < kV; ++y) v[u][y] = 0.f;
-                    }
+                    for (int y = 0; y < kV; ++y) o[y] = fmaf(wu, v[u][y], o[y]);
                 }
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-#pragma unroll
-                    for (int y = 0; y < kV; ++y) o[y] = fmaf(wu[u], v[u][y], o[y]);
             }
         }
         if (G > 1) {
