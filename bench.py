@@ -1022,6 +1022,74 @@ def run_stage_only(args):
     return 0
 
 
+def measure_window(args, dev, stream):
+    """Windowed tree-verify attention: 16 sequences of 16,384 committed tokens,
+    window 4096 and 4 sinks, 24/4 heads of 256 dims in bf16, at budget 22 and as
+    the single-token decode step; back-to-back calls between CUDA events."""
+    import torch
+    from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
+    B, L, window, sinks, Hq, Hkv, D = 16, 16384, 4096, 4, 24, 4, 256
+    g = torch.Generator(device=dev).manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device=dev, dtype=torch.bfloat16)  # noqa: E731
+    per = (L + 64) // 64
+    k_pool, v_pool = r(B * per, Hkv, 64, D), r(B * per, Hkv, 64, D)
+    table = torch.randperm(B * per, generator=g, device=dev).to(torch.int32).view(B, per)
+    ctx = torch.full((B,), L, dtype=torch.int32, device=dev)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    peak, kind = peak_hbm()
+    res = {}
+    for N in (22, 1):
+        q, kt, vt = r(B, N, Hq, D), r(B, N, Hkv, D), r(B, N, Hkv, D)
+        parent = torch.tensor([[max(-1, (i - 1) // 2) if i else -1 for i in range(N)]] * B, dtype=torch.int32, device=dev)
+        anc, out = torch.empty(B, N, dtype=torch.int64, device=dev), torch.empty_like(q)
+        ws = torch.empty(LT.lucetree_verify_attn_workspace(B, N, Hq, Hkv, D), dtype=torch.uint8, device=dev)
+        LT.lucetree_build_anc_mask(parent, anc, st)
+        stream.wait_stream(torch.cuda.current_stream(dev))
+        ms = time_spans(lambda: LT.lucetree_verify_attn_win(q, k_pool, v_pool, table, ctx, kt, vt, anc, window, sinks, out,
+                                                            st, ws, stream=stream), stream, dev, min(args.steps, 500))
+        kv = B * (window + sinks) * Hkv * D * 2 * 2
+        t = float(np.median(ms))
+        res["budget %d" % N] = {"ms": t, "kv_bytes": kv, "GBps": kv / t / 1e6, "frac_of_hbm_peak": kv / t / 1e6 / peak,
+                                "peak_kind": kind}
+    res["device_status"] = int(st.item())
+    return res
+
+
+def measure_beam(args, dev, stream):
+    """Beam selection: 8 requests of 8 beams over 151,936 fp32 logits."""
+    import torch
+    from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
+    B, K, V = 8, 8, 151936
+    g = torch.Generator(device=dev).manual_seed(0)
+    sets = [3 * torch.randn(B, K, V, generator=g, device=dev) for _ in range(4)]  # together larger than L2
+    cum = -torch.rand(B, K, generator=g, device=dev)
+    score = torch.empty(B, K, device=dev)
+    token, row, fin = (torch.empty(B, K, dtype=torch.int32, device=dev) for _ in range(3))
+    ws = torch.empty(LT.lucetree_beam_select_workspace(B, K, K, V), dtype=torch.uint8, device=dev)
+    stream.wait_stream(torch.cuda.current_stream(dev))
+    turn = [0]
+
+    def call():
+        turn[0] += 1
+        LT.lucetree_beam_select(sets[turn[0] % len(sets)], cum, None, 2, score, token, row, fin, ws, stream=stream)
+
+    t = float(np.median(time_spans(call, stream, dev, min(args.steps, 500), group=20)))
+    peak, kind = peak_hbm()
+    nbytes = B * K * V * 4
+    return {"ms": t, "logit_bytes": nbytes, "GBps": nbytes / t / 1e6, "frac_of_hbm_peak": nbytes / t / 1e6 / peak,
+            "peak_kind": kind}
+
+
+def _run_measure(name, measure, args):
+    import torch
+    from speculative_decoding_tree_ddtree_gb300.build import build
+    build()
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    print(json.dumps({name: measure(args, dev, torch.cuda.Stream(device=dev))}), flush=True)
+    return 0
+
+
 def run_delta_only(args):
     import torch
     from speculative_decoding_tree_ddtree_gb300.build import build
@@ -1069,6 +1137,8 @@ def build_parser() -> argparse.ArgumentParser:
                     help="with --lmhead-only: a smaller vocabulary (profiler captures)")
     ap.add_argument("--no-delta", action="store_true", help="skip the recurrent-state (delta rule) measurement")
     ap.add_argument("--delta-only", action="store_true", help="time only the recurrent-state tree pass and commit")
+    ap.add_argument("--window-only", action="store_true", help="time only the windowed attention")
+    ap.add_argument("--beam-only", action="store_true", help="time only the beam selection")
     ap.add_argument("--no-stage", action="store_true", help="skip the host-resident page staging measurement")
     ap.add_argument("--no-vq", action="store_true", help="skip the quantised-V attention measurement")
     ap.add_argument("--vq-only", action="store_true", help="time only the quantised-V attention calls")
@@ -1085,6 +1155,10 @@ def main(argv=None):
         return run_lmhead_only(args)
     if args.delta_only:
         return run_delta_only(args)
+    if args.window_only:
+        return _run_measure("window", measure_window, args)
+    if args.beam_only:
+        return _run_measure("beam", measure_beam, args)
     if args.stage_only:
         return run_stage_only(args)
     if args.vq_only:

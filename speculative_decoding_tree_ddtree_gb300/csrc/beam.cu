@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamLaunch L)
         if (warp < half && warp + half < K) s_cand[warp][lane] = merge32(s_cand[warp][lane], s_cand[warp + half][lane]);
     }
     if (warp == 0 && lane < a.beams_out) {
-        const Cand c = s_cand[0][lane];
+        Cand c = s_cand[0][lane];
+        if (c.index >= (unsigned)K * (unsigned)a.vocab) c = Cand{order_double(-INFINITY), 0};  // only after NaN logits
         const int beam = (int)(c.index / (unsigned)a.vocab), token = (int)(c.index % (unsigned)a.vocab);
         const size_t at = (size_t)b * a.beams_out + lane;
         a.out_score[at] = (float)order_value(c.score);

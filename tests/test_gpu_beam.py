@@ -59,10 +59,10 @@ def check(logits, cum, finished, eos, Kout, dev=None):
         assert np.array_equal(g.numpy(), w)
     g, w = got[0].double().numpy(), want[0]
     assert np.array_equal(np.isneginf(g), np.isneginf(w))
-    fine = ~np.isneginf(w)
+    g, w = g[~np.isneginf(w)], w[~np.isneginf(w)]
     # the sum's fp32 terms are off by a few 2^-24 each (difference, product, exponential of 2 ulp) and so is its
     # logarithm; one more rounding of the score
-    assert np.all(np.abs(g - w)[fine] <= 16 * 2.0 ** -24 + 2.0 ** -24 * np.abs(w[fine]))
+    assert np.all(np.abs(g - w) <= 16 * 2.0 ** -24 + 2.0 ** -24 * np.abs(w))
 
 
 def draw(B, K, V, dtype, seed, spread=3.0):
@@ -139,6 +139,27 @@ def test_short_rows_of_any_alignment(cuda_dev):
             dev = flat[offset:offset + 75].view(3, 25)[:, :V][None]
             dev.copy_(logits)
             check(logits, cum, None, 1, min(9, 3 * V), dev=dev)
+
+
+def test_equal_rows_tie_wherever_they_lie(cuda_dev):
+    # rows 1003 elements apart start on every 4-byte boundary: their sums have to be the same bits
+    for dtype in TYPES:
+        flat = torch.zeros(2 * 7 * 1003 + 8, device="cuda").to(TYPES[dtype])
+        row, _ = draw(1, 1, 1000, dtype, seed=4)
+        for offset in range(4):
+            dev = flat[offset:offset + 2 * 7 * 1003].view(14, 1003)[:, :1000].unflatten(0, (2, 7))
+            dev.copy_(row.expand(2, 7, 1000))
+            check(row.expand(2, 7, 1000).contiguous(), torch.full((2, 7), -2.0), None, -1, 30, dev=dev)
+
+
+def test_nan_logits_stay_inside_the_outputs(cuda_dev):
+    # outside the contract, but what comes back still names rows and tokens that exist
+    for bits in (0x7FC00000, 0xFFC00000 - (1 << 32)):
+        nan = torch.tensor([bits], dtype=torch.int32).view(torch.float32)
+        logits = nan.expand(2 * 3 * 70).reshape(2, 3, 70).contiguous()
+        logits[1, 1, 5] = 1.0
+        score, token, row, fin = call(logits.cuda(), torch.zeros(2, 3), torch.zeros(2, 3, dtype=torch.int32), 5, 32)
+        assert ((token >= 0) & (token < 70)).all() and (row // 3 == torch.arange(2)[:, None]).all()
 
 
 def test_without_the_optional_outputs(cuda_dev):
