@@ -173,6 +173,16 @@ __device__ inline void add_sums(float& m, float& s, float m2, float s2) {
     m = top;
 }
 
+// The warp's (m, s) in every lane.
+__device__ inline void warp_sums(float& m, float& s) {
+    float top;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(m));
+    s = m == -INFINITY ? 0.f : s * exp_diff(m, top);
+    m = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+}
+
 __device__ inline bool row_ended(const lucetree_beam_args& a, int row) {
     return a.finished && a.finished[row] != 0;
 }
@@ -195,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     __shared__ u64 s_list[kWarps][32];
     __shared__ u64 s_buf[kWarps][32 + 32 * kE];  // what one vector of every lane may add to 31 waiting keys
     __shared__ float2 s_sum[kWarps];
+    __shared__ int s_left[kWarps];
     const lucetree_beam_args& a = L.a;
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
@@ -254,10 +265,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     __syncthreads();
     const u64 threads = s_list[0][lane];
     const u64 limit = __shfl_sync(0xffffffffu, threads, a.beams_out - 1);  // 0: fewer threads than that have a vector
-    // a warp goes through one thread's vectors at a time; the few keys that count
-    // wait in shared memory until 32 of them are sorted and merged in
+    // A warp goes through one thread's vectors at a time; keys that count wait in shared
+    // memory until 32 of them are sorted and merged into the warp's list.  Most
+    // warps never have 32: what is left over is put together and sorted by one warp.
     u64 list = 0;
     int waiting = 0;
+    bool listed = false;
     for (int i = warp; i < a.beams_out; i += kWarps) {
         const u64 key = __shfl_sync(0xffffffffu, threads, i);
         if (key == 0) break;
@@ -282,32 +295,59 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
                 if ((pass >> e) & 1u) s_buf[warp][at++] = pack_key(f[e], (unsigned)(v * kE + e));
             waiting += __shfl_sync(0xffffffffu, upto, 31);
             __syncwarp();
-            for (; waiting >= 32; waiting -= 32) list = merge32(list, sort32(s_buf[warp][waiting - 32 + lane]));
+            for (; waiting >= 32; waiting -= 32) {
+                list = merge32(list, sort32(s_buf[warp][waiting - 32 + lane]));
+                listed = true;
+            }
             __syncwarp();
         }
     }
-    if (waiting > 0) list = merge32(list, sort32(lane < waiting ? s_buf[warp][lane] : 0));
     if (chunk == L.chunks - 1 && warp == 0) {
         const int i = nv * kE + lane;
         const bool in = i < a.vocab;
         const float f = in ? scalar(x + i) : -INFINITY;
         if (in) add_sums(m, s, f, f == -INFINITY ? 0.f : 1.f);
-        list = merge32(list, sort32(in ? pack_key(f, (unsigned)i) : 0));
+        if (waiting + kE > 32) {  // (the tail has fewer than kE elements)
+            list = merge32(list, sort32(lane < waiting ? s_buf[warp][lane] : 0));
+            listed = true;
+            waiting = 0;
+        }
+        __syncwarp();
+        if (in) s_buf[warp][waiting + lane] = pack_key(f, (unsigned)i);
+        waiting += __popc(__ballot_sync(0xffffffffu, in));
+        __syncwarp();
     }
     // the CTA's sum and list
+    warp_sums(m, s);
+    if (lane == 0) {
+        s_sum[warp] = make_float2(m, s);
+        s_left[warp] = waiting;
+    }
+    const bool any_listed = __syncthreads_or(listed);  // (every warp has read the threads' list)
+    int at = 0, left = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        add_sums(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
-    if (lane == 0) s_sum[warp] = make_float2(m, s);
-    __syncthreads();  // every warp has read the threads' list
-    merge_warps(s_list, list);
+    for (int w = 0; w < kWarps; ++w) {
+        at += w < warp ? s_left[w] : 0;
+        left += s_left[w];
+    }
+    u64* all = &s_list[0][0];  // fewer than 32 keys of each warp
+    if (lane < waiting) all[at + lane] = s_buf[warp][lane];
+    __syncthreads();
+    if (warp == 0) {
+        for (int g = 0; g < left; g += 32) list = merge32(list, sort32(g + lane < left ? all[g + lane] : 0));
+    }
+    if (any_listed) {
+        __syncthreads();
+        merge_warps(s_list, list);
+        list = s_list[0][lane];
+    }
     if (warp == 0) {
         const size_t at = (size_t)row * L.chunks + chunk;
-        L.keys[at * 32 + lane] = s_list[0][lane];
-        if (lane == 0) {
-            for (int w = 1; w < kWarps; ++w) add_sums(m, s, s_sum[w].x, s_sum[w].y);
-            L.sums[at] = make_float2(m, s);
-        }
+        L.keys[at * 32 + lane] = list;
+        m = lane < kWarps ? s_sum[lane].x : -INFINITY;
+        s = lane < kWarps ? s_sum[lane].y : 0.f;
+        warp_sums(m, s);
+        if (lane == 0) L.sums[at] = make_float2(m, s);
     }
 }
 
