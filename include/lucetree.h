@@ -26,6 +26,11 @@
  * lucetree_delta_tree advances a layer's state along the tree and
  * lucetree_delta_commit keeps the accepted node's state.  For KV pages kept
  * in host memory, lucetree_stage_pages brings them into the device pool.
+ * lucetree_verify_attn_win is the attention of layers with a sliding window and
+ * sinks.  For sequences that fork and end, lucetree_beam_select picks the
+ * continuations, lucetree_reorder_pages, lucetree_trim_pages and
+ * lucetree_compact_pages keep page tables and reference counts, and
+ * lucetree_copy_pages and lucetree_reorder_states move the data.
  *
  * Conventions for every call:
  *   - All array pointers are DEVICE pointers unless a parameter says "host".
@@ -168,8 +173,9 @@ typedef struct lucetree_win_args {
  * positions that no node sees may hold anything, NaN included.  N = 1 with
  * mask 1 is the single-token decode step.  A window of at least L_b + N
  * positions is the full attention.  Softmax statistics, sums and partial
- * outputs are fp32; P is rounded to fp16 for the tensor cores as in
- * lucetree_verify_attn, and a 16-bit output is rounded once from fp32.  A row
+ * outputs are fp32, and a 16-bit output is rounded once from them.  P is
+ * rounded for the tensor cores: to fp16 as in lucetree_verify_attn (bf16 V is
+ * then converted exactly while |v| < 65536), with a bf16 output to bf16.  A row
  * that sees no key (its mask lacks the node itself, which raises BAD_NODE)
  * gives zeros and lse = -infinity.  Workspace as
  * lucetree_verify_attn_workspace.  Errors as lucetree_verify_attn, plus

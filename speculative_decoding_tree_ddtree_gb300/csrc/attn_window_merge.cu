@@ -5,7 +5,9 @@
 // segment with a CTA boundary inside it has partial sums, so every CTA first lists
 // those segments (at most one for each boundary).  Then one to eight warps take a
 // row at a time: its partials' maxima and sums in one load of the lanes, their O rows a
-// few at a time.  Bound by those trips to L2, so few rows are spread over many warps.
+// few at a time.  Bound by those trips to L2, so few rows are spread over many warps
+// (528 rows of 33 partials: one warp a row 28 us for the whole call, up to eight 24;
+// with the list made before the wait and O loaded with its weights 22).
 #include "attn_window.cuh"
 
 namespace lucetree {

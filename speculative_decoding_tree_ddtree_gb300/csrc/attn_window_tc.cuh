@@ -20,9 +20,12 @@
 //   - the softmax's passes (try, undo, shift) are one loop around one copy of the
 //     code, and it runs once over nothing while the first tile loads: a cold
 //     instruction cache costs microseconds in calls of a few tiles.
-// Bounded by HBM for long windows (K and V once), by the chain of the first tile
-// and the epilogue for short ones, by shared-memory bandwidth (operands of both
-// products pass through it) where a KV head has over about a hundred rows.
+// Bounded by HBM while it streams with few rows (16 sequences decoding at window
+// 4096: 2.9 us a tile on every SM, 6.8 TB/s; 54 us the call with start, last tile
+// and merge); by the bytes in flight that the ring beside Q and P^T allows with many
+// (32 sequences at budget 22, window 8192: 3.3 us a tile, 209 us, 5.2 TB/s); by the
+// chain of lengths, page ids, first tile and epilogue in calls of a tile or two per
+// CTA (one sequence at window 4096: 22 us; 8 nodes over 260 keys: 10.5 us).
 #pragma once
 
 #include <type_traits>
