@@ -157,7 +157,7 @@ typedef struct lucetree_win_args {
     int window;              /* >= 1: positions a node sees up to and with its own */
     int sinks;               /* >= 0: first positions of the sequence that stay visible */
     int out_dtype;           /* LUCETREE_F32, or attn.dtype */
-    void* out;               /* [B][N][Hq][D] in out_dtype, 16-byte aligned */
+    void* out;               /* [B][N][Hq][D] in out_dtype, 16-byte aligned; must not overlap q or the tree's K/V */
 } lucetree_win_args;
 
 /*
@@ -449,7 +449,8 @@ typedef struct lucetree_beam_args {
     const float* cum;        /* [batch][beams_in] log-probability of each beam so far; -inf = a dead beam */
     const int32_t* finished; /* [batch][beams_in] non-zero: the beam has ended, or NULL: none has */
     int eos;                 /* token that ends a beam; outside [0, vocab) = none */
-    float* out_score;        /* [batch][beams_out], best first */
+    float* out_score;        /* [batch][beams_out], best first; with beams_out == beams_in it may be cum, and
+                                out_finished may be finished; no other overlap */
     int32_t* out_token;      /* [batch][beams_out] */
     int32_t* out_row;        /* [batch][beams_out]: row b * beams_in + beam that it continues */
     int32_t* out_finished;   /* [batch][beams_out] 0 / 1, or NULL */
@@ -573,7 +574,8 @@ typedef struct lucetree_reorder_args {
     const int32_t* table_in;   /* [rows_in][max_pages_per_seq] */
     const int32_t* ctx_in;     /* [rows_in] committed lengths */
     int rows_in;
-    const int32_t* src;        /* [rows_out]: the old row that each new row continues, -1 = the new row is empty */
+    const int32_t* src;        /* [rows_out]: the old row that each new row continues, -1 = the new row is empty;
+                                  must not overlap an output */
     int rows_out;
     int max_pages_per_seq;
     int reserve;               /* positions [L, L + reserve) that every new row must map, 0..LUCETREE_MAX_RESERVE */

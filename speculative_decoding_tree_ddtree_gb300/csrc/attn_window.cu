@@ -70,6 +70,12 @@ extern "C" lucetree_status lucetree_verify_attn_win(const lucetree_win_args* w, 
     const long long tiles = ((long long)a.max_pages_per_seq + 2) / 2;
     if ((long long)a.B * a.N * a.Hq > 0x7fffffffll || (long long)a.B * a.Hkv * tiles > 0x7fffffffll)
         return LUCETREE_ERR_UNSUPPORTED;
+    // rows are written while others are still to be read
+    const long long rows = (long long)a.B * a.N, q_elems = rows * a.Hq * a.D, t_bytes = rows * a.Hkv * a.D * 2;
+    const long long out_bytes = q_elems * (w->out_dtype == LUCETREE_F32 ? 4 : 2);
+    if (bytes_overlap(w->out, out_bytes, a.q, q_elems * 2) || bytes_overlap(w->out, out_bytes, a.k_tree, t_bytes) ||
+        bytes_overlap(w->out, out_bytes, a.v_tree, t_bytes))
+        return LUCETREE_ERR_INVALID_ARG;
     W.window = w->window;
     W.sinks = w->sinks;
     W.out_dtype = w->out_dtype;

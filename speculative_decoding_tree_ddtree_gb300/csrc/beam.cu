@@ -563,6 +563,14 @@ lucetree_status lucetree_beam_select(const lucetree_beam_args* a, void* workspac
     if (!a->logits || !a->cum || !a->out_score || !a->out_token || !a->out_row || a->row_stride < a->vocab ||
         (reinterpret_cast<uintptr_t>(a->logits) & (elem - 1)) != 0)
         return LUCETREE_ERR_INVALID_ARG;
+    // a request's own beams may be updated in place; other overlaps mix up requests
+    const long long before = 4ll * a->batch * a->beams_in, after = 4ll * a->batch * a->beams_out;
+    const bool same = a->beams_in == a->beams_out;
+    if (bytes_overlap(a->cum, before, a->out_score, after) && !(same && (const void*)a->cum == a->out_score))
+        return LUCETREE_ERR_INVALID_ARG;
+    if (a->finished && a->out_finished && bytes_overlap(a->finished, before, a->out_finished, after) &&
+        !(same && a->finished == a->out_finished))
+        return LUCETREE_ERR_INVALID_ARG;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
     if (!workspace || workspace_bytes < beam_workspace_bytes(a->batch, a->beams_in, a->vocab, dev) ||

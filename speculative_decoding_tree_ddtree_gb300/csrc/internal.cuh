@@ -218,6 +218,12 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 // when the driver does not provide it).
 EncodeTiledFn tensor_map_encoder();
 
+// Whether [a, a + an) and [b, b + bn) bytes share any.
+inline bool bytes_overlap(const void* a, long long an, const void* b, long long bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
 // Per-device record of the CUDA context in which a kernel's dynamic
 // shared-memory limit was last raised (0 = never).
 typedef std::atomic<unsigned long long> SmemLimitSeen[kMaxDevices];

@@ -721,13 +721,8 @@ namespace {
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-bool overlap(const void* a, long long an, const void* b, long long bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
-}
-
 // `b` may be `a` itself, not a part of it
-bool crosses(const void* a, const void* b, long long n) { return a != b && overlap(a, n, b, n); }
+bool crosses(const void* a, const void* b, long long n) { return a != b && bytes_overlap(a, n, b, n); }
 
 lucetree_status ws_check(const void* workspace, size_t have, size_t want) {
     if (!workspace || have < want || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LUCETREE_ERR_WORKSPACE;
@@ -758,10 +753,12 @@ lucetree_status lucetree_reorder_pages(const lucetree_reorder_args* a, void* wor
     if (a->reserve > LUCETREE_MAX_RESERVE || a->num_pages > kMaxPages) return LUCETREE_ERR_UNSUPPORTED;
     static_assert(LUCETREE_MAX_RESERVE / kPage + 1 <= kMaxTail, "a row's tail pages fit one 64-bit mask");
     const long long row = 4ll * a->max_pages_per_seq;
-    if (overlap(a->table_in, row * a->rows_in, a->table_out, row * a->rows_out) ||
-        overlap(a->ctx_in, 4ll * a->rows_in, a->ctx_out, 4ll * a->rows_out) ||
+    if (bytes_overlap(a->table_in, row * a->rows_in, a->table_out, row * a->rows_out) ||
+        bytes_overlap(a->ctx_in, 4ll * a->rows_in, a->ctx_out, 4ll * a->rows_out) ||
         crosses(a->ref_in, a->ref_out, 4ll * a->num_pages))
         return LUCETREE_ERR_INVALID_ARG;
+    for (const int32_t* out : {a->ctx_out, a->copy_src, a->copy_dst})
+        if (bytes_overlap(a->src, 4ll * a->rows_out, out, 4ll * a->rows_out)) return LUCETREE_ERR_INVALID_ARG;
     const lucetree_status st =
         ws_check(workspace, workspace_bytes, reorder_workspace_bytes(a->rows_in, a->rows_out, a->num_pages));
     if (st != LUCETREE_OK) return st;
@@ -819,7 +816,7 @@ lucetree_status lucetree_reorder_states(const lucetree_reorder_states_args* a, v
     if (a->rows_in < 1 || a->rows_out < 1 || a->row_bytes < 16 || a->row_bytes % 16 != 0) return LUCETREE_ERR_INVALID_ARG;
     if (!a->state_in || !a->state_out || !a->src || !a->status || !al16(a->state_in) || !al16(a->state_out))
         return LUCETREE_ERR_INVALID_ARG;
-    if (overlap(a->state_in, a->row_bytes * a->rows_in, a->state_out, a->row_bytes * a->rows_out))
+    if (bytes_overlap(a->state_in, a->row_bytes * a->rows_in, a->state_out, a->row_bytes * a->rows_out))
         return LUCETREE_ERR_INVALID_ARG;
     return done(launch_reorder_states(*a, reinterpret_cast<cudaStream_t>(stream)));
 }

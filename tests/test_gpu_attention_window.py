@@ -187,6 +187,68 @@ def test_a_batch_larger_than_a_warp(cuda_dev):
     check(make(ctx, 2, 2, 1, 128, "f16", 90, 4, "chain", seed=1), torch.float16)
 
 
+def test_more_sequences_than_the_merge_lists_at_once(cuda_dev):
+    rng = np.random.default_rng(8)
+    ctx = tuple(int(x) for x in rng.integers(0, 400, size=1100))
+    check(make(ctx, 1, 2, 1, 128, "bf16", 150, 4, "chain", seed=3), torch.bfloat16)
+
+
+def test_pages_past_four_gigabytes(cuda_dev):
+    s = make((900, 300), 5, 8, 4, 256, "bf16", 200, 4, "random", seed=12)
+    ref, _, bound, _ = reference(s, p_step=P_STEP[torch.bfloat16])
+    LT = _lt()
+    used = s["k_pool"].shape[0]
+    pools = []
+    for name in ("k_pool", "v_pool"):
+        big = torch.empty(40000, 4, PAGE, 256, dtype=torch.bfloat16, device="cuda")  # 5.2 GB
+        big[40000 - used:] = s[name].cuda()
+        pools.append(big)
+    table = torch.where(s["page_table"] >= 0, s["page_table"] + 40000 - used, s["page_table"]).to(torch.int32).cuda()
+    d = {k: s[k].cuda() for k in ("q", "ctx_len", "k_tree", "v_tree", "anc_mask")}
+    out, st = torch.empty_like(d["q"]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(LT.lucetree_verify_attn_workspace(2, 5, 8, 4, 256), dtype=torch.uint8, device="cuda")
+    LT.lucetree_verify_attn_win(d["q"], *pools, table, d["ctx_len"], d["k_tree"], d["v_tree"], d["anc_mask"], 200, 4, out,
+                                st, ws)
+    assert int(st.item()) == 0
+    assert ((out.cpu().double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
+
+
+def test_pages_that_are_missing_are_left_out(cuda_dev):
+    # every page of the first tiles is missing: the keys that remain give the answer
+    s = make((1000,), 4, 4, 1, 128, "f16", 600, 0, "chain", seed=13)
+    gone = (1000 - 600 + 1) // PAGE, (1000 - 600 + 1) // PAGE + 5
+    s["page_table"][0, gone[0]:gone[1]] = -1
+    out, _, status = call(s, torch.float32)
+    assert status == _lt().DEV_BAD_PAGE
+    # a node at depth d, at t = 1000 + d, sees p iff t - p < window: the first one left is p = 64 * gone[1], so
+    # the same keys lie in a window of t - p + 1 positions
+    for i in range(4):
+        t = dict(s, window=1000 + i - gone[1] * PAGE + 1)
+        ref, _, bound, _ = reference(t)
+        assert ((out[0, i].double() - ref[0, i]).abs() <= bound[0, i] + 2.0 ** -24 * ref[0, i].abs()).all()
+
+
+def test_two_calls_at_once(cuda_dev):
+    LT = _lt()
+    sets = [make((1500, 700, 90), 22, 12, 2, 128, "bf16", 400, 4, "random", seed=s) for s in (21, 22)]
+    want = [reference(s, p_step=P_STEP[torch.bfloat16]) for s in sets]
+    dev = [{k: v.cuda() for k, v in s.items() if torch.is_tensor(v)} for s in sets]
+    outs = [torch.empty_like(d["q"]) for d in dev]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = [torch.empty(LT.lucetree_verify_attn_workspace(3, 22, 12, 2, 128), dtype=torch.uint8, device="cuda")
+          for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for i, d in enumerate(dev):
+            LT.lucetree_verify_attn_win(d["q"], d["k_pool"], d["v_pool"], d["page_table"], d["ctx_len"], d["k_tree"],
+                                        d["v_tree"], d["anc_mask"], 400, 4, outs[i], st, ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for o, (ref, _, bound, _) in zip(outs, want):
+        assert ((o.cpu().double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
+
+
 def test_wide_window_is_the_full_attention(cuda_dev):
     LT = _lt()
     s = make((700, 65, 1300), 22, 24, 4, 256, "bf16", 4000, 0, "random", seed=2)

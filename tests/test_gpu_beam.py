@@ -162,6 +162,21 @@ def test_nan_logits_stay_inside_the_outputs(cuda_dev):
         assert ((token >= 0) & (token < 70)).all() and (row // 3 == torch.arange(2)[:, None]).all()
 
 
+def test_scores_and_flags_updated_in_place(cuda_dev):
+    LT = _lt()
+    B, K, V = 5, 6, 3001
+    logits, cum = draw(B, K, V, "bf16", seed=11)
+    finished = (torch.rand(B, K, generator=torch.Generator().manual_seed(2)) < 0.3).int()
+    want = reference(logits, cum, finished, 9, K)
+    c, f, x = cum.cuda(), finished.cuda(), logits.cuda()
+    token, row = (torch.empty(B, K, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = torch.empty(LT.lucetree_beam_select_workspace(B, K, K, V), dtype=torch.uint8, device="cuda")
+    LT.lucetree_beam_select(x, c, f, 9, c, token, row, f, ws)
+    assert np.array_equal(token.cpu().numpy(), want[1]) and np.array_equal(row.cpu().numpy(), want[2])
+    assert np.array_equal(f.cpu().numpy(), want[3])
+    assert np.all(np.abs(c.double().cpu().numpy() - want[0]) <= 16 * 2.0 ** -24 + 2.0 ** -24 * np.abs(want[0]))
+
+
 def test_without_the_optional_outputs(cuda_dev):
     logits, cum = draw(2, 2, 500, "f32", seed=1)
     got = call(logits.cuda(), cum, None, 4, 3, done=False)

@@ -289,6 +289,54 @@ def test_reorder_states(cuda_dev, rows, rows_out, shape):
     assert int(st.item()) == LT.DEV_BAD_ROW
 
 
+def test_captured_and_replayed(cuda_dev):
+    LT = _lt()
+    rng = np.random.default_rng(17)
+    table, L, ref = draw_pool(rng, 6, 20, 40, rng.integers(0, 1200, size=6), extra=0)
+    pools = torch.randn(len(ref), 2, PAGE, 8, generator=torch.Generator().manual_seed(1)).cuda()
+    t, c, f, src, st = _dev(table), _dev(L), _dev(ref), _dev([0] * 6), _status()
+    k, v = pools.clone(), pools.clone()
+    out, ctx, f2, cs, cd = _new(6, 20), _new(6), _new(len(ref)), _new(6), _new(6)
+    ms, md, mn, live = _new(len(ref) // 2), _new(len(ref) // 2), _new(1), _new(1)
+    state, state2 = torch.randn(6, 8, device="cuda"), torch.zeros(6, 8, device="cuda")
+    ws = torch.empty(max(LT.lucetree_reorder_pages_workspace(6, 6, len(ref)), LT.lucetree_compact_pages_workspace(len(ref))),
+                     dtype=torch.uint8, device="cuda")
+
+    def go():
+        LT.lucetree_reorder_pages(t, c, src, 9, f, out, ctx, f2, cs, cd, st, ws)
+        LT.lucetree_copy_pages(cs, cd, k, v, st)
+        LT.lucetree_reorder_states(state, src, state2, st)
+        LT.lucetree_trim_pages(out, ctx, 200, 4, f2, out, f2, st)
+        LT.lucetree_compact_pages(out, f2, out, f2, ms, md, mn, live, st, ws)
+        LT.lucetree_copy_pages(ms, md, k, v, st, count=mn)
+
+    go()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for pick in ([0, 0, 1, 5, -1, 3], [5, 4, 3, 2, 1, 0], [2, 2, 2, 2, 2, 2]):
+        src.copy_(_dev(pick))
+        k.copy_(pools)
+        v.copy_(pools)
+        graph.replay()
+        torch.cuda.synchronize()
+        o, cx, rf, a, b, short = ref_reorder(table, L, ref, np.array(pick), 9)
+        want = pools.clone()
+        for x, y in zip(a, b):
+            if x >= 0:
+                want[int(y)] = pools[int(x)]
+        o, rf = ref_trim(o, cx, 200, 4, rf)
+        o, rf, a, b, n, lv = ref_compact(o, rf)
+        for x, y in zip(a[:n], b[:n]):
+            want[int(y)] = want[int(x)]
+        assert not short and np.array_equal(out.cpu().numpy(), o) and np.array_equal(f2.cpu().numpy(), rf)
+        assert int(live.item()) == lv and torch.equal(k, want) and torch.equal(v, want)
+        for r, x in enumerate(pick):
+            assert x < 0 or torch.equal(state2[r], state[x])
+    assert int(st.item()) == 0
+
+
 def test_a_search_over_a_windowed_cache(cuda_dev):
     """Two requests: a prompt each, forked into beams by a selection, windowed
     attention and commits on the forks, a second selection that drops and

@@ -134,15 +134,17 @@ def test_sizes_of_workspaces():
 
 @pytest.mark.parametrize("entry,kind,ok,cases", [
     ("lucetree_beam_select", LT.BeamArgs,
-     dict(dtype=2, batch=2, beams_in=3, beams_out=4, vocab=50, row_stride=50, logits=FAKE, cum=FAKE, out_score=FAKE,
+     dict(dtype=2, batch=2, beams_in=3, beams_out=4, vocab=50, row_stride=50, logits=FAKE, cum=FAKE, out_score=FAKE + 24,
           out_token=FAKE, out_row=FAKE),
-     [(dict(), 3), (dict(dtype=3), 2), (dict(batch=0), 1), (dict(beams_in=40), 2), (dict(row_stride=49), 1),
+     [(dict(), 3), (dict(out_score=FAKE), 1), (dict(out_score=FAKE + 20), 1), (dict(beams_out=3, out_score=FAKE), 3),
+      (dict(beams_out=3, out_score=FAKE + 4), 1), (dict(finished=FAKE, out_finished=FAKE), 1),
+      (dict(beams_out=3, out_score=FAKE, finished=FAKE, out_finished=FAKE), 3), (dict(dtype=3), 2), (dict(batch=0), 1), (dict(beams_in=40), 2), (dict(row_stride=49), 1),
       (dict(logits=None), 1), (dict(logits=FAKE + 2), 1), (dict(dtype=1, logits=FAKE + 1), 1), (dict(cum=None), 1),
       (dict(out_row=None), 1), (dict(vocab=1), 1)]),
     ("lucetree_reorder_pages", LT.ReorderArgs,
-     dict(table_in=FAKE, ctx_in=FAKE + 4096, rows_in=3, src=FAKE, rows_out=3, max_pages_per_seq=4, reserve=2, ref_in=FAKE,
+     dict(table_in=FAKE, ctx_in=FAKE + 4096, rows_in=3, src=FAKE + 8192, rows_out=3, max_pages_per_seq=4, reserve=2, ref_in=FAKE,
           num_pages=9, table_out=FAKE + 48, ctx_out=FAKE, ref_out=FAKE, copy_src=FAKE, copy_dst=FAKE, status=FAKE),
-     [(dict(), 3), (dict(table_out=FAKE + 44), 1), (dict(table_out=FAKE), 1), (dict(ctx_out=FAKE + 4104), 1),
+     [(dict(), 3), (dict(src=FAKE), 1), (dict(copy_src=FAKE + 8200), 1), (dict(table_out=FAKE + 44), 1), (dict(table_out=FAKE), 1), (dict(ctx_out=FAKE + 4104), 1),
       (dict(ref_out=FAKE + 4), 1), (dict(reserve=4033), 2), (dict(reserve=-1), 1), (dict(rows_in=0), 1),
       (dict(num_pages=0), 1), (dict(num_pages=(1 << 30) + 1), 2), (dict(src=None), 1), (dict(copy_dst=None), 1)]),
     ("lucetree_compact_pages", LT.CompactArgs,

@@ -65,7 +65,7 @@ def test_c_entry_refuses_before_any_launch():
               v_pool=fake, num_pages=3, page_table=fake, max_pages_per_seq=2, ctx_len=fake, k_tree=fake, v_tree=fake,
               anc_mask=fake, status=fake)
 
-    def rc(window=5, sinks=0, out_dtype=LT.LUCETREE_F32, out=fake, **attn):
+    def rc(window=5, sinks=0, out_dtype=LT.LUCETREE_F32, out=fake + 65536, **attn):
         w = LT.WinArgs()
         w.attn = LT.AttnArgs(**{**ok, **attn})
         w.window, w.sinks, w.out_dtype, w.out = window, sinks, out_dtype, out
@@ -73,7 +73,7 @@ def test_c_entry_refuses_before_any_launch():
 
     assert lib.lucetree_verify_attn_win(None, None, 0, None) == 1
     assert rc() == 3  # all fine but the workspace
-    for bad in (dict(window=0), dict(sinks=-1), dict(out=None), dict(out=fake + 4), dict(q=None), dict(anc_mask=None),
+    for bad in (dict(window=0), dict(sinks=-1), dict(out=None), dict(out=fake + 65536 + 4), dict(out=fake), dict(out=fake + 4080), dict(q=None), dict(anc_mask=None),
                 dict(num_pages=0), dict(scale=float("inf"))):
         assert rc(**bad) == 1, bad
     for bad in (dict(out_dtype=LT.LUCETREE_F16), dict(out_dtype=7), dict(dtype=LT.LUCETREE_F32), dict(D=64),
