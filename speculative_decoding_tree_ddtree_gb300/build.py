@@ -16,6 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "lucetree")
 LIB = os.path.join(PKG, "liblucetree.so")
+MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,8 +48,42 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def build_marshal(force: bool = False) -> str | None:
+    """The binding's tensor checks as a Python extension (host code, against the
+    installed torch).  The binding makes the same checks in Python where it is
+    missing, so a host without Python's headers only gets a notice."""
+    import sysconfig
+
+    import torch
+    stamp = os.path.join(BUILD, "marshal.torch")
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC) \
+            and os.path.exists(stamp) and open(stamp).read() == torch.__version__:
+        return MARSHAL
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f'-DMARSHAL_TORCH_VERSION="{torch.__version__}"', "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr if r.returncode != 0 else ""
+    except OSError as e:
+        why = str(e)
+    if why:
+        print(f"the binding's tensor checks stay in Python:\n{why[-2000:]}", file=sys.stderr)
+        return None
+    os.replace(tmp, MARSHAL)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra: list | None = None) -> str:
     if not force and up_to_date():
+        build_marshal()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -64,7 +100,9 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        marshal = ex.submit(build_marshal, force)
         objs = list(ex.map(one, sources()))
+        marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -16,8 +16,8 @@
 // Launch 2, one CTA per request, merges the chunks' lists and sums row by row,
 // turns the rows' lists into scores in 64 bits (neighbouring candidates of
 // different rows are closer than fp32 keeps beside a long sum) and merges those.
-// 8 requests of 8 beams over 151,936 fp32 logits (39 MB): 20.6 us, 1.9 TB/s; 32 of
-// bf16 logits, a quarter of the beams finished: 29.8 us.  Bound by the fixed part
+// 8 requests of 8 beams over 151,936 fp32 logits (39 MB): 17.9 us, 2.2 TB/s; 32 of
+// bf16 logits, a quarter of the beams finished: 27.5 us.  Bound by the fixed part
 // of a chunk (its sorts start when the stream ends: all CTAs run in one wave) and the
 // second launch; smaller chunks cost more (8 CTAs per SM: 27 us).
 #include <type_traits>

@@ -8,6 +8,8 @@ error status, a ``LucetreeError`` is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 
@@ -305,9 +307,10 @@ def _dims(t, name: str, ndim: int):
     """The shape of a required tensor of rank ndim."""
     if t is None:
         raise LucetreeError(f"{name} is required")
-    if t.dim() != ndim:
-        raise LucetreeError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != ndim:
+        raise LucetreeError(f"{name}: expected {ndim} dimensions, got shape {tuple(shape)}")
+    return shape
 
 
 def _expect(t, name: str, shape: tuple, dtypes: tuple):
@@ -339,39 +342,48 @@ def _device() -> int:
     return torch.cuda.current_device()
 
 
-def _arg(t, name: str, shape, dtypes: tuple, dev: int) -> int:
-    """Address of a required tensor of this shape (None: any) and element type,
-    contiguous and on device dev."""
+# Kinds of element types that _arg checks for (None: any).
+_K_ANY, _K_I32, _K_F32, _K_W32, _K_W64, _K_F16, _K_BF16 = range(7)
+_KINDS = (None, _I32, _F32, _W32, _W64, (torch.float16,), (torch.bfloat16,))
+
+
+def _arg(t, name: str, kind: int, dev: int, *shape) -> int:
+    """Address of a required contiguous tensor of this kind of elements on device
+    dev, of this shape (none given: any shape but an empty one)."""
     if t is None:
         raise LucetreeError(f"{name} is required")
-    if t.dtype not in dtypes or (shape is not None and t.shape != shape):
-        _expect(t, name, t.shape if shape is None else shape, dtypes)
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, name, dev)
-    return t.data_ptr()
-
-
-def _refuse(t, name: str, dev: int):
+    dtypes = _KINDS[kind]
+    if (dtypes is not None and t.dtype not in dtypes) or (shape and t.shape != shape):
+        _expect(t, name, shape or tuple(t.shape), dtypes or (t.dtype,))
+    if not shape and t.numel() < 1:
+        raise LucetreeError(f"{name}: expected a tensor that is not empty")
     if t.get_device() != dev:
         raise LucetreeError(f"{name}: lucetree takes tensors of the current device, cuda:{dev}, got {t.device}")
-    raise LucetreeError(f"{name}: lucetree takes contiguous tensors")
-
-
-def _any(t, name: str, dev: int) -> int:
-    """Address of a contiguous tensor of any shape and type on device dev."""
-    if t is None:
-        raise LucetreeError(f"{name} is required")
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, name, dev)
+    if not t.is_contiguous():
+        raise LucetreeError(f"{name}: lucetree takes contiguous tensors")
     return t.data_ptr()
 
 
-def _status_arg(t, dev: int) -> int:
-    if t is None or t.dtype not in _W32 or t.numel() < 1:
-        _expect_status(t)
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, "status", dev)
-    return t.data_ptr()
+def _load_marshal():
+    """_arg in one C call (binding/marshal.cpp), if it was built for this torch."""
+    path = os.path.join(_PKG, "_marshal.so")
+    if not os.path.exists(path):
+        return _arg
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(m)
+    except ImportError:  # built for another torch or machine
+        return _arg
+    if m.torch_version != torch.__version__:
+        return _arg
+    mask = lambda dtypes: sum(1 << m.type_of(torch.empty(0, dtype=d)) for d in dtypes or ())  # noqa: E731
+    m.set_slow(_arg, [mask(k) for k in _KINDS])
+    return m.arg
+
+
+_arg_slow = _arg
+_arg = _load_marshal()
 
 
 # the raw handle of a device's current stream, without the Stream object around it
@@ -490,20 +502,20 @@ def lucetree_verify_attn_win(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_t
     B, N, Hq, D = _dims(q, "q", 4)
     P, Hkv, page, _ = _dims(k_pool, "k_pool", 4)
     maxp = _dims(page_table, "page_table", 2)[1]
-    kind = (q.dtype,)
     code = dtype_code(q)
-    pool, tree = (P, Hkv, page, D), (B, N, Hkv, D)
-    out_at = _arg(out, "out", (B, N, Hq, D), _F32 + kind, dev)
+    kind = _K_BF16 if code == LUCETREE_BF16 else _K_F16
+    out_f32 = out is not None and out.dtype == torch.float32
     args = _WIN_ARGS.pack(
         code, B, N, Hq, Hkv, D, page, float(D) ** -0.5 if scale is None else float(scale),
-        _any(q, "q", dev), _arg(k_pool, "k_pool", pool, kind, dev), _arg(v_pool, "v_pool", pool, kind, dev), P,
-        _arg(page_table, "page_table", (B, maxp), _I32, dev), maxp, _arg(ctx_len, "ctx_len", (B,), _I32, dev),
-        _arg(k_tree, "k_tree", tree, kind, dev), _arg(v_tree, "v_tree", tree, kind, dev),
-        _arg(anc_mask, "anc_mask", (B, N), _W64, dev), 0,
-        0 if lse is None else _arg(lse, "lse", (B, N, Hq), _F32, dev), _status_arg(status, dev),
-        _i32(window, "window", 1), _i32(sinks, "sinks"), LUCETREE_F32 if out.dtype == torch.float32 else code, out_at)
-    ws = _any(workspace, "workspace", dev)
-    _check(load().lucetree_verify_attn_win(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
+        _arg(q, "q", kind, dev, B, N, Hq, D), _arg(k_pool, "k_pool", kind, dev, P, Hkv, page, D),
+        _arg(v_pool, "v_pool", kind, dev, P, Hkv, page, D), P, _arg(page_table, "page_table", _K_I32, dev, B, maxp), maxp,
+        _arg(ctx_len, "ctx_len", _K_I32, dev, B), _arg(k_tree, "k_tree", kind, dev, B, N, Hkv, D),
+        _arg(v_tree, "v_tree", kind, dev, B, N, Hkv, D), _arg(anc_mask, "anc_mask", _K_W64, dev, B, N), 0,
+        0 if lse is None else _arg(lse, "lse", _K_F32, dev, B, N, Hq), _arg(status, "status", _K_W32, dev),
+        _i32(window, "window", 1), _i32(sinks, "sinks"), LUCETREE_F32 if out_f32 else code,
+        _arg(out, "out", _K_F32 if out_f32 else kind, dev, B, N, Hq, D))
+    _check(load().lucetree_verify_attn_win(args, _arg(workspace, "workspace", _K_ANY, dev), workspace.nbytes,
+                                           _raw_stream(stream, dev)))
 
 
 def lucetree_verify_attn_kq_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
@@ -887,15 +899,14 @@ def lucetree_beam_select(logits, cum, finished, eos: int, out_score, out_token, 
     dev = _device()
     if logits.get_device() != dev:
         raise LucetreeError(f"logits: lucetree takes tensors of the current device, cuda:{dev}, got {logits.device}")
-    old, new = (B, K), (B, Kout)
     args = _BEAM_ARGS.pack(
         LUCETREE_F32 if logits.dtype == torch.float32 else dtype_code(logits), B, K, Kout, V, stride, logits.data_ptr(),
-        _arg(cum, "cum", old, _F32, dev), 0 if finished is None else _arg(finished, "finished", old, _I32, dev), int(eos),
-        _arg(out_score, "out_score", new, _F32, dev), _arg(out_token, "out_token", new, _I32, dev),
-        _arg(out_row, "out_row", new, _I32, dev),
-        0 if out_finished is None else _arg(out_finished, "out_finished", new, _I32, dev))
-    ws = _any(workspace, "workspace", dev)
-    _check(load().lucetree_beam_select(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
+        _arg(cum, "cum", _K_F32, dev, B, K), 0 if finished is None else _arg(finished, "finished", _K_I32, dev, B, K),
+        int(eos), _arg(out_score, "out_score", _K_F32, dev, B, Kout), _arg(out_token, "out_token", _K_I32, dev, B, Kout),
+        _arg(out_row, "out_row", _K_I32, dev, B, Kout),
+        0 if out_finished is None else _arg(out_finished, "out_finished", _K_I32, dev, B, Kout))
+    _check(load().lucetree_beam_select(args, _arg(workspace, "workspace", _K_ANY, dev), workspace.nbytes,
+                                       _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- page tables, counts and copies
@@ -920,14 +931,13 @@ def lucetree_reorder_pages(table_in, ctx_in, src, reserve: int, ref_in, table_ou
     pages = _dims(ref_in, "ref_in", 1)[0]
     dev = _device()
     args = _REORDER_ARGS.pack(
-        _arg(table_in, "table_in", (rows_in, P), _I32, dev), _arg(ctx_in, "ctx_in", (rows_in,), _I32, dev), rows_in,
-        _arg(src, "src", (rows,), _I32, dev), rows, P, _i32(reserve, "reserve"),
-        _arg(ref_in, "ref_in", (pages,), _I32, dev), pages, _arg(table_out, "table_out", (rows, P), _I32, dev),
-        _arg(ctx_out, "ctx_out", (rows,), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
-        _arg(copy_src, "copy_src", (rows,), _I32, dev), _arg(copy_dst, "copy_dst", (rows,), _I32, dev),
-        _status_arg(status, dev))
-    ws = _any(workspace, "workspace", dev)
-    _check(load().lucetree_reorder_pages(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
+        _arg(table_in, "table_in", _K_I32, dev, rows_in, P), _arg(ctx_in, "ctx_in", _K_I32, dev, rows_in), rows_in,
+        _arg(src, "src", _K_I32, dev, rows), rows, P, _i32(reserve, "reserve"), _arg(ref_in, "ref_in", _K_I32, dev, pages),
+        pages, _arg(table_out, "table_out", _K_I32, dev, rows, P), _arg(ctx_out, "ctx_out", _K_I32, dev, rows),
+        _arg(ref_out, "ref_out", _K_I32, dev, pages), _arg(copy_src, "copy_src", _K_I32, dev, rows),
+        _arg(copy_dst, "copy_dst", _K_I32, dev, rows), _arg(status, "status", _K_W32, dev))
+    _check(load().lucetree_reorder_pages(args, _arg(workspace, "workspace", _K_ANY, dev), workspace.nbytes,
+                                         _raw_stream(stream, dev)))
 
 
 def lucetree_trim_pages(table_in, ctx_len, window: int, sinks: int, ref_in, table_out, ref_out, status, stream=None):
@@ -938,10 +948,10 @@ def lucetree_trim_pages(table_in, ctx_len, window: int, sinks: int, ref_in, tabl
     pages = _dims(ref_in, "ref_in", 1)[0]
     dev = _device()
     args = _TRIM_ARGS.pack(
-        _arg(table_in, "table_in", (rows, P), _I32, dev), _arg(ctx_len, "ctx_len", (rows,), _I32, dev), rows, P,
-        _i32(window, "window", 1), _i32(sinks, "sinks"), _arg(ref_in, "ref_in", (pages,), _I32, dev), pages,
-        _arg(table_out, "table_out", (rows, P), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
-        _status_arg(status, dev))
+        _arg(table_in, "table_in", _K_I32, dev, rows, P), _arg(ctx_len, "ctx_len", _K_I32, dev, rows), rows, P,
+        _i32(window, "window", 1), _i32(sinks, "sinks"), _arg(ref_in, "ref_in", _K_I32, dev, pages), pages,
+        _arg(table_out, "table_out", _K_I32, dev, rows, P), _arg(ref_out, "ref_out", _K_I32, dev, pages),
+        _arg(status, "status", _K_W32, dev))
     _check(load().lucetree_trim_pages(args, _raw_stream(stream, dev)))
 
 
@@ -960,14 +970,14 @@ def lucetree_compact_pages(table_in, ref_in, table_out, ref_out, copy_src, copy_
     rows, P = _dims(table_in, "table_in", 2)
     pages = _dims(ref_in, "ref_in", 1)[0]
     dev = _device()
-    half = (pages // 2,)
+    half = pages // 2
     args = _COMPACT_ARGS.pack(
-        _arg(table_in, "table_in", (rows, P), _I32, dev), rows, P, _arg(ref_in, "ref_in", (pages,), _I32, dev), pages,
-        _arg(table_out, "table_out", (rows, P), _I32, dev), _arg(ref_out, "ref_out", (pages,), _I32, dev),
-        _arg(copy_src, "copy_src", half, _I32, dev), _arg(copy_dst, "copy_dst", half, _I32, dev),
-        _arg(copy_n, "copy_n", (1,), _I32, dev), _arg(live, "live", (1,), _I32, dev), _status_arg(status, dev))
-    ws = _any(workspace, "workspace", dev)
-    _check(load().lucetree_compact_pages(args, ws, workspace.nbytes, _raw_stream(stream, dev)))
+        _arg(table_in, "table_in", _K_I32, dev, rows, P), rows, P, _arg(ref_in, "ref_in", _K_I32, dev, pages), pages,
+        _arg(table_out, "table_out", _K_I32, dev, rows, P), _arg(ref_out, "ref_out", _K_I32, dev, pages),
+        _arg(copy_src, "copy_src", _K_I32, dev, half), _arg(copy_dst, "copy_dst", _K_I32, dev, half),
+        _arg(copy_n, "copy_n", _K_I32, dev, 1), _arg(live, "live", _K_I32, dev, 1), _arg(status, "status", _K_W32, dev))
+    _check(load().lucetree_compact_pages(args, _arg(workspace, "workspace", _K_ANY, dev), workspace.nbytes,
+                                         _raw_stream(stream, dev)))
 
 
 def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=None):
@@ -982,10 +992,10 @@ def lucetree_copy_pages(src, dst, k_pool, v_pool, status, count=None, stream=Non
         raise LucetreeError(f"v_pool: expected a pool of {pages} pages, got shape {tuple(v_pool.shape)}")
     dev = _device()
     args = _COPY_PAGES_ARGS.pack(
-        _arg(src, "src", (n,), _I32, dev), _arg(dst, "dst", (n,), _I32, dev), n,
-        0 if count is None else _arg(count, "count", (1,), _I32, dev), _any(k_pool, "k_pool", dev),
-        0 if v_pool is None else _any(v_pool, "v_pool", dev), k_pool.numel() // pages * k_pool.element_size(),
-        0 if v_pool is None else v_pool.numel() // pages * v_pool.element_size(), pages, _status_arg(status, dev))
+        _arg(src, "src", _K_I32, dev, n), _arg(dst, "dst", _K_I32, dev, n), n,
+        0 if count is None else _arg(count, "count", _K_I32, dev, 1), _arg(k_pool, "k_pool", _K_ANY, dev),
+        0 if v_pool is None else _arg(v_pool, "v_pool", _K_ANY, dev), k_pool.nbytes // pages,
+        0 if v_pool is None else v_pool.nbytes // pages, pages, _arg(status, "status", _K_W32, dev))
     _check(load().lucetree_copy_pages(args, _raw_stream(stream, dev)))
 
 
@@ -995,12 +1005,13 @@ def lucetree_reorder_states(state_in, src, state_out, status, stream=None):
     rows = _dims(src, "src", 1)[0]
     if state_in is None or state_in.dim() < 2 or state_in.shape[0] < 1:
         raise LucetreeError("state_in: expected states [rows][...]")
-    shape, kind = state_in.shape, (state_in.dtype,)
+    shape = state_in.shape
+    if state_out is None or state_out.dtype != state_in.dtype:
+        _expect(state_out, "state_out", (rows, *shape[1:]), (state_in.dtype,))
     dev = _device()
     args = _REORDER_STATES_ARGS.pack(
-        _any(state_in, "state_in", dev), _arg(state_out, "state_out", (rows, *shape[1:]), kind, dev),
-        _arg(src, "src", (rows,), _I32, dev), shape[0], rows, state_in.numel() // shape[0] * state_in.element_size(),
-        _status_arg(status, dev))
+        _arg(state_in, "state_in", _K_ANY, dev), _arg(state_out, "state_out", _K_ANY, dev, rows, *shape[1:]),
+        _arg(src, "src", _K_I32, dev, rows), shape[0], rows, state_in.nbytes // shape[0], _arg(status, "status", _K_W32, dev))
     _check(load().lucetree_reorder_states(args, _raw_stream(stream, dev)))
 
 
