@@ -13,11 +13,13 @@
 // Keys are 64-bit integers whose order is (logit descending, index ascending),
 // lists of 32 lie across a warp's lanes, and sorts and merges are bitonic
 // networks of shuffles.
-// Launch 2, one CTA per request, merges the chunks' lists and sums row by row,
-// turns the rows' lists into scores in 64 bits (neighbouring candidates of
-// different rows are closer than fp32 keeps beside a long sum) and merges those.
-// 8 requests of 8 beams over 151,936 fp32 logits (39 MB): 17.9 us, 2.2 TB/s; 32 of
-// bf16 logits, a quarter of the beams finished: 27.5 us.  Bound by the fixed part
+// Launch 2, one CTA per request, adds the chunks' sums up row by row, turns the
+// chunks' lists into scores of some 48 bits (neighbouring candidates of different
+// rows are closer than fp32 keeps beside a long sum) and takes the best: 2.7 us from
+// the last chunk's end, of which 0.6 are the wait itself and 0.9 the loads (merging sorted
+// lists by bitonic networks with fp64 scores: 5.5).
+// 8 requests of 8 beams over 151,936 fp32 logits (39 MB): 16.0 us, 2.4 TB/s; 32 of
+// bf16 logits, a quarter of the beams finished: 23.9 us.  Bound by the fixed part
 // of a chunk (its sorts start when the stream ends: all CTAs run in one wave) and the
 // second launch; smaller chunks cost more (8 CTAs per SM: 27 us).
 #include <type_traits>
@@ -34,6 +36,7 @@ typedef unsigned long long u64;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;
+constexpr int kMergeThreads = 256;  // as many registers as a CTA of the scan: it fits where one is free
 constexpr int kU = 8;  // 16-byte loads in flight per thread
 
 struct BeamLaunch {
@@ -352,147 +355,248 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     }
 }
 
-// A candidate of the request: score as an ordered integer, then beam * vocab + token.
-struct Cand {
-    u64 score;
-    unsigned index;
-};
-__device__ inline bool better(const Cand& p, const Cand& q) {
-    return p.score > q.score || (p.score == q.score && p.index < q.index);
-}
-__device__ inline Cand shfl_xor(const Cand& c, int stride) {
-    return Cand{__shfl_xor_sync(0xffffffffu, c.score, stride), __shfl_xor_sync(0xffffffffu, c.index, stride)};
-}
-__device__ inline Cand exchange(const Cand& c, int stride, bool keep_best) {
-    const Cand o = shfl_xor(c, stride);
-    return better(c, o) == keep_best ? c : o;
-}
-__device__ inline Cand sort32(Cand c) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int stride = size >> 1; stride > 0; stride >>= 1)
-            c = exchange(c, stride, ((lane & stride) == 0) == ((lane & size) == 0));
-    return c;
-}
-__device__ inline Cand merge32(const Cand& a, const Cand& b) {
-    const int lane = threadIdx.x & 31;
-    const Cand r{__shfl_sync(0xffffffffu, b.score, 31 - lane), __shfl_sync(0xffffffffu, b.index, 31 - lane)};
-    Cand c = better(a, r) ? a : r;
-#pragma unroll
-    for (int stride = 16; stride > 0; stride >>= 1) c = exchange(c, stride, (lane & stride) == 0);
-    return c;
+// A float as an ordered integer.
+__device__ inline unsigned order_float(float x) {
+    const unsigned u = __float_as_uint(x == 0.f ? 0.f : x);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ inline u64 order_double(double x) {
-    if (x == 0.0) x = 0.0;
-    const u64 u = (u64)__double_as_longlong(x);
-    return (u >> 63) ? ~u : (u | (1ull << 63));
-}
-__device__ inline double order_value(u64 u) {
-    return __longlong_as_double((long long)((u >> 63) ? u & ~(1ull << 63) : ~u));
+// x + y as a float and its rounding error (Knuth's two-sum).
+__device__ inline float2 two_sum(float x, float y) {
+    const float s = __fadd_rn(x, y), z = __fsub_rn(s, x);
+    return make_float2(s, __fadd_rn(__fsub_rn(x, __fsub_rn(s, z)), __fsub_rn(y, z)));
 }
 
-// log(s) of a positive s to about 2^-24 absolute, nearly without fp64 (whose rate here is
-// 1/64): s = 2^k f with f in [3/4, 3/2), and the logarithm of f, at most 0.41, in fp32.
-__device__ inline double log_of(double s) {
+// Scores are sums of two floats, some 48 bits (neighbouring candidates of different
+// rows are closer than fp32 keeps beside a long sum; fp64 runs at 1/64 of its rate),
+// and a quarter of their value, so that three finite terms cannot overflow.
+constexpr float kQuarter = 0.25f;
+
+// A quarter of m + log(s): s = 2^k f with f in [3/4, 3/2), the logarithm of f, at most 0.41,
+// in fp32 and k log 2 in two parts, of which the first has 16 bits (Cody and Waite).
+__device__ inline float2 quarter_lse(float m, float s) {
     int k;
-    float f = frexpf((float)s, &k);  // in [1/2, 1)
+    float f = frexpf(s, &k);  // in [1/2, 1)
     if (f < 0.75f) {
         f *= 2.f;
         --k;
     }
-    return 0.6931471805599453 * k + (double)log1pf(f - 1.f);
+    constexpr float kHigh = 45426.f / 65536.f, kLow = (float)(0.6931471805599453 - 45426.0 / 65536.0);
+    const float2 t = two_sum(m * kQuarter, kQuarter * (kHigh * k));
+    const float low = kQuarter * fmaf(kLow, (float)k, log1pf(f - 1.f));
+    const float2 u = two_sum(t.x, low);
+    return two_sum(u.x, u.y + t.y);
 }
 
-// One CTA of kMergeWarps warps for a request of no more beams than that.
-template <int kMergeWarps>
-__global__ void __launch_bounds__(32 * kMergeWarps) beam_merge_kernel(BeamLaunch L) {
-    __shared__ u64 s_keys[kMergeWarps][32];
-    __shared__ Cand s_cand[kMergeWarps][32];
-    __shared__ double s_lse[kMergeWarps];
+// A candidate of the request: its score as an ordered integer, and beam * vocab + token.
+struct Cand {
+    u64 score;
+    unsigned index;
+};
+constexpr u64 kNoScore = 0;  // of no candidate; below that of -inf
+
+// (no branches)
+__device__ inline bool better(const Cand& p, const Cand& q) {
+    return (p.score > q.score) | ((p.score == q.score) & (p.index < q.index));
+}
+__device__ inline Cand better_of(const Cand& p, const Cand& q) { return better(q, p) ? q : p; }
+__device__ inline Cand shfl_xor(const Cand& c, int o) {
+    return Cand{__shfl_xor_sync(0xffffffffu, c.score, o), __shfl_xor_sync(0xffffffffu, c.index, o)};
+}
+__device__ inline u64 order_score(float2 x) { return ((u64)order_float(x.x) << 32) | order_float(x.y); }
+__device__ inline float score_value(u64 score) {
+    const unsigned u = (unsigned)(score >> 32);
+    return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u) * (1.f / kQuarter);
+}
+
+// One CTA per request.  A list of Kout keys lies across `width` lanes (a power of two),
+// every eighth list in the same warp, so that the good ones are spread over the
+// warps.  The Kout-th best of 32 candidates, the first ones of lists, is no better
+// than the Kout-th best of all: what is behind it drops out, and the few that are left
+// (some 20 of 576 for eight beams of nine chunks) are ranked by counting.
+// The steps run over nothing while the scan is still at work: a cold instruction cache
+// costs more than the work itself.  First each in a warp of its own: behind the scan's
+// loads one miss after the other would take longer than the scan (up to 14 us).
+__global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(BeamLaunch L) {
+    constexpr int kMergeWarps = kMergeThreads / 32;
+    constexpr int kLeft = kMergeThreads;  // candidates that are ranked by counting
+    constexpr int kHold = 4;              // lists of a lane that are loaded at once and kept
+    static_assert(kMergeWarps * 4 == 32, "four candidates of each warp are compared");
+    enum { kLive, kEnded, kDead };
+    __shared__ Cand s_first[32], s_left[kLeft], s_limit;
+    __shared__ float2 s_lse[LUCETREE_MAX_BEAMS];
+    __shared__ float s_cum[LUCETREE_MAX_BEAMS];
+    __shared__ int s_state[LUCETREE_MAX_BEAMS];
+    __shared__ int s_n;
     const lucetree_beam_args& a = L.a;
-    pdl_wait();
-    if (threadIdx.x == 0) pdl_trigger();
-    const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int K = a.beams_in;
-    // `per` warps to a row merge its chunks' lists
-    const int per = kMergeWarps / K;
-    const int k = warp / per, w = warp % per;
-    const int row = b * K + k;
-    const bool mine = k < K;
-    const bool ended = mine && row_ended(a, row);
-    const bool dead = mine && !ended && a.cum[row] == -INFINITY;
-    u64 list = 0;
-    if (mine && !ended && !dead) {
-        const u64* keys = L.keys + (size_t)row * L.chunks * 32;
-        for (int c = w; c < L.chunks; c += 4 * per) {
-            u64 next[4];
+    const int b = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int K = a.beams_in, Kout = a.beams_out, chunks = L.chunks;
+    const int width = 1 << (32 - __clz(Kout - 1));  // (1 for Kout = 1)
+    const int j = lane & (width - 1);
+    const int lists = K * chunks, per_pass = kMergeThreads / width;
+    const int first_list = j < Kout ? (lane / width) * kMergeWarps + warp : lists;
+    const u64* keys = L.keys + (size_t)b * lists * 32 + j;
+    int beam[kHold];  // of the lane's first lists
 #pragma unroll
-            for (int x = 0; x < 4; ++x) next[x] = c + x * per < L.chunks ? keys[(size_t)(c + x * per) * 32 + lane] : 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (c + x * per < L.chunks) list = merge32(list, next[x]);
+    for (int x = 0; x < kHold; ++x) beam[x] = min(first_list + x * per_pass, lists - 1) / chunks;
+    // (the inputs are those that the scan has waited for)
+    const float cum_t = t < K ? a.cum[b * K + t] : 0.f;
+    const bool ended_t = t < K && row_ended(a, b * K + t);
+
+    auto key_of = [&](int l, int k) -> u64 { return l < lists && s_state[k] == kLive ? keys[(size_t)l * 32] : 0; };
+    auto cand_of = [&](int l, int k, u64 key) -> Cand {
+        if (l >= lists) return Cand{kNoScore, ~0u};
+        const float2 lse = s_lse[k];
+        const float cum = s_cum[k] * kQuarter, x = key_value(key) * kQuarter;
+        const float2 d = two_sum(x, -lse.x), e = two_sum(d.x, cum);
+        float2 score = two_sum(e.x, (d.y + e.y) - lse.y);
+        int token = (int)key_index(key);
+        bool have = key != 0;
+        if (!(x > -INFINITY)) score = make_float2(-INFINITY, 0.f);
+        if (s_state[k] != kLive || !(lse.x > -INFINITY)) {
+            // the row's tokens in order, all at -inf, but after the one candidate of a beam that has ended
+            const bool one = s_state[k] == kEnded && a.eos >= 0 && a.eos < a.vocab;
+            have = l == k * chunks && j < a.vocab;
+            token = one ? (j == 0 ? a.eos : (j - 1 < a.eos ? j - 1 : j)) : j;
+            score = make_float2(one && j == 0 ? cum : -INFINITY, 0.f);
         }
-    }
-    s_keys[warp][lane] = list;
-    if (mine && !ended && !dead && w == per - 1) {
-        // log-sum-exp of the row from its chunks
-        const float2* sums = L.sums + (size_t)row * L.chunks;
-        float m = -INFINITY;
-        for (int c = lane; c < L.chunks; c += 32) m = fmaxf(m, sums[c].x);
+        return have ? Cand{order_score(score), (unsigned)k * (unsigned)a.vocab + (unsigned)token} : Cand{kNoScore, ~0u};
+    };
+    auto write = [&](bool warm, int at, const Cand& c) {
+        const int beam = (int)(c.index / (unsigned)a.vocab), token = (int)(c.index % (unsigned)a.vocab);
+        const size_t o = (size_t)b * Kout + at;
+        const float score = score_value(c.score);
+        if (warm) return;
+        a.out_score[o] = score;
+        a.out_token[o] = token;
+        a.out_row[o] = b * K + beam;
+        if (a.out_finished) a.out_finished[o] = (s_state[beam] == kEnded || token == a.eos) ? 1 : 0;
+    };
+
+#pragma unroll 1
+    for (int warm = 2; warm >= 0; --warm) {
+        auto mine = [&](int w) { return warm < 2 || warp == w; };
+        u64 key[kHold];
+        if (!warm) {
+            if (t < K) {
+                s_cum[t] = cum_t;
+                s_state[t] = ended_t ? kEnded : cum_t == -INFINITY ? kDead : kLive;
+            }
+            __syncthreads();
+            pdl_wait();
+            if (t == 0) {
+                pdl_trigger();
+                s_n = 0;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        double s = 0.0;
-        for (int c = lane; c < L.chunks; c += 32)
-            if (sums[c].x > -INFINITY) s += (double)(sums[c].y * exp_diff(sums[c].x, m));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) s_lse[k] = m > -INFINITY ? (double)m + log_of(s) : -INFINITY;
-    }
-    __syncthreads();
-    Cand cand{0, ~0u};  // none: behind every candidate
-    if (mine && w == 0) {
-        for (int o = 1; o < per; ++o) list = merge32(list, s_keys[warp + o][lane]);
-        const float cum = a.cum[row];
-        int token = lane;
-        double score = -INFINITY;
-        bool have = lane < a.vocab;
-        if (ended) {
-            // one candidate, then the other tokens in order at -inf
-            const bool eos = a.eos >= 0 && a.eos < a.vocab;
-            if (eos) token = lane == 0 ? a.eos : (lane - 1 < a.eos ? lane - 1 : lane);
-            if (eos && lane == 0) score = cum;
-        } else if (!dead) {
-            const double lse = s_lse[k];
-            if (lse > -INFINITY) {
-                have = list != 0;
-                token = have ? (int)key_index(list) : 0;
-                const float x = key_value(list);
-                if (have && x > -INFINITY) score = (double)cum + ((double)x - lse);
-                if (!(score == score)) score = -INFINITY;
+            for (int x = 0; x < kHold; ++x) key[x] = key_of(first_list + x * per_pass, beam[x]);
+        }
+        // log-sum-exp of the rows from their chunks
+        if (mine(0)) {
+#pragma unroll 1
+            for (int k = warp; k < K; k += kMergeWarps) {
+                const float2* sums = L.sums + (size_t)(b * K + k) * chunks;
+                if (!warm && s_state[k] != kLive) continue;
+                float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+                for (int c = lane; c < chunks; c += 32) {
+                    const float2 x = warm ? make_float2(0.f, 1.f) : sums[c];
+                    add_sums(m, s, x.x, x.y);
+                }
+                warp_sums(m, s);
+                const float2 lse = m > -INFINITY ? quarter_lse(m, s) : make_float2(-INFINITY, 0.f);
+                if (lane == 0) s_lse[k] = lse;
             }
         }
-        if (have) cand = Cand{order_double(score), (unsigned)k * (unsigned)a.vocab + (unsigned)token};
-        // scores follow the logits' order, but ties of rounded scores and -inf follow the index
-        const Cand next{__shfl_down_sync(0xffffffffu, cand.score, 1), __shfl_down_sync(0xffffffffu, cand.index, 1)};
-        if (__any_sync(0xffffffffu, lane < 31 && better(next, cand))) cand = sort32(cand);
-    }
-    if (mine && w == 0) s_cand[k][lane] = cand;
-    for (int half = kMergeWarps / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        if (warp < half && warp + half < K) s_cand[warp][lane] = merge32(s_cand[warp][lane], s_cand[warp + half][lane]);
-    }
-    if (warp == 0 && lane < a.beams_out) {
-        Cand c = s_cand[0][lane];
-        if (c.index >= (unsigned)K * (unsigned)a.vocab) c = Cand{order_double(-INFINITY), 0};  // only after NaN logits
-        const int beam = (int)(c.index / (unsigned)a.vocab), token = (int)(c.index % (unsigned)a.vocab);
-        const size_t at = (size_t)b * a.beams_out + lane;
-        a.out_score[at] = (float)order_value(c.score);
-        a.out_token[at] = token;
-        a.out_row[at] = b * K + beam;
-        if (a.out_finished) a.out_finished[at] = (row_ended(a, b * K + beam) || token == a.eos) ? 1 : 0;
+        if (!warm) __syncthreads();
+        // the best candidate of every lane, and of the lists that share a lane's eighth
+        Cand c[kHold];
+        if (mine(1)) {
+            Cand top{kNoScore, ~0u};
+#pragma unroll
+            for (int x = 0; x < kHold; ++x) {
+                c[x] = cand_of(first_list + x * per_pass, beam[x], warm ? (u64)t << 32 : key[x]);
+                top = better_of(top, c[x]);
+            }
+#pragma unroll 1
+            for (int l = first_list + kHold * per_pass; l < lists && !warm; l += per_pass)
+                top = better_of(top, cand_of(l, l / chunks, key_of(l, l / chunks)));
+            __syncwarp();
+#pragma unroll 1
+            for (int o = width; o < 8; o <<= 1) top = better_of(top, shfl_xor(top, o));
+            const int group = width > 8 ? width : 8;  // lanes of which the first eighth is taken
+            if ((lane & (group - 1)) < group / 8)
+                s_first[warp * 4 + (lane / group) * (group / 8) + (lane & (group - 1))] = top;
+        }
+        if (!warm) __syncthreads();
+        if (mine(2)) {
+            const Cand one = s_first[lane];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int i = warp * 4 + x;
+                const Cand d = s_first[i];
+                // (several may be no candidate)
+                const bool ahead = better(one, d) | ((one.score == d.score) & (one.index == d.index) & (lane < i));
+                if (__popc(__ballot_sync(0xffffffffu, ahead)) == Kout - 1 && lane == 0) s_limit = d;
+            }
+        }
+        if (!warm) __syncthreads();
+        if (mine(3)) {
+            const Cand limit = s_limit;
+            auto keep = [&](const Cand& c) {
+                if ((c.score == kNoScore) | better(limit, c)) return;
+                const unsigned at = warm ? t : atomicAdd(&s_n, 1);  // (any order: they are ranked)
+                if (at < kLeft) s_left[at] = c;
+            };
+#pragma unroll
+            for (int x = 0; x < kHold; ++x) keep(warm ? Cand{limit.score | 1, 0} : c[x]);
+#pragma unroll 1
+            for (int l = first_list + kHold * per_pass; l < lists && !warm; l += per_pass)
+                keep(cand_of(l, l / chunks, key_of(l, l / chunks)));
+        }
+        if (!warm) __syncthreads();
+        const int n = warm ? 32 : s_n;
+        if (n <= kLeft) {
+            if (mine(4)) {
+                // lane x of a warp ends up with the rank of its x-th candidate
+                const Cand none{kNoScore, ~0u};
+                const Cand d0 = lane < n ? s_left[lane] : none, d1 = lane + 32 < n ? s_left[lane + 32] : none;
+                int rank = Kout;
+#pragma unroll 2
+                for (int i = warp, x = 0; i < n; i += kMergeWarps, ++x) {
+                    const Cand d = s_left[i];
+                    int ahead = __popc(__ballot_sync(0xffffffffu, better(d0, d))) + __popc(__ballot_sync(0xffffffffu, better(d1, d)));
+#pragma unroll 1
+                    for (int g = 64; g < n; g += 32)
+                        ahead += __popc(__ballot_sync(0xffffffffu, g + lane < n && better(s_left[g + lane], d)));
+                    if (lane == x) rank = ahead;
+                }
+                if (rank < Kout) write(warm, rank, s_left[warp + kMergeWarps * lane]);
+                // (there are fewer than Kout candidates only after NaN logits)
+                if (t >= n && t < Kout) write(warm, t, Cand{order_score(make_float2(-INFINITY, 0.f)), 0});
+            }
+        } else {
+            // The good candidates share a few warps: one best after the other.
+            Cand last{~0ull, 0};
+#pragma unroll 1
+            for (int r = 0; r < Kout; ++r) {
+                Cand best{kNoScore, ~0u};
+#pragma unroll 1
+                for (int l = first_list; l < lists; l += per_pass) {
+                    const Cand c = cand_of(l, l / chunks, key_of(l, l / chunks));
+                    if (better(last, c)) best = better_of(best, c);
+                }
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) best = better_of(best, shfl_xor(best, o));
+                if (lane == 0) s_first[warp] = best;
+                __syncthreads();
+#pragma unroll 1
+                for (int w = 0; w < kMergeWarps; ++w) best = better_of(best, s_first[w]);
+                if (t == 0) write(false, r, best);
+                last = best;
+                __syncthreads();
+            }
+        }
     }
 }
 
@@ -536,9 +640,7 @@ cudaError_t launch_beam_select(const lucetree_beam_args& a, void* workspace, int
     else if (a.dtype == LUCETREE_BF16) e = launch_scan<__nv_bfloat16>(L, aligned, grid, stream);
     else e = launch_scan<__half>(L, aligned, grid, stream);
     if (e != cudaSuccess) return e;
-    // (16 warps against 32: 17.9 and 18.9 us for 8 requests of 8 beams, 27.5 and 27.8 for 32)
-    if (a.beams_in <= 16) return launch_pdl(beam_merge_kernel<16>, dim3(a.batch), dim3(512), 0, stream, L);
-    return launch_pdl(beam_merge_kernel<32>, dim3(a.batch), dim3(1024), 0, stream, L);
+    return launch_pdl(beam_merge_kernel, dim3(a.batch), dim3(kMergeThreads), 0, stream, L);
 }
 
 }  // namespace lucetree

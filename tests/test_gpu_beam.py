@@ -212,3 +212,30 @@ def test_captured_replayed_and_two_streams_at_once(cuda_dev):
         graph.replay()
         torch.cuda.synchronize()
         assert np.array_equal(outs[0][1].cpu().numpy(), want[i][1])
+
+
+@pytest.mark.parametrize("step,K,Kout", [(8, 32, 32), (8, 16, 32), (4, 32, 17), (1, 32, 32)])
+def test_good_candidates_crowded_into_some_chunks(cuda_dev, step, K, Kout):
+    """Every `step`-th chunk of a request holds all its good candidates, more than Kout each."""
+    V, sms = 50000, torch.cuda.get_device_properties(0).multi_processor_count
+    chunks = max(1, 4 * sms // K)  # (other cuts are no less right, only easier)
+    logits, cum = draw(1, K, V, "f32", 41)
+    g = torch.Generator().manual_seed(42)
+    for i in range(0, K * chunks, step):
+        k, first = divmod(i, chunks)
+        first = V // 4 * first // chunks * 4 + 8
+        logits[0, k, first:first + 120:3] = 40 + 5 * torch.rand(40, generator=g)
+    check(logits, cum, None, -1, Kout)
+
+
+@pytest.mark.parametrize("Kout", [1, 2, 3, 4, 9, 16])
+def test_one_beam_far_ahead(cuda_dev, Kout):
+    """All candidates come from one row."""
+    logits, cum = draw(3, 6, 20000, "bf16", 43)
+    cum[:, 4] += 1000
+    check(logits, cum, None, -1, Kout)
+
+
+def test_equal_scores_everywhere(cuda_dev):
+    """One value in every row: the order is that of beams and tokens alone."""
+    check(torch.full((2, 8, 9000), 0.5), torch.full((2, 8), -1.0), None, -1, 32)
