@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     const u64 limit = __shfl_sync(0xffffffffu, threads, a.beams_out - 1);  // 0: fewer threads than that have a vector
     // A warp goes through one thread's vectors at a time; keys that count wait in shared
     // memory until 32 of them are sorted and merged into the warp's list.  Most
-    // warps never have 32: what is left over is put together and sorted by one warp.
+    // warps never have 32: what is left over is put together and ranked.
     u64 list = 0;
     int waiting = 0;
     bool listed = false;
@@ -337,21 +337,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     u64* all = &s_list[0][0];  // fewer than 32 keys of each warp
     if (lane < waiting) all[at + lane] = s_buf[warp][lane];
     __syncthreads();
-    if (warp == 0) {
-        for (int g = 0; g < left; g += 32) list = merge32(list, sort32(g + lane < left ? all[g + lane] : 0));
+    const size_t place = (size_t)row * L.chunks + chunk;
+    u64* out = L.keys + place * 32;
+    if (!any_listed && left <= 64) {
+        const u64 k0 = lane < left ? all[lane] : 0, k1 = lane + 32 < left ? all[lane + 32] : 0;
+#pragma unroll 1
+        for (int i = warp; i < left; i += kWarps) {
+            const u64 d = all[i];
+            const int ahead = __popc(__ballot_sync(0xffffffffu, k0 > d)) + __popc(__ballot_sync(0xffffffffu, k1 > d));
+            if (lane == 0 && ahead < a.beams_out) out[ahead] = d;
+        }
+        if (t >= left && t < a.beams_out) out[t] = 0;
+    } else {
+        if (warp == 0) {
+#pragma unroll 1
+            for (int g = 0; g < left; g += 32) list = merge32(list, sort32(g + lane < left ? all[g + lane] : 0));
+        }
+        if (any_listed) {
+            __syncthreads();
+            merge_warps(s_list, list);
+            list = s_list[0][lane];
+        }
+        if (warp == 0) out[lane] = list;
     }
-    if (any_listed) {
-        __syncthreads();
-        merge_warps(s_list, list);
-        list = s_list[0][lane];
-    }
     if (warp == 0) {
-        const size_t at = (size_t)row * L.chunks + chunk;
-        L.keys[at * 32 + lane] = list;
         m = lane < kWarps ? s_sum[lane].x : -INFINITY;
         s = lane < kWarps ? s_sum[lane].y : 0.f;
         warp_sums(m, s);
-        if (lane == 0) L.sums[at] = make_float2(m, s);
+        if (lane == 0) L.sums[place] = make_float2(m, s);
     }
 }
 
