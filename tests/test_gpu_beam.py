@@ -239,3 +239,16 @@ def test_one_beam_far_ahead(cuda_dev, Kout):
 def test_equal_scores_everywhere(cuda_dev):
     """One value in every row: the order is that of beams and tokens alone."""
     check(torch.full((2, 8, 9000), 0.5), torch.full((2, 8), -1.0), None, -1, 32)
+
+
+@pytest.mark.parametrize("B,K,V,live", [(1, 4, 4096, 1), (3, 5, 3000, 2), (4, 8, 20001, 0), (4, 8, 20001, 32), (40, 8, 5000, 37),
+                                        (76, 8, 1100, 300), (100, 8, 700, 500), (1, 32, 60000, 3)])
+def test_any_number_of_ended_and_dead_beams(cuda_dev, B, K, V, live):
+    """Live rows anywhere among ended and dead ones, up to more rows than run at once."""
+    logits, cum = draw(B, K, V, "bf16", 50 + live)
+    g = torch.Generator().manual_seed(51 + live)
+    order = torch.randperm(B * K, generator=g)[: B * K - live]
+    finished = torch.zeros(B * K, dtype=torch.int32)
+    finished[order[::2]] = 1
+    cum.view(-1)[order[1::2]] = float("-inf")
+    check(logits, cum, finished.view(B, K), 7, min(K, 8))
