@@ -64,15 +64,14 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
     const PlanDims& p = W.L.plan;
     if (threadIdx.x == 0) pdl_trigger();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    int before;
-    const Cut cut(flat_tiles(W, 0, &before), p.Cg);
+    int before, tiles = p.B > kSeqs ? flat_tiles(W, 0, &before) : 0;
     // ---- segments with a CTA boundary inside, by the sequences' tile offsets.  This
     // reads the lengths before the wait below: the attention kernel lets this
     // one start only after its own wait, so its inputs are final.
     int base = 0, n_split = 0;
     for (int b0 = 0; b0 < p.B; b0 += kSeqs) {
         const int nb = min(p.B - b0, kSeqs);
-        __syncthreads();
+        if (b0 > 0) __syncthreads();
         int run = base;
         for (int i0 = 0; i0 < nb; i0 += kMergeThreads) {
             const int i = i0 + t, n = i < nb ? seq_tiles(W, b0 + i) * p.Hkv : 0;
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
                 const int x = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += x;
             }
-            __syncthreads();
+            if (i0 > 0) __syncthreads();
             if (lane == 31) s_warp[warp] = incl;
             __syncthreads();
             int pre = 0, all = 0;
@@ -95,6 +94,8 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
             run += all;
         }
         if (t == 0) s_off[nb] = run;
+        if (p.B <= kSeqs) tiles = run;
+        const Cut cut(tiles, p.Cg);
         __syncthreads();
         for (int cb = 1; cb < cut.n; cb += kMergeThreads) {
             const int c = cb + t;
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
             }
             // in the order of boundaries: every CTA makes the same list
             const unsigned who = __ballot_sync(0xffffffffu, sp.count > 0);
-            __syncthreads();
+            if (cb > 1) __syncthreads();
             if (lane == 0) s_warp[warp] = __popc(who);
             __syncthreads();
             int at = n_split + __popc(who & ((1u << lane) - 1u));
