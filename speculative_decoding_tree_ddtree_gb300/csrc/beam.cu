@@ -15,13 +15,13 @@
 // networks of shuffles.
 // Launch 2, one CTA per request, adds the chunks' sums up row by row, turns the
 // chunks' lists into scores of some 48 bits (neighbouring candidates of different
-// rows are closer than fp32 keeps beside a long sum) and takes the best: 2.7 us from
-// the last chunk's end, of which 0.6 are the wait itself and 0.9 the loads (merging sorted
-// lists by bitonic networks with fp64 scores: 5.5).
-// 8 requests of 8 beams over 151,936 fp32 logits (39 MB): 16.0 us, 2.4 TB/s; 32 of
-// bf16 logits, a quarter of the beams finished: 23.9 us.  Bound by the fixed part
+// rows are closer than fp32 keeps beside a long sum) and takes the best: 3.6 us from
+// the last chunk's end, of which 0.6 are the wait itself and 1.0 the loads (merging sorted
+// lists by bitonic networks with fp64 scores: 6.1).
+// 8 requests of 8 beams over 151,936 fp32 logits (39 MB): 15.8 us, 2.5 TB/s; 32 of
+// bf16 logits, a quarter of the beams finished: 23.6 us.  Bound by the fixed part
 // of a chunk (its sorts start when the stream ends: all CTAs run in one wave) and the
-// second launch; smaller chunks cost more (8 CTAs per SM: 27 us).
+// second launch; smaller chunks cost more (twice as many: 19.0 us).
 #include <type_traits>
 
 #include "beam.h"
