@@ -49,6 +49,21 @@ cudaError_t launch_window(const WinLaunch& W, cudaStream_t stream) {
     return a.D == 256 ? launch_bf16_256(m, W, stream) : launch_bf16_128(m, W, stream);
 }
 
+// A CTA to each segment where that costs at most one tile's time more than an even
+// cut: it saves the partial sums and the launch that joins them, about 2.7 us, against
+// 1.6 (D = 128) to 3.1 us (D = 256, 132 rows) a tile.  Segment by segment against cut:
+// 8 nodes of 4 heads, window 1 (a tile) 8.6 and 9.6 us, window 60 (two) 9.7 and 10.8,
+// window 190 (three) 11.5 and 10.9; 13 x 3 rows of 35 segments 9.6 and 11.6, 11.3 and
+// 12.4, 12.9 and 12.8; 6 rows of 64 segments, D = 256, 9.4 and 11.9, 12.8 and 13.6,
+// 15.4 and 18.8; 132 rows 19.9 and 21.6, but 22.3 and 19.9 with two tiles: no tile more
+// with many rows.
+bool stay_whole(const WinLaunch& W) {
+    const PlanDims& p = W.L.plan;
+    if ((long long)p.S * p.rg.NG > grid_ctas(p)) return false;
+    const long long most = most_tiles(W.window, W.sinks, p.max_pages), cut = (p.S * most + p.Cg - 1) / p.Cg;
+    return most - cut <= (p.rg.RG <= 64 ? 1 : 0);
+}
+
 }  // namespace
 
 }  // namespace win
@@ -84,8 +99,10 @@ extern "C" lucetree_status lucetree_verify_attn_win(const lucetree_win_args* w, 
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return LUCETREE_ERR_WORKSPACE;
     W.L.ws = reinterpret_cast<float*>(workspace);
+    W.alone = win::stay_whole(W);
+    if (W.alone) W.L.plan.Cg = W.L.plan.S;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (win::launch_window(W, s) != cudaSuccess) return LUCETREE_ERR_CUDA;
-    if (win::launch_merge(W, s) != cudaSuccess) return LUCETREE_ERR_CUDA;
+    if (!W.alone && win::launch_merge(W, s) != cudaSuccess) return LUCETREE_ERR_CUDA;
     return LUCETREE_OK;
 }

@@ -21,6 +21,7 @@ struct WinLaunch {
     int window, sinks;
     int out_dtype;  // LUCETREE_F32 or a.dtype
     void* out;
+    bool alone;     // CTA c of a row group has segment c to itself: no partial sums
 };
 
 struct Span {
@@ -83,6 +84,13 @@ struct Cut {
     __device__ int cta_of(int tile) const { return cta_of_tile(tile, T, n); }
 };
 
+// Tiles of a segment at most, whatever its length.
+inline int most_tiles(int window, int sinks, int max_pages) {
+    // the window - 1 positions before a depth-0 node, wherever they begin in a page
+    const int wp = window > 1 ? (window - 2) / kPage + 2 : 0, sp = sinks / kPage + (sinks % kPage != 0);
+    return wp >= max_pages || sp >= max_pages - wp ? (max_pages + 2) / 2 : (wp + sp + 2) / 2;
+}
+
 // Where a CTA starts: its tile range and the segment of its first tile, found by
 // the whole warp from one read of the lengths.
 struct Start {
@@ -96,6 +104,13 @@ __device__ inline Start start_of(const WinLaunch& W, int cta) {
     const PlanDims& p = W.L.plan;
     const int lane = threadIdx.x & 31;
     Start s = {0, 0, 0, 0, 0, 0};
+    if (W.alone) {
+        s.b = cta / p.Hkv;
+        s.g = cta % p.Hkv;
+        s.L = seq_len_quiet(W.L.a.ctx_len, s.b, p.max_pages);
+        s.t1 = tiles_of(span_of(s.L, W.window, W.sinks));
+        return s;
+    }
     int before, nT = p.B > 32 ? flat_tiles(W, 0, &before) : 0, off = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int L = b0 + lane < p.B ? seq_len_quiet(W.L.a.ctx_len, b0 + lane, p.max_pages) : 0;

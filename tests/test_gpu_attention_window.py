@@ -310,3 +310,13 @@ def test_captured_and_replayed_on_another_stream(cuda_dev):
         ref, _, bound, _ = reference(s, p_step=P_STEP[out.dtype])
         assert ((out.cpu().double() - ref).abs() <= bound + 2.0 ** -8 * (ref.abs() + bound)).all()
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 64), (2, 4), (60, 4), (63, 0), (130, 0), (190, 4), (260, 70)])
+@pytest.mark.parametrize("ctx,N,Hq,Hkv,D", [((700, 0, 5, 1000), 8, 8, 2, 128), ((900, 333), 22, 24, 4, 256),
+                                            ((400,) * 40, 3, 8, 4, 128), ((640, 77), 40, 6, 1, 128)])
+def test_segments_of_a_few_tiles(cuda_dev, window, sinks, ctx, N, Hq, Hkv, D):
+    """Few and many rows, one and several row groups, fewer and more segments than SMs, at the
+    sizes where a segment is left to one CTA or cut."""
+    s = make(ctx, N, Hq, Hkv, D, "bf16", window, sinks, "random", seed=window + sinks)
+    check(s, torch.bfloat16)
