@@ -567,13 +567,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool part = tree;   // some lane's key does not count for all rows
                 if (tree) {
                     valid = valid && key < p.N;
-                    const int dj = valid ? max(__popcll(ms->anc[key]) - 1, 0) : 0;
-                    const bool sink = (long long)pc.L + dj < W.sinks;
+                    if (W.window >= p.N) {
+                        // every ancestor is near: the nodes whose masks have my key's bit, by a vote of the
+                        // warp for each of its keys (node by node it took as long as the softmax)
+                        const uint32_t up = (quarter & 1) * 32, n = p.N > (int)up ? min(p.N - (int)up, 32) : 0;
+                        const uint32_t a0 = lane < p.N ? (uint32_t)(ms->anc[lane] >> up) : 0u;
+                        const uint32_t a1 = lane + 32 < p.N ? (uint32_t)(ms->anc[lane + 32] >> up) : 0u;
+#pragma unroll 4
+                        for (uint32_t k = 0; k < n; ++k) {
+                            const uint32_t lo = __ballot_sync(0xffffffffu, (a0 >> k) & 1u);
+                            const uint32_t hi = __ballot_sync(0xffffffffu, (a1 >> k) & 1u);
+                            if (lane == k) desc = (uint64_t)hi << 32 | lo;
+                        }
+                    } else {
+                        const int dj = valid ? max(__popcll(ms->anc[key]) - 1, 0) : 0;
+                        const bool sink = (long long)pc.L + dj < W.sinks;
 #pragma unroll 1
-                    for (int i = 0; i < p.N; ++i) {
-                        const uint64_t anc = ms->anc[i];
-                        const bool near = __popcll(anc) - 1 - dj < W.window;
-                        if (((anc >> key) & 1u) && (near || sink)) desc |= 1ull << i;
+                        for (int i = 0; i < p.N; ++i) {
+                            const uint64_t anc = ms->anc[i];
+                            const bool near = __popcll(anc) - 1 - dj < W.window;
+                            if (((anc >> key) & 1u) && (near || sink)) desc |= 1ull << i;
+                        }
                     }
                 } else if (valid) {
                     const int pos = page_of(pc.w, v) * kPage + key;
