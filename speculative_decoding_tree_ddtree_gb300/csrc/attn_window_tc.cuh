@@ -23,9 +23,9 @@
 // Bounded by HBM while it streams with few rows (16 sequences decoding at window
 // 4096: 2.9 us a tile on every SM, 6.8 TB/s; 54 us the call with start, last tile
 // and merge); by the bytes in flight that the ring beside Q and P^T allows with many
-// (32 sequences at budget 22, window 8192: 3.3 us a tile, 209 us, 5.2 TB/s); by the
+// (32 sequences at budget 22, window 8192: 3.3 us a tile, 208 us, 5.2 TB/s); by the
 // chain of lengths, page ids, first tile and epilogue in calls of a tile or two per
-// CTA (one sequence at window 4096: 22 us; 8 nodes over 260 keys: 10.5 us).
+// CTA (one sequence at window 4096: 20 us; 8 nodes over 260 keys: 10.2 us).
 #pragma once
 
 #include <type_traits>
@@ -617,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 //   kShift  the tile's column maxima move the shifts, the sums and O^T
                 //           columns so far move with them, then the pass again.
                 // A range's first tile, or one with a row that has seen no key yet, has no
-                // shifts to go by and starts at kShift.  kWarm: the passes over nothing,
-                // while the CTA's first tile loads.
+                // shifts to go by and starts at kShift.  kWarm: the passes that the CTA's
+                // first tile needs over nothing, while it loads (both copies of the
+                // exponent pass took longer than that with 144 rows: 21.4 us a call, now 20.4).
                 enum { kWarm, kTry, kUndo, kShift };
                 int phase = j == 0 ? kWarm : first || ms->empty_cols != 0 ? kShift : kTry;
                 uint32_t ph[kNa * 8];
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (true) {
                     if (phase == kShift || phase == kWarm) {
 #pragma unroll 1
-                        for (int cc = 0; cc < nch; ++cc) {
+                        for (int cc = 0; cc < (phase == kWarm ? min(nch, 1) : nch); ++cc) {
                             const int c = cb + cc;
                             uint32_t r[16];
                             tmem_ld16(tl + 16 * c, r);
@@ -750,10 +751,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     };
-                    if (!bad && (!plain || phase == kWarm)) pass(std::true_type{});
-                    if (!bad && (plain || phase == kWarm)) pass(std::false_type{});
+                    if (!bad && !plain) pass(std::true_type{});
+                    if (!bad && plain) pass(std::false_type{});
                     if (phase == kWarm) {
-                        // (nothing has been multiplied yet: the plain copy has summed up whatever TMEM held)
+                        // (nothing has been multiplied yet: it has summed up whatever TMEM held)
 #pragma unroll
                         for (int i = 0; i < kNa * 8; ++i) lpart[i] = 0;
                     }
