@@ -470,9 +470,10 @@ LUCETREE_API lucetree_status lucetree_beam_select_workspace(int batch, int beams
  * them, so there are always beams_out candidates.  With beams_in = 1 this
  * opens a search, or grows a node of a draft tree into its best children;
  * out_row is the `src` of lucetree_reorder_pages and lucetree_reorder_states.
- * The order within a row is that of the logits; sums are fp32, scores sums of
- * two floats (48 bits) and rounded once to fp32, so candidates of different
- * beams closer than a row's sum is exact may come in either order.  NaN and +inf
+ * The order within a row is that of the logits, as far as 48 bits of a score
+ * tell them apart; sums are fp32, scores sums of two floats (those 48 bits)
+ * and rounded once to fp32, so candidates of different beams closer than a
+ * row's sum is exact may come in either order.  NaN and +inf
  * logits are outside the contract.  The logits are read once.
  */
 LUCETREE_API lucetree_status lucetree_beam_select(const lucetree_beam_args* args, void* workspace,

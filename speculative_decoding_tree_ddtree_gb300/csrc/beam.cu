@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(B
 #pragma unroll
     for (int x = 0; x < kHold; ++x) beam[x] = min(first_list + x * per_pass, lists - 1) / chunks;
     // (the inputs are those that the scan has waited for)
-    const float cum_t = t < K ? a.cum[b * K + t] : 0.f;
-    const bool ended_t = t < K && row_ended(a, b * K + t);
+    const float cum_t = t < K ? __ldcg(a.cum + b * K + t) : 0.f;
+    const bool ended_t = t < K && a.finished && __ldcg(a.finished + b * K + t) != 0;
 
     auto key_of = [&](int l, int k) -> u64 { return l < lists && s_state[k] == kLive ? keys[(size_t)l * 32] : 0; };
     auto cand_of = [&](int l, int k, u64 key) -> Cand {
@@ -465,7 +465,6 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(B
         float2 score = two_sum(e.x, (d.y + e.y) - lse.y);
         int token = (int)key_index(key);
         bool have = key != 0;
-        if (!(x > -INFINITY)) score = make_float2(-INFINITY, 0.f);
         if (s_state[k] != kLive || !(lse.x > -INFINITY)) {
             // the row's tokens in order, all at -inf, but after the one candidate of a beam that has ended
             const bool one = s_state[k] == kEnded && a.eos >= 0 && a.eos < a.vocab;
@@ -473,6 +472,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(B
             token = one ? (j == 0 ? a.eos : (j - 1 < a.eos ? j - 1 : j)) : j;
             score = make_float2(one && j == 0 ? cum : -INFINITY, 0.f);
         }
+        if (!(score.x > -INFINITY)) score = make_float2(-INFINITY, 0.f);  // (a masked logit: NaN in the errors)
         return have ? Cand{order_score(score), (unsigned)k * (unsigned)a.vocab + (unsigned)token} : Cand{kNoScore, ~0u};
     };
     auto write = [&](bool warm, int at, const Cand& c) {

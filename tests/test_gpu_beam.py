@@ -252,3 +252,14 @@ def test_any_number_of_ended_and_dead_beams(cuda_dev, B, K, V, live):
     finished[order[::2]] = 1
     cum.view(-1)[order[1::2]] = float("-inf")
     check(logits, cum, finished.view(B, K), 7, min(K, 8))
+
+
+def test_scores_that_are_not_numbers_come_last(cuda_dev):
+    """A beam whose score so far is NaN counts as -inf; the others are chosen as without it."""
+    logits, cum = draw(2, 5, 3000, "f16", 60)
+    bad = cum.clone()
+    bad[:, 3] = float("nan")
+    cum[:, 3] = float("-inf")
+    got, want = call(logits.cuda(), bad, None, -1, 6), reference(logits, cum, None, -1, 6)
+    assert np.array_equal(got[1].numpy(), want[1]) and np.array_equal(got[2].numpy(), want[2])
+    assert not torch.isnan(got[0]).any()
