@@ -68,11 +68,13 @@ def build_marshal(force: bool = False) -> str | None:
            "-ltorch_python", "-ltorch_cpu", "-lc10"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
-        why = r.stderr if r.returncode != 0 else ""
+        why = (r.stderr or f"exit code {r.returncode}") if r.returncode != 0 else ""
     except OSError as e:
         why = str(e)
     if why:
         print(f"the binding's tensor checks stay in Python:\n{why[-2000:]}", file=sys.stderr)
+        if os.path.exists(MARSHAL):  # of an older source
+            os.remove(MARSHAL)
         return None
     os.replace(tmp, MARSHAL)
     os.makedirs(BUILD, exist_ok=True)
