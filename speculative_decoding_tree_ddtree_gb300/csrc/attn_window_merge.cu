@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
             m = top;
         }
         if (!has_row) continue;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN stays, and is flagged)
         bool finite = true;
 #pragma unroll
         for (int y = 0; y < kV; ++y) {
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(WinLau
         const size_t row = ((size_t)sp.b * p.N + i) * p.Hq + h;
         store_row<kV>(reinterpret_cast<TO*>(W.out) + row * D + lane * kV, o);
         if (!finite) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
-        if (a.lse && lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 

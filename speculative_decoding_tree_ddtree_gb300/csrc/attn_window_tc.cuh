@@ -613,9 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // shifts, kept in registers (fp16 or bf16 pairs), sums added, the largest
                 // exponent tracked.
                 //   kTry    with the shifts as they are; if no exponent exceeds kTau, done;
-                //   kUndo   else the same pass with the sums subtracted (exact);
+                //   kUndo   else the same pass with the sums subtracted.  What is left is off by at
+                //           most 2^-24 p, which kShift scales with the sum to 2^-24 of the
+                //           tile's largest term.  From an exponent of 128 on p is infinite and
+                //           what is left is not a number;
                 //   kShift  the tile's column maxima move the shifts, the sums and O^T
-                //           columns so far move with them, then the pass again.
+                //           columns so far move with them, then the pass again.  Such a column's
+                //           alpha is 0 (at most 2^-128, flushed), which sets its old sum to 0.
                 // A range's first tile, or one with a row that has seen no key yet, has no
                 // shifts to go by and starts at kShift.  kWarm: the passes that the CTA's
                 // first tile needs over nothing, while it loads (both copies of the
@@ -674,10 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int cc = 0; cc < kNa; ++cc) {
                             if (cc >= nch) continue;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                lpart[cc * 8 + k] = fma2(
-                                    lpart[cc * 8 + k],
-                                    *reinterpret_cast<const uint64_t*>(ms->alpha + 16 * (cb + cc) + 2 * k), 0);
+                            for (int k = 0; k < 8; ++k) {
+                                const float2 al = *reinterpret_cast<const float2*>(ms->alpha + 16 * (cb + cc) + 2 * k);
+                                const float2 l = unpack2(lpart[cc * 8 + k]);
+                                lpart[cc * 8 + k] = pack2(al.x > 0.f ? l.x * al.x : 0.f, al.y > 0.f ? l.y * al.y : 0.f);
+                            }
                         }
                         if (!first) {
                             // O^T columns accumulated so far move with their shift, once
@@ -824,8 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float l = (ms->col_red[0][col] + ms->col_red[1][col]) + (ms->col_red[2][col] + ms->col_red[3][col]);
                 const float m = -ms->neg_m[col];
                 if (whole) {
-                    ms->alpha[col] = l > 0.f ? 1.f / l : 0.f;
-                    if (a.lse) a.lse[ms->out_row[col]] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                    // (0: no key; a sum that is not a number makes the row one, and is flagged below)
+                    ms->alpha[col] = l != 0.f ? 1.f / l : 0.f;
+                    if (a.lse) a.lse[ms->out_row[col]] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 } else {
                     slot[(size_t)RG * D + col] = m;
                     slot[(size_t)RG * D + RG + col] = l;
