@@ -36,7 +36,7 @@
 // current shifts (one streaming pass: P kept in registers, sums accumulated,
 // largest exponent tracked; padding columns carry a shift of +inf, so they give
 // P = 0 without a column test); if any exponent exceeds 8 (log2 domain) the pass is taken
-// back out exactly, the tile's column maxima are found (warp shuffles +
+// back out, the tile's column maxima are found (warp shuffles +
 // shared memory) and the partial sums and already-accumulated O^T columns are
 // rescaled before the tile is redone.  The first tile of every range goes
 // straight to that path.  Sums are reduced across lanes once per range.
@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             return __all_sync(0xffffffffu, w);
         };
         // One streaming pass over my chunks of S^T: P = 2^(s*scale*log2e - m)
-        // with the current shifts; lpart += P (sign +1) or -= P (sign -1, the
-        // exact undo of a pass made with the same shifts); optionally keeps
+        // with the current shifts; lpart += P (sign +1) or -= P (sign -1: takes
+        // back a pass made with the same shifts); optionally keeps
         // P (fp16 pairs) in registers `ph` and tracks the largest exponent.
         // Invalid keys and padding columns give P = 0.
         // P stays in registers so that the pass can run while PV of the
@@ -918,7 +918,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // pass 0: exponents with the current shifts (P kept in registers,
                 //         sums added, largest exponent voted across the CTA)
                 // pass 1: if an exponent exceeded kTau, the same pass with the sums
-                //         subtracted (exact undo)
+                //         subtracted.  What is left is off by at most 2^-24 P, which
+                //         pass 2 scales with the sum to 2^-24 of the tile's largest
+                //         term.  From an exponent of 128 on P is infinite and what is
+                //         left is not a number, but such a column's alpha is 0 (at most
+                //         2^-128, flushed), which sets its old sum to 0
                 // pass 2: exact column maxima move the shifts, then P and sums again
                 // The first tile of a range has no shifts yet and starts at pass 2.
                 float ex = -INFINITY;
@@ -965,7 +969,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int cc = 0; cc < kNa; ++cc) {
                         if (cc >= nch) continue;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) lpart[cc * 16 + k] *= ms->alpha[16 * (cb + cc) + k];
+                        for (int k = 0; k < 16; ++k) {
+                            // (alpha 0: what pass 1 left may not be a number)
+                            const float al = ms->alpha[16 * (cb + cc) + k];
+                            lpart[cc * 16 + k] = al > 0.f ? lpart[cc * 16 + k] * al : 0.f;
+                        }
                     }
                     if (!first) {
                         // O^T columns accumulated so far move with their shift, once
