@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(B
         bool have = key != 0;
         if (s_state[k] != kLive || !(lse.x > -INFINITY)) {
             // the row's tokens in order, all at -inf, but after the one candidate of a beam that has ended
-            const bool one = s_state[k] == kEnded && a.eos >= 0 && a.eos < a.vocab;
+            // (with a score: at -inf eos is a token like the others)
+            const bool one = s_state[k] == kEnded && cum > -INFINITY && a.eos >= 0 && a.eos < a.vocab;
             have = l == k * chunks && j < a.vocab;
             token = one ? (j == 0 ? a.eos : (j - 1 < a.eos ? j - 1 : j)) : j;
             score = make_float2(one && j == 0 ? cum : -INFINITY, 0.f);
