@@ -446,7 +446,7 @@ typedef struct lucetree_beam_args {
     int vocab;               /* beams_in * vocab < 2^32 - 1 */
     long long row_stride;    /* elements from one row of logits to the next, >= vocab */
     const void* logits;      /* [batch][beams_in] rows of vocab, aligned to their type */
-    const float* cum;        /* [batch][beams_in] log-probability of each beam so far; -inf = a dead beam */
+    const float* cum;        /* [batch][beams_in] log-probability of each beam so far; -inf = a dead beam, and so is NaN */
     const int32_t* finished; /* [batch][beams_in] non-zero: the beam has ended, or NULL: none has */
     int eos;                 /* token that ends a beam; outside [0, vocab) = none */
     float* out_score;        /* [batch][beams_out], best first; with beams_out == beams_in it may be cum, and
@@ -474,7 +474,7 @@ LUCETREE_API lucetree_status lucetree_beam_select_workspace(int batch, int beams
  * tell them apart; sums are fp32, scores sums of two floats (those 48 bits)
  * and rounded once to fp32, so candidates of different beams closer than a
  * row's sum is exact may come in either order.  NaN and +inf
- * logits are outside the contract.  The logits are read once.
+ * logits and cum = +inf are outside the contract.  The logits are read once.
  */
 LUCETREE_API lucetree_status lucetree_beam_select(const lucetree_beam_args* args, void* workspace,
                                                   size_t workspace_bytes, void* stream);

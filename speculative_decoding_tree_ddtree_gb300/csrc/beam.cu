@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
     const int row = blockIdx.y, chunk = blockIdx.x, t = threadIdx.x;
-    // rows that ended or are dead need no logits (launch 2 knows their candidates)
-    if (row_ended(a, row) || a.cum[row] == -INFINITY) return;
+    // rows that ended or are dead (at -inf or NaN) need no logits (launch 2 knows their candidates)
+    if (row_ended(a, row) || !(a.cum[row] > -INFINITY)) return;
     const int warp = t >> 5, lane = t & 31;
     const T* x = reinterpret_cast<const T*>(a.logits) + (long long)row * a.row_stride;
     // vectors of kE elements by index, so that a row's sum does not depend on where
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(B
         if (!warm) {
             if (t < K) {
                 s_cum[t] = cum_t;
-                s_state[t] = ended_t ? kEnded : cum_t == -INFINITY ? kDead : kLive;
+                s_state[t] = ended_t ? kEnded : cum_t > -INFINITY ? kLive : kDead;
             }
             __syncthreads();
             pdl_wait();
