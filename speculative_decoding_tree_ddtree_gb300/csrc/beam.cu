@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) beam_scan_kernel(BeamLau
         }
     }
     if (chunk == L.chunks - 1 && warp == 0) {
-        const int i = nv * kE + lane;
-        const bool in = i < a.vocab;
+        const bool in = lane < a.vocab - nv * kE;  // (nv * kE + lane may pass 2^31)
+        const int i = nv * kE + (in ? lane : 0);
         const float f = in ? scalar(x + i) : -INFINITY;
         if (in) add_sums(m, s, f, f == -INFINITY ? 0.f : 1.f);
         if (waiting + kE > 32) {  // (the tail has fewer than kE elements)
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) beam_merge_kernel(B
 // than that, and no chunk of fewer than four elements a thread.
 int beam_chunks(int rows, int vocab, int sms) {
     int chunks = kCtasPerSm * sms / rows;
-    const int most = (vocab + 4 * kThreads - 1) / (4 * kThreads);
+    const int most = (int)((vocab + 4ll * kThreads - 1) / (4 * kThreads));
     if (chunks > most) chunks = most;
     return chunks < 1 ? 1 : chunks;
 }
