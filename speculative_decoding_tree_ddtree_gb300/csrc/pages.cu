@@ -54,8 +54,8 @@ struct RowSpan {
     bool ok;
 };
 
-// The pages that row b's length and the reserve take.
-__device__ inline RowSpan row_span(const lucetree_reorder_args& a, int b, uint32_t* status) {
+// The pages that row b's length and the reserve take.  `goes_on`: some new row maps the reserve.
+__device__ inline RowSpan row_span(const lucetree_reorder_args& a, int b, uint32_t* status, bool goes_on = false) {
     RowSpan s{a.ctx_in[b], 0, 0, true};
     if (s.L < 0 || (long long)s.L > (long long)a.max_pages_per_seq * kPage) {
         if (status) atomicOr(status, LUCETREE_DEV_BAD_CTX);
@@ -65,7 +65,7 @@ __device__ inline RowSpan row_span(const lucetree_reorder_args& a, int b, uint32
     }
     s.full = s.L / kPage;
     const long long end = ((long long)s.L + a.reserve + kPage - 1) / kPage;
-    if (end > a.max_pages_per_seq && status) atomicOr(status, LUCETREE_DEV_BAD_CTX);
+    if (end > a.max_pages_per_seq && goes_on) atomicOr(status, LUCETREE_DEV_BAD_CTX);
     s.end = (int)(end < a.max_pages_per_seq ? end : a.max_pages_per_seq);
     return s;
 }
@@ -146,8 +146,9 @@ __device__ inline void plan_rows(const ReorderLaunch& R, int* s_warp) {
     // tail pages that no other row holds stay with the first row that takes the parent
     for (int b = t; b < a.rows_in; b += kChunk) {
         uint64_t kept = 0;
-        const RowSpan s = row_span(a, b, a.status);
-        if (now(&R.w.children[b]) > 0)
+        const bool goes_on = now(&R.w.children[b]) > 0;
+        const RowSpan s = row_span(a, b, a.status, goes_on);
+        if (goes_on)
             for (int c = s.full; c < s.end; ++c) {
                 const int page = a.table_in[(size_t)b * a.max_pages_per_seq + c];
                 if (page_ok(page, a.num_pages) && a.ref_in[page] == 1) kept |= 1ull << (c - s.full);
