@@ -664,7 +664,7 @@ LUCETREE_API lucetree_status lucetree_compact_pages_workspace(int num_pages, siz
  * at or past `live` moves to the k-th free page before it.  Tables and counts
  * take the new numbers; no page that moves is a target, so the copies may run
  * in any order.  Device check: BAD_PAGE (an entry out of range, or one that
- * names a free page at or past `live`: it becomes -1).
+ * names a free page: it becomes -1).
  */
 LUCETREE_API lucetree_status lucetree_compact_pages(const lucetree_compact_args* args, void* workspace,
                                                     size_t workspace_bytes, void* stream);

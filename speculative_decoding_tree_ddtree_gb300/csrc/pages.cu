@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kChunk) trim_small_kernel(lucetree_trim_args a
 struct CompactLaunch {
     lucetree_compact_args a;
     int32_t* used_count;  // [chunks]
-    int32_t* rank;        // [num_pages] of a page at or past the live count: its place among the movers, or -1
+    int32_t* rank;        // [num_pages] -1: free; else of a page at or past the live count: its place among the movers
     int chunks;
 };
 
@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(kChunk) compact_rank_kernel(CompactLaunch C) {
             const int k = used ? used_before - low_used : -1;
             C.rank[page] = k;
             if (used) a.copy_src[k] = page;
-        } else if (!used) {
-            a.copy_dst[page - used_before] = page;
+        } else {
+            C.rank[page] = used ? 0 : -1;
+            if (!used) a.copy_dst[page - used_before] = page;
         }
     }
     const int cap = a.num_pages / 2;  // no more pages can move
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kThreads) compact_apply_kernel(CompactLaunch C
     for (long long e = at; e < n; e += step) {
         int page = a.table_in[e];
         if (page != -1) {
-            if (!page_ok(page, a.num_pages) || (page >= live && C.rank[page] < 0)) {
+            if (!page_ok(page, a.num_pages) || C.rank[page] < 0) {
                 atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
                 page = -1;
             } else if (page >= live) {
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kChunk) compact_small_kernel(CompactLaunch C) 
     constexpr int kMine = kSmallPages / kChunk;
     const lucetree_compact_args& a = C.a;
     __shared__ int s_warp[kChunk / 32];
-    __shared__ int16_t s_name[kSmallPages];      // new number of a page at or past the live count, -1 if free
+    __shared__ int16_t s_name[kSmallPages];      // new number of a page, -1 if free
     __shared__ int16_t s_hole[kSmallPages / 2];  // free pages before it
     static_assert(kSmallPages <= 32767 + 1, "page numbers in 16 bits");
     pdl_wait();
@@ -514,6 +515,7 @@ __global__ void __launch_bounds__(kChunk) compact_small_kernel(CompactLaunch C) 
         const int p = i * kChunk + t;
         if (p >= a.num_pages) continue;
         if (p < live) {
+            s_name[p] = ref[i] > 0 ? (int16_t)p : (int16_t)-1;
             if (ref[i] > 0 && a.ref_out != a.ref_in) a.ref_out[p] = ref[i];
         } else if (ref[i] > 0) {
             const int k = used_before[i] - low_used, to = s_hole[k];
@@ -537,12 +539,9 @@ __global__ void __launch_bounds__(kChunk) compact_small_kernel(CompactLaunch C) 
     for (int e = t; e < n; e += kChunk) {
         int page = a.table_in[e];
         if (page != -1) {
-            if (!page_ok(page, a.num_pages) || (page >= live && s_name[page] < 0)) {
-                atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
-                page = -1;
-            } else if (page >= live) {
-                page = s_name[page];
-            }
+            const int name = page_ok(page, a.num_pages) ? s_name[page] : -1;
+            if (name < 0) atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
+            page = name;
         }
         a.table_out[e] = page;
     }
