@@ -610,8 +610,9 @@ LUCETREE_API lucetree_status lucetree_reorder_pages_workspace(int rows_in, int r
  * Device checks: BAD_ROW (src out of range: the new row is empty), BAD_CTX (a
  * length outside the table: that row keeps its pages and its new rows are
  * empty; or L + reserve past the table where a new row continues it: mapped as
- * far as it goes), BAD_PAGE (an entry out of range, or a count that would fall
- * below zero), NO_PAGE (no free page left: the entry is -1).
+ * far as it goes), BAD_PAGE (an entry out of range, or one that names a free
+ * page: read as -1; or a count that would fall below zero), NO_PAGE (no free
+ * page left: the entry is -1).
  */
 LUCETREE_API lucetree_status lucetree_reorder_pages(const lucetree_reorder_args* args, void* workspace,
                                                     size_t workspace_bytes, void* stream);

@@ -210,6 +210,12 @@ __device__ inline int free_page(const ReorderPlan& w, int chunks, int k) {
     return -1;
 }
 
+// Whether table entry `page` names a page that has a holder.  A free one may be handed to a
+// new row in this very call, so it is read as if it were missing.
+__device__ inline bool held_page(const ReorderLaunch& R, int page) {
+    return page_ok(page, R.a.num_pages) && !((R.w.free_bits[page >> 5] >> (page & 31)) & 1u);
+}
+
 // Columns [c0, c1) of row y: y < rows_out: the new rows; behind them the old ones, whose
 // pages gain a holder for each row that takes them and lose the old one.  The
 // thread is number t of n, whole warps.
@@ -225,7 +231,7 @@ __device__ inline void apply_row(const ReorderLaunch& R, int y, int c0, int c1, 
         for (int c = c0 + t; c < c1; c += n) {
             const int page = a.table_in[(size_t)b * P + c];
             if (page == -1) continue;
-            if (!page_ok(page, a.num_pages)) {
+            if (!held_page(R, page)) {
                 atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
                 continue;
             }
@@ -248,7 +254,7 @@ __device__ inline void apply_row(const ReorderLaunch& R, int y, int c0, int c1, 
         int page = -1;
         if (b >= 0 && c < s.full) {
             page = in[c];
-            if (!page_ok(page, a.num_pages)) page = -1;
+            if (!held_page(R, page)) page = -1;
         }
         out[c] = page;
     }
@@ -269,7 +275,7 @@ __device__ inline void apply_row(const ReorderLaunch& R, int y, int c0, int c1, 
             if (page < 0) atomicOr(a.status, LUCETREE_DEV_NO_PAGE);
             else a.ref_out[page] = 1;
             if (k == 0) {
-                const bool copy = s.L % kPage != 0 && page >= 0 && page_ok(old, a.num_pages);
+                const bool copy = s.L % kPage != 0 && page >= 0 && held_page(R, old);
                 a.copy_src[r] = copy ? old : -1;
                 a.copy_dst[r] = copy ? page : -1;
             }
