@@ -763,8 +763,12 @@ lucetree_status lucetree_reorder_pages(const lucetree_reorder_args* a, void* wor
         bytes_overlap(a->ctx_in, 4ll * a->rows_in, a->ctx_out, 4ll * a->rows_out) ||
         crosses(a->ref_in, a->ref_out, 4ll * a->num_pages))
         return LUCETREE_ERR_INVALID_ARG;
+    const long long src_bytes = 4ll * a->rows_out;
     for (const int32_t* out : {a->ctx_out, a->copy_src, a->copy_dst})
-        if (bytes_overlap(a->src, 4ll * a->rows_out, out, 4ll * a->rows_out)) return LUCETREE_ERR_INVALID_ARG;
+        if (bytes_overlap(a->src, src_bytes, out, src_bytes)) return LUCETREE_ERR_INVALID_ARG;
+    if (bytes_overlap(a->src, src_bytes, a->table_out, row * a->rows_out) ||
+        bytes_overlap(a->src, src_bytes, a->ref_out, 4ll * a->num_pages))
+        return LUCETREE_ERR_INVALID_ARG;
     const lucetree_status st =
         ws_check(workspace, workspace_bytes, reorder_workspace_bytes(a->rows_in, a->rows_out, a->num_pages));
     if (st != LUCETREE_OK) return st;
