@@ -450,7 +450,8 @@ typedef struct lucetree_beam_args {
     const int32_t* finished; /* [batch][beams_in] non-zero: the beam has ended, or NULL: none has */
     int eos;                 /* token that ends a beam; outside [0, vocab) = none */
     float* out_score;        /* [batch][beams_out], best first; with beams_out == beams_in it may be cum, and
-                                out_finished may be finished; no other overlap */
+                                out_finished may be finished; no other overlap of an output with cum,
+                                finished or another output */
     int32_t* out_token;      /* [batch][beams_out] */
     int32_t* out_row;        /* [batch][beams_out]: row b * beams_in + beam that it continues */
     int32_t* out_finished;   /* [batch][beams_out] 0 / 1, or NULL */

@@ -672,6 +672,22 @@ static lucetree_status beam_sizes(int batch, int beams_in, int beams_out, int vo
     return LUCETREE_OK;
 }
 
+// An output under an input (but for the two updates in place) or under another output:
+// a request's results would change what other requests still read.
+static bool outputs_overlap(const lucetree_beam_args& a) {
+    const long long before = 4ll * a.batch * a.beams_in, after = 4ll * a.batch * a.beams_out;
+    const void* in[2] = {a.cum, a.finished};
+    const void* out[4] = {a.out_score, a.out_finished, a.out_token, a.out_row};
+    for (int o = 0; o < 4; ++o) {
+        if (!out[o]) continue;
+        for (int i = 0; i < 2; ++i)
+            if (i != o && in[i] && bytes_overlap(in[i], before, out[o], after)) return true;
+        for (int p = 0; p < o; ++p)
+            if (out[p] && bytes_overlap(out[p], after, out[o], after)) return true;
+    }
+    return false;
+}
+
 lucetree_status lucetree_beam_select_workspace(int batch, int beams_in, int beams_out, int vocab, size_t* bytes) {
     if (!bytes) return LUCETREE_ERR_INVALID_ARG;
     const lucetree_status st = beam_sizes(batch, beams_in, beams_out, vocab);
@@ -706,6 +722,7 @@ lucetree_status lucetree_beam_select(const lucetree_beam_args* a, void* workspac
     if (!workspace || workspace_bytes < beam_workspace_bytes(a->batch, a->beams_in, a->vocab, dev) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return LUCETREE_ERR_WORKSPACE;
+    if (outputs_overlap(*a)) return LUCETREE_ERR_INVALID_ARG;
     if (launch_beam_select(*a, workspace, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return LUCETREE_ERR_CUDA;
     return LUCETREE_OK;

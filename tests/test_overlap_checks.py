@@ -24,3 +24,21 @@ def test_source_rows_under_an_output():
         assert rc(src=at) == 1, at
     for at in (AT + 16384 + 48, AT + 16384 - 12, AT + 12288 + 36, AT + 12288 - 12):
         assert rc(src=at) == 3, at
+
+
+def test_outputs_of_a_selection():
+    ok = dict(dtype=2, batch=2, beams_in=4, beams_out=4, vocab=50, row_stride=50, logits=AT, cum=AT + 4096,
+              finished=AT + 8192, eos=1, out_score=AT + 12288, out_token=AT + 16384, out_row=AT + 20480,
+              out_finished=AT + 24576)
+    outs = ("out_score", "out_token", "out_row", "out_finished")
+    lib = LT.load()
+
+    def rc(**change):
+        a = LT.BeamArgs(**{**ok, **change})
+        return lib.lucetree_beam_select(ctypes.byref(a), 1 << 24, 1 << 20, None)
+
+    for at in (-28, 0, 28):                            # (32 bytes each)
+        for name in outs:
+            for other in ("cum", "finished", *outs):
+                if name != other and (name, other, at) not in (("out_score", "cum", 0), ("out_finished", "finished", 0)):
+                    assert rc(**{name: ok[other] + at}) == 1, (name, other, at)
