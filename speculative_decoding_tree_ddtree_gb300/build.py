@@ -51,10 +51,15 @@ def up_to_date() -> bool:
 def build_marshal(force: bool = False) -> str | None:
     """The binding's tensor checks as a Python extension (host code, against the
     installed torch).  The binding makes the same checks in Python where it is
-    missing, so a host without Python's headers only gets a notice."""
+    missing, so a host without Python's headers, or without torch (where only the C
+    library is of use), gets a notice."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        print(f"the binding's tensor checks are not built: {e}", file=sys.stderr)
+        return None
     stamp = os.path.join(BUILD, "marshal.torch")
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC) \
             and os.path.exists(stamp) and open(stamp).read() == torch.__version__:
