@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -17,7 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "lucetree")
 LIB = os.path.join(PKG, "liblucetree.so")
 MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+# named for the Python that it is built for: another one neither loads nor reuses it
+SUFFIX = importlib.machinery.EXTENSION_SUFFIXES[0]
+MARSHAL = os.path.join(PKG, "_marshal" + SUFFIX)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -60,7 +63,7 @@ def build_marshal(force: bool = False) -> str | None:
     except ImportError as e:
         print(f"the binding's tensor checks are not built: {e}", file=sys.stderr)
         return None
-    stamp = os.path.join(BUILD, "marshal.torch")
+    stamp = os.path.join(BUILD, "marshal" + SUFFIX + ".torch")
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC) \
             and os.path.exists(stamp) and open(stamp).read() == torch.__version__:
         return MARSHAL

@@ -365,15 +365,15 @@ def _arg(t, name: str, kind: int, dev: int, *shape) -> int:
 
 
 def _load_marshal():
-    """_arg in one C call (binding/marshal.cpp), if it was built for this torch."""
-    path = os.path.join(_PKG, "_marshal.so")
+    """_arg in one C call (binding/marshal.cpp), if it was built for this Python and torch."""
+    path = os.path.join(_PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
     if not os.path.exists(path):
         return _arg
     try:
         loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
         loader.exec_module(m)
-    except ImportError:  # built for another torch or machine
+    except ImportError:  # built for another torch
         return _arg
     if m.torch_version != torch.__version__:
         return _arg
