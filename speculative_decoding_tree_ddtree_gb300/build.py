@@ -63,10 +63,20 @@ def build_marshal(force: bool = False) -> str | None:
     except ImportError as e:
         print(f"the binding's tensor checks are not built: {e}", file=sys.stderr)
         return None
-    stamp = os.path.join(BUILD, "marshal" + SUFFIX + ".torch")
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC) \
-            and os.path.exists(stamp) and open(stamp).read() == torch.__version__:
+    # what was tried last, and how it went; a failure is tried again with `force`
+    stamp = os.path.join(BUILD, "marshal" + SUFFIX + ".last")
+    key = f"{torch.__version__} {os.path.getmtime(MARSHAL_SRC)}"
+    last = open(stamp).read() if os.path.exists(stamp) else ""
+    if not force and last == "failed " + key:
+        return None
+    if not force and last == "built " + key and os.path.exists(MARSHAL):
         return MARSHAL
+
+    def note(how):
+        os.makedirs(BUILD, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(f"{how} {key}")
+
     root = os.path.dirname(torch.__file__)
     inc = os.path.join(root, "include")
     tmp = MARSHAL + f".tmp{os.getpid()}"
@@ -83,11 +93,10 @@ def build_marshal(force: bool = False) -> str | None:
         print(f"the binding's tensor checks stay in Python:\n{why[-2000:]}", file=sys.stderr)
         if os.path.exists(MARSHAL):  # of an older source
             os.remove(MARSHAL)
+        note("failed")
         return None
     os.replace(tmp, MARSHAL)
-    os.makedirs(BUILD, exist_ok=True)
-    with open(stamp, "w") as f:
-        f.write(torch.__version__)
+    note("built")
     return MARSHAL
 
 

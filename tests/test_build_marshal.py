@@ -28,3 +28,19 @@ def test_a_build_for_another_python_is_not_loaded(monkeypatch, tmp_path):
     assert LT._load_marshal() is LT._arg_slow
     shutil.copy(path, tmp_path / B.os.path.basename(path))
     assert LT._load_marshal() is not LT._arg_slow
+
+
+def test_a_build_that_failed_is_not_tried_every_time(monkeypatch, tmp_path):
+    log, cxx = tmp_path / "log", tmp_path / "cxx"
+    cxx.write_text(f"#!/bin/sh\necho run >> {log}\necho no headers >&2\nexit 1\n")
+    cxx.chmod(0o755)
+    monkeypatch.setenv("CXX", str(cxx))
+    monkeypatch.setattr(B, "BUILD", str(tmp_path / "build"))
+    monkeypatch.setattr(B, "MARSHAL", str(tmp_path / "_marshal.so"))
+    runs = lambda: len(log.read_text().split())  # noqa: E731
+    assert B.build_marshal() is None and B.build_marshal() is None and runs() == 1
+    assert B.build_marshal(force=True) is None and runs() == 2
+    src = tmp_path / "marshal.cpp"
+    src.write_text("// changed")
+    monkeypatch.setattr(B, "MARSHAL_SRC", str(src))
+    assert B.build_marshal() is None and runs() == 3
