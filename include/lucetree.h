@@ -566,7 +566,10 @@ LUCETREE_API lucetree_status lucetree_stage_pages(const lucetree_stage_args* arg
  * The calls below change tables and counts together and say which pages' data
  * has to move; lucetree_copy_pages then moves it in each layer's pools.  Where
  * several choices are possible the lowest page and row numbers go first, so
- * results depend on the inputs alone.
+ * results depend on the inputs alone.  UNSUPPORTED: more than 2^30 pages to
+ * reorder or compact; to reorder or trim, rows (in and out together) or
+ * max_pages_per_seq within 65,535 of 2^31; and new rows that could ask for 2^31
+ * new pages together.
  */
 
 #define LUCETREE_MAX_RESERVE 4032 /* positions past the committed length that lucetree_reorder_pages maps at most */

@@ -27,6 +27,8 @@ constexpr int kMaxTail = 64;            // tail pages of a row (one 64-bit mask)
 // 11.7; but 25,000 entries 93 against 73, and 6,000 entries 120 against 111.
 constexpr int kSmallPages = 8192, kSmallRows = 512, kSmallEntries = 2048;
 constexpr int kMaxPages = 1 << 30;      // chunk and page numbers stay within an int
+// ... and so do row and column numbers with one more step of a kernel's loop (65,535 rows, kCols columns)
+constexpr int kMaxRows = 0x7fffffff - 65535, kMaxCols = 0x7fffffff - kCols;
 
 int chunks_of(int num_pages) { return (num_pages + kChunk - 1) / kChunk; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -657,7 +659,7 @@ cudaError_t launch_trim_pages(const lucetree_trim_args& a, cudaStream_t stream) 
     if (a.num_pages <= kSmallPages && (long long)a.rows * a.max_pages_per_seq <= kSmallEntries)
         return launch_pdl(trim_small_kernel, dim3(1), dim3(kChunk), 0, stream, a);
     if (a.ref_out != a.ref_in) {
-        const unsigned ctas = (unsigned)((a.num_pages + 4 * kThreads - 1) / (4 * kThreads));
+        const unsigned ctas = (unsigned)((a.num_pages + 4ll * kThreads - 1) / (4 * kThreads));
         cudaError_t e = launch_pdl(copy_counts_kernel, dim3(ctas), dim3(kThreads), 0, stream, a.ref_in, a.ref_out, a.num_pages);
         if (e != cudaSuccess) return e;
     }
@@ -756,7 +758,10 @@ lucetree_status lucetree_reorder_pages(const lucetree_reorder_args* a, void* wor
     if (!a->table_in || !a->ctx_in || !a->src || !a->ref_in || !a->table_out || !a->ctx_out || !a->ref_out ||
         !a->copy_src || !a->copy_dst || !a->status)
         return LUCETREE_ERR_INVALID_ARG;
-    if (a->reserve > LUCETREE_MAX_RESERVE || a->num_pages > kMaxPages) return LUCETREE_ERR_UNSUPPORTED;
+    if (a->reserve > LUCETREE_MAX_RESERVE || a->num_pages > kMaxPages || a->max_pages_per_seq > kMaxCols ||
+        (long long)a->rows_in + a->rows_out > kMaxRows ||
+        (long long)a->rows_out * ((a->reserve + 2ll * kPage - 2) / kPage) > 0x7fffffffll)  // ranks of new pages
+        return LUCETREE_ERR_UNSUPPORTED;
     static_assert(LUCETREE_MAX_RESERVE / kPage + 1 <= kMaxTail, "a row's tail pages fit one 64-bit mask");
     const long long row = 4ll * a->max_pages_per_seq;
     if (bytes_overlap(a->table_in, row * a->rows_in, a->table_out, row * a->rows_out) ||
@@ -781,6 +786,7 @@ lucetree_status lucetree_trim_pages(const lucetree_trim_args* a, void* stream) {
         return LUCETREE_ERR_INVALID_ARG;
     if (!a->table_in || !a->ctx_len || !a->ref_in || !a->table_out || !a->ref_out || !a->status)
         return LUCETREE_ERR_INVALID_ARG;
+    if (a->rows > kMaxRows || a->max_pages_per_seq > kMaxCols) return LUCETREE_ERR_UNSUPPORTED;
     if (crosses(a->table_in, a->table_out, 4ll * a->max_pages_per_seq * a->rows) ||
         crosses(a->ref_in, a->ref_out, 4ll * a->num_pages))
         return LUCETREE_ERR_INVALID_ARG;
