@@ -21,11 +21,17 @@ constexpr int kChunk = 1024;            // pages per chunk: one thread each, 32 
 constexpr int kCols = 1024;             // table columns per CTA
 constexpr int kThreads = 256;
 constexpr int kMaxTail = 64;            // tail pages of a row (one 64-bit mask)
-// Up to these sizes one CTA does the whole of a call: a launch costs as much as its
-// pass over a thousand entries.  Measured (reorder + copies + states; trim + compact +
-// copies): 80 entries 9.2 us against 11.7 us in several launches, 63 entries 8.9 against
-// 11.7; but 25,000 entries 93 against 73, and 6,000 entries 120 against 111.
-constexpr int kSmallPages = 8192, kSmallRows = 512, kSmallEntries = 2048;
+// Up to these sizes one CTA does the whole of a call: a launch more costs as much as its
+// pass over a few pages and rows, a warp to a row.  One CTA against several launches, us of
+// GPU time (rows in and out alike x columns, pages of the pool):
+//   reorder   4 x 16, 1,500  6.6 / 7.2   16 x 64, 1,500  7.0 / 7.5   16 x 96, 1,500  7.2 / 7.4
+//             16 x 64, 4,096 7.8 / 7.4   24 x 32, 1,500  7.9 / 7.3   1 x 512, 412    7.9 / 6.5
+//   trim      4 x 16, 1,500  2.4 / 3.2   16 x 64, 1,500  3.1 / 3.1   32 x 16, 1,500  2.6 / 3.1
+//             15 x 60, 4,096 3.5 / 3.3   48 x 16, 1,500  3.1 / 3.1   16 x 96, 1,500  3.8 / 3.1
+//             counts in place (one launch either way)  4 x 16  2.0 / 1.9   16 x 64  2.7 / 1.8
+//   compact   16 x 64, 1,500 4.7 / 6.7   32 x 64, 1,793  4.9 / 6.2   1 x 2,048, 2,028 4.9 / 5.9
+//             16 x 64, 4,096 8.1 / 6.6   64 x 64, 3,546  8.5 / 6.7
+constexpr int kSmallPages = 2048, kSmallRows = 32, kSmallCols = 96, kSmallTrimCols = 64, kSmallEntries = 2048;
 constexpr int kMaxPages = 1 << 30;      // chunk and page numbers stay within an int
 // ... and so do row and column numbers with one more step of a kernel's loop (65,535 rows, kCols columns)
 constexpr int kMaxRows = 0x7fffffff - 65535, kMaxCols = 0x7fffffff - kCols;
@@ -367,10 +373,8 @@ __global__ void __launch_bounds__(kThreads) copy_counts_kernel(const int32_t* fr
 __global__ void __launch_bounds__(kChunk) trim_small_kernel(lucetree_trim_args a) {
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    if (a.ref_out != a.ref_in) {
-        for (int p = threadIdx.x; p < a.num_pages; p += kChunk) a.ref_out[p] = a.ref_in[p];
-        __syncthreads();
-    }
+    for (int p = threadIdx.x; p < a.num_pages; p += kChunk) a.ref_out[p] = a.ref_in[p];
+    __syncthreads();
     for (int b = threadIdx.x >> 5; b < a.rows; b += kChunk / 32)
         trim_row(a, b, 0, a.max_pages_per_seq, threadIdx.x & 31, 32);
 }
@@ -646,8 +650,7 @@ cudaError_t launch_reorder_pages(const lucetree_reorder_args& a, void* workspace
     R.w.free_bits = reinterpret_cast<uint32_t*>(take((size_t)R.chunks * 128));
     R.w.free_count = reinterpret_cast<int32_t*>(take((size_t)R.chunks * 4));
     const long long all = (long long)a.rows_in + a.rows_out;
-    if (a.num_pages <= kSmallPages && a.rows_in <= kSmallRows && a.rows_out <= kSmallRows &&
-        all * a.max_pages_per_seq <= kSmallEntries)
+    if (a.num_pages <= kSmallPages && all <= kSmallRows && a.max_pages_per_seq <= kSmallCols)
         return launch_pdl(reorder_small_kernel, dim3(1), dim3(kChunk), 0, stream, R);
     cudaError_t e = launch_pdl(reorder_plan_kernel, dim3(1 + R.chunks), dim3(kChunk), 0, stream, R);
     if (e != cudaSuccess) return e;
@@ -656,7 +659,7 @@ cudaError_t launch_reorder_pages(const lucetree_reorder_args& a, void* workspace
 }
 
 cudaError_t launch_trim_pages(const lucetree_trim_args& a, cudaStream_t stream) {
-    if (a.num_pages <= kSmallPages && (long long)a.rows * a.max_pages_per_seq <= kSmallEntries)
+    if (a.ref_out != a.ref_in && a.num_pages <= kSmallPages && a.rows <= kSmallRows && a.max_pages_per_seq <= kSmallTrimCols)
         return launch_pdl(trim_small_kernel, dim3(1), dim3(kChunk), 0, stream, a);
     if (a.ref_out != a.ref_in) {
         const unsigned ctas = (unsigned)((a.num_pages + 4ll * kThreads - 1) / (4 * kThreads));
