@@ -49,19 +49,25 @@ cudaError_t launch_window(const WinLaunch& W, cudaStream_t stream) {
     return a.D == 256 ? launch_bf16_256(m, W, stream) : launch_bf16_128(m, W, stream);
 }
 
-// A CTA to each segment where that costs at most one tile's time more than an even
-// cut: it saves the partial sums and the launch that joins them, about 2.7 us, against
-// 1.6 (D = 128) to 3.1 us (D = 256, 132 rows) a tile.  Segment by segment against cut:
-// 8 nodes of 4 heads, window 1 (a tile) 8.6 and 9.6 us, window 60 (two) 9.7 and 10.8,
-// window 190 (three) 11.5 and 10.9; 13 x 3 rows of 35 segments 9.6 and 11.6, 11.3 and
-// 12.4, 12.9 and 12.8; 6 rows of 64 segments, D = 256, 9.4 and 11.9, 12.8 and 13.6,
-// 15.4 and 18.8; 132 rows 19.9 and 21.6, but 22.3 and 19.9 with two tiles: no tile more
-// with many rows.
+// A CTA to each segment where that costs no tile more than an even cut, or one tile where
+// that is worth it: it saves the partial sums and the launch that joins them, whose time
+// grows with the number of segments, against a tile's, which grows with D and the rows.
+// Segment by segment against cut, us, two tiles against one (window 60):
+//   D = 128, 4 segments    32 rows  9.1 / 10.2   64  11.1 / 11.3   96  12.4 / 12.5   112  15.5 / 14.5
+//            16            32       9.2 / 11.2   64  11.2 / 12.4   96  12.6 / 12.8   112  15.7 / 14.6
+//            24            32       9.3 / 10.5   64  11.2 / 11.6   96  12.6 / 13.6   112  15.7 / 16.3
+//   D = 256, 4              6      11.7 / 10.7   72  15.2 / 13.6                     132  20.5 / 17.6
+//            24             6      11.8 / 11.6   72  15.3 / 14.4                     132  20.5 / 19.4
+//            40             6      12.0 / 12.6   72  15.5 / 16.1                     132  20.5 / 21.1
+//            60             6      12.1 / 12.8   72  15.7 / 16.9                     132  20.6 / 23.1
+// (one tile either way: 30 x 4 segments of 132 rows, D = 256, 18.9 / 21.3)
 bool stay_whole(const WinLaunch& W) {
     const PlanDims& p = W.L.plan;
-    if ((long long)p.S * p.rg.NG > grid_ctas(p)) return false;
+    const long long ctas = (long long)p.S * p.rg.NG;
+    if (ctas > grid_ctas(p)) return false;
     const long long most = most_tiles(W.window, W.sinks, p.max_pages), cut = (p.S * most + p.Cg - 1) / p.Cg;
-    return most - cut <= (p.rg.RG <= 64 ? 1 : 0);
+    const bool one_more = p.D == 128 ? p.rg.RG <= 96 || ctas >= 24 : ctas >= 40;
+    return most - cut <= (one_more ? 1 : 0);
 }
 
 }  // namespace
