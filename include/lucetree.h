@@ -170,13 +170,18 @@ typedef struct lucetree_win_args {
  *   - itself and ancestor j iff t_j < sinks or t_i - t_j < window.
  * Only the pages of the sinks and of the window of a depth-0 node are read:
  * table entries between them may be -1 (see lucetree_trim_pages).  K and V of
- * positions that no node sees may hold anything, NaN included.  N = 1 with
- * mask 1 is the single-token decode step.  A window of at least L_b + N
- * positions is the full attention.  Softmax statistics, sums and partial
- * outputs are fp32, and a 16-bit output is rounded once from them.  P is
+ * positions that no node sees may hold anything, NaN included, and a tree node
+ * that is not finite changes only the rows of nodes that see it (with V, all of
+ * such a row and its lse become NaN, and NONFINITE is raised), so the padding of
+ * a batch may hold anything.  A committed V inside some nodes' windows has to be
+ * finite.  N = 1 with mask 1 is the single-token decode step.  A window of at
+ * least L_b + N positions is the full attention.  Softmax statistics, sums and
+ * partial outputs are fp32, and a 16-bit output is rounded once from them.  P is
  * rounded for the tensor cores: to fp16 as in lucetree_verify_attn (bf16 V is
- * then converted exactly while |v| < 65536), with a bf16 output to bf16.  A row
- * that sees no key (its mask lacks the node itself, which raises BAD_NODE)
+ * then converted exactly while |v| < 65536), with a bf16 output to bf16, which
+ * costs as much as the output's own rounding (an fp32 output is the choice with
+ * more bits; it takes up to a quarter longer).  A row that sees no key (its mask
+ * lacks the node itself, which raises BAD_NODE)
  * gives zeros and lse = -infinity.  Workspace as
  * lucetree_verify_attn_workspace.  Errors as lucetree_verify_attn, plus
  * INVALID_ARG (window, sinks, out) and UNSUPPORTED (out_dtype).

@@ -11,7 +11,8 @@
 //   - masks: in the one or two tiles with the window's edge a key counts for rows
 //     of nodes deep enough, in the tree's page for the nodes' descendants; one bit
 //     per (key, row) in warps that need it, none elsewhere.  Rows of V that no row
-//     sees are zeroed on chip (0 * NaN would poison the sum);
+//     sees are zeroed on chip (0 * NaN would poison the sum), and so are tree nodes
+//     whose V is not finite, where the epilogue makes the rows that see them NaN;
 //   - PV16 (bf16 with a bf16 output): P is rounded to bf16 and V is multiplied as
 //     it lands.  Half a step of bf16 is 2^-8 of a term, as much as the
 //     output's own rounding, and the terms' roundings are independent, so they
@@ -72,6 +73,7 @@ struct Misc {
     uint64_t vfull[kMaxSlots];   // V chunk n at [n % kMaxSlots]: landed ...
     uint64_t vready[kMaxSlots];  // ... made the operand
     uint64_t s_full, s_free, q_full, q_empty, p_full, pv_done, drain;
+    uint64_t vbad;  // nodes of the piece's tree whose V is not finite (0 where the piece ends before the tree)
     uint32_t tmem_base;
     int abort_flag;
     int empty_cols;  // a query row has seen no key of its range so far
@@ -129,6 +131,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return ~0ull >> (64 - n); }  // 1 <= n <= 64
+
+// Whether one of eight values of V is not finite as the operand of PV (0 x is 0 or, for
+// what is not finite, NaN; where bf16 becomes fp16, 65536 is not: 2^16 2^112 overflows).
+template <bool BF16, bool CONVERT>
+__device__ __forceinline__ bool not_finite(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (BF16) {
+            __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[k]), y = *reinterpret_cast<__nv_bfloat162*>(&sum);
+            if constexpr (CONVERT) x = __hmul2(x, __bfloat162bfloat162(__ushort_as_bfloat16(0x7780)));  // 2^112
+            y = __hfma2(x, __bfloat162bfloat162(__ushort_as_bfloat16(0)), y);
+            sum = *reinterpret_cast<uint32_t*>(&y);
+        } else {
+            const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&w[k]), __half2half2(__ushort_as_half(0)),
+                                      *reinterpret_cast<__half2*>(&sum));
+            sum = *reinterpret_cast<const uint32_t*>(&y);
+        }
+    }
+    return (sum & 0x7FFF7FFFu) != 0;
+}
 
 // An operand's 64-row halves: pool rows, or (tree: 0 or 1) the sequence's tree nodes.
 struct Operand {
@@ -520,9 +544,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (st == 0) ms->cur.start(start);
 
         while (true) {
-            if (st == 0) ms->cur.next_piece(W);
+            if (st == 0) {
+                ms->cur.next_piece(W);
+                ms->vbad = 0;
+            }
             bar_sync(1, kSoftmaxThreads);
             if (!ms->cur.live) break;
+            // V of the tree's nodes is visible to some rows and not to others (0 * NaN): nodes that
+            // are not finite are found here, while the first tile loads, two units of 16 bytes a thread
+            // with the loads below (0.3 us of a call of one tile for each CTA; in the V warps, where V is
+            // in shared memory, 32 sequences with an fp32 output took 272 us instead of 267)
+            constexpr int kNodeUnits = D / 8;
+            const bool has_tree = pc.te == tiles_of(pc.w);
+            const int tree_units = has_tree ? p.N * kNodeUnits : 0;
+            auto tree_unit = [&](int u) {
+                const size_t row = ((size_t)pc.b * p.N + u / kNodeUnits) * p.Hkv + pc.g;
+                return u < tree_units ? __ldg(reinterpret_cast<const uint4*>(a.v_tree) + row * kNodeUnits + u % kNodeUnits)
+                                      : make_uint4(0, 0, 0, 0);
+            };
+            uint4 vt[2] = {tree_unit(st), tree_unit(st + kSoftmaxThreads)};
             // no shift yet (-inf); padding columns keep +inf, so their exponents are -inf and P = 0
             for (int col = st; col < RGP; col += kSoftmaxThreads) {
                 ms->neg_m[col] = col < R_seg ? INFINITY : -INFINITY;
@@ -535,6 +575,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int i = st; i < p.N; i += kSoftmaxThreads)
                 ms->anc[i] = a.anc_mask[(size_t)pc.b * p.N + i] & low_bits(p.N);
+#pragma unroll 1
+            for (int u = st; u < tree_units; u += 2 * kSoftmaxThreads) {
+                if (u > st) {
+                    vt[0] = tree_unit(u);
+                    vt[1] = tree_unit(u + kSoftmaxThreads);
+                }
+                if (not_finite<BF16, kConvert>(vt[0]))
+                    atomicOr(reinterpret_cast<unsigned long long*>(&ms->vbad), 1ull << (u / kNodeUnits));
+                if (not_finite<BF16, kConvert>(vt[1]))
+                    atomicOr(reinterpret_cast<unsigned long long*>(&ms->vbad), 1ull << ((u + kSoftmaxThreads) / kNodeUnits));
+            }
             if (st == 0) {
                 ms->empty_cols = 0;
                 if (pc.g == 0 && rg == 0) seq_len(a.ctx_len, pc.b, p.max_pages, a.status);  // flags a bad length
@@ -799,6 +850,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(ph[4 * bi], ph[4 * bi + 1], ph[4 * bi + 2], ph[4 * bi + 3]);
                     }
                 }
+                if (__builtin_expect(t == pc.te - 1 && ms->vbad != 0, 0)) {
+                    // V(j) is in the ring until its PV, which waits for this warp's P^T: the chunks of
+                    // the tree's half, as the V warps left them (ring position as there)
+                    const uint32_t vbase = ((j + 1 < n_tiles ? j + 2 : j + 1) + j) * kChunks;
+#pragma unroll 1
+                    for (int c = (pc.w.vp & 1); c < kChunks; c += 2) {
+                        const uint32_t vn = j * kChunks + c;
+                        if (!bad && !wait_all(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) bad = true;
+                        uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
+                        for (int u = st; u < kChunkBytes / 16 && !bad; u += kSoftmaxThreads)
+                            if ((ms->vbad >> ((u & 511) >> 3)) & 1ull) base[u] = make_uint4(0, 0, 0, 0);
+                    }
+                }
                 tc_fence_before();
                 fence_proxy_async_smem();  // P^T stores -> tensor-core reads
                 __syncwarp();              // every lane's stores and fence come before lane 0's arrive
@@ -846,6 +910,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
+            if (__builtin_expect(ms->vbad != 0, 0)) {
+                for (int col = st; col < R_seg; col += kSoftmaxThreads) {
+                    const uint64_t anc = ms->anc[ms->node[col]];
+                    bool hit = false;
+                    for (uint64_t rest = anc & ms->vbad; rest != 0 && !hit; rest &= rest - 1) {
+                        const int dj = max(__popcll(ms->anc[__ffsll((long long)rest) - 1]) - 1, 0);
+                        hit = __popcll(anc) - 1 - dj < W.window || (long long)pc.L + dj < W.sinks;
+                    }
+                    if (!hit) continue;
+                    const float nan = __int_as_float(0x7FC00000);
+                    if (!whole) {
+                        slot[(size_t)RG * D + RG + col] = nan;
+                        continue;
+                    }
+                    ms->alpha[col] = nan;
+                    if (a.lse) a.lse[ms->out_row[col]] = nan;
+                }
+                bar_sync(1, kSoftmaxThreads);
+            }
             bool finite = true;
 #pragma unroll 1
             for (int x = 0; x < nch * Lay::kDh; ++x) {
