@@ -22,11 +22,12 @@
 //     code, and it runs once over nothing while the first tile loads: a cold
 //     instruction cache costs microseconds in calls of a few tiles.
 // Bounded by HBM while it streams with few rows (16 sequences decoding at window
-// 4096: 2.9 us a tile on every SM, 6.8 TB/s; 54 us the call with start, last tile
+// 4096: 2.9 us a tile on every SM, 6.8 TB/s; 56 us the call with start, last tile
 // and merge); by the bytes in flight that the ring beside Q and P^T allows with many
-// (32 sequences at budget 22, window 8192: 3.3 us a tile, 208 us, 5.2 TB/s); by the
+// (32 sequences at budget 22, window 8192: 3.3 us a tile, 210 us, 5.2 TB/s); by the
 // chain of lengths, page ids, first tile and epilogue in calls of a tile or two per
-// CTA (one sequence at window 4096: 20 us; 8 nodes over 260 keys: 10.2 us).
+// CTA (one sequence at window 4096: 21 us; 8 nodes over 260 keys: 10.4 us).  Keys whose
+// scores grow by 12 (log2) a tile, so that every tile moves the shifts: 446 us instead of 210.
 #pragma once
 
 #include <type_traits>
@@ -73,7 +74,7 @@ struct Misc {
     uint64_t vfull[kMaxSlots];   // V chunk n at [n % kMaxSlots]: landed ...
     uint64_t vready[kMaxSlots];  // ... made the operand
     uint64_t s_full, s_free, q_full, q_empty, p_full, pv_done, drain;
-    uint64_t vbad;  // nodes of the piece's tree whose V is not finite (0 where the piece ends before the tree)
+    uint32_t vbad[2];  // nodes of the piece's tree whose V is not finite (0 where the piece ends before the tree)
     uint32_t tmem_base;
     int abort_flag;
     int empty_cols;  // a query row has seen no key of its range so far
@@ -546,23 +547,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (true) {
             if (st == 0) {
                 ms->cur.next_piece(W);
-                ms->vbad = 0;
+                ms->vbad[0] = ms->vbad[1] = 0;
             }
             bar_sync(1, kSoftmaxThreads);
             if (!ms->cur.live) break;
             // V of the tree's nodes is visible to some rows and not to others (0 * NaN): nodes that
             // are not finite are found here, while the first tile loads, two units of 16 bytes a thread
-            // with the loads below (0.3 us of a call of one tile for each CTA; in the V warps, where V is
-            // in shared memory, 32 sequences with an fp32 output took 272 us instead of 267)
-            constexpr int kNodeUnits = D / 8;
-            const bool has_tree = pc.te == tiles_of(pc.w);
-            const int tree_units = has_tree ? p.N * kNodeUnits : 0;
-            auto tree_unit = [&](int u) {
-                const size_t row = ((size_t)pc.b * p.N + u / kNodeUnits) * p.Hkv + pc.g;
-                return u < tree_units ? __ldg(reinterpret_cast<const uint4*>(a.v_tree) + row * kNodeUnits + u % kNodeUnits)
-                                      : make_uint4(0, 0, 0, 0);
-            };
-            uint4 vt[2] = {tree_unit(st), tree_unit(st + kSoftmaxThreads)};
+            // with the loads below (one tile for each CTA 20.9 -> 21.3 us, 32 sequences 206 -> 209.5, with
+            // an fp32 output 266.5 either way; in the V warps, where V is in shared memory, 272)
+            constexpr int kNodeUnits = D / 8, kNodeStep = kSoftmaxThreads / kNodeUnits;
+            static_assert(kSoftmaxThreads % kNodeUnits == 0, "a thread's units are kNodeStep nodes apart");
+            const int tree_nodes = pc.te == tiles_of(pc.w) ? p.N : 0;
+            int vi = st / kNodeUnits;
+            const uint4* vt = reinterpret_cast<const uint4*>(a.v_tree) +
+                              (((size_t)pc.b * p.N + vi) * p.Hkv + pc.g) * kNodeUnits + st % kNodeUnits;
+            uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+            if (vi < tree_nodes) v0 = __ldg(vt);
+            if (vi + kNodeStep < tree_nodes) v1 = __ldg(vt + p.Hkv * kSoftmaxThreads);
             // no shift yet (-inf); padding columns keep +inf, so their exponents are -inf and P = 0
             for (int col = st; col < RGP; col += kSoftmaxThreads) {
                 ms->neg_m[col] = col < R_seg ? INFINITY : -INFINITY;
@@ -575,16 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int i = st; i < p.N; i += kSoftmaxThreads)
                 ms->anc[i] = a.anc_mask[(size_t)pc.b * p.N + i] & low_bits(p.N);
-#pragma unroll 1
-            for (int u = st; u < tree_units; u += 2 * kSoftmaxThreads) {
-                if (u > st) {
-                    vt[0] = tree_unit(u);
-                    vt[1] = tree_unit(u + kSoftmaxThreads);
-                }
-                if (not_finite<BF16, kConvert>(vt[0]))
-                    atomicOr(reinterpret_cast<unsigned long long*>(&ms->vbad), 1ull << (u / kNodeUnits));
-                if (not_finite<BF16, kConvert>(vt[1]))
-                    atomicOr(reinterpret_cast<unsigned long long*>(&ms->vbad), 1ull << ((u + kSoftmaxThreads) / kNodeUnits));
+            while (vi < tree_nodes) {
+                if (not_finite<BF16, kConvert>(v0)) atomicOr(&ms->vbad[vi >> 5], 1u << (vi & 31));
+                if (not_finite<BF16, kConvert>(v1)) atomicOr(&ms->vbad[(vi + kNodeStep) >> 5], 1u << ((vi + kNodeStep) & 31));
+                if ((vi += 2 * kNodeStep) >= tree_nodes) break;
+                vt += 2 * p.Hkv * kSoftmaxThreads;
+                v0 = __ldg(vt);
+                v1 = make_uint4(0, 0, 0, 0);
+                if (vi + kNodeStep < tree_nodes) v1 = __ldg(vt + p.Hkv * kSoftmaxThreads);
             }
             if (st == 0) {
                 ms->empty_cols = 0;
@@ -850,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(ph[4 * bi], ph[4 * bi + 1], ph[4 * bi + 2], ph[4 * bi + 3]);
                     }
                 }
-                if (__builtin_expect(t == pc.te - 1 && ms->vbad != 0, 0)) {
+                if (__builtin_expect(t == pc.te - 1 && (ms->vbad[0] | ms->vbad[1]) != 0, 0)) {
                     // V(j) is in the ring until its PV, which waits for this warp's P^T: the chunks of
                     // the tree's half, as the V warps left them (ring position as there)
                     const uint32_t vbase = ((j + 1 < n_tiles ? j + 2 : j + 1) + j) * kChunks;
@@ -860,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!bad && !wait_all(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) bad = true;
                         uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
                         for (int u = st; u < kChunkBytes / 16 && !bad; u += kSoftmaxThreads)
-                            if ((ms->vbad >> ((u & 511) >> 3)) & 1ull) base[u] = make_uint4(0, 0, 0, 0);
+                            if ((ms->vbad[(u & 511) >> 8] >> ((u >> 3) & 31)) & 1u) base[u] = make_uint4(0, 0, 0, 0);
                     }
                 }
                 tc_fence_before();
@@ -910,11 +909,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            if (__builtin_expect(ms->vbad != 0, 0)) {
+            if (__builtin_expect((ms->vbad[0] | ms->vbad[1]) != 0, 0)) {
                 for (int col = st; col < R_seg; col += kSoftmaxThreads) {
                     const uint64_t anc = ms->anc[ms->node[col]];
                     bool hit = false;
-                    for (uint64_t rest = anc & ms->vbad; rest != 0 && !hit; rest &= rest - 1) {
+                    for (uint64_t rest = anc & ((uint64_t)ms->vbad[1] << 32 | ms->vbad[0]); rest != 0 && !hit; rest &= rest - 1) {
                         const int dj = max(__popcll(ms->anc[__ffsll((long long)rest) - 1]) - 1, 0);
                         hit = __popcll(anc) - 1 - dj < W.window || (long long)pc.L + dj < W.sinks;
                     }
