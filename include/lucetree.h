@@ -141,7 +141,8 @@ LUCETREE_API lucetree_status lucetree_verify_attn_workspace(int B, int N, int Hq
  * the committed prefix on the tensor cores, then one merge launch that adds
  * the tree block and combines the splits by log-sum-exp.
  * Scores and sums are fp32; the P.V product runs on fp16 operands on chip
- * (P rounded to fp16, bf16 V converted exactly while |v| < 65536).
+ * (P rounded to fp16; bf16 V of the pool converted, exactly from 2^-17 to below
+ * 65536 and to within 2^-25 below that).
  * Device checks: ctx_len outside [0, max_pages_per_seq*64] -> BAD_CTX (the
  * sequence is treated as empty); page id out of range -> BAD_PAGE (those keys
  * are skipped); a mask without its own bit -> BAD_NODE; an output row that is
@@ -177,11 +178,11 @@ typedef struct lucetree_win_args {
  * finite.  N = 1 with mask 1 is the single-token decode step.  A window of at
  * least L_b + N positions is the full attention.  Softmax statistics, sums and
  * partial outputs are fp32, and a 16-bit output is rounded once from them.  P is
- * rounded for the tensor cores: to fp16 as in lucetree_verify_attn (bf16 V is
- * then converted exactly while |v| < 65536), with a bf16 output to bf16, which
- * costs as much as the output's own rounding (an fp32 output is the choice with
- * more bits; it takes up to a quarter longer).  A row that sees no key (its mask
- * lacks the node itself, which raises BAD_NODE)
+ * rounded for the tensor cores: to fp16 as in lucetree_verify_attn (and bf16 V is
+ * converted as there, the tree's too), with a bf16 output to bf16, which costs as
+ * much as the output's own rounding and leaves V as it is (an fp32 output is the
+ * choice with more bits; it takes up to a quarter longer).  A row that sees no
+ * key (its mask lacks the node itself, which raises BAD_NODE)
  * gives zeros and lse = -infinity.  Workspace as
  * lucetree_verify_attn_workspace.  Errors as lucetree_verify_attn, plus
  * INVALID_ARG (window, sinks, out) and UNSUPPORTED (out_dtype).

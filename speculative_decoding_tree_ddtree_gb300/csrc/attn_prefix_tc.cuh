@@ -19,9 +19,10 @@
 // runs on fp16: P^T is written as fp16 (11 significant bits, enough for the
 // 2e-3 bar; bf16 P with its 8 bits is not), and bf16 V chunks are converted
 // to fp16 in shared memory once they land, which is exact for every bf16
-// value of magnitude below 65536 (the fp16 range; a larger one becomes inf
-// and the merge flags the row's non-finite output).  An MMA's A and B then
-// always share one type.
+// value of magnitude from 2^-17 (whose last bit is fp16's smallest, 2^-24; below,
+// a value is off by at most half of that) to below 65536 (the fp16 range; a larger
+// one becomes inf and the merge flags the row's non-finite output).  An MMA's A
+// and B then always share one type.
 //
 // Software pipeline.  The MMA warp issues QK(t+1) as soon as the softmax has
 // released S^T(t) (after its exponent vote), before PV(t); so the scores of
@@ -247,7 +248,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 // Two bf16 (one 32-bit word) -> two fp16 (round to nearest), exact for
-// magnitudes below 65536; larger magnitudes become inf.
+// magnitudes from 2^-17 to below 65536; larger magnitudes become inf.
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
@@ -607,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (VQ == 0) {
         // ============================================================ V conversion (warps 2, 3)
-        // Each 16-bit V chunk, once landed: bf16 -> fp16 in place (exact below
-        // 65536; a larger magnitude becomes inf and the merge flags the row),
+        // Each 16-bit V chunk, once landed: bf16 -> fp16 in place (exact from
+        // 2^-17 to below 65536; a larger magnitude becomes inf and the merge flags the row),
         // and the rows of keys at or past L in a partial page zeroed (the pool
         // holds arbitrary data there and 0 * NaN would poison O^T); then
         // vready.  Doing this here rather than in the softmax warps keeps a

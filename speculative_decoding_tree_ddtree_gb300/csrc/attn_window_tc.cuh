@@ -17,7 +17,7 @@
 //     it lands.  Half a step of bf16 is 2^-8 of a term, as much as the
 //     output's own rounding, and the terms' roundings are independent, so they
 //     average out in the sum.  Otherwise P is fp16 (2^-11) and bf16 V is converted
-//     in shared memory (exact below 65536);
+//     in shared memory (exact from 2^-17 to below 65536);
 //   - the softmax's passes (try, undo, shift) are one loop around one copy of the
 //     code, and it runs once over nothing while the first tile loads: a cold
 //     instruction cache costs microseconds in calls of a few tiles.
