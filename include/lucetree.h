@@ -27,7 +27,8 @@
  * lucetree_delta_commit keeps the accepted node's state.  For KV pages kept
  * in host memory, lucetree_stage_pages brings them into the device pool.
  * lucetree_verify_attn_win is the attention of layers with a sliding window and
- * sinks.  For sequences that fork and end, lucetree_beam_select picks the
+ * sinks.  lucetree_rope gives queries and keys their positions, and
+ * lucetree_append_kv stores new tokens' keys and values in the paged cache.  For sequences that fork and end, lucetree_beam_select picks the
  * continuations, lucetree_reorder_pages, lucetree_trim_pages and
  * lucetree_compact_pages keep page tables and reference counts, and
  * lucetree_copy_pages and lucetree_reorder_states move the data.
@@ -407,6 +408,129 @@ LUCETREE_API lucetree_status lucetree_verify_attn_kq(const lucetree_attn_args* a
  * lucetree_commit.  bf16, D = 256.
  */
 LUCETREE_API lucetree_status lucetree_commit_kq(const lucetree_commit_args* args, uint8_t* k_exp, void* stream);
+
+/* Which dims of a head turn together (lucetree_rope, lucetree_append_kv). */
+#define LUCETREE_ROPE_HALF 0  /* dims i and i + rot_dims / 2 */
+#define LUCETREE_ROPE_PAIRS 1 /* dims 2 i and 2 i + 1 */
+
+/* How the angles are stretched for contexts longer than the trained one (lucetree_rope_steps). */
+#define LUCETREE_ROPE_NONE 0
+#define LUCETREE_ROPE_LINEAR 1
+#define LUCETREE_ROPE_NTK 2
+#define LUCETREE_ROPE_BANDS 3
+#define LUCETREE_ROPE_YARN 4
+
+/* Arguments of lucetree_rope_steps. */
+typedef struct lucetree_rope_config {
+    int rot_dims;          /* r: the first r dims of a head are rotated; even, 2..1024 */
+    int scaling;           /* LUCETREE_ROPE_NONE .. LUCETREE_ROPE_YARN */
+    double base;           /* > 1 */
+    double factor;         /* s >= 1: stretch (not read with NONE) */
+    double orig_ctx;       /* BANDS, YARN: the trained context C */
+    double low, high;      /* BANDS, YARN: turns over C, 0 < low < high */
+    double magnitude;      /* YARN: factor of the rotated dims, 0 = 0.1 ln(s) + 1; others: not read (1) */
+    const double* factors; /* [r / 2] (host) divisors of the angles, > 0, after the scaling; or NULL */
+} lucetree_rope_config;
+
+/*
+ * The angle per position of each rotated pair i in [0, r / 2), f_i, as
+ * steps[i] = frac(f_i / 2 pi) 2^64 (HOST output; the caller copies it to the
+ * device once and keeps it), and the factor of the rotated dims.  An integer
+ * times a step, modulo 2^64, is the angle's fraction of a turn, so an angle is as
+ * exact at position 10^6 as at 1.  With f = base^(-2 i / r):
+ *   NONE    f
+ *   LINEAR  f / s
+ *   NTK     f for the base base s^(r / (r - 2)); r > 2
+ *   BANDS   with n = C f / 2 pi turns over the trained context and
+ *           w = clamp((n - low) / (high - low), 0, 1): w f + (1 - w) f / s
+ *   YARN    with d(n) = r ln(C / 2 pi n) / (2 ln base), lo = max(floor(d(high)), 0),
+ *           hi = min(ceil(d(low)), r - 1), w = clamp((i - lo) / max(hi - lo, 0.001), 0, 1):
+ *           w f / s + (1 - w) f, and the magnitude
+ * Errors: INVALID_ARG.  No CUDA call is made.
+ */
+LUCETREE_API lucetree_status lucetree_rope_steps(const lucetree_rope_config* config, uint64_t* steps, float* magnitude);
+
+/* Arguments of lucetree_rope.  Token t = b * N + i. */
+typedef struct lucetree_rope_args {
+    int dtype;                  /* LUCETREE_F16 / LUCETREE_BF16 */
+    int B, N, Hq, Hkv, D;       /* D a multiple of 16 up to 1024 */
+    const void* q;              /* token t's [Hq][D] at element t * q_stride */
+    const void* k;              /* [Hkv][D] at t * k_stride */
+    const void* v;              /* [Hkv][D] at t * v_stride, or NULL */
+    long long q_stride, k_stride, v_stride; /* multiples of 8, at least a token's elements: views of one
+                                   projection's output are fine */
+    const uint64_t* steps;      /* device [rot_dims / 2] */
+    int rot_dims;               /* even, 2..D */
+    int layout;                 /* LUCETREE_ROPE_HALF / LUCETREE_ROPE_PAIRS */
+    float magnitude;            /* finite */
+    const int32_t* ctx_len;     /* [B] and ... */
+    const uint64_t* anc_mask;   /* ... [B][N], N <= 64: node i is at position ctx_len + its proper ancestors; or ... */
+    const int32_t* positions;   /* ... [B][N]: any positions, negative ones too (the other two are then not read) */
+    void* q_out;                /* [B][N][Hq][D] */
+    void* k_out;                /* [B][N][Hkv][D] */
+    void* v_out;                /* [B][N][Hkv][D]: v, laid out as the attention reads it; with v */
+    uint32_t* status;
+} lucetree_rope_args;
+
+/*
+ * Rotary positions of the tree's (or any) queries and keys: a pair (x, y) of
+ * rotated dims becomes m (x cos a - y sin a, x sin a + y cos a) with a = position *
+ * f_i; other dims are copied.  The products are fp32 and rounded once to the
+ * output.  Pointers are 16-byte aligned and no output overlaps an input or another
+ * output.  Errors: INVALID_ARG, UNSUPPORTED (dtype, D, layout, N > 64 with masks).
+ * Device checks: BAD_CTX (a negative ctx_len, read as 0), BAD_NODE (a mask without
+ * its own bit: the node counts as a child of the root).
+ */
+LUCETREE_API lucetree_status lucetree_rope(const lucetree_rope_args* args, void* stream);
+
+/* Arguments of lucetree_append_kv. */
+typedef struct lucetree_append_args {
+    int dtype;                  /* of q, k, v and 16-bit pools: LUCETREE_F16 / LUCETREE_BF16 */
+    int B, rows, Hq, Hkv, D;    /* sequences; rows of new tokens of all of them, >= 0; D a multiple of 16 up to 1024 */
+    int page_size;              /* must be LUCETREE_PAGE_SIZE */
+    const void* q;              /* row t's [Hq][D] at element t * q_stride, or NULL */
+    const void* k;              /* [Hkv][D] at t * k_stride */
+    const void* v;
+    long long q_stride, k_stride, v_stride; /* multiples of 8, at least a row's elements */
+    const int32_t* start;       /* [B + 1]: rows [start[b], start[b + 1]) are the new tokens of sequence b,
+                                   0 <= start[0] <= .. <= start[B] <= rows; other rows are left out */
+    const uint64_t* steps;      /* device [rot_dims / 2], or NULL: k and q are not rotated */
+    int rot_dims, layout;       /* as for lucetree_rope; not read without steps */
+    float magnitude;
+    const int32_t* page_table;  /* [B][max_pages_per_seq]; maps positions [L_b, L_b + new) */
+    int max_pages_per_seq;
+    int num_pages;
+    const int32_t* ctx_len_in;  /* [B] L_b */
+    int32_t* ctx_len_out;       /* [B] L_b + new tokens of b; must not overlap ctx_len_in */
+    int k_format;               /* LUCETREE_K_SAME, or LUCETREE_K_E4M3 (bf16, D = 256) */
+    int v_format;               /* LUCETREE_V_SAME, or LUCETREE_V_INT8 / LUCETREE_V_INT4 (D = 256) */
+    void* k_pool;               /* [num_pages][Hkv][page_size][D] in dtype, or codes; updated in place */
+    void* v_pool;               /* (int4: [num_pages][Hkv][page_size][D / 2]) */
+    uint8_t* k_exp;             /* [num_pages][Hkv][page_size], with E4M3 codes */
+    uint8_t* v_exp;             /* [num_pages][Hkv][page_size], with integer codes */
+    void* q_out;                /* [rows][Hq][D], with q */
+    uint32_t* status;
+} lucetree_append_args;
+
+/*
+ * Appends the new tokens of B sequences (prompts, parts of prompts, single
+ * tokens, none) to the paged cache: row start[b] + j goes to position p = L_b + j,
+ * page page_table[b][p / 64], slot p % 64.  With steps, k (and q, into q_out) are
+ * rotated to position p on the way, as by lucetree_rope.  Storing a row of codes:
+ *   E4M3  as lucetree_commit_kq, from the rotated fp32 values (one rounding)
+ *   INT8  e = 127 - x with x the largest integer such that max|v| 2^x <= 127 (INT4: 7),
+ *   INT4  code = round(v 2^x), ties to even
+ * and rows of zeros, or whose e would leave [1, 254], as zeros with e = 0.  Rows
+ * that are not finite are outside the contract of codes.  No other byte of pools
+ * and q_out changes.  Pointers are 16-byte aligned (indices and exponents to their
+ * type); no output overlaps an input or another output.  Errors: INVALID_ARG,
+ * UNSUPPORTED (dtype, D, layout, formats, page_size, tables of 2^25 pages or more).
+ * Device checks: BAD_ROW (start is not as above: nothing is appended), BAD_CTX
+ * (a length outside the table: nothing is appended to that sequence), BAD_PAGE (a
+ * position past the table or a page out of range: that row is not stored, and the
+ * length counts only the rows before the first such one).
+ */
+LUCETREE_API lucetree_status lucetree_append_kv(const lucetree_append_args* args, void* stream);
 
 /* Arguments of lucetree_lmhead_argmax. */
 typedef struct lucetree_lmhead_args {

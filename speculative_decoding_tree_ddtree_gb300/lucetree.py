@@ -36,6 +36,8 @@ DEV_TIMEOUT = 0x20
 DEV_NONFINITE = 0x40
 DEV_BAD_ROW = 0x80
 DEV_NO_PAGE = 0x100
+LUCETREE_ROPE_HALF, LUCETREE_ROPE_PAIRS = 0, 1
+LUCETREE_ROPE_NONE, LUCETREE_ROPE_LINEAR, LUCETREE_ROPE_NTK, LUCETREE_ROPE_BANDS, LUCETREE_ROPE_YARN = range(5)
 MAX_BEAMS = 32  # LUCETREE_MAX_BEAMS
 MAX_RESERVE = 4032  # LUCETREE_MAX_RESERVE of include/lucetree.h
 
@@ -72,6 +74,9 @@ EXPORTED = (
     "lucetree_reorder_states",
     "lucetree_beam_select_workspace",
     "lucetree_beam_select",
+    "lucetree_rope_steps",
+    "lucetree_rope",
+    "lucetree_append_kv",
 )
 
 
@@ -201,6 +206,39 @@ class ReorderStatesArgs(ctypes.Structure):
     ]
 
 
+class RopeConfig(ctypes.Structure):
+    _fields_ = [
+        ("rot_dims", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("orig_ctx", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+        ("magnitude", ctypes.c_double), ("factors", ctypes.c_void_p),
+    ]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+        ("D", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong),
+        ("steps", ctypes.c_void_p), ("rot_dims", ctypes.c_int), ("layout", ctypes.c_int), ("magnitude", ctypes.c_float),
+        ("ctx_len", ctypes.c_void_p), ("anc_mask", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("rows", ctypes.c_int), ("Hq", ctypes.c_int),
+        ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("page_size", ctypes.c_int), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_longlong),
+        ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong), ("start", ctypes.c_void_p),
+        ("steps", ctypes.c_void_p), ("rot_dims", ctypes.c_int), ("layout", ctypes.c_int), ("magnitude", ctypes.c_float),
+        ("page_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("ctx_len_in", ctypes.c_void_p), ("ctx_len_out", ctypes.c_void_p), ("k_format", ctypes.c_int),
+        ("v_format", ctypes.c_int), ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+        ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
 # The same layouts for struct.pack, which fills a whole argument struct at once
 # (the calls of small steps are bound by the host).
 _WIN_ARGS = struct.Struct("@7if3PiPi7P3iP")
@@ -210,9 +248,11 @@ _TRIM_ARGS = struct.Struct("@2P4iPi3P")
 _COMPACT_ARGS = struct.Struct("@P2iPi7P")
 _COPY_PAGES_ARGS = struct.Struct("@2Pi3P2qiP")
 _REORDER_STATES_ARGS = struct.Struct("@3P2iqP")
+_ROPE_ARGS = struct.Struct("@6i3P3qP2if7P")
+_APPEND_ARGS = struct.Struct("@7i3P3q2P2ifP2i2P2i6P")
 for _packer, _kind in ((_WIN_ARGS, WinArgs), (_BEAM_ARGS, BeamArgs), (_REORDER_ARGS, ReorderArgs), (_TRIM_ARGS, TrimArgs),
                        (_COMPACT_ARGS, CompactArgs), (_COPY_PAGES_ARGS, CopyPagesArgs),
-                       (_REORDER_STATES_ARGS, ReorderStatesArgs)):
+                       (_REORDER_STATES_ARGS, ReorderStatesArgs), (_ROPE_ARGS, RopeArgs), (_APPEND_ARGS, AppendArgs)):
     assert _packer.size == ctypes.sizeof(_kind), _kind.__name__
 
 
@@ -263,6 +303,9 @@ def load(path: str | None = None):
     lib.lucetree_beam_select_workspace.argtypes = [I, I, I, I, ctypes.POINTER(SZ)]
     lib.lucetree_beam_select.argtypes = [P, P, SZ, P]
     lib.lucetree_reorder_states.argtypes = [P, P]
+    lib.lucetree_rope_steps.argtypes = [ctypes.POINTER(RopeConfig), P, ctypes.POINTER(ctypes.c_float)]
+    lib.lucetree_rope.argtypes = [P, P]
+    lib.lucetree_append_kv.argtypes = [P, P]
     for name in EXPORTED:
         if name not in ("lucetree_status_string", "lucetree_abi_version"):
             getattr(lib, name).restype = I
@@ -343,8 +386,8 @@ def _device() -> int:
 
 
 # Kinds of element types that _arg checks for (None: any).
-_K_ANY, _K_I32, _K_F32, _K_W32, _K_W64, _K_F16, _K_BF16 = range(7)
-_KINDS = (None, _I32, _F32, _W32, _W64, (torch.float16,), (torch.bfloat16,))
+_K_ANY, _K_I32, _K_F32, _K_W32, _K_W64, _K_F16, _K_BF16, _K_U8 = range(8)
+_KINDS = (None, _I32, _F32, _W32, _W64, (torch.float16,), (torch.bfloat16,), _U8)
 
 
 def _arg(t, name: str, kind: int, dev: int, *shape) -> int:
@@ -362,6 +405,38 @@ def _arg(t, name: str, kind: int, dev: int, *shape) -> int:
     if not t.is_contiguous():
         raise LucetreeError(f"{name}: lucetree takes contiguous tensors")
     return t.data_ptr()
+
+
+def _rows(t, name: str, kind: int, dev: int, *shape) -> tuple:
+    """(address, elements from one row to the next) of a required tensor [.., heads, dims] whose rows of heads * dims
+    are contiguous and equally far apart, as a view of one projection's output is."""
+    if t is None:
+        raise LucetreeError(f"{name} is required")
+    _expect(t, name, shape, _KINDS[kind] or (t.dtype,))
+    if t.get_device() != dev:
+        raise LucetreeError(f"{name}: lucetree takes tensors of the current device, cuda:{dev}, got {t.device}")
+    row = shape[-2] * shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    want, step, below = 1, None, 1  # below: rows of the dims after this one
+    for i in range(len(shape) - 1, -1, -1):
+        n, stride = shape[i], t.stride(i)
+        if i >= len(shape) - 2:
+            if n != 1 and stride != want:
+                raise LucetreeError(f"{name}: a row's heads and dims have to be contiguous, got strides {t.stride()}")
+            want *= n
+        elif n != 1:
+            if step is None:
+                if stride % below:
+                    raise LucetreeError(f"{name}: rows have to be equally far apart, got strides {t.stride()}")
+                step = stride // below
+            if stride != step * below:
+                raise LucetreeError(f"{name}: rows have to be equally far apart, got strides {t.stride()}")
+            below *= n
+    step = row if step is None else step
+    if step < row:
+        raise LucetreeError(f"{name}: rows overlap: strides {t.stride()}")
+    return t.data_ptr(), step
 
 
 def _load_marshal():
@@ -382,8 +457,12 @@ def _load_marshal():
     return m.arg
 
 
-_arg_slow = _arg
+_arg_slow, _rows_slow = _arg, _rows
 _arg = _load_marshal()
+_compiled = getattr(_arg, "__self__", None)
+if hasattr(_compiled, "set_slow_rows"):  # (not in a build of an older source)
+    _compiled.set_slow_rows(_rows_slow)
+    _rows = _compiled.rows
 
 
 # the raw handle of a device's current stream, without the Stream object around it
@@ -1016,6 +1095,89 @@ def lucetree_reorder_states(state_in, src, state_out, status, stream=None):
 
 
 # ---------------------------------------------------------------- failure path self-test
+
+def lucetree_rope_steps(rot_dims: int, base: float, scaling: int = LUCETREE_ROPE_NONE, factor: float = 1.0,
+                        orig_ctx: float = 0.0, low: float = 0.0, high: float = 0.0, magnitude: float = 0.0,
+                        factors=None):
+    """(steps int64 [rot_dims / 2] on the host, magnitude): the angles per position that lucetree_rope and
+    lucetree_append_kv take (steps on the device; copy them once and keep them).  factors: divisors of the angles."""
+    c = RopeConfig()
+    c.rot_dims, c.scaling = _i32(rot_dims, "rot_dims", 2), _i32(scaling, "scaling")
+    c.base, c.factor, c.orig_ctx, c.low, c.high, c.magnitude = base, factor, orig_ctx, low, high, magnitude
+    if factors is not None:
+        factors = torch.as_tensor(factors, dtype=torch.float64, device="cpu").contiguous()
+        _expect(factors, "factors", (rot_dims // 2,), (torch.float64,))
+        c.factors = factors.data_ptr()
+    steps, m = torch.zeros(rot_dims // 2, dtype=torch.int64), ctypes.c_float(0)
+    _check(load().lucetree_rope_steps(ctypes.byref(c), steps.data_ptr(), ctypes.byref(m)))
+    return steps, m.value
+
+
+def lucetree_rope(q, k, steps, layout: int, q_out, k_out, status, ctx_len=None, anc_mask=None, positions=None, v=None,
+                  v_out=None, magnitude: float = 1.0, stream=None):
+    """Rotates q [B][N][Hq][D] and k [B][N][Hkv][D] (views of one projection's output are fine) to the positions of
+    the tree's nodes (ctx_len and anc_mask) or to `positions` [B][N]; v is copied.  Outputs are contiguous."""
+    dev = _device()
+    B, N, Hq, D = _dims(q, "q", 4)
+    Hkv = _dims(k, "k", 4)[2]
+    code = dtype_code(q)
+    kind = _K_BF16 if code == LUCETREE_BF16 else _K_F16
+    if (v is None) != (v_out is None):
+        raise LucetreeError("v and v_out go together")
+    if (positions is None) == (ctx_len is None) or (ctx_len is None) != (anc_mask is None):
+        raise LucetreeError("positions, or ctx_len and anc_mask")
+    qp, qs = _rows(q, "q", kind, dev, B, N, Hq, D)
+    kp, ks = _rows(k, "k", kind, dev, B, N, Hkv, D)
+    vp, vs = (0, 0) if v is None else _rows(v, "v", kind, dev, B, N, Hkv, D)
+    pairs = _dims(steps, "steps", 1)[0]
+    args = _ROPE_ARGS.pack(
+        code, B, N, Hq, Hkv, D, qp, kp, vp, qs, ks, vs, _arg(steps, "steps", _K_W64, dev, pairs), 2 * pairs,
+        _i32(layout, "layout"), magnitude, 0 if ctx_len is None else _arg(ctx_len, "ctx_len", _K_I32, dev, B),
+        0 if anc_mask is None else _arg(anc_mask, "anc_mask", _K_W64, dev, B, N),
+        0 if positions is None else _arg(positions, "positions", _K_I32, dev, B, N),
+        _arg(q_out, "q_out", kind, dev, B, N, Hq, D), _arg(k_out, "k_out", kind, dev, B, N, Hkv, D),
+        0 if v_out is None else _arg(v_out, "v_out", kind, dev, B, N, Hkv, D), _arg(status, "status", _K_W32, dev))
+    _check(load().lucetree_rope(args, _raw_stream(stream, dev)))
+
+
+def lucetree_append_kv(k, v, start, page_table, ctx_len_in, ctx_len_out, k_pool, v_pool, status, q=None, q_out=None,
+                       steps=None, layout: int = LUCETREE_ROPE_HALF, magnitude: float = 1.0, k_exp=None,
+                       v_format: int = LUCETREE_V_SAME, v_exp=None, stream=None):
+    """Appends rows [start[b], start[b + 1]) of k and v [rows][Hkv][D] to sequence b of the paged cache, with `steps`
+    rotated to their positions (and q [rows][Hq][D] into q_out).  k_exp: k_pool holds E4M3 codes; v_format and v_exp:
+    v_pool holds integer codes."""
+    dev = _device()
+    T, Hkv, D = _dims(k, "k", 3)
+    code = dtype_code(k)
+    kind = _K_BF16 if code == LUCETREE_BF16 else _K_F16
+    B, maxp = _dims(page_table, "page_table", 2)
+    P, _, page, _ = _dims(k_pool, "k_pool", 4)
+    if v_format not in (LUCETREE_V_SAME, LUCETREE_V_INT8, LUCETREE_V_INT4):
+        raise LucetreeError(f"unsupported V format {v_format}")
+    if (v_format == LUCETREE_V_SAME) != (v_exp is None):
+        raise LucetreeError("v_exp goes with codes in v_pool")
+    if (q is None) != (q_out is None):
+        raise LucetreeError("q and q_out go together")
+    kp, ks = _rows(k, "k", kind, dev, T, Hkv, D)
+    vp, vs = _rows(v, "v", kind, dev, T, Hkv, D)
+    Hq, qp, qs = 0, 0, 0
+    if q is not None:
+        Hq = _dims(q, "q", 3)[1]
+        qp, qs = _rows(q, "q", kind, dev, T, Hq, D)
+    pairs = 0 if steps is None else _dims(steps, "steps", 1)[0]
+    vd = D // 2 if v_format == LUCETREE_V_INT4 else D
+    args = _APPEND_ARGS.pack(
+        code, B, T, Hq, Hkv, D, page, qp, kp, vp, qs, ks, vs, _arg(start, "start", _K_I32, dev, B + 1),
+        0 if steps is None else _arg(steps, "steps", _K_W64, dev, pairs), 2 * pairs, _i32(layout, "layout"), magnitude,
+        _arg(page_table, "page_table", _K_I32, dev, B, maxp), maxp, P, _arg(ctx_len_in, "ctx_len_in", _K_I32, dev, B),
+        _arg(ctx_len_out, "ctx_len_out", _K_I32, dev, B), LUCETREE_K_SAME if k_exp is None else LUCETREE_K_E4M3, v_format,
+        _arg(k_pool, "k_pool", kind if k_exp is None else _K_U8, dev, P, Hkv, page, D),
+        _arg(v_pool, "v_pool", kind if v_exp is None else _K_U8, dev, P, Hkv, page, vd),
+        0 if k_exp is None else _arg(k_exp, "k_exp", _K_U8, dev, P, Hkv, page),
+        0 if v_exp is None else _arg(v_exp, "v_exp", _K_U8, dev, P, Hkv, page),
+        0 if q_out is None else _arg(q_out, "q_out", kind, dev, T, Hq, D), _arg(status, "status", _K_W32, dev))
+    _check(load().lucetree_append_kv(args, _raw_stream(stream, dev)))
+
 
 def lucetree_selftest_wait_timeout(status, limit_cycles: int, waited_cycles=None, stream=None):
     """One block waits on a barrier nothing arrives on; after ~limit_cycles SM
