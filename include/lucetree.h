@@ -27,7 +27,8 @@
  * lucetree_delta_commit keeps the accepted node's state.  For KV pages kept
  * in host memory, lucetree_stage_pages brings them into the device pool.
  * lucetree_verify_attn_win is the attention of layers with a sliding window and
- * sinks.  lucetree_rope gives queries and keys their positions, and
+ * sinks, lucetree_verify_attn_shared (with lucetree_shared_plan) that of a batch
+ * that shares prefixes.  lucetree_rope gives queries and keys their positions, and
  * lucetree_append_kv stores new tokens' keys and values in the paged cache.  For sequences that fork and end, lucetree_beam_select picks the
  * continuations, lucetree_reorder_pages, lucetree_trim_pages and
  * lucetree_compact_pages keep page tables and reference counts, and
@@ -190,6 +191,76 @@ typedef struct lucetree_win_args {
  */
 LUCETREE_API lucetree_status lucetree_verify_attn_win(const lucetree_win_args* args, void* workspace,
                                                       size_t workspace_bytes, void* stream);
+
+/* Arguments of lucetree_shared_plan (sizes as in lucetree_attn_args). */
+typedef struct lucetree_shared_plan_args {
+    int B, N, Hq, Hkv, D;
+    const int32_t* page_table;  /* [B][max_pages_per_seq] */
+    int max_pages_per_seq;
+    int num_pages;
+    const int32_t* ctx_len;     /* [B] */
+    int groups;                 /* 1..B */
+    const int32_t* group_start; /* [groups + 1]: sequences [group_start[g], group_start[g + 1]) are group g;
+                                   0 = group_start[0] <= .. <= group_start[groups] = B */
+    int32_t* shared_pages;      /* [groups] out */
+    void* plan;                 /* out, 256-byte aligned, no initialisation */
+    size_t plan_bytes;          /* at least lucetree_shared_plan_bytes */
+    uint32_t* status;
+} lucetree_shared_plan_args;
+
+/* Bytes of a plan for these sizes on the CURRENT device.  Errors: INVALID_ARG, UNSUPPORTED. */
+LUCETREE_API lucetree_status lucetree_shared_plan_bytes(int B, int N, int Hq, int Hkv, int D, int groups,
+                                                        size_t* bytes);
+
+/*
+ * Once per decoding step, for the attention of all its layers (whose pools have the
+ * same page numbering): shared_pages[g] = the number of leading pages that all
+ * sequences of group g map to the same pool pages and have filled (their positions
+ * lie below every sequence's ctx_len), 0 for a group of one sequence; and a plan of
+ * the attention's work, which lucetree_verify_attn_shared reads.  The groups say only
+ * which sequences may have pages in common (the continuations of one prompt, the
+ * beams of a request, in consecutive rows as lucetree_reorder_pages leaves them):
+ * results do not depend on them, times do.  Errors: INVALID_ARG (also an output that
+ * overlaps an input or the other output), UNSUPPORTED, WORKSPACE (plan_bytes).
+ * Device checks: BAD_ROW (group_start is not as above: nothing is shared), BAD_CTX (a
+ * length outside the table, read as 0).
+ */
+LUCETREE_API lucetree_status lucetree_shared_plan(const lucetree_shared_plan_args* args, void* stream);
+
+/* Arguments of lucetree_verify_attn_shared. */
+typedef struct lucetree_shared_args {
+    lucetree_attn_args attn; /* as for lucetree_verify_attn, except: attn.out is not used (NULL is fine), and
+                                ctx_len is read by the plan alone */
+    int groups;              /* as the plan's */
+    const void* plan;        /* of lucetree_shared_plan for the same sizes, page table, lengths and device */
+    size_t plan_bytes;
+    int out_dtype;           /* LUCETREE_F32, or attn.dtype */
+    void* out;               /* [B][N][Hq][D] in out_dtype, 16-byte aligned; must not overlap q, the tree's K/V or
+                                the plan */
+} lucetree_shared_args;
+
+/* Workspace bytes of lucetree_verify_attn_shared on the CURRENT device (256-byte aligned, no initialisation). */
+LUCETREE_API lucetree_status lucetree_verify_attn_shared_workspace(int B, int N, int Hq, int Hkv, int D, int groups,
+                                                                   size_t* bytes);
+
+/*
+ * lucetree_verify_attn of a batch in which groups of sequences share their first
+ * pages: the same sums, but a group's common pages are read once for the rows of
+ * all its sequences.  Softmax statistics, sums and partial outputs are fp32; P and
+ * V are rounded as in lucetree_verify_attn_win (with a bf16 output P is bf16 and V as
+ * it is), and a 16-bit output is rounded once.  Keys past a sequence's length may hold
+ * anything, NaN included, and a tree node that is not finite changes only the rows
+ * of nodes that see it (with V, all of such a row and its lse become NaN, and
+ * NONFINITE is raised); committed V has to be finite.  A row that sees no key (no
+ * committed one, and its mask lacks the node itself, which raises BAD_NODE) gives
+ * zeros and lse = -infinity.  The page table's entries and the plan have to agree:
+ * a table that has changed needs a new plan.  Errors as lucetree_verify_attn, plus
+ * INVALID_ARG (groups, out, plan), UNSUPPORTED (out_dtype) and WORKSPACE (plan_bytes).
+ * Device checks as there (BAD_CTX is the plan's), plus BAD_ROW (the plan was made for
+ * other sizes: nothing is written).
+ */
+LUCETREE_API lucetree_status lucetree_verify_attn_shared(const lucetree_shared_args* args, void* workspace,
+                                                         size_t workspace_bytes, void* stream);
 
 /* Size of the device array that backs lucetree_verify_attn_noalloc: 32 MiB. */
 #define LUCETREE_NOALLOC_SCRATCH_BYTES (32u << 20)

@@ -1,0 +1,195 @@
+// attn_shared_merge.cu -- joins the partial sums of a row: those of its row block in
+// the group's common pages and those of its sequence's own pages.
+//
+// With weights w_k = 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k.  One to eight
+// warps take a row at a time: its partials' maxima and sums in one load of the
+// lanes, their O rows a few at a time.  Bound by those trips to L2, so few rows are spread
+// over many warps.  Rows that one piece holds all keys of are left alone.
+#include "attn_shared.cuh"
+#include "attn_window.cuh"
+
+namespace lucetree {
+namespace shr {
+
+namespace {
+
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kCtasPerSm = 2;
+
+using win::store_out;
+
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float (&v)[N]) {
+#pragma unroll
+    for (int x = 0; x < N; x += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p + x);
+        v[x] = f.x;
+        v[x + 1] = f.y;
+        v[x + 2] = f.z;
+        v[x + 3] = f.w;
+    }
+}
+
+template <int N, typename TO>
+__device__ __forceinline__ void store_row(TO* p, const float (&v)[N]) {
+    if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+        for (int x = 0; x < N; x += 4) *reinterpret_cast<float4*>(p + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+    } else {
+        alignas(16) TO t[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) store_out(t + x, v[x]);
+        if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+        else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
+    }
+}
+
+template <typename TO, int D>
+__global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const __grid_constant__ Launch W) {
+    constexpr int kV = D / 32;   // output dims of a lane
+    constexpr int kU = 32 / kV;  // partials in flight
+    __shared__ float s_o[kMergeWarps][D];
+    __shared__ float2 s_ml[kMergeWarps];
+    const lucetree_attn_args& a = W.a;
+    const Dims& d = W.d;
+    if (threadIdx.x == 0) pdl_trigger();
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    pdl_wait();  // the partial sums
+    if (!plan_fits(W)) return;
+    const size_t sf = slot_floats(d.RG, D), of = slot_floats(d.own.RG, D);
+    const long long rows = (long long)d.B * d.N * d.Hq, warps = (long long)gridDim.x * kMergeWarps;
+    // warps to a row: as many as keep every row in flight
+    int G = kMergeWarps;
+    while (G > 1 && rows * G > warps) G >>= 1;
+    const int member = warp % G;
+    for (long long x0 = (long long)blockIdx.x * (kMergeWarps / G); x0 < rows; x0 += warps / G) {
+        const long long x = x0 + warp / G;
+        const int b = (int)(x < rows ? x / ((long long)d.N * d.Hq) : 0), r = (int)(x % ((long long)d.N * d.Hq));
+        const int i = r / d.Hq, h = r % d.Hq, g = h / d.G, hg = h % d.G;
+        const int rg = i / d.own.NPG;
+        const Seg seg = W.plan.seg[((size_t)b * d.Hkv + g) * d.own.NG + rg];
+        const Seq q = W.plan.seq[b];
+        const bool has_row = x < rows && seg.count > 0;
+        int parts = 0, step = 0, row = 0;  // of the common pages: pieces, slots from one to the next, row of a slot
+        size_t base = 0;
+        if (has_row && q.used > 0) {
+            const Group grp = W.plan.grp[q.group];
+            const int node = (b - q.first) * d.N + i;
+            parts = grp.parts;
+            step = grp.blocks;
+            base = (size_t)grp.base + (size_t)g * parts * step + node / d.NPG;
+            row = node % d.NPG * d.G + hg;
+        }
+        const int own_row = (i - rg * d.own.NPG) * d.G + hg;
+        const int count = has_row ? parts + seg.count : 0;
+        // partial j's O row, and its maximum (the sum lies `rows of a slot` floats behind)
+        auto o_at = [&](int j) {
+            return j < parts ? W.shared_ws + (base + (size_t)j * step) * sf + (size_t)row * D
+                             : W.own_ws + (size_t)(seg.first + j - parts) * of + (size_t)own_row * D;
+        };
+        float m = -INFINITY, l = 0.f, o[kV] = {};
+        // this warp's partials are member, member + G, ..
+        const int mine = has_row ? (count - member + G - 1) / G : 0;
+        for (int k0 = 0; k0 < mine; k0 += 32) {
+            const int n = min(32, mine - k0);
+            float v[kU][kV];
+            auto load = [&](int u0) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    if (u0 + u < n) {
+                        load_row<kV>(o_at(member + (k0 + u0 + u) * G) + lane * kV, v[u]);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < kV; ++y) v[u][y] = 0.f;
+                    }
+                }
+            };
+            load(0);  // with the maxima and sums, not after them
+            float mk = -INFINITY, lk = 0.f;
+            if (lane < n) {
+                const int j = member + (k0 + lane) * G;
+                const bool shared = j < parts;
+                const int R = shared ? d.RG : d.own.RG, at = shared ? row : own_row;
+                const float* s = o_at(j) + (size_t)(R - at) * D + at;
+                mk = s[0];
+                lk = s[R];
+            }
+            float top = fmaxf(m, mk);
+#pragma unroll
+            for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+            const float w = mk > -INFINITY ? exp2f(mk - top) : 0.f;  // (0 past n)
+            float sum = w * lk;
+#pragma unroll
+            for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+            const float keep = m > -INFINITY ? exp2f(m - top) : 0.f;
+            l = fmaf(l, keep, sum);
+            m = top;
+#pragma unroll
+            for (int y = 0; y < kV; ++y) o[y] *= keep;
+            for (int u0 = 0; u0 < n; u0 += kU) {
+                if (u0 > 0) load(u0);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const float wu = __shfl_sync(0xffffffffu, w, u0 + u);
+#pragma unroll
+                    for (int y = 0; y < kV; ++y) o[y] = fmaf(wu, v[u][y], o[y]);
+                }
+            }
+        }
+        if (G > 1) {
+            // the members' parts on their common shift; the first member adds them up
+            __syncthreads();
+            if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+            for (int y = 0; y < kV; ++y) s_o[warp][y * 32 + lane] = o[y];
+            __syncthreads();
+            if (member != 0) continue;
+            float top = m;
+            for (int w = 1; w < G; ++w) top = fmaxf(top, s_ml[warp + w].x);
+            const float keep = m > -INFINITY ? exp2f(m - top) : 0.f;
+            l *= keep;
+#pragma unroll
+            for (int y = 0; y < kV; ++y) o[y] *= keep;
+            for (int w = 1; w < G; ++w) {
+                const float2 ml = s_ml[warp + w];
+                const float wt = ml.x > -INFINITY ? exp2f(ml.x - top) : 0.f;
+                l = fmaf(wt, ml.y, l);
+#pragma unroll
+                for (int y = 0; y < kV; ++y) o[y] = fmaf(wt, s_o[warp + w][y * 32 + lane], o[y]);
+            }
+            m = top;
+        }
+        if (!has_row) continue;
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN stays, and is flagged)
+        bool finite = true;
+#pragma unroll
+        for (int y = 0; y < kV; ++y) {
+            o[y] *= inv;
+            finite = finite && isfinite(o[y]);
+        }
+        store_row<kV>(reinterpret_cast<TO*>(W.out) + x * D + lane * kV, o);
+        if (!finite) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
+        if (a.lse && lane == 0) a.lse[x] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+}
+
+template <typename TO>
+cudaError_t launch(const Launch& W, cudaStream_t stream) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const long long rows = (long long)W.d.B * W.d.N * W.d.Hq, cap = (long long)kCtasPerSm * device_sm_count(dev);
+    const dim3 grid((unsigned)(rows < cap ? rows : cap)), block(kMergeThreads);
+    if (W.d.D == 256) return launch_pdl(merge_kernel<TO, 256>, grid, block, 0, stream, W);
+    return launch_pdl(merge_kernel<TO, 128>, grid, block, 0, stream, W);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_merge(const Launch& W, cudaStream_t stream) {
+    if (W.out_dtype == LUCETREE_F32) return launch<float>(W, stream);
+    return W.out_dtype == LUCETREE_BF16 ? launch<__nv_bfloat16>(W, stream) : launch<__half>(W, stream);
+}
+
+}  // namespace shr
+}  // namespace lucetree

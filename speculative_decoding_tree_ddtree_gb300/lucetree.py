@@ -77,6 +77,10 @@ EXPORTED = (
     "lucetree_rope_steps",
     "lucetree_rope",
     "lucetree_append_kv",
+    "lucetree_shared_plan_bytes",
+    "lucetree_shared_plan",
+    "lucetree_verify_attn_shared_workspace",
+    "lucetree_verify_attn_shared",
 )
 
 
@@ -206,6 +210,23 @@ class ReorderStatesArgs(ctypes.Structure):
     ]
 
 
+class SharedPlanArgs(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("page_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("ctx_len", ctypes.c_void_p), ("groups", ctypes.c_int), ("group_start", ctypes.c_void_p),
+        ("shared_pages", ctypes.c_void_p), ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class SharedArgs(ctypes.Structure):
+    _fields_ = [
+        ("attn", AttnArgs), ("groups", ctypes.c_int), ("plan", ctypes.c_void_p), ("plan_bytes", ctypes.c_size_t),
+        ("out_dtype", ctypes.c_int), ("out", ctypes.c_void_p),
+    ]
+
+
 class RopeConfig(ctypes.Structure):
     _fields_ = [
         ("rot_dims", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
@@ -248,11 +269,14 @@ _TRIM_ARGS = struct.Struct("@2P4iPi3P")
 _COMPACT_ARGS = struct.Struct("@P2iPi7P")
 _COPY_PAGES_ARGS = struct.Struct("@2Pi3P2qiP")
 _REORDER_STATES_ARGS = struct.Struct("@3P2iqP")
+_SHARED_PLAN_ARGS = struct.Struct("@5iP2iPi3PNP")
+_SHARED_ARGS = struct.Struct("@7if3PiPi7PiPNiP")
 _ROPE_ARGS = struct.Struct("@6i3P3qP2if7P")
 _APPEND_ARGS = struct.Struct("@7i3P3q2P2ifP2i2P2i6P")
 for _packer, _kind in ((_WIN_ARGS, WinArgs), (_BEAM_ARGS, BeamArgs), (_REORDER_ARGS, ReorderArgs), (_TRIM_ARGS, TrimArgs),
                        (_COMPACT_ARGS, CompactArgs), (_COPY_PAGES_ARGS, CopyPagesArgs),
-                       (_REORDER_STATES_ARGS, ReorderStatesArgs), (_ROPE_ARGS, RopeArgs), (_APPEND_ARGS, AppendArgs)):
+                       (_REORDER_STATES_ARGS, ReorderStatesArgs), (_ROPE_ARGS, RopeArgs), (_APPEND_ARGS, AppendArgs),
+                       (_SHARED_PLAN_ARGS, SharedPlanArgs), (_SHARED_ARGS, SharedArgs)):
     assert _packer.size == ctypes.sizeof(_kind), _kind.__name__
 
 
@@ -306,6 +330,10 @@ def load(path: str | None = None):
     lib.lucetree_rope_steps.argtypes = [ctypes.POINTER(RopeConfig), P, ctypes.POINTER(ctypes.c_float)]
     lib.lucetree_rope.argtypes = [P, P]
     lib.lucetree_append_kv.argtypes = [P, P]
+    lib.lucetree_shared_plan_bytes.argtypes = [I, I, I, I, I, I, ctypes.POINTER(SZ)]
+    lib.lucetree_shared_plan.argtypes = [P, P]
+    lib.lucetree_verify_attn_shared_workspace.argtypes = [I, I, I, I, I, I, ctypes.POINTER(SZ)]
+    lib.lucetree_verify_attn_shared.argtypes = [P, P, SZ, P]
     for name in EXPORTED:
         if name not in ("lucetree_status_string", "lucetree_abi_version"):
             getattr(lib, name).restype = I
@@ -595,6 +623,59 @@ def lucetree_verify_attn_win(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_t
         _arg(out, "out", _K_F32 if out_f32 else kind, dev, B, N, Hq, D))
     _check(load().lucetree_verify_attn_win(args, _arg(workspace, "workspace", _K_ANY, dev), workspace.nbytes,
                                            _raw_stream(stream, dev)))
+
+
+def lucetree_shared_plan_bytes(B: int, N: int, Hq: int, Hkv: int, D: int, groups: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().lucetree_shared_plan_bytes(B, N, Hq, Hkv, D, groups, ctypes.byref(n)))
+    return int(n.value)
+
+
+def lucetree_shared_plan(page_table, ctx_len, group_start, N: int, Hq: int, Hkv: int, D: int, num_pages: int, shared_pages,
+                         plan, status, stream=None):
+    """shared_pages int32 [groups]: leading pages that the sequences group_start[g] .. group_start[g + 1] - 1 have in
+    common; plan (bytes from lucetree_shared_plan_bytes): what lucetree_verify_attn_shared reads, for all layers of a
+    decoding step."""
+    dev = _device()
+    B, maxp = _dims(page_table, "page_table", 2)
+    groups = _dims(group_start, "group_start", 1)[0] - 1
+    args = _SHARED_PLAN_ARGS.pack(
+        B, _i32(N, "N", 1), _i32(Hq, "Hq", 1), _i32(Hkv, "Hkv", 1), _i32(D, "D", 1),
+        _arg(page_table, "page_table", _K_I32, dev, B, maxp), maxp, _i32(num_pages, "num_pages", 1),
+        _arg(ctx_len, "ctx_len", _K_I32, dev, B), groups, _arg(group_start, "group_start", _K_I32, dev, groups + 1),
+        _arg(shared_pages, "shared_pages", _K_I32, dev, groups), _arg(plan, "plan", _K_ANY, dev), plan.nbytes,
+        _arg(status, "status", _K_W32, dev))
+    _check(load().lucetree_shared_plan(args, _raw_stream(stream, dev)))
+
+
+def lucetree_verify_attn_shared_workspace(B: int, N: int, Hq: int, Hkv: int, D: int, groups: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().lucetree_verify_attn_shared_workspace(B, N, Hq, Hkv, D, groups, ctypes.byref(n)))
+    return int(n.value)
+
+
+def lucetree_verify_attn_shared(q, k_pool, v_pool, page_table, ctx_len, k_tree, v_tree, anc_mask, groups: int, plan, out,
+                                status, workspace, lse=None, scale: float | None = None, stream=None):
+    """As lucetree_verify_attn for a batch whose groups of sequences share their first pages, which are read once for a
+    group; plan from lucetree_shared_plan for the same page table and lengths.  out fp32 or in q's dtype."""
+    dev = _device()
+    B, N, Hq, D = _dims(q, "q", 4)
+    P, Hkv, page, _ = _dims(k_pool, "k_pool", 4)
+    maxp = _dims(page_table, "page_table", 2)[1]
+    code = dtype_code(q)
+    kind = _K_BF16 if code == LUCETREE_BF16 else _K_F16
+    out_f32 = out is not None and out.dtype == torch.float32
+    args = _SHARED_ARGS.pack(
+        code, B, N, Hq, Hkv, D, page, float(D) ** -0.5 if scale is None else float(scale),
+        _arg(q, "q", kind, dev, B, N, Hq, D), _arg(k_pool, "k_pool", kind, dev, P, Hkv, page, D),
+        _arg(v_pool, "v_pool", kind, dev, P, Hkv, page, D), P, _arg(page_table, "page_table", _K_I32, dev, B, maxp), maxp,
+        _arg(ctx_len, "ctx_len", _K_I32, dev, B), _arg(k_tree, "k_tree", kind, dev, B, N, Hkv, D),
+        _arg(v_tree, "v_tree", kind, dev, B, N, Hkv, D), _arg(anc_mask, "anc_mask", _K_W64, dev, B, N), 0,
+        0 if lse is None else _arg(lse, "lse", _K_F32, dev, B, N, Hq), _arg(status, "status", _K_W32, dev),
+        _i32(groups, "groups", 1), _arg(plan, "plan", _K_ANY, dev), plan.nbytes, LUCETREE_F32 if out_f32 else code,
+        _arg(out, "out", _K_F32 if out_f32 else kind, dev, B, N, Hq, D))
+    _check(load().lucetree_verify_attn_shared(args, _arg(workspace, "workspace", _K_ANY, dev), workspace.nbytes,
+                                              _raw_stream(stream, dev)))
 
 
 def lucetree_verify_attn_kq_workspace(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
