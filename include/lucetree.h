@@ -192,7 +192,7 @@ typedef struct lucetree_win_args {
 LUCETREE_API lucetree_status lucetree_verify_attn_win(const lucetree_win_args* args, void* workspace,
                                                       size_t workspace_bytes, void* stream);
 
-/* Arguments of lucetree_shared_plan (sizes as in lucetree_attn_args). */
+/* Arguments of lucetree_shared_plan (sizes as in lucetree_attn_args, but Hq / Hkv <= 128). */
 typedef struct lucetree_shared_plan_args {
     int B, N, Hq, Hkv, D;
     const int32_t* page_table;  /* [B][max_pages_per_seq] */

@@ -17,22 +17,21 @@ namespace {
 // Sizes that the kernels take; the plan of a batch for the current device.
 lucetree_status dims_of(int B, int N, int Hq, int Hkv, int D, int groups, Dims* d) {
     if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || groups <= 0 || groups > B) return LUCETREE_ERR_INVALID_ARG;
-    if (N > LUCETREE_MAX_NODES || Hq % Hkv != 0 || (D != 128 && D != 256) || Hq / Hkv > kRowsMax)
+    if (N > LUCETREE_MAX_NODES || Hq % Hkv != 0 || (D != 128 && D != 256) || Hq / Hkv > kBlockRows)
         return LUCETREE_ERR_UNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
     const int ctas = prefix_grid_ctas(dev);
     // 32-bit numbers of rows, pieces and words of the plan
-    if ((long long)B * N * Hq > 0x7fffffffll || (long long)B * Hkv * LUCETREE_MAX_NODES > 0x7ffffffll || ctas > kMaxCtas)
+    if ((long long)B * N * Hq > 0x7ff00000ll || (long long)B * Hkv * LUCETREE_MAX_NODES > 0x7ffffffll || ctas > kMaxCtas)
         return LUCETREE_ERR_UNSUPPORTED;
     *d = make_dims(B, N, Hq, Hkv, D, groups, ctas);
     return LUCETREE_OK;
 }
 
-// 32-bit numbers of tiles: every segment's, as if nothing were shared, and the row blocks'.
+// 32-bit numbers of pages and tiles: every segment's, as if nothing were shared.
 bool tiles_fit(const Dims& d, int max_pages) {
-    const long long per = ((long long)max_pages + 3) / 2;
-    return (d.segs() + d.max_items()) * per < 0x7fffffffll && (long long)d.B * max_pages < (1ll << 40);
+    return (long long)d.B * d.NG * d.Hkv * (max_pages + 8ll) < 0x7fffffffll;
 }
 
 cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
@@ -54,9 +53,9 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
     // pools as [num_pages * Hkv * 64 rows][D]; box = one 64-token page x 64 dims
     const cuuint64_t pool_dims[2] = {D, (cuuint64_t)a.num_pages * a.Hkv * kPage}, pool_strides[1] = {row};
     const cuuint32_t pool_box[2] = {64, (cuuint32_t)kPage};
-    // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x the nodes of a row block, or of a row group
+    // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x the nodes of a block of either kind
     const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.N}, q_strides[2] = {row, (cuuint64_t)a.Hq * row};
-    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPG}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.own.NPG};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPG}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPGo};
     // tree K/V as [B*N nodes][Hkv][D]; box = 64 dims of one head of a sequence's N nodes
     const cuuint64_t t_dims[3] = {D, (cuuint64_t)a.Hkv, (cuuint64_t)a.B * a.N}, t_strides[2] = {row, (cuuint64_t)a.Hkv * row};
     const cuuint32_t t_box[3] = {64, 1, (cuuint32_t)a.N};
@@ -144,8 +143,7 @@ extern "C" lucetree_status lucetree_verify_attn_shared(const lucetree_shared_arg
     const size_t need = shr::workspace_bytes(W.d);
     if (!workspace || workspace_bytes < need || !shr::aligned(workspace, 256)) return LUCETREE_ERR_WORKSPACE;
     W.a = a;
-    W.shared_ws = reinterpret_cast<float*>(workspace);
-    W.own_ws = W.shared_ws + (size_t)W.d.max_items() * shr::slot_floats(W.d.RG, W.d.D);
+    W.ws = reinterpret_cast<float*>(workspace);
     W.scale_log2 = full.scale_log2;
     W.out_dtype = w->out_dtype;
     W.out = w->out;

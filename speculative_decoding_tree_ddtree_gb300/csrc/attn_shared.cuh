@@ -1,13 +1,14 @@
 // attn_shared.cuh -- the plan of tree-verify attention over shared prefixes.
 //
-// Sequences of a group have their first `used` pages in common.  Those pages are one
-// key segment for all rows of the group (nodes of consecutive sequences, times the
-// heads of a KV head), cut into row blocks of at most kRowsMax rows; what a
-// sequence has for itself (its other pages and, as a last page, its tree) is a
-// segment of its own rows, cut into row groups as in the windowed attention.  Two
-// pages make a key tile.  The plan cuts both kinds into pieces, a list for
-// each CTA; a piece that does not hold all keys of its rows leaves a partial
-// (O, max, sum) in its slot of the workspace, and the merge joins a row's slots.
+// Rows (nodes of consecutive sequences of a group, times the query heads of a KV head)
+// are taken in blocks of at most kBlockRows.  A block's key list is made of 64-key
+// pages: the group's common pages, which all of its rows see, then for each of its
+// sequences the pages that it has for itself and a page with its tree's nodes, which
+// that sequence's rows see.  Two pages make a key tile.  In a group without common
+// pages to read once, a block holds rows of one sequence.  The segments (block, KV
+// head) form one flat list of tiles that is cut over the CTAs; a piece that does not
+// hold all tiles of its segment leaves partial sums (O, max, sum), which the merge
+// joins.
 #pragma once
 
 #include "internal.cuh"
@@ -16,71 +17,89 @@ namespace lucetree {
 namespace shr {
 
 constexpr int kMagic = 0x6c745370;
-constexpr int kMaxParts = 4;  // a CTA's fair share of tiles is cut into at most so many shared pieces
+constexpr int kBlockRows = 128;  // the MMA's M
 constexpr int kMaxCtas = 1024;
 
 struct Dims {
     int B, N, Hq, Hkv, G, D, groups;
-    int C;          // CTAs
-    RowGroups own;  // of a sequence's rows
-    int NPG, RG;    // of a shared row block: nodes (of any sequences of the group), rows
-    __host__ __device__ int segs() const { return B * Hkv * own.NG; }
-    __host__ __device__ long long max_items() const {
-        return (long long)kMaxParts * C + (long long)Hkv * ((long long)B * N / NPG + groups);
-    }
-    __host__ __device__ long long max_own() const { return (long long)C + (long long)B * Hkv * own.NG; }
+    int C;         // CTAs
+    int NPG;       // nodes of a block in a group that shares pages
+    int NG, NPGo;  // other groups: blocks of a sequence, and their nodes
+    __host__ __device__ int max_blocks() const { return B * NG; }
+    __host__ __device__ int max_segs() const { return B * NG * Hkv; }
+    __host__ __device__ long long max_pieces() const { return (long long)C + max_segs(); }
+    __host__ __device__ int max_nodes() const { return NPG > NPGo ? NPG : NPGo; }
 };
+
+// Nodes of a block: as few blocks as hold `nodes`, of equal size; whole sequences of N
+// where that takes no block more.
+inline int block_nodes(long long nodes, int N, int cap) {
+    const long long blocks = (nodes + cap - 1) / cap;
+    long long per = (nodes + blocks - 1) / blocks;
+    const long long whole = (per + N - 1) / N * N;
+    if (whole <= cap) per = whole;
+    else if (cap >= N && (nodes + cap / N * N - 1) / (cap / N * N) <= blocks) per = cap / N * N;
+    return (int)per;
+}
 
 inline Dims make_dims(int B, int N, int Hq, int Hkv, int D, int groups, int ctas) {
     Dims d;
     d.B = B; d.N = N; d.Hq = Hq; d.Hkv = Hkv; d.G = Hq / Hkv; d.D = D; d.groups = groups; d.C = ctas;
-    d.own = make_row_groups(N, d.G);
-    // row blocks of equal size for a group of the mean number of sequences
-    const long long nodes = (long long)((B + groups - 1) / groups) * N;
-    const long long cap = kRowsMax / d.G, blocks = (nodes + cap - 1) / cap;
-    d.NPG = (int)((nodes + blocks - 1) / blocks);
-    d.RG = d.NPG * d.G;
+    const int cap = kBlockRows / d.G;
+    d.NPG = block_nodes((long long)((B + groups - 1) / groups) * N, N, cap);  // by the mean group
+    d.NG = (N + cap - 1) / cap;
+    d.NPGo = (N + d.NG - 1) / d.NG;
+    d.NG = (N + d.NPGo - 1) / d.NPGo;
     return d;
 }
 
-// What a CTA does at a time: tiles [ta, te) of a segment's list of pages for some rows.
-struct Piece {
-    int b, g;           // sequence whose table row names the pages, KV head
-    int node0, nodes;   // rows: nodes [node0, node0 + nodes) of all sequences' nodes
-    int page0, vp;      // the segment's pages: vp of them from column page0 on, then the tree's if own
-    int ta, te;
-    int keys;           // committed keys from the first of page0 on
-    int slot;           // of its kind's partial sums
-    int own;            // a sequence's own segment (else a group's)
-    int reread;         // other row blocks read the same keys
+// A block of rows and its key list.
+struct Block {
+    int group;
+    int b0, seqs;      // its sequences
+    int node0, nodes;  // its rows' nodes, of all sequences' nodes
+    int used;          // common pages
+    int vp;            // pages of the key list
+    int pre;           // weight of the blocks before it
 };
-static_assert(sizeof(Piece) == 48, "three 16-byte words");
+static_assert(sizeof(Block) == 32, "two 16-byte words");
+
+// What a CTA does at a time: tiles [ta, te) of a segment.
+struct Piece {
+    int block, g;
+    int ta, te;
+    int slot;  // row of the partial sums, -1: all tiles
+    int own;   // rows of a sequence without common pages
+    int reread;  // other blocks read most of its pages too
+    int pad;
+};
+static_assert(sizeof(Piece) == 32, "two 16-byte words");
 
 struct Cta {
-    int own0, owns;  // its own-segment pieces [own0, own0 + owns)
-    int tiles;       // of all its pieces
-    int items;       // shared pieces: cta, cta + C, ..
+    int first, pieces, tiles, pad;
 };
 
 struct Group {
-    int used;   // pages that are read once for the group
-    int base;   // first shared piece (and slot)
-    int parts;  // pieces of a row block and KV head
-    int blocks; // row blocks
+    int used;     // pages that are read once for the group
+    int block0;   // its first block
+    int blocks;
+    int seq0, n;  // its first sequence, and how many
 };
 
 struct Seq {
     int group, first;  // its group and that one's first sequence
-    int L, used, off;  // committed length, pages read with the group, flat number of its first own tile
+    int L, used;
+    int off;           // pages of the sequences before it, without those that are read with their groups, with their trees
+    int pad;
 };
 
 struct Seg {
-    int first, count;  // its pieces, which are its slots too; count < 0: one piece that holds all its rows' keys
+    int first, count;  // CTAs that have its tiles; count 1: no partial sums
 };
 
 struct Head {
     int magic, B, N, Hq, Hkv, D, groups, C, max_pages, num_pages;
-    int parts;  // shared pieces
+    int blocks;
     int pad[5];
 };
 
@@ -88,11 +107,11 @@ struct Plan {  // a plan's parts in its buffer
     Head* head;
     Cta* cta;
     Group* grp;
-    Seq* seq;
-    Seg* seg;
+    Seq* seq;      // [B + 1]
+    Block* blk;    // [blocks + 1]
+    Seg* seg;      // [segments], in the order of the flat list: group, KV head, block
     int* lcp;      // pages that a row has in common with its group's first
-    Piece* item;   // shared pieces, [part][row block] of each KV head of each group
-    Piece* piece;  // own pieces
+    Piece* piece;  // [CTA + segment]
 };
 
 __host__ __device__ inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -109,28 +128,32 @@ __host__ __device__ inline size_t plan_bytes(const Dims& d, Plan* p, void* at) {
     q.head = reinterpret_cast<Head*>(take(sizeof(Head)));
     q.cta = reinterpret_cast<Cta*>(take(sizeof(Cta) * (size_t)d.C));
     q.grp = reinterpret_cast<Group*>(take(sizeof(Group) * (size_t)d.groups));
-    q.seq = reinterpret_cast<Seq*>(take(sizeof(Seq) * (size_t)d.B));
-    q.seg = reinterpret_cast<Seg*>(take(sizeof(Seg) * (size_t)d.segs()));
+    q.seq = reinterpret_cast<Seq*>(take(sizeof(Seq) * ((size_t)d.B + 1)));
+    q.blk = reinterpret_cast<Block*>(take(sizeof(Block) * ((size_t)d.max_blocks() + 1)));
+    q.seg = reinterpret_cast<Seg*>(take(sizeof(Seg) * (size_t)d.max_segs()));
     q.lcp = reinterpret_cast<int*>(take(sizeof(int) * (size_t)d.B));
-    q.item = reinterpret_cast<Piece*>(take(sizeof(Piece) * (size_t)d.max_items()));
-    q.piece = reinterpret_cast<Piece*>(take(sizeof(Piece) * (size_t)d.max_own()));
+    q.piece = reinterpret_cast<Piece*>(take(sizeof(Piece) * (size_t)d.max_pieces()));
     if (p) *p = q;
     return n;
 }
 
-// Floats of a slot of partial sums: O [rows][D], max [rows], sum [rows].
-__host__ __device__ inline size_t slot_floats(int rows, int D) { return ((size_t)rows * (D + 2) + 63) / 64 * 64; }
-
-__host__ __device__ inline size_t workspace_bytes(const Dims& d) {
-    return sizeof(float) * ((size_t)d.max_items() * slot_floats(d.RG, d.D) + (size_t)d.max_own() * slot_floats(d.own.RG, d.D));
+// Partial sums by rows: O [rows][D], then max [rows], then sum [rows].  The piece of
+// segment s in CTA r has the rows from row0(s) + kBlockRows r on: row0 counts the rows
+// of the segments before s, and a segment has at most kBlockRows.
+__host__ __device__ inline size_t partial_rows(const Dims& d) {
+    return (size_t)d.B * d.N * d.Hq + (size_t)kBlockRows * d.C;
+}
+__host__ __device__ inline size_t workspace_bytes(const Dims& d) { return partial_rows(d) * (d.D + 2) * sizeof(float); }
+// ... with n_g sequences from seq0 on in the segment's group, whose block starts at node0.
+__host__ __device__ inline int row0_of(const Dims& d, int seq0, int n_g, int g, int node0) {
+    return d.G * (d.Hkv * d.N * seq0 + g * n_g * d.N + (node0 - seq0 * d.N));
 }
 
 struct Launch {
     lucetree_attn_args a;  // a.out is not used
     Dims d;
     Plan plan;
-    float* shared_ws;      // slots of shared pieces
-    float* own_ws;         // slots of own pieces
+    float* ws;
     float scale_log2;
     int out_dtype;         // LUCETREE_F32 or a.dtype
     void* out;

@@ -1,10 +1,9 @@
-// attn_shared_merge.cu -- joins the partial sums of a row: those of its row block in
-// the group's common pages and those of its sequence's own pages.
+// attn_shared_merge.cu -- joins the partial sums of rows whose segment several CTAs share.
 //
 // With weights w_k = 2^(m_k - max m), out = sum w_k O_k / sum w_k l_k.  One to eight
 // warps take a row at a time: its partials' maxima and sums in one load of the
 // lanes, their O rows a few at a time.  Bound by those trips to L2, so few rows are spread
-// over many warps.  Rows that one piece holds all keys of are left alone.
+// over many warps.  Rows whose segment lies in one CTA are left alone.
 #include "attn_shared.cuh"
 #include "attn_window.cuh"
 
@@ -57,7 +56,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     pdl_wait();  // the partial sums
     if (!plan_fits(W)) return;
-    const size_t sf = slot_floats(d.RG, D), of = slot_floats(d.own.RG, D);
+    const size_t pr = partial_rows(d);
     const long long rows = (long long)d.B * d.N * d.Hq, warps = (long long)gridDim.x * kMergeWarps;
     // warps to a row: as many as keep every row in flight
     int G = kMergeWarps;
@@ -65,29 +64,21 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
     const int member = warp % G;
     for (long long x0 = (long long)blockIdx.x * (kMergeWarps / G); x0 < rows; x0 += warps / G) {
         const long long x = x0 + warp / G;
-        const int b = (int)(x < rows ? x / ((long long)d.N * d.Hq) : 0), r = (int)(x % ((long long)d.N * d.Hq));
-        const int i = r / d.Hq, h = r % d.Hq, g = h / d.G, hg = h % d.G;
-        const int rg = i / d.own.NPG;
-        const Seg seg = W.plan.seg[((size_t)b * d.Hkv + g) * d.own.NG + rg];
+        const int node = (int)((x < rows ? x : 0) / d.Hq), h = (int)(x % d.Hq), g = h / d.G;
+        // the row's segment, and where its partial sums lie
+        const int b = node / d.N;
         const Seq q = W.plan.seq[b];
-        const bool has_row = x < rows && seg.count > 0;
-        int parts = 0, step = 0, row = 0;  // of the common pages: pieces, slots from one to the next, row of a slot
-        size_t base = 0;
-        if (has_row && q.used > 0) {
-            const Group grp = W.plan.grp[q.group];
-            const int node = (b - q.first) * d.N + i;
-            parts = grp.parts;
-            step = grp.blocks;
-            base = (size_t)grp.base + (size_t)g * parts * step + node / d.NPG;
-            row = node % d.NPG * d.G + hg;
-        }
-        const int own_row = (i - rg * d.own.NPG) * d.G + hg;
-        const int count = has_row ? parts + seg.count : 0;
-        // partial j's O row, and its maximum (the sum lies `rows of a slot` floats behind)
-        auto o_at = [&](int j) {
-            return j < parts ? W.shared_ws + (base + (size_t)j * step) * sf + (size_t)row * D
-                             : W.own_ws + (size_t)(seg.first + j - parts) * of + (size_t)own_row * D;
-        };
+        Group grp = {0, 0, d.B * d.NG, 0, d.B};
+        if (q.group >= 0) grp = W.plan.grp[q.group];
+        const int k = grp.used > 0 ? (node - grp.seq0 * d.N) / d.NPG : (b - grp.seq0) * d.NG + (node - b * d.N) / d.NPGo;
+        const int node0 = grp.used > 0 ? grp.seq0 * d.N + k * d.NPG : b * d.N + (node - b * d.N) / d.NPGo * d.NPGo;
+        const Seg seg = W.plan.seg[(size_t)grp.block0 * d.Hkv + (size_t)g * grp.blocks + k];
+        const bool has_row = x < rows && seg.count > 1;
+        const int count = has_row ? seg.count : 0;
+        const size_t first = (size_t)row0_of(d, grp.seq0, grp.n, g, node0) + (size_t)kBlockRows * seg.first +
+                             (node - node0) * d.G + h % d.G;
+        // partial j's O row
+        auto o_at = [&](int j) { return W.ws + (first + (size_t)kBlockRows * j) * D; };
         float m = -INFINITY, l = 0.f, o[kV] = {};
         // this warp's partials are member, member + G, ..
         const int mine = has_row ? (count - member + G - 1) / G : 0;
@@ -108,12 +99,9 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             load(0);  // with the maxima and sums, not after them
             float mk = -INFINITY, lk = 0.f;
             if (lane < n) {
-                const int j = member + (k0 + lane) * G;
-                const bool shared = j < parts;
-                const int R = shared ? d.RG : d.own.RG, at = shared ? row : own_row;
-                const float* s = o_at(j) + (size_t)(R - at) * D + at;
+                const float* s = W.ws + pr * D + first + (size_t)kBlockRows * (member + (k0 + lane) * G);
                 mk = s[0];
-                lk = s[R];
+                lk = s[pr];
             }
             float top = fmaxf(m, mk);
 #pragma unroll

@@ -2,16 +2,10 @@
 // common, and the cut of the attention's work over the CTAs.
 //
 // One launch.  The CTAs of a cluster compare table rows with their group's first row (a
-// warp a row); then the first CTA lays the work out:
-//   - a group uses its common pages if that saves tiles: one pass over them for its row
-//     blocks instead of one for each sequence's row groups;
-//   - with T tiles a CTA's fair share, the common pages of a row block are cut into
-//     parts of at most X = T / m tiles, m = 1 .. kMaxParts chosen by the rounds that the
-//     CTAs then need; part after part, row blocks side by side, so that CTAs
-//     that read the same keys do it at the same time and the second finds them in L2;
-//   - own tiles fill the CTAs up to a common level: one flat list, cut in CTA order.
-// Bound by its chain of dependent steps (about a dozen); it runs once for all layers of
-// a decoding step.
+// warp a row); then the first CTA lays out blocks of rows and their key lists and cuts
+// the flat list of tiles evenly over the CTAs, with an allowance for each segment's
+// queries and output.  Bound by its chain of dependent steps (about a dozen); it
+// runs once for all layers of a decoding step.
 #include "attn_shared.cuh"
 
 namespace lucetree {
@@ -22,7 +16,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClusterMax = 8;
-constexpr int kPieceCost = 2;  // tiles' time that a piece's queries and partial sums take
+constexpr int kPieceCost = 2;  // tiles' time that a segment's queries, first tile and output take
 
 struct PlanLaunch {
     Dims d;
@@ -63,15 +57,23 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* before) {
 }
 
 __device__ __forceinline__ int pages_of(int L) { return L / kPage + (L % kPage != 0); }
-__device__ __forceinline__ int own_tiles(int L, int used) { return (pages_of(L) - used + 2) / 2; }
+__device__ __forceinline__ int tiles_of(const Block& b) { return (b.vp + 1) / 2; }
+
+// The last of n numbers that grow (at(0) <= x) which is at most x.
+template <typename F>
+__device__ __forceinline__ int last_at_most(int n, long long x, F at) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (at(mid) <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
     __shared__ int s_warp[kWarps];
-    __shared__ int s_sum[kMaxParts + 1];
-    __shared__ int s_load[kMaxCtas];
-    __shared__ int s_begin[kMaxCtas + 1];  // own tiles of the CTAs that have some
-    __shared__ int s_cta[kMaxCtas];        // which those are
-    __shared__ int s_n;
+    __shared__ int s_seg[kMaxCtas + 1], s_tile[kMaxCtas + 1];  // where each CTA that has tiles begins
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
     const Dims& d = A.d;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
         if (lane == 0) {
             if (A.ctx_len[b] != L) atomicOr(A.status, LUCETREE_DEV_BAD_CTX);
             P.lcp[b] = n;
-            P.seq[b] = Seq{g, first, L, 0, 0};
+            P.seq[b] = Seq{g, first, L, 0, 0, 0};
         }
     }
     if (gridDim.x > 1) cluster_sync();
@@ -144,228 +146,183 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
         if (z - a < 2) n = 0;
         if (lane == 0) {
             A.shared_pages[g] = n;
-            const long long blocks = ((long long)(z - a) * d.N + d.NPG - 1) / d.NPG, tiles = (n + 1) / 2;
-            const long long saved = (long long)(z - a) * d.own.NG * n / 2 - blocks * (tiles + kPieceCost);
-            P.grp[g] = Group{saved > 0 ? n : 0, 0, 0, (int)blocks};
+            // pages are read once for a block: fewer blocks than without
+            const long long blocks = ((long long)(z - a) * d.N + d.NPG - 1) / d.NPG;
+            if (blocks >= (long long)(z - a) * d.NG) n = 0;
+            P.grp[g] = Group{n, 0, n > 0 ? (int)blocks : (z - a) * d.NG, a, z - a};
         }
     }
-    if (t <= kMaxParts) s_sum[t] = 0;
     __syncthreads();
-
-    // ---------------------------------------------------- tiles
-    int own_all = 0;
+    int blocks = 0;
+    for (int g0 = 0; g0 < d.groups; g0 += kThreads) {
+        const int g = g0 + t;
+        int before;
+        const int all = block_scan(g < d.groups ? P.grp[g].blocks : 0, s_warp, &before);
+        if (g < d.groups) P.grp[g].block0 = blocks + before;
+        blocks += all;
+    }
+    if (bad) blocks = d.B * d.NG;
+    int off = 0;
     for (int b0 = 0; b0 < d.B; b0 += kThreads) {
         const int b = b0 + t;
+        Seq s = {0, 0, 0, 0, 0, 0};
         int n = 0, before;
-        Seq s = {0, 0, 0, 0, 0};
         if (b < d.B) {
             s = P.seq[b];
             s.used = s.group >= 0 ? P.grp[s.group].used : 0;
-            n = own_tiles(s.L, s.used) * d.Hkv * d.own.NG;
+            n = pages_of(s.L) - s.used + 1;
         }
         const int all = block_scan(n, s_warp, &before);
         if (b < d.B) {
-            s.off = own_all + before;
+            s.off = off + before;
             P.seq[b] = s;
         }
-        own_all += all;
+        off += all;
     }
-    int mine = 0;
-    for (int g = t; g < d.groups; g += kThreads) mine += (P.grp[g].used + 1) / 2 * P.grp[g].blocks * d.Hkv;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0 && mine) atomicAdd(&s_sum[0], mine);
+    if (t == 0) P.seq[d.B] = Seq{-1, 0, 0, 0, off, 0};
     __syncthreads();
-    const int shared_all = s_sum[0];
-    const int fair = max(1, (int)(((long long)shared_all + own_all + d.C - 1) / d.C));
 
-    // ---------------------------------------------------- parts of the shared tiles
-    int x = 1;
-    if (shared_all > 0) {
-        int n[kMaxParts] = {};
-        for (int g = t; g < d.groups; g += kThreads) {
-            const Group q = P.grp[g];
-            if (q.used == 0) continue;
-            const int tiles = (q.used + 1) / 2;
-#pragma unroll
-            for (int m = 1; m <= kMaxParts; ++m) {
-                const int len = (fair + m - 1) / m;
-                n[m - 1] += (tiles + len - 1) / len * q.blocks * d.Hkv;
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < kMaxParts; ++m) {
-            const int all = __reduce_add_sync(0xffffffffu, n[m]);
-            if (lane == 0 && all) atomicAdd(&s_sum[m + 1], all);
-        }
-        __syncthreads();
-        int best = 0x7fffffff;
-#pragma unroll
-        for (int m = 1; m <= kMaxParts; ++m) {
-            const int len = (fair + m - 1) / m, rounds = (s_sum[m] + d.C - 1) / d.C;
-            // the fullest CTA, or all with the pieces' own cost
-            const int cost = max(rounds * (len + kPieceCost), fair + (int)((long long)s_sum[m] * kPieceCost / d.C));
-            if (cost < best) {
-                best = cost;
-                x = len;
-            }
-        }
-    }
-    int items = 0;
-    for (int g0 = 0; g0 < d.groups; g0 += kThreads) {
-        const int g = g0 + t;
-        Group q = {0, 0, 0, 0};
+    // ---------------------------------------------------- blocks
+    int weight = 0;
+    for (int x0 = 0; x0 < blocks; x0 += kThreads) {
+        const int x = x0 + t;
+        Block k = {};
         int n = 0, before;
-        if (g < d.groups) {
-            q = P.grp[g];
-            q.parts = ((q.used + 1) / 2 + x - 1) / x;
-            n = q.parts * q.blocks * d.Hkv;
+        if (x < blocks) {
+            Group q = {0, 0, blocks, 0, d.B};
+            k.group = -1;
+            if (!bad) {
+                k.group = last_at_most(d.groups, x, [&](int g) { return P.grp[g].block0; });
+                q = P.grp[k.group];
+            }
+            k.used = q.used;
+            if (q.used > 0) {
+                k.node0 = q.seq0 * d.N + (x - q.block0) * d.NPG;
+                k.nodes = min(d.NPG, (q.seq0 + q.n) * d.N - k.node0);
+            } else {
+                const int b = q.seq0 + (x - q.block0) / d.NG, i = (x - q.block0) % d.NG * d.NPGo;
+                k.node0 = b * d.N + i;
+                k.nodes = min(d.NPGo, d.N - i);
+            }
+            k.b0 = k.node0 / d.N;
+            k.seqs = (k.node0 + k.nodes - 1) / d.N - k.b0 + 1;
+            k.vp = k.used + P.seq[k.b0 + k.seqs].off - P.seq[k.b0].off;
+            n = tiles_of(k) + kPieceCost;
         }
         const int all = block_scan(n, s_warp, &before);
-        if (g < d.groups) {
-            q.base = items + before;
-            P.grp[g] = q;
+        if (x < blocks) {
+            k.pre = weight + before;
+            P.blk[x] = k;
         }
-        items += all;
+        weight += all;
+    }
+    if (t == 0) {
+        Block end = {};
+        end.pre = weight;
+        P.blk[blocks] = end;
     }
     __syncthreads();
 
-    // ---------------------------------------------------- shared pieces
-    for (int c = t; c < d.C; c += kThreads) s_load[c] = 0;
-    __syncthreads();
-    for (int i = t; i < items; i += kThreads) {
-        int lo = 0, hi = d.groups - 1;  // the last group that begins at or before it (empty ones begin where the next does)
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (P.grp[mid].base <= i) lo = mid;
-            else hi = mid - 1;
-        }
-        const Group q = P.grp[lo];
-        const int rest = i - q.base, block = rest % q.blocks, part = rest / q.blocks % q.parts, g = rest / q.blocks / q.parts;
-        const int a = A.group_start[lo], z = A.group_start[lo + 1], tiles = (q.used + 1) / 2;
-        const int node = block * d.NPG;
-        Piece p;
-        p.b = a;
-        p.g = g;
-        p.node0 = a * d.N + node;
-        p.nodes = min(d.NPG, (z - a) * d.N - node);
-        p.page0 = 0;
-        p.vp = q.used;
-        p.ta = (int)((long long)tiles * part / q.parts);
-        p.te = (int)((long long)tiles * (part + 1) / q.parts);
-        p.keys = q.used * kPage;
-        p.slot = i;
-        p.own = 0;
-        p.reread = q.blocks > 1;
-        P.item[i] = p;
-        atomicAdd(&s_load[i % d.C], p.te - p.ta + kPieceCost);
-    }
-    __syncthreads();
-
-    // ---------------------------------------------------- own tiles fill up to a level
-    if (warp == 0) {
-        const int least = fair >= 8 ? 2 : 1;  // no room for less
-        auto room = [&](int level, int c) {
-            const int r = c < d.C ? level - s_load[c] : 0;
-            return r >= least ? r : 0;
+    // ---------------------------------------------------- the cut
+    // Groups' weights follow each other in the flat list, a group's KV heads, a head's
+    // blocks; a block's first kPieceCost units are no tiles.
+    const long long total = (long long)weight * d.Hkv;
+    const int groups = bad ? 1 : d.groups;
+    auto first_block = [&](int g) { return g >= groups ? blocks : bad ? 0 : P.grp[g].block0; };
+    int n = 0;
+    for (int c0 = 0; c0 < d.C; c0 += kThreads) {
+        const int c = c0 + t;
+        // the segment and tile where CTA x begins
+        auto begin = [&](int x, int& seg, int& tile) {
+            long long w = total / d.C * x + total % d.C * x / d.C;
+            if (w >= total) {
+                seg = blocks * d.Hkv;
+                tile = 0;
+                return;
+            }
+            const int g = last_at_most(groups, w, [&](int y) { return (long long)P.blk[first_block(y)].pre * d.Hkv; });
+            const int k0 = first_block(g), k1 = first_block(g + 1), base = P.blk[k0].pre, per = P.blk[k1].pre - base;
+            w -= (long long)base * d.Hkv;
+            const int h = (int)(w / per), rest = (int)(w % per);
+            const int k = k0 + last_at_most(k1 - k0, rest + base, [&](int y) { return P.blk[k0 + y].pre; });
+            seg = k0 * d.Hkv + h * (k1 - k0) + (k - k0);
+            const int tiles = tiles_of(P.blk[k]);
+            tile = rest + base - P.blk[k].pre - kPieceCost;
+            if (tile <= 1) tile = 0;  // no piece of a tile next to the segment's border
+            else if (tile >= tiles - 1) {
+                tile = 0;
+                ++seg;
+            }
         };
-        int top = 0;
-        for (int c = lane; c < d.C; c += 32) top = max(top, s_load[c]);
-        top = __reduce_max_sync(0xffffffffu, top);
-        int lo = 0, hi = top + least + own_all / d.C + 1;  // the lowest level with room for all is in (lo, hi]
-        while (hi - lo > 1) {
-            const int mid = lo + (hi - lo) / 2;
-            long long sum = 0;
-            for (int c = lane; c < d.C; c += 32) sum += room(mid, c);
-            // (a lane's sum stays below 2^31: stop counting at what is needed)
-            const unsigned part = (unsigned)(sum > own_all ? own_all : sum);
-            unsigned long long all = part;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            if (all >= (unsigned long long)own_all) hi = mid;
-            else lo = mid;
+        int seg = 0, tile = 0, seg1 = 0, tile1 = 0, before;
+        if (c < d.C) {
+            begin(c, seg, tile);
+            begin(c + 1, seg1, tile1);
         }
-        int n = 0, at = 0;
-        for (int c0 = 0; c0 < d.C; c0 += 32) {
-            const int c = c0 + lane, r = min(room(hi, c), own_all);
-            long long incl = r;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const long long from = at + incl - r;
-            const bool has = r > 0 && from < own_all;
-            const unsigned who = __ballot_sync(0xffffffffu, has);
-            if (has) {
-                const int k = n + __popc(who & ((1u << lane) - 1u));
-                s_begin[k] = (int)from;
-                s_cta[k] = c;
-            }
-            n += __popc(who);
-            const long long end = at + __shfl_sync(0xffffffffu, incl, 31);
-            at = (int)(end < own_all ? end : own_all);
+        const bool has = c < d.C && (seg != seg1 || tile != tile1);
+        const int all = block_scan(has ? 1 : 0, s_warp, &before);
+        if (has) {
+            s_seg[n + before] = seg;
+            s_tile[n + before] = tile;
         }
-        if (lane == 0) {
-            s_begin[n] = own_all;
-            s_n = n;
-        }
+        n += all;
+    }
+    const int segs = blocks * d.Hkv;
+    if (t == 0) {
+        s_seg[n] = segs;
+        s_tile[n] = 0;
     }
     __syncthreads();
-    const int n = s_n, per_seq = d.Hkv * d.own.NG;
-    // the segment that an own tile is in
-    auto seg_of = [&](int tile) {
-        int lo = 0, hi = d.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (P.seq[mid].off <= tile) lo = mid;
-            else hi = mid - 1;
-        }
-        const Seq s = P.seq[lo];
-        return lo * per_seq + (tile - s.off) / own_tiles(s.L, s.used);
+
+    // ---------------------------------------------------- pieces
+    // the block and KV head of a segment
+    auto block_of = [&](int s, int& g) {
+        const int q = last_at_most(groups, s / d.Hkv, [&](int y) { return first_block(y); });
+        const int k0 = first_block(q), per = first_block(q + 1) - k0, rest = s - k0 * d.Hkv;
+        g = rest / per;
+        return k0 + rest % per;
     };
-    for (int c = t; c < d.C; c += kThreads) {
-        const int its = (items - c + d.C - 1) / d.C;
-        P.cta[c] = Cta{0, 0, s_load[c] - max(its, 0) * kPieceCost, max(its, 0)};
+    for (int r = t; r < d.C; r += kThreads) {
+        Cta c = {0, 0, 0, 0};
+        if (r < n) {
+            c.first = r + s_seg[r];
+            c.pieces = s_seg[r + 1] - s_seg[r] + (s_tile[r + 1] > 0);
+        }
+        P.cta[r] = c;
     }
     __syncthreads();
-    for (int k = t; k < n; k += kThreads) {
-        const int from = s_begin[k], to = s_begin[k + 1], s0 = seg_of(from), s1 = seg_of(to - 1);
-        Cta& c = P.cta[s_cta[k]];
-        c.own0 = k + s0;
-        c.owns = s1 - s0 + 1;
-        c.tiles += to - from;
-    }
-    // a segment's pieces: one in each CTA that has some of its tiles, numbered by CTA and segment
-    for (int s = t; s < d.B * per_seq; s += kThreads) {
-        const int b = s / per_seq, rest = s % per_seq, g = rest / d.own.NG, rg = rest % d.own.NG;
-        const Seq q = P.seq[b];
-        const int tiles = own_tiles(q.L, q.used), from = q.off + rest * tiles;
+    for (int s = t; s < segs; s += kThreads) {
+        int g;
+        const int k = block_of(s, g);
+        const Block b = P.blk[k];
+        const int tiles = tiles_of(b);
+        // the CTAs that have its first and its last tile: the last ones that begin at or before them
         auto cta_of = [&](int tile) {
             int lo = 0, hi = n - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
-                if (s_begin[mid] <= tile) lo = mid;
+                if (s_seg[mid] < s || (s_seg[mid] == s && s_tile[mid] <= tile)) lo = mid;
                 else hi = mid - 1;
             }
             return lo;
         };
-        const int k0 = cta_of(from), k1 = cta_of(from + tiles - 1);
-        P.seg[s] = Seg{k0 + s, k0 == k1 && q.used == 0 ? -1 : k1 - k0 + 1};
-        for (int k = k0; k <= k1; ++k) {
+        const int r0 = cta_of(0), r1 = cta_of(tiles - 1);
+        P.seg[s] = Seg{r0, r1 - r0 + 1};
+        Group q = {0, 0, blocks, 0, d.B};
+        if (!bad) q = P.grp[b.group];
+        const int alike = q.used > 0 ? q.blocks : d.NG, row0 = r0 != r1 ? row0_of(d, q.seq0, q.n, g, b.node0) : 0;
+        for (int r = r0; r <= r1; ++r) {
             Piece p;
-            p.b = b;
+            p.block = k;
             p.g = g;
-            p.node0 = b * d.N + rg * d.own.NPG;
-            p.nodes = min(d.own.NPG, d.N - rg * d.own.NPG);
-            p.page0 = q.used;
-            p.vp = pages_of(q.L) - q.used;
-            p.ta = max(s_begin[k] - from, 0);
-            p.te = min(s_begin[k + 1] - from, tiles);
-            p.keys = q.L - q.used * kPage;
-            p.slot = k0 == k1 && q.used == 0 ? -1 : k + s;
-            p.own = 1;
-            p.reread = d.own.NG > 1;
-            P.piece[k + s] = p;
+            p.ta = r == r0 ? 0 : s_tile[r];
+            p.te = r == r1 ? tiles : s_tile[r + 1];
+            p.slot = r0 == r1 ? -1 : row0 + kBlockRows * r;
+            p.own = b.used == 0;
+            p.reread = alike > 1;
+            p.pad = 0;
+            P.piece[r + s] = p;
+            atomicAdd(&P.cta[r].tiles, p.te - p.ta);
         }
     }
     if (t == 0) {
@@ -374,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
         h.B = d.B; h.N = d.N; h.Hq = d.Hq; h.Hkv = d.Hkv; h.D = d.D; h.groups = d.groups; h.C = d.C;
         h.max_pages = A.max_pages;
         h.num_pages = A.num_pages;
-        h.parts = items;
+        h.blocks = blocks;
         *P.head = h;
     }
 }

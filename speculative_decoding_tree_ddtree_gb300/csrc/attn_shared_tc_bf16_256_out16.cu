@@ -5,7 +5,7 @@ namespace lucetree {
 namespace shr {
 
 cudaError_t launch_bf16_256_out16(const Maps& m, const Launch& W, cudaStream_t stream) {
-    return launch_rgp<256, true, true>(m, W, stream);
+    return launch_one<256, true, true>(m, W, stream);
 }
 
 }  // namespace shr

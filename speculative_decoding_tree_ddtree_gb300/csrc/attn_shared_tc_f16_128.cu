@@ -5,7 +5,7 @@ namespace lucetree {
 namespace shr {
 
 cudaError_t launch_f16_128(const Maps& m, const Launch& W, cudaStream_t stream) {
-    return launch_rgp<128, false, false>(m, W, stream);
+    return launch_one<128, false, false>(m, W, stream);
 }
 
 }  // namespace shr

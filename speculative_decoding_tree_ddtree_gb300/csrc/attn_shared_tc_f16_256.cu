@@ -5,7 +5,7 @@ namespace lucetree {
 namespace shr {
 
 cudaError_t launch_f16_256(const Maps& m, const Launch& W, cudaStream_t stream) {
-    return launch_rgp<256, false, false>(m, W, stream);
+    return launch_one<256, false, false>(m, W, stream);
 }
 
 }  // namespace shr

@@ -5,7 +5,7 @@ import torch
 
 PAGE = 64
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
-ROWS_MAX, MAX_PARTS = 144, 4
+BLOCK_ROWS = 128
 
 
 def batch(groups, N, seed=0, spare=3, reserve=0):
@@ -40,27 +40,28 @@ def common(ctx, start, table, pages):
     return out
 
 
-def row_groups(N, G):
-    NG = max(1, -(-N * G // ROWS_MAX))
-    NPG = -(-N // NG)
-    while NPG * G > ROWS_MAX and NPG > 1:
-        NG += 1
-        NPG = -(-N // NG)
-    return -(-N // NPG), NPG
+def block_nodes(nodes, N, cap):
+    blocks = -(-nodes // cap)
+    per = -(-nodes // blocks)
+    whole = -(-per // N) * N
+    if whole <= cap:
+        return whole
+    if cap >= N and -(-nodes // (cap // N * N)) <= blocks:
+        return cap // N * N
+    return per
 
 
 def read_plan(plan, B, N, Hq, Hkv, D, groups):
     """A plan's parts as arrays of 32-bit words."""
     raw = plan.cpu().numpy().tobytes()
     head = np.frombuffer(raw, np.int32, 16)
-    C, G = int(head[7]), Hq // Hkv
-    NG, NPG = row_groups(N, G)
-    nodes = -(-B // groups) * N
-    blocks = -(-nodes // (ROWS_MAX // G))
-    block = -(-nodes // blocks)
-    sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups, 4), seq=(B, 5), seg=(B * Hkv * NG, 2), lcp=(B, 1),
-                 item=(MAX_PARTS * C + Hkv * (B * N // block + groups), 12), piece=(C + B * Hkv * NG, 12))
-    at, out = 0, dict(NG=NG, NPG=NPG, block=block, C=C)
+    C, cap = int(head[7]), BLOCK_ROWS // (Hq // Hkv)
+    NG = -(-N // cap)
+    NPGo = -(-N // NG)
+    NG = -(-N // NPGo)
+    sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups, 5), seq=(B + 1, 6), blk=(B * NG + 1, 8), seg=(B * NG * Hkv, 2),
+                 lcp=(B, 1), piece=(C + B * NG * Hkv, 8))
+    at, out = 0, dict(NG=NG, NPGo=NPGo, NPG=block_nodes(-(-B // groups) * N, N, cap), C=C)
     for name, (n, w) in sizes.items():
         out[name] = np.frombuffer(raw, np.int32, n * w, at).reshape(n, w)
         at += -(-4 * n * w // 16) * 16
@@ -69,73 +70,59 @@ def read_plan(plan, B, N, Hq, Hkv, D, groups):
 
 
 def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
-    """Every tile of every segment belongs to exactly one piece of one CTA, and every number is in its range."""
-    B, groups = len(ctx), len(start) - 1
+    """Every row is in exactly one block, every page of a block's sequences in its key list, and every tile of every
+    segment in exactly one piece of one CTA; the rows of partial sums do not overlap."""
+    B, groups, G = len(ctx), len(start) - 1, Hq // Hkv
     p = read_plan(plan, B, N, Hq, Hkv, D, groups)
-    C, NG, NPG, block = p["C"], p["NG"], p["NPG"], p["block"]
+    C, NG, NPGo, NPG = p["C"], p["NG"], p["NPGo"], p["NPG"]
+    assert max(NPG, NPGo) * G <= BLOCK_ROWS
     assert list(p["head"][0, 1:10]) == [B, N, Hq, Hkv, D, groups, C, table.shape[1], pages]
-    items = int(p["head"][0, 10])
-    assert items <= len(p["item"])
-    both = common(ctx, start, table, pages)
+    blocks = int(p["head"][0, 10])
+    assert blocks <= B * NG
+    both, of = common(ctx, start, table, pages), [max(g for g in range(groups) if start[g] <= b) for b in range(B)]
     used = p["grp"][:, 0]
     assert all(u in (0, n) for u, n in zip(used, both))
-    seen_item, seen_own, tiles_done, own_done = set(), set(), {}, {}
-    for c in range(C):
-        own0, owns, tiles, its = p["cta"][c]
-        total = 0
-        for k in range(its):
-            i = c + k * C
-            assert i < items and i not in seen_item
-            seen_item.add(i)
-            b, g, node0, nodes, page0, vp, ta, te, keys, slot, own, reread = p["item"][i]
-            grp = list(start).index(b, 0) if start.tolist().count(b) == 1 else max(x for x in range(groups) if start[x] == b)
-            z = start[grp + 1]
-            assert own == 0 and slot == i and page0 == 0 and vp == used[grp] > 0 and keys == vp * PAGE and 0 <= g < Hkv
-            assert 0 <= ta < te <= (vp + 1) // 2 and (node0 - b * N) % block == 0
-            assert 1 <= nodes <= block and node0 + nodes <= z * N and (nodes == block or node0 + nodes == z * N)
-            assert i == p["grp"][grp, 1] + (g * p["grp"][grp, 2] + part_of(ta, (vp + 1) // 2, p["grp"][grp, 2])) * \
-                p["grp"][grp, 3] + (node0 - b * N) // block
-            tiles_done.setdefault((grp, g, node0), []).append((ta, te))
-            total += te - ta
-        for k in range(owns):
-            i = own0 + k
-            assert 0 <= i < len(p["piece"]) and i not in seen_own
-            seen_own.add(i)
-            b, g, node0, nodes, page0, vp, ta, te, keys, slot, own, reread = p["piece"][i]
-            grp = max(x for x in range(groups) if start[x] <= b)
-            u = used[grp]
-            assert own == 1 and 0 <= b < B and 0 <= g < Hkv and page0 == u and vp == -(-int(ctx[b]) // PAGE) - u >= 0
-            assert keys == ctx[b] - u * PAGE >= 0 and (node0 - b * N) % NPG == 0
-            rg = (node0 - b * N) // NPG
-            assert 0 <= rg < NG and nodes == min(NPG, N - rg * NPG) and 0 <= ta < te <= (vp + 2) // 2
-            s = (b * Hkv + g) * NG + rg
-            first, count = p["seg"][s]
-            whole = (ta, te) == (0, (vp + 2) // 2) and u == 0
-            assert (slot == -1) == whole == (count < 0)
-            if not whole:
-                assert slot == i and first <= i < first + count
-            own_done.setdefault(s, []).append((ta, te))
-            total += te - ta
-        assert total == tiles
-    assert seen_item == set(range(items))
+    own = [-(-int(ctx[b]) // PAGE) - used[of[b]] + 1 for b in range(B)]
+    assert list(p["seq"][:, 4]) == list(np.concatenate([[0], np.cumsum(own)]))
+    node = 0
+    for k in range(blocks):
+        group, b0, seqs, node0, nodes, u, vp, _ = p["blk"][k]
+        assert node0 == node and 1 <= nodes <= (NPG if u else NPGo)
+        assert b0 == node0 // N and seqs == (node0 + nodes - 1) // N - b0 + 1 and (seqs == 1 or u)
+        assert group == of[b0] == of[b0 + seqs - 1] and u == used[group] and vp == u + sum(own[b0:b0 + seqs])
+        node += nodes
+    assert node == B * N
+    # segments in the flat order: group, KV head, block
+    segs = []
     for g in range(groups):
-        n = (start[g + 1] - start[g]) * N
-        if used[g]:
-            for h in range(Hkv):
-                for x in range(-(-n // block)):
-                    joins(tiles_done.pop((g, h, start[g] * N + x * block)), (used[g] + 1) // 2)
-    assert not tiles_done
-    for s in range(B * Hkv * NG):
-        b = s // (Hkv * NG)
-        u = used[max(x for x in range(groups) if start[x] <= b)]
-        joins(own_done[s], (-(-int(ctx[b]) // PAGE) - u + 2) // 2)
-        if p["seg"][s, 1] > 0:
-            assert p["seg"][s, 1] == len(own_done[s])
+        mine = [k for k in range(blocks) if p["blk"][k, 0] == g]
+        segs += [(k, h) for h in range(Hkv) for k in mine]
+    done, rows, total = {}, [], 0
+    for c in range(C):
+        first, n, tiles, _ = p["cta"][c]
+        count = 0
+        for i in range(first, first + n):
+            assert 0 <= i < len(p["piece"])
+            block, g, ta, te, slot, alone, _, _ = p["piece"][i]
+            s = i - c
+            assert segs[s] == (block, g) and 0 <= ta < te <= (p["blk"][block, 6] + 1) // 2
+            assert alone == (p["blk"][block, 5] == 0)
+            whole = (ta, te) == (0, (p["blk"][block, 6] + 1) // 2)
+            assert (slot < 0) == whole == (p["seg"][s, 1] == 1) and p["seg"][s, 0] <= c < p["seg"][s].sum()
+            if not whole:
+                rows.append((slot, p["blk"][block, 4] * G))
+            done.setdefault(s, []).append((ta, te))
+            count += te - ta
+        assert count == tiles
+    for s, (k, _) in enumerate(segs):
+        joins(done[s], (p["blk"][k, 6] + 1) // 2)
+        assert len(done[s]) == p["seg"][s, 1]
+    at = 0
+    for slot, n in sorted(rows):
+        assert slot >= at
+        at = slot + n
+    assert at <= B * N * Hq + BLOCK_ROWS * C
     return p
-
-
-def part_of(ta, tiles, parts):
-    return next(j for j in range(parts) if tiles * j // parts == ta)
 
 
 def joins(ranges, tiles):

@@ -104,11 +104,11 @@ def near(out, lse, ref, rows=slice(None)):
     want, want_lse, bound, lse_bound = (t[rows] for t in ref)
     out = out[rows]
     bound = bound + (0 if out.dtype == torch.float32 else torch.finfo(out.dtype).eps / 2) * (want.abs() + bound)
-    assert torch.isfinite(out).all()
-    assert ((out.double() - want).abs() <= bound + 2.0 ** -24 * want.abs()).all(), \
-        float(((out.double() - want).abs() / bound).max())
+    assert bool(torch.isfinite(out).all())
+    far = float(((out.double() - want).abs() / (bound + 2.0 ** -24 * want.abs())).max())
+    assert far <= 1
     if lse is not None:
-        assert ((lse[rows].double() - want_lse).abs() <= lse_bound).all()
+        assert bool(((lse[rows].double() - want_lse).abs() <= lse_bound).all())
 
 
 def check(s, out_dtype, **kw):
@@ -130,7 +130,7 @@ CASES = [
     ([(33, [2150, 2200])],                                                   64, 12,  2, 128, "bf16"),
     ([(16, [1100, 1090, 1080])],                                             22, 24,  4, 256, "bf16"),
     ([(50, [3200 + 3 * i for i in range(40)])],                               1,  6,  1, 256, "f16"),
-    ([(12, [800, 850, 900, 820])],                                            2, 144, 1, 128, "f16"),
+    ([(12, [800, 850, 900, 820])],                                            2, 128, 1, 128, "f16"),
     ([(70, [4490, 4480 + 63])],                                              64,  8,  8, 128, "bf16"),
     ([(24, [1536 + i for i in range(8)]) for _ in range(6)],                  1, 24,  4, 256, "bf16"),
     ([(100, [6400, 9000, 6500])],                                             4,  3,  3, 256, "bf16"),

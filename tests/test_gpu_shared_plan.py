@@ -40,7 +40,7 @@ BATCHES = [
     ([(1, [64, 64])], 1, 4, 4),
     ([(100, [6400] * 40)], 64, 12, 2),
     ([(100, [6401, 100000])], 1, 2, 1),
-    ([(31, [1984 + i for i in range(7)]), (33, [2112] * 3)], 7, 144, 1),
+    ([(31, [1984 + i for i in range(7)]), (33, [2112] * 3)], 7, 128, 1),
 ]
 
 

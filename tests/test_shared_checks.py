@@ -82,7 +82,7 @@ def test_sizes():
         assert f(4, 3, 4, 2, 128, 2, None) == 1
         for bad in ((0, 3, 4, 2, 128, 1), (4, 0, 4, 2, 128, 1), (4, 3, 4, 2, 128, 0), (4, 3, 4, 2, 128, 5), (4, 3, 0, 2, 128, 1)):
             assert f(*bad, ctypes.byref(n)) == 1, bad
-        for bad in ((4, 65, 4, 2, 128, 1), (4, 3, 5, 2, 128, 1), (4, 3, 4, 2, 64, 1), (4, 3, 145, 1, 128, 1),
+        for bad in ((4, 65, 4, 2, 128, 1), (4, 3, 5, 2, 128, 1), (4, 3, 4, 2, 64, 1), (4, 3, 129, 1, 128, 1),
                     (1 << 26, 3, 16, 1, 128, 1), (1 << 21, 1, 2, 2, 128, 1)):
             assert f(*bad, ctypes.byref(n)) == 2, bad
 
