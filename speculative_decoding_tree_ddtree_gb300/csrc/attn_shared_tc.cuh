@@ -410,73 +410,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ============================================================ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_f16(128, 128, BF16 ? 1u : 0u, 0, 0);
-            constexpr uint32_t id_pv = idesc_f16(128, 128, PV16 ? 1u : 0u, 0, 1);
-            constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
-            constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
-            const uint32_t aQ = smem_u32(sQ), aS = smem_u32(sSlots);
-            uint32_t chunk = 0, jq = 0;
-            uint32_t first_bits = 0;  // bit k: the k-th last QK issued opened a piece
-            bool ok = true;
-            Cursor qk;
-            qk.start(start);
-            // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
-            // (MMAs of one thread run in order).
-            auto next_qk = [&]() {
-                qk.step(W);
-                if (!qk.live) return;
-                if (qk.first() && !(ok = mbar_wait(&ms->q_full, qk.piece_no & 1))) return;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    const int slot = chunk % kNS;
-                    if (!(ok = mbar_wait(&ms->full[slot], (chunk / kNS) & 1))) return;
-                    tc_fence_after();
+        // The whole warp goes through the loop, one elected lane issues: addresses and descriptors
+        // are then the warp's, in uniform registers (from one lane's registers an MMA took as long to
+        // issue as to run twice).
+        constexpr uint32_t id_qk = idesc_f16(128, 128, BF16 ? 1u : 0u, 0, 0);
+        constexpr uint32_t id_pv = idesc_f16(128, 128, PV16 ? 1u : 0u, 0, 1);
+        constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
+        constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
+        const uint32_t aQ = smem_u32(sQ), aS = smem_u32(sSlots);
+        const bool leader = elect_one();
+        uint32_t slot = 0, turn = 0, jq = 0;  // ring position and its pass; tiles whose QK is issued
+        uint32_t vslot = 0, vturn = 0;        // the same of V's barriers
+        uint32_t first_bits = 0;              // bit k: the k-th last QK issued opened a piece
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool w = mbar_wait(bar, parity);
+            ok = __all_sync(0xffffffffu, w);
+            return ok;
+        };
+        Cursor qk;
+        qk.start(start);
+        // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
+        // (MMAs of one thread run in order).
+        auto next_qk = [&]() {
+            qk.step(W);
+            if (!qk.live) return;
+            if (qk.first() && !wait(&ms->q_full, qk.piece_no & 1)) return;
+            const uint32_t dS = tmem + (jq & 1) * 128;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (!wait(&ms->full[slot], turn & 1)) return;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
                     for (int sub = 0; sub < 4; ++sub)
-                        mma_f16_ss(tmem + (jq & 1) * 128, make_desc(hi_k, aQ + c * kChunkBytes + sub * 32),
+                        mma_f16_ss(dS, make_desc(hi_k, aQ + c * kChunkBytes + sub * 32),
                                    make_desc(hi_k, aS + slot * kChunkBytes + sub * 32), id_qk, (c | sub) != 0);
                     mma_commit(&ms->empty[slot]);
-                    ++chunk;
                 }
+                __syncwarp();
+                if (++slot == (uint32_t)kNS) {
+                    slot = 0;
+                    ++turn;
+                }
+            }
+            if (leader) {
                 mma_commit(&ms->s_full[jq & 1]);
                 if (qk.last()) mma_commit(&ms->q_empty);
-                first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
-                ++jq;
-            };
-            next_qk();
-            if (ok && n_tiles > 1) next_qk();
-            for (uint32_t j = 0; ok && j < n_tiles; ++j) {
-                if (aborted(ms)) break;
-                // O += P(j) . V(j) once the softmax has written P(j)
-                if (!(ok = mbar_wait(&ms->p_full[j & 1], (j >> 1) & 1))) break;
+            }
+            __syncwarp();
+            first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
+            ++jq;
+        };
+        next_qk();
+        if (ok && n_tiles > 1) next_qk();
+        for (uint32_t j = 0; ok && j < n_tiles; ++j) {
+            if (__any_sync(0xffffffffu, aborted(ms))) break;
+            // O += P(j) . V(j) once the softmax has written P(j)
+            if (!wait(&ms->p_full[j & 1], (j >> 1) & 1)) break;
+            const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
+            // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..; P's columns of a page
+            // begin where S's did
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (!wait(&ms->vready[vslot], vturn & 1)) break;
                 tc_fence_after();
-                const bool first = (first_bits >> (jq - 1 - j)) & 1u;
-                // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..; P's columns of a page
-                // begin where S's did
-#pragma unroll 1
-                for (int c = 0; c < kChunks && ok; ++c) {
-                    const int slot = chunk % kNS;
-                    const uint32_t vn = j * kChunks + c;
-                    if (!(ok = mbar_wait(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1))) break;
-                    tc_fence_after();
+                if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ts(tmem + L::kColO + 128 * (c >> 1), tmem + (j & 1) * 128 + 64 * (c & 1) + 8 * ks,
+                        mma_f16_ts(tmem + L::kColO + 128 * (c >> 1), aP + 64 * (c & 1) + 8 * ks,
                                    make_desc(hi_v, aS + slot * kChunkBytes + ks * 2048), id_pv,
-                                   !(first && (c & 1) == 0 && ks == 0));
+                                   (c & 1) == 0 && ks == 0 ? more : 1u);
                     mma_commit(&ms->empty[slot]);
-                    ++chunk;
                 }
-                if (!ok) break;
-                mma_commit(&ms->pv_done[j & 1]);
-                if (j + 2 < n_tiles) next_qk();
+                __syncwarp();
+                if (++slot == (uint32_t)kNS) {
+                    slot = 0;
+                    ++turn;
+                }
+                if (++vslot == (uint32_t)kMaxSlots) {
+                    vslot = 0;
+                    ++vturn;
+                }
             }
-            if (!ok || aborted(ms)) {
-                set_abort(ms, a.status);
-                mma_commit(&ms->drain);  // every MMA issued so far has finished before TMEM is freed
-                mbar_wait(&ms->drain, 0, 200000000ll);
-            }
+            if (!ok) break;
+            if (leader) mma_commit(&ms->pv_done[j & 1]);
+            __syncwarp();
+            if (j + 2 < n_tiles) next_qk();
+        }
+        if (!ok || __any_sync(0xffffffffu, aborted(ms))) {
+            set_abort(ms, a.status);
+            if (leader) mma_commit(&ms->drain);  // every MMA issued so far has finished before TMEM is freed
+            mbar_wait(&ms->drain, 0, 200000000ll);
         }
         __syncwarp();
     } else if (warp < 4) {
