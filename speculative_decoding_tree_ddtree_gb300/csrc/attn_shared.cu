@@ -53,13 +53,16 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
     // pools as [num_pages * Hkv * 64 rows][D]; box = one 64-token page x 64 dims
     const cuuint64_t pool_dims[2] = {D, (cuuint64_t)a.num_pages * a.Hkv * kPage}, pool_strides[1] = {row};
     const cuuint32_t pool_box[2] = {64, (cuuint32_t)kPage};
+    // V: the same as [D / 64][rows][64], box = 128 dims, 64 after the other 64
+    const cuuint64_t v_dims[3] = {64, pool_dims[1], D / 64}, v_strides[2] = {row, 128};
+    const cuuint32_t v_box[3] = {64, (cuuint32_t)kPage, 2};
     // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x the nodes of a block of either kind
     const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.N}, q_strides[2] = {row, (cuuint64_t)a.Hq * row};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPG}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPGo};
     // tree K/V as [B*N nodes][Hkv][D]; box = 64 dims of one head of a sequence's N nodes
     const cuuint64_t t_dims[3] = {D, (cuuint64_t)a.Hkv, (cuuint64_t)a.B * a.N}, t_strides[2] = {row, (cuuint64_t)a.Hkv * row};
     const cuuint32_t t_box[3] = {64, 1, (cuuint32_t)a.N};
-    if (!map(&m.k, 2, a.k_pool, pool_dims, pool_strides, pool_box) || !map(&m.v, 2, a.v_pool, pool_dims, pool_strides, pool_box) ||
+    if (!map(&m.k, 2, a.k_pool, pool_dims, pool_strides, pool_box) || !map(&m.v, 3, a.v_pool, v_dims, v_strides, v_box) ||
         !map(&m.q, 3, a.q, q_dims, q_strides, q_box) || !map(&m.qown, 3, a.q, q_dims, q_strides, o_box) ||
         !map(&m.kt, 3, a.k_tree, t_dims, t_strides, t_box) || !map(&m.vt, 3, a.v_tree, t_dims, t_strides, t_box))
         return cudaErrorInvalidValue;

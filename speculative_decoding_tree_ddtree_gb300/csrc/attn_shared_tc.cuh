@@ -299,46 +299,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         // A tile's pages: pool row, or for a tree's page -1 - (first node)
         struct Operand {
-            int at[2];
+            int at0, at1;
             int g;
             uint64_t pol;
         };
-        auto issue = [&](bool is_v, const Operand& o) -> bool {
-#pragma unroll 1
+        const bool leader = elect_one();
+        uint32_t slot = 0, turn = 0, vslot = 0;  // ring position and its pass; position of V's barriers
+        auto next_slot = [&]() {
+            const bool w = mbar_wait(&ms->empty[slot], (turn & 1) ^ 1);
+            return __all_sync(0xffffffffu, w);  // lanes agree on a timeout
+        };
+        auto issue_k = [&](const Operand& o) -> bool {
+            const bool tree0 = o.at0 < 0, tree1 = o.at1 < 0;
+            const uint32_t bytes = (tree0 ? tree_bytes : 8192u) + (tree1 ? tree_bytes : 8192u);
+#pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                const int slot = chunk % kNS;
-                const bool w = mbar_wait(&ms->empty[slot], ((chunk / kNS) & 1) ^ 1);
-                if (!__all_sync(0xffffffffu, w)) return false;  // lanes agree on a timeout
-                if (lane == 0) {
+                // [128 keys: page 0 then page 1][dims 64 * c .. +63]
+                if (!next_slot()) return false;
+                if (leader) {
                     uint8_t* dst = sSlots + slot * kChunkBytes;
                     uint64_t* bar = &ms->full[slot];
-                    if (is_v) {
-                        mbar_arrive(bar);  // this fill's phase of full[slot]; the data signal is vfull
-                        bar = &ms->vfull[vchunk % kMaxSlots];
-                        // [64 keys of page c & 1][dims 128 * (c >> 1) .. +127]
-                        const int x = 128 * (c >> 1), at = o.at[c & 1];
-                        if (at < 0) {
-                            mbar_arrive_expect_tx(bar, 2 * tree_bytes);
-                            tma_load_3d(dst, &tm_vt, x, o.g, -1 - at, bar);
-                            tma_load_3d(dst + 8192, &tm_vt, x + 64, o.g, -1 - at, bar);
-                        } else {
-                            mbar_arrive_expect_tx(bar, kChunkBytes);
-                            tma_load_2d_hint(dst, &tm_v, x, at, bar, o.pol);
-                            tma_load_2d_hint(dst + 8192, &tm_v, x + 64, at, bar, o.pol);
-                        }
-                    } else {
-                        // [128 keys: page 0 then page 1][dims 64 * c .. +63]
-                        mbar_arrive_expect_tx(bar, (o.at[0] < 0 ? tree_bytes : 8192u) + (o.at[1] < 0 ? tree_bytes : 8192u));
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
+                    else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
+                    if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
+                    else tma_load_2d_hint(dst + 8192, &tm_k, 64 * c, o.at1, bar, o.pol);
+                }
+                __syncwarp();
+                ++chunk;
+                if (++slot == (uint32_t)kNS) {
+                    slot = 0;
+                    ++turn;
+                }
+            }
+            return true;
+        };
+        auto issue_v = [&](const Operand& o) -> bool {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (o.at[h] < 0) tma_load_3d(dst + 8192 * h, &tm_kt, 64 * c, o.g, -1 - o.at[h], bar);
-                            else tma_load_2d_hint(dst + 8192 * h, &tm_k, 64 * c, o.at[h], bar, o.pol);
-                        }
+            for (int c = 0; c < kChunks; ++c) {
+                // [64 keys of page c & 1][dims 128 * (c >> 1) .. +127], 64 dims after the other 64
+                if (!next_slot()) return false;
+                const int at = c & 1 ? o.at1 : o.at0;
+                const bool tree = at < 0;
+                if (leader) {
+                    uint8_t* dst = sSlots + slot * kChunkBytes;
+                    mbar_arrive(&ms->full[slot]);  // this fill's phase of full[slot]; the data signal is vfull
+                    uint64_t* bar = &ms->vfull[vslot];
+                    mbar_arrive_expect_tx(bar, tree ? 2 * tree_bytes : (uint32_t)kChunkBytes);
+                    if (tree) {
+                        tma_load_3d(dst, &tm_vt, 128 * (c >> 1), o.g, -1 - at, bar);
+                        tma_load_3d(dst + 8192, &tm_vt, 128 * (c >> 1) + 64, o.g, -1 - at, bar);
+                    } else {
+                        tma_load_3d_hint(dst, &tm_v, 0, at, 2 * (c >> 1), bar, o.pol);
                     }
                 }
                 __syncwarp();
                 ++chunk;
-                vchunk += is_v ? 1u : 0u;
+                ++vchunk;
+                if (++slot == (uint32_t)kNS) {
+                    slot = 0;
+                    ++turn;
+                }
+                if (++vslot == (uint32_t)kMaxSlots) vslot = 0;
             }
             return true;
         };
@@ -355,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return p.id >= 0 ? (p.id * d.Hkv + cur.pc.g) * kPage : oob_row;
         };
         int at_cur = 0, at_next = 0;
-        Operand v_op = {{0, 0}, 0, pol_once};  // of the tile whose V is still to be loaded
+        Operand v_op = {0, 0, 0, pol_once};  // of the tile whose V is still to be loaded
         bool have_v = false;
         // K(t), then V(t-1); after the last tile its V alone
         while (ok && cur.live) {
@@ -372,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool w = mbar_wait(&ms->q_empty, (cur.piece_no - 1) & 1);
                         if (!(ok = __all_sync(0xffffffffu, w))) break;
                     }
-                    if (lane == 0) {
+                    if (leader) {
                         const int rows = (cur.pc.own ? d.NPGo : d.NPG) * d.G;
                         const CUtensorMap* tm = cur.pc.own ? &tm_qown : &tm_q;
                         mbar_arrive_expect_tx(&ms->q_full, kChunks * rows * 128);
@@ -386,13 +408,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     at_cur = at_next;
                 }
                 if ((rel & 15) == 0) at_next = load_batch(cur.t + 16);
-                op.at[0] = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15));
-                op.at[1] = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15) + 1);
+                op.at0 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15));
+                op.at1 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15) + 1);
                 op.g = cur.pc.g;
                 op.pol = cur.pc.reread ? pol_again : pol_once;
             }
-#pragma unroll 1
-            for (int is_v = have_k ? 0 : 1; is_v < (have_v ? 2 : 1) && ok; ++is_v) ok = issue(is_v != 0, is_v ? v_op : op);
+            if (have_k) ok = issue_k(op);
+            if (ok && have_v) ok = issue_v(v_op);
             v_op = op;
             have_v = have_k;
         }
