@@ -98,9 +98,9 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
     return r;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -259,7 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 2)
         for (int i = lane; i < kBadSets * kBadWords; i += 32) ms->vbad[i / kBadWords][i % kBadWords] = 0;
-    // (rows of Q past a block's own are whatever lies there: their rows of S and O are never used)
+    // rows of Q that no piece loads: their rows of S and O are never used, but finite
+    for (int i = d.max_nodes() * d.G * 8 + threadIdx.x; i < kBlockRows * 8; i += kThreads)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) reinterpret_cast<uint4*>(sQ + c * kChunkBytes)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
     if (warp == 1) {
         tmem_alloc(&ms->tmem_base, kTmemCols);
         tmem_relinquish();
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_k = [&](const Operand& o) -> bool {
             const bool tree0 = o.at0 < 0, tree1 = o.at1 < 0;
             const uint32_t bytes = (tree0 ? tree_bytes : 8192u) + (tree1 ? tree_bytes : 8192u);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 // [128 keys: page 0 then page 1][dims 64 * c .. +63]
                 if (!next_slot()) return false;
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         auto issue_v = [&](const Operand& o) -> bool {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 // [64 keys of page c & 1][dims 128 * (c >> 1) .. +127], 64 dims after the other 64
                 if (!next_slot()) return false;
@@ -386,9 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool have_k = cur.live;
             if (have_k) {
                 const int rel = cur.t - cur.pc.ta;
+                if (rel == 0) blk = load_block(W, cur.pc.block);
+                if ((rel & 15) == 0) at_cur = at_next;
+                if (rel == 0 || (rel & 15) == 8) {
+                    at_next = load_batch(cur.t + (rel == 0 ? 0 : 8));
+                    if (rel == 0) at_cur = at_next;
+                }
                 if (rel == 0) {
-                    blk = load_block(W, cur.pc.block);
-                    at_cur = load_batch(cur.pc.ta);
                     // a new segment: its queries replace the previous ones once their last QK is done
                     if (cur.piece_no > 0) {
                         const bool w = mbar_wait(&ms->q_empty, (cur.piece_no - 1) & 1);
@@ -404,10 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     ++q_loads;
-                } else if ((rel & 15) == 0) {
-                    at_cur = at_next;
                 }
-                if ((rel & 15) == 0) at_next = load_batch(cur.t + 16);
                 op.at0 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15));
                 op.at1 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15) + 1);
                 op.g = cur.pc.g;
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!qk.live) return;
             if (qk.first() && !wait(&ms->q_full, qk.piece_no & 1)) return;
             const uint32_t dS = tmem + (jq & 1) * 128;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 if (!wait(&ms->full[slot], turn & 1)) return;
                 tc_fence_after();
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
             // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..; P's columns of a page
             // begin where S's did
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 if (!wait(&ms->vready[vslot], vturn & 1)) break;
                 tc_fence_after();
@@ -546,14 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur.step(W);
             if (!cur.live) break;
             const int rel = cur.t - cur.pc.ta;
-            auto load_words = [&](int tb) { return page_word(page_at(W, blk, 2 * tb + lane)); };
-            if (rel == 0) {
-                blk = load_block(W, cur.pc.block);
-                word_cur = load_words(cur.t);
-            } else if ((rel & 15) == 0) {
-                word_cur = word_next;
+            if (rel == 0) blk = load_block(W, cur.pc.block);
+            if ((rel & 15) == 0) word_cur = word_next;
+            if (rel == 0 || (rel & 15) == 8) {
+                word_next = page_word(page_at(W, blk, 2 * (cur.t + (rel == 0 ? 0 : 8)) + lane));
+                if (rel == 0) word_cur = word_next;
             }
-            if ((rel & 15) == 0) word_next = load_words(cur.t + 16);
             // ring position of V(j)'s first chunk: the K operands before it
             // (K(0) .. K(j+1), or .. K(j) for the last tile) and V(0) .. V(j-1)
             const uint32_t vbase = ((j + 1 < n_tiles ? j + 2 : j + 1) + j) * kChunks;
@@ -630,7 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Block blk = load_block(W, cur.pc.block);
             const bool mine = row < blk.nodes * d.G;
             const int node = blk.node0 + (mine ? row / d.G : 0);
-            const int b = node / d.N, i = node - b * d.N, seq = b - blk.b0;
+            const int b = node / d.N, i = node - b * d.N;
+            // (rows past the block's own go along with what all rows see, so that their warp needs no masks)
+            const int seq = mine || blk.seqs == 1 ? b - blk.b0 : -2;
             const uint64_t anc = __ldg(a.anc_mask + node) & low_bits(d.N);
             const long long out_row = (long long)node * d.Hq + cur.pc.g * d.G + row % d.G;
             if (mine && half == 0 && !((anc >> i) & 1u)) atomicOr(a.status, LUCETREE_DEV_BAD_NODE);
@@ -641,97 +646,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = cur.pc.ta; t < cur.pc.te; ++t) {
                 const int rel = t - cur.pc.ta;
                 const bool first = rel == 0;
-                if ((rel & 31) == 0) {
-                    if (first) word_next = page_word(page_at(W, blk, 2 * (t + lane) + half));
-                    word_cur = word_next;
-                } else if ((rel & 31) == 16) {
-                    word_next = page_word(page_at(W, blk, 2 * (t + 16 + lane) + half));
+                if ((rel & 31) == 0) word_cur = word_next;
+                if (first || (rel & 31) == 16) {
+                    word_next = page_word(page_at(W, blk, 2 * (t + (first ? 0 : 16) + lane) + half));
+                    if (first) word_cur = word_next;
                 }
                 const int word = __shfl_sync(0xffffffffu, word_cur, rel & 31);
                 const int owner = (word >> 8) - 1;
                 uint64_t vis = word & 0x80 ? anc : low_bits(word & 0x7f);
-                if (!mine || (owner >= 0 && owner != seq)) vis = 0;
+                if (owner >= 0 && owner != seq) vis = 0;
                 const bool plain = __all_sync(0xffffffffu, vis == ~0ull);
                 const bool none = __all_sync(0xffffffffu, vis == 0);
 
                 if (!wait_all(&ms->s_full[j & 1], (j >> 1) & 1)) bad = true;
                 if (!bad) tc_fence_after();
                 const uint32_t ts = tl + (j & 1) * 128 + half * 64;
-                uint32_t ph[32];     // P as 16-bit pairs
-                float sum = 0.f;     // of the tile
-                float ex = -INFINITY;
-                // P = 2^(s * scale * log2 e - m) with the current shift; 16 columns at a time,
-                // the next ones' load in flight
-                auto pass = [&](auto masked) {
-                    uint64_t acc[4] = {0, 0, 0, 0};
-                    const uint64_t scale = pack2(sl2, sl2), m2 = pack2(neg_m, neg_m);
-                    uint32_t rn[16];
-                    tmem_ld16(ts, rn);
-                    float e0 = -INFINITY, e1 = -INFINITY;
+                uint32_t x[64];  // scores in units of log2; masked ones -infinity
+                float top = -INFINITY;
+                if (!bad && !none) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[16];
-                        tmem_wait_ld_regs16(rn);
+                    for (int c = 0; c < 4; ++c) tmem_ld16(ts + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) r[k] = rn[k];
-                        if (c < 3) tmem_ld16(ts + 16 * (c + 1), rn);
-                        const uint32_t on = masked.value ? (uint32_t)(vis >> (16 * c)) & 0xFFFFu : 0xFFFFu;
+                    for (int c = 0; c < 4; ++c) tmem_wait_ld_regs16(*reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
+                    const uint64_t scale = pack2(sl2, sl2);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float2 x = unpack2(fma2(pack2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), scale, m2));
-                            if constexpr (masked.value) {
-                                if (!((on >> (2 * k)) & 1u)) x.x = -INFINITY;
-                                if (!((on >> (2 * k + 1)) & 1u)) x.y = -INFINITY;
-                            }
-                            e0 = fmaxf(e0, x.x);
-                            e1 = fmaxf(e1, x.y);
-                            const float p0 = ex2(x.x), p1 = ex2(x.y);
-                            acc[k & 3] = add2(acc[k & 3], pack2(p0, p1));
-                            ph[8 * c + k] = PV16 ? pack_bf162(p0, p1) : pack_half2(p0, p1);
-                        }
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 y = unpack2(mul2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale));
+                        x[2 * k] = __float_as_uint(y.x);
+                        x[2 * k + 1] = __float_as_uint(y.y);
                     }
-                    const float2 s = unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
-                    sum = s.x + s.y;
-                    ex = fmaxf(e0, e1);
-                };
-                auto exponents = [&]() {
-                    if (none) {
+                    if (!plain) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) ph[k] = 0;
-                        sum = 0.f;
-                        ex = -INFINITY;
-                    } else if (plain) {
-                        pass(std::false_type{});
-                    } else {
-                        pass(std::true_type{});
+                        for (int k = 0; k < 64; ++k)
+                            if (!((vis >> k) & 1u)) x[k] = 0xFF800000u;
                     }
-                };
-                if (!first && !bad) exponents();
-                // one barrier decides; a second one only when it says "again", to tell a timeout
-                // (somewhere) from shifts that have to move
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x[k]));
+                    top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                }
+                // one barrier decides whether shifts have to move (a row without one has neg_m = infinity)
                 const bool bad_now = bad || aborted(ms);
-                if (bar_sync_or(1, kSoftmaxThreads, bad_now || first || ex > kTau)) {
-                    // the row's maximum over the tile, both pages
-                    float top = -INFINITY;
-                    if (!bad && !none) {
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t r[16];
-                            tmem_ld16(ts + 16 * c, r);
-                            tmem_wait_ld_regs16(r);
-                            const uint32_t on = (uint32_t)(vis >> (16 * c));
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if ((on >> k) & 1u) top = fmaxf(top, __uint_as_float(r[k]) * sl2);
-                        }
-                    }
-                    ms->xchg[half][row] = top;
+                if (bar_sync_or(1, kSoftmaxThreads, bad_now || first || top + neg_m > kTau)) {
+                    ms->xchg[half][row] = top;  // for the row's other page
                     if (bar_sync_or(1, kSoftmaxThreads, bad_now)) {
                         bad = true;
                         break;
                     }
-                    top = fmaxf(top, ms->xchg[half ^ 1][row]);
-                    const float mo = -neg_m, mn = fmaxf(mo, top);
+                    const float mo = -neg_m, mn = fmaxf(mo, fmaxf(top, ms->xchg[half ^ 1][row]));
                     // (the shift of a row that has seen no key stays -infinity: its sum is 0)
                     const float alpha = mn > mo ? ex2(mo - mn) : 1.f;
                     neg_m = -mn;
@@ -756,15 +718,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_wait_st();
                         }
                     }
-                    if (!bad) exponents();
                     // (nobody overwrites the exchanged maxima before everybody has read them)
                     if (bar_sync_or(1, kSoftmaxThreads, bad)) {
                         bad = true;
                         break;
                     }
                 }
-                l += sum;
-                // P over S: [row][32 columns of two keys each] where my page's S began
+                // P = 2^(x - m) as 16-bit pairs, over S: [row][32 columns of two keys each] where my
+                // page's S began
+                uint32_t ph[32];
+                if (none) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) ph[k] = 0;
+                } else {
+                    const float shift = neg_m == INFINITY ? 0.f : neg_m;  // (no key yet: every x is -infinity)
+                    const uint64_t m2 = pack2(shift, shift);
+                    uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 y = unpack2(add2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), m2));
+                        const float p0 = ex2(y.x), p1 = ex2(y.y);
+                        acc[k & 3] = add2(acc[k & 3], pack2(p0, p1));
+                        ph[k] = PV16 ? pack_bf162(p0, p1) : pack_half2(p0, p1);
+                    }
+                    const float2 s = unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+                    l += s.x + s.y;
+                }
                 tmem_st16(ts, *reinterpret_cast<uint32_t(*)[16]>(&ph[0]));
                 tmem_st16(ts + 16, *reinterpret_cast<uint32_t(*)[16]>(&ph[16]));
                 tmem_wait_st();
