@@ -106,11 +106,10 @@ struct Head {
 struct Plan {  // a plan's parts in its buffer
     Head* head;
     Cta* cta;
-    Group* grp;
+    Group* grp;    // [groups + 1]
     Seq* seq;      // [B + 1]
     Block* blk;    // [blocks + 1]
     Seg* seg;      // [segments], in the order of the flat list: group, KV head, block
-    int* lcp;      // pages that a row has in common with its group's first
     Piece* piece;  // [CTA + segment]
 };
 
@@ -127,11 +126,10 @@ __host__ __device__ inline size_t plan_bytes(const Dims& d, Plan* p, void* at) {
     Plan q;
     q.head = reinterpret_cast<Head*>(take(sizeof(Head)));
     q.cta = reinterpret_cast<Cta*>(take(sizeof(Cta) * (size_t)d.C));
-    q.grp = reinterpret_cast<Group*>(take(sizeof(Group) * (size_t)d.groups));
+    q.grp = reinterpret_cast<Group*>(take(sizeof(Group) * ((size_t)d.groups + 1)));
     q.seq = reinterpret_cast<Seq*>(take(sizeof(Seq) * ((size_t)d.B + 1)));
     q.blk = reinterpret_cast<Block*>(take(sizeof(Block) * ((size_t)d.max_blocks() + 1)));
     q.seg = reinterpret_cast<Seg*>(take(sizeof(Seg) * (size_t)d.max_segs()));
-    q.lcp = reinterpret_cast<int*>(take(sizeof(int) * (size_t)d.B));
     q.piece = reinterpret_cast<Piece*>(take(sizeof(Piece) * (size_t)d.max_pieces()));
     if (p) *p = q;
     return n;

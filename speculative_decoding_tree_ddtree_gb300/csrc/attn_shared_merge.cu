@@ -68,8 +68,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
         // the row's segment, and where its partial sums lie
         const int b = node / d.N;
         const Seq q = W.plan.seq[b];
-        Group grp = {0, 0, d.B * d.NG, 0, d.B};
-        if (q.group >= 0) grp = W.plan.grp[q.group];
+        const Group grp = W.plan.grp[q.group];
         const int k = grp.used > 0 ? (node - grp.seq0 * d.N) / d.NPG : (b - grp.seq0) * d.NG + (node - b * d.N) / d.NPGo;
         const int node0 = grp.used > 0 ? grp.seq0 * d.N + k * d.NPG : b * d.N + (node - b * d.N) / d.NPGo * d.NPGo;
         const Seg seg = W.plan.seg[(size_t)grp.block0 * d.Hkv + (size_t)g * grp.blocks + k];

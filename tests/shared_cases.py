@@ -59,8 +59,8 @@ def read_plan(plan, B, N, Hq, Hkv, D, groups):
     NG = -(-N // cap)
     NPGo = -(-N // NG)
     NG = -(-N // NPGo)
-    sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups, 5), seq=(B + 1, 6), blk=(B * NG + 1, 8), seg=(B * NG * Hkv, 2),
-                 lcp=(B, 1), piece=(C + B * NG * Hkv, 8))
+    sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups + 1, 5), seq=(B + 1, 6), blk=(B * NG + 1, 8), seg=(B * NG * Hkv, 2),
+                 piece=(C + B * NG * Hkv, 8))
     at, out = 0, dict(NG=NG, NPGo=NPGo, NPG=block_nodes(-(-B // groups) * N, N, cap), C=C)
     for name, (n, w) in sizes.items():
         out[name] = np.frombuffer(raw, np.int32, n * w, at).reshape(n, w)
@@ -80,7 +80,7 @@ def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
     blocks = int(p["head"][0, 10])
     assert blocks <= B * NG
     both, of = common(ctx, start, table, pages), [max(g for g in range(groups) if start[g] <= b) for b in range(B)]
-    used = p["grp"][:, 0]
+    used = p["grp"][:groups, 0]
     assert all(u in (0, n) for u, n in zip(used, both))
     own = [-(-int(ctx[b]) // PAGE) - used[of[b]] + 1 for b in range(B)]
     assert list(p["seq"][:, 4]) == list(np.concatenate([[0], np.cumsum(own)]))
