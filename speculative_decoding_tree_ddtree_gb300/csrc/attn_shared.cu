@@ -17,7 +17,7 @@ namespace {
 // Sizes that the kernels take; the plan of a batch for the current device.
 lucetree_status dims_of(int B, int N, int Hq, int Hkv, int D, int groups, Dims* d) {
     if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || groups <= 0 || groups > B) return LUCETREE_ERR_INVALID_ARG;
-    if (N > LUCETREE_MAX_NODES || Hq % Hkv != 0 || (D != 128 && D != 256) || Hq / Hkv > kBlockRows)
+    if (N > LUCETREE_MAX_NODES || Hq % Hkv != 0 || (D != 128 && D != 256) || Hq / Hkv > kRows)
         return LUCETREE_ERR_UNSUPPORTED;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
@@ -53,16 +53,19 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
     // pools as [num_pages * Hkv * 64 rows][D]; box = one 64-token page x 64 dims
     const cuuint64_t pool_dims[2] = {D, (cuuint64_t)a.num_pages * a.Hkv * kPage}, pool_strides[1] = {row};
     const cuuint32_t pool_box[2] = {64, (cuuint32_t)kPage};
-    // V: the same as [D / 64][rows][64], box = 128 dims, 64 after the other 64
+    // V (K of a pair): the same as [D / 64][rows][64], box = 128 dims, 64 after the other 64 (V of a pair
+    // with D = 128: half of the dims)
     const cuuint64_t v_dims[3] = {64, pool_dims[1], D / 64}, v_strides[2] = {row, 128};
-    const cuuint32_t v_box[3] = {64, (cuuint32_t)kPage, 2};
-    // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x the nodes of a block of either kind
+    const cuuint32_t w_box[3] = {64, (cuuint32_t)kPage, 2}, v_box[3] = {64, (cuuint32_t)kPage, p.pair == 2 && D == 128 ? 1u : 2u};
+    // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x a CTA's nodes of a block of either kind
     const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.N}, q_strides[2] = {row, (cuuint64_t)a.Hq * row};
-    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPG}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.NPGo};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(false)}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(true)};
     // tree K/V as [B*N nodes][Hkv][D]; box = 64 dims of one head of a sequence's N nodes
     const cuuint64_t t_dims[3] = {D, (cuuint64_t)a.Hkv, (cuuint64_t)a.B * a.N}, t_strides[2] = {row, (cuuint64_t)a.Hkv * row};
     const cuuint32_t t_box[3] = {64, 1, (cuuint32_t)a.N};
-    if (!map(&m.k, 2, a.k_pool, pool_dims, pool_strides, pool_box) || !map(&m.v, 3, a.v_pool, v_dims, v_strides, v_box) ||
+    const bool k_ok = p.pair == 2 ? map(&m.k, 3, a.k_pool, v_dims, v_strides, w_box)
+                                  : map(&m.k, 2, a.k_pool, pool_dims, pool_strides, pool_box);
+    if (!k_ok || !map(&m.v, 3, a.v_pool, v_dims, v_strides, v_box) ||
         !map(&m.q, 3, a.q, q_dims, q_strides, q_box) || !map(&m.qown, 3, a.q, q_dims, q_strides, o_box) ||
         !map(&m.kt, 3, a.k_tree, t_dims, t_strides, t_box) || !map(&m.vt, 3, a.v_tree, t_dims, t_strides, t_box))
         return cudaErrorInvalidValue;

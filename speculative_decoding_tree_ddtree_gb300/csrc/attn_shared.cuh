@@ -1,7 +1,7 @@
 // attn_shared.cuh -- the plan of tree-verify attention over shared prefixes.
 //
 // Rows (nodes of consecutive sequences of a group, times the query heads of a KV head)
-// are taken in blocks of at most kBlockRows.  A block's key list is made of 64-key
+// are taken in blocks of at most 128, or of 256 for a pair of CTAs.  A block's key list is made of 64-key
 // pages: the group's common pages, which all of its rows see, then for each of its
 // sequences the pages that it has for itself and a page with its tree's nodes, which
 // that sequence's rows see.  Two pages make a key tile.  In a group without common
@@ -17,18 +17,22 @@ namespace lucetree {
 namespace shr {
 
 constexpr int kMagic = 0x6c745370;
-constexpr int kBlockRows = 128;  // the MMA's M
+constexpr int kRows = 128;  // of a CTA: the MMA's M
 constexpr int kMaxCtas = 1024;
 
 struct Dims {
     int B, N, Hq, Hkv, G, D, groups;
-    int C;         // CTAs
+    int pair;      // CTAs of a block: 1, or 2 with half of its nodes each
+    int C;         // CTAs, or pairs of CTAs
     int NPG;       // nodes of a block in a group that shares pages
     int NG, NPGo;  // other groups: blocks of a sequence, and their nodes
+    __host__ __device__ int block_rows() const { return pair * kRows; }
+    // nodes of a block in its first CTA, of either kind of group
+    __host__ __device__ int half(bool own) const { return ((own ? NPGo : NPG) + pair - 1) / pair; }
     __host__ __device__ int max_blocks() const { return B * NG; }
     __host__ __device__ int max_segs() const { return B * NG * Hkv; }
     __host__ __device__ long long max_pieces() const { return (long long)C + max_segs(); }
-    __host__ __device__ int max_nodes() const { return NPG > NPGo ? NPG : NPGo; }
+    __host__ __device__ int max_nodes() const { return half(false) > half(true) ? half(false) : half(true); }
 };
 
 // Nodes of a block: as few blocks as hold `nodes`, of equal size; whole sequences of N
@@ -44,9 +48,14 @@ inline int block_nodes(long long nodes, int N, int cap) {
 
 inline Dims make_dims(int B, int N, int Hq, int Hkv, int D, int groups, int ctas) {
     Dims d;
-    d.B = B; d.N = N; d.Hq = Hq; d.Hkv = Hkv; d.G = Hq / Hkv; d.D = D; d.groups = groups; d.C = ctas;
-    const int cap = kBlockRows / d.G;
-    d.NPG = block_nodes((long long)((B + groups - 1) / groups) * N, N, cap);  // by the mean group
+    d.B = B; d.N = N; d.Hq = Hq; d.Hkv = Hkv; d.G = Hq / Hkv; d.D = D; d.groups = groups;
+    // Pairs where the mean group's rows are more than one CTA's: a pair reads keys once for twice
+    // the rows.
+    const long long nodes = (long long)((B + groups - 1) / groups) * N;
+    d.pair = ctas >= 2 && nodes * d.G > kRows ? 2 : 1;
+    d.C = ctas / d.pair;
+    const int cap = kRows / d.G * d.pair;
+    d.NPG = block_nodes(nodes, N, cap);
     d.NG = (N + cap - 1) / cap;
     d.NPGo = (N + d.NG - 1) / d.NG;
     d.NG = (N + d.NPGo - 1) / d.NPGo;
@@ -136,10 +145,10 @@ __host__ __device__ inline size_t plan_bytes(const Dims& d, Plan* p, void* at) {
 }
 
 // Partial sums by rows: O [rows][D], then max [rows], then sum [rows].  The piece of
-// segment s in CTA r has the rows from row0(s) + kBlockRows r on: row0 counts the rows
-// of the segments before s, and a segment has at most kBlockRows.
+// segment s in CTA r has the rows from row0(s) + block_rows() r on: row0 counts the rows
+// of the segments before s, and a segment has at most block_rows().
 __host__ __device__ inline size_t partial_rows(const Dims& d) {
-    return (size_t)d.B * d.N * d.Hq + (size_t)kBlockRows * d.C;
+    return (size_t)d.B * d.N * d.Hq + (size_t)d.block_rows() * d.C;
 }
 __host__ __device__ inline size_t workspace_bytes(const Dims& d) { return partial_rows(d) * (d.D + 2) * sizeof(float); }
 // ... with n_g sequences from seq0 on in the segment's group, whose block starts at node0.

@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
         const Seg seg = W.plan.seg[(size_t)grp.block0 * d.Hkv + (size_t)g * grp.blocks + k];
         const bool has_row = x < rows && seg.count > 1;
         const int count = has_row ? seg.count : 0;
-        const size_t first = (size_t)row0_of(d, grp.seq0, grp.n, g, node0) + (size_t)kBlockRows * seg.first +
+        const size_t first = (size_t)row0_of(d, grp.seq0, grp.n, g, node0) + (size_t)d.block_rows() * seg.first +
                              (node - node0) * d.G + h % d.G;
         // partial j's O row
-        auto o_at = [&](int j) { return W.ws + (first + (size_t)kBlockRows * j) * D; };
+        auto o_at = [&](int j) { return W.ws + (first + (size_t)d.block_rows() * j) * D; };
         float m = -INFINITY, l = 0.f, o[kV] = {};
         // this warp's partials are member, member + G, ..
         const int mine = has_row ? (count - member + G - 1) / G : 0;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             load(0);  // with the maxima and sums, not after them
             float mk = -INFINITY, lk = 0.f;
             if (lane < n) {
-                const float* s = W.ws + pr * D + first + (size_t)kBlockRows * (member + (k0 + lane) * G);
+                const float* s = W.ws + pr * D + first + (size_t)d.block_rows() * (member + (k0 + lane) * G);
                 mk = s[0];
                 lk = s[pr];
             }

@@ -7,6 +7,7 @@
 // queries and output.  Bound by its chain of dependent steps (about a dozen); it
 // runs once for all layers of a decoding step.
 #include "attn_shared.cuh"
+#include "tc_ptx.cuh"
 
 namespace lucetree {
 namespace shr {
@@ -31,10 +32,6 @@ struct PlanLaunch {
     int32_t* shared_pages;
     uint32_t* status;
 };
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // (Functions of their own, not inlined: the kernel runs through its code once, and the fetch of
 // its instructions is much of what it takes: 47 KB of them 9.9 to 13.4 us, 26 KB 8.4 to 12.3.)
@@ -136,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
             (gridDim.x > 1 ? P.seq : seqs)[b] = Seq{g, first, L, n, 0, 0};
         }
     }
-    if (gridDim.x > 1) cluster_sync();
+    if (gridDim.x > 1) tc::cluster_sync();
     else __syncthreads();
     if (!lead) return;
     if (gridDim.x > 1 && seqs != P.seq) {
@@ -312,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
         p.g = at.x;
         p.ta = s == s_seg[r] ? s_tile[r] : 0;
         p.te = s == s_seg[r + 1] ? s_tile[r + 1] : tiles;
-        p.slot = p.ta == 0 && p.te == tiles ? -1 : row0_of(d, q.seq0, q.n, at.x, blks[k].node0) + kBlockRows * r;
+        p.slot = p.ta == 0 && p.te == tiles ? -1 : row0_of(d, q.seq0, q.n, at.x, blks[k].node0) + d.block_rows() * r;
         p.own = q.used == 0;
         p.reread = (q.used > 0 ? q.blocks : d.NG) > 1;
         p.pad = 0;

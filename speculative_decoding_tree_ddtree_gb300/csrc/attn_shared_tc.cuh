@@ -46,26 +46,30 @@ constexpr int kSoftmaxThreads = 32 * kSmWarps;
 constexpr int kThreads = 128 + kSoftmaxThreads;
 constexpr int kMaxSlots = 12;
 constexpr int kBadSets = 8;    // pieces whose V may be in the ring at once, and more
-constexpr int kBadWords = 8;   // tree nodes of a block's sequences: at most 126 + 2 N
+constexpr int kBadWords = 12;  // tree nodes of a block's sequences: at most 254 + 2 N
 
 struct Misc {
-    float xchg[2][kBlockRows];  // a row's values for the other warpgroup's half
-    uint64_t full[kMaxSlots];
-    uint64_t empty[kMaxSlots];
+    float xchg[2][kRows];        // a row's values for the other warpgroup's half
+    uint64_t empty[kMaxSlots];   // of ring slots
+    uint64_t kfull[kMaxSlots];   // K chunk n at [n % kMaxSlots]: landed ...
+    uint64_t kpeer[kMaxSlots];   // ... in a pair's second CTA too
     uint64_t vfull[kMaxSlots];   // V chunk n at [n % kMaxSlots]: landed ...
     uint64_t vready[kMaxSlots];  // ... made the operand
     uint64_t s_full[2], p_full[2];  // of tiles j, at [j & 1]
     uint64_t pv_done[2];            // (PV(j - 2) is done once S(j) is there: two of them tell PV(j) from it)
-    uint64_t q_full, q_empty, drain;
+    uint64_t q_full, q_peer, q_empty, drain;
     uint32_t vbad[kBadSets][kBadWords];  // piece n at [n % kBadSets]: tree nodes whose V is not finite
     uint32_t tmem_base;
     int abort_flag;
 };
 
-template <int D>
+template <int D, bool PAIR>
 struct Lay {
-    static constexpr int kChunks = D / 64;  // ring chunks per operand
-    static constexpr int kQBytes = kChunks * kChunkBytes;
+    // Ring chunks per operand.  One CTA: K [128 keys][64 dims], V [64 keys][128 dims].  A pair, whose
+    // CTAs hold half of each operand: K [64 keys of its page][128 dims]; V its half of the dims,
+    // [64 keys][128 dims] or, with D = 128, [128 keys][64 dims].  16 KB each.
+    static constexpr int kChunks = PAIR ? D / 128 : D / 64;
+    static constexpr int kQBytes = D / 64 * kChunkBytes;
     static constexpr int kMiscBytes = (sizeof(Misc) + 127) / 128 * 128;
     static constexpr int kRaw = (kSmemLimit - 1024 - kQBytes - kMiscBytes) / kChunkBytes;
     static constexpr int kNS = kRaw > kMaxSlots ? kMaxSlots : kRaw;
@@ -213,13 +217,13 @@ __device__ __forceinline__ Page page_at(const Launch& W, const Block& b, int v) 
 // In one word: keys, tree, sequence + 1.
 __device__ __forceinline__ int page_word(const Page& p) { return p.keys | (p.tree ? 0x80 : 0) | (p.seq + 1) << 8; }
 
-template <int D, bool BF16, bool PV16>
+template <int D, bool BF16, bool PV16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qown,
                      const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                      const __grid_constant__ Launch W) {
-    using L = Lay<D>;
+    using L = Lay<D, PAIR>;
     static_assert(BF16 || !PV16, "fp16 inputs run PV on fp16 anyway");
     constexpr bool kConvert = BF16 && !PV16;  // V to fp16 on chip
     constexpr int kChunks = L::kChunks;
@@ -234,24 +238,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const lucetree_attn_args& a = W.a;
     const Dims& d = W.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_rank() : 0u;  // CTA of the pair
 
     // ---------------------------------------------------------------- set-up
     // (reads no global memory: it overlaps the previous kernel's tail)
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kNS; ++i) {
-            mbar_init(&ms->full[i], 1);
-            mbar_init(&ms->empty[i], 1);
-        }
         for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(&ms->empty[i], 1);
+            mbar_init(&ms->kfull[i], 1);
+            mbar_init(&ms->kpeer[i], 1);
             mbar_init(&ms->vfull[i], 1);
-            mbar_init(&ms->vready[i], kConvWarps);
+            mbar_init(&ms->vready[i], PAIR ? 2 * kConvWarps : kConvWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ms->s_full[i], 1);
-            mbar_init(&ms->p_full[i], kSmWarps);
+            mbar_init(&ms->p_full[i], PAIR ? 2 * kSmWarps : kSmWarps);
             mbar_init(&ms->pv_done[i], 1);
         }
         mbar_init(&ms->q_full, 1);
+        mbar_init(&ms->q_peer, 1);
         mbar_init(&ms->q_empty, 1);
         mbar_init(&ms->drain, 1);
         ms->abort_flag = 0;
@@ -260,13 +265,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2)
         for (int i = lane; i < kBadSets * kBadWords; i += 32) ms->vbad[i / kBadWords][i % kBadWords] = 0;
     // rows of Q that no piece loads: their rows of S and O are never used, but finite
-    for (int i = d.max_nodes() * d.G * 8 + threadIdx.x; i < kBlockRows * 8; i += kThreads)
+    for (int i = d.max_nodes() * d.G * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) reinterpret_cast<uint4*>(sQ + c * kChunkBytes)[i] = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D / 64; ++c) reinterpret_cast<uint4*>(sQ + c * kChunkBytes)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (warp == 1) {
-        tmem_alloc(&ms->tmem_base, kTmemCols);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(&ms->tmem_base, kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&ms->tmem_base, kTmemCols);
+            tmem_relinquish();
+        }
     }
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&tm_k);
@@ -278,17 +288,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = ms->tmem_base;
+    auto teardown = [&]() {
+        if constexpr (PAIR) cluster_sync();  // the other CTA's arrivals and MMAs have come
+        if (warp == 1) {
+            if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
+            else tmem_dealloc(tmem, kTmemCols);
+        }
+    };
 
     // inputs may come from the previous kernel on the stream
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
     const bool fits = plan_fits(W);
-    const Cta start = fits ? W.plan.cta[blockIdx.x] : Cta{0, 0, 0, 0};
+    const Cta start = fits ? W.plan.cta[blockIdx.x / d.pair] : Cta{0, 0, 0, 0};
     if (start.tiles == 0) {  // uniform across the CTA: nothing to do but give TMEM back
         if (!fits && threadIdx.x == 0) atomicOr(a.status, LUCETREE_DEV_BAD_ROW);
-        if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+        teardown();
         return;
     }
     const uint32_t n_tiles = (uint32_t)start.tiles;
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int oob_row = a.num_pages * d.Hkv * kPage;  // first row past the pool: zero fill
         const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
         const uint32_t tree_bytes = (uint32_t)d.N * 128u;  // one 64-dim box of the tree's nodes
-        uint32_t chunk = 0, vchunk = 0;
+        uint32_t chunk = 0, vchunk = 0;  // of K, of V
         int q_loads = 0;
         bool ok = true;
         // A tile's pages: pool row, or for a tree's page -1 - (first node)
@@ -308,63 +326,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t pol;
         };
         const bool leader = elect_one();
-        uint32_t slot = 0, turn = 0, vslot = 0;  // ring position and its pass; position of V's barriers
+        uint32_t slot = 0, turn = 0;  // ring position and its pass
         auto next_slot = [&]() {
             const bool w = mbar_wait(&ms->empty[slot], (turn & 1) ^ 1);
             return __all_sync(0xffffffffu, w);  // lanes agree on a timeout
         };
+        auto advance = [&]() {
+            if (++slot == (uint32_t)kNS) {
+                slot = 0;
+                ++turn;
+            }
+        };
         auto issue_k = [&](const Operand& o) -> bool {
             const bool tree0 = o.at0 < 0, tree1 = o.at1 < 0;
-            const uint32_t bytes = (tree0 ? tree_bytes : 8192u) + (tree1 ? tree_bytes : 8192u);
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
-                // [128 keys: page 0 then page 1][dims 64 * c .. +63]
                 if (!next_slot()) return false;
                 if (leader) {
                     uint8_t* dst = sSlots + slot * kChunkBytes;
-                    uint64_t* bar = &ms->full[slot];
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
-                    else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
-                    if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
-                    else tma_load_2d_hint(dst + 8192, &tm_k, 64 * c, o.at1, bar, o.pol);
+                    uint64_t* bar = &ms->kfull[chunk % kMaxSlots];
+                    if constexpr (PAIR) {
+                        // [64 keys of page `rank`][dims 128 * c .. +127], 64 dims after the other 64
+                        const int at = rank ? o.at1 : o.at0;
+                        mbar_arrive_expect_tx(bar, at < 0 ? 2 * tree_bytes : (uint32_t)kChunkBytes);
+                        if (at < 0) {
+                            tma_load_3d(dst, &tm_kt, 128 * c, o.g, -1 - at, bar);
+                            tma_load_3d(dst + 8192, &tm_kt, 128 * c + 64, o.g, -1 - at, bar);
+                        } else {
+                            tma_load_3d_hint(dst, &tm_k, 0, at, 2 * c, bar, o.pol);
+                        }
+                    } else {
+                        // [128 keys: page 0 then page 1][dims 64 * c .. +63]
+                        mbar_arrive_expect_tx(bar, (tree0 ? tree_bytes : 8192u) + (tree1 ? tree_bytes : 8192u));
+                        if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
+                        else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
+                        if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
+                        else tma_load_2d_hint(dst + 8192, &tm_k, 64 * c, o.at1, bar, o.pol);
+                    }
                 }
                 __syncwarp();
                 ++chunk;
-                if (++slot == (uint32_t)kNS) {
-                    slot = 0;
-                    ++turn;
-                }
+                advance();
             }
             return true;
         };
         auto issue_v = [&](const Operand& o) -> bool {
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
-                // [64 keys of page c & 1][dims 128 * (c >> 1) .. +127], 64 dims after the other 64
                 if (!next_slot()) return false;
-                const int at = c & 1 ? o.at1 : o.at0;
-                const bool tree = at < 0;
                 if (leader) {
                     uint8_t* dst = sSlots + slot * kChunkBytes;
-                    mbar_arrive(&ms->full[slot]);  // this fill's phase of full[slot]; the data signal is vfull
-                    uint64_t* bar = &ms->vfull[vslot];
-                    mbar_arrive_expect_tx(bar, tree ? 2 * tree_bytes : (uint32_t)kChunkBytes);
-                    if (tree) {
-                        tma_load_3d(dst, &tm_vt, 128 * (c >> 1), o.g, -1 - at, bar);
-                        tma_load_3d(dst + 8192, &tm_vt, 128 * (c >> 1) + 64, o.g, -1 - at, bar);
+                    uint64_t* bar = &ms->vfull[vchunk % kMaxSlots];
+                    if constexpr (PAIR && D == 128) {
+                        // [128 keys: page 0 then page 1][dims 64 * rank .. +63]
+                        mbar_arrive_expect_tx(bar, (o.at0 < 0 ? tree_bytes : 8192u) + (o.at1 < 0 ? tree_bytes : 8192u));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = h ? o.at1 : o.at0;
+                            if (at < 0) tma_load_3d(dst + 8192 * h, &tm_vt, 64 * rank, o.g, -1 - at, bar);
+                            else tma_load_3d_hint(dst + 8192 * h, &tm_v, 0, at, rank, bar, o.pol);
+                        }
                     } else {
-                        tma_load_3d_hint(dst, &tm_v, 0, at, 2 * (c >> 1), bar, o.pol);
+                        // [64 keys of a page][128 dims], 64 dims after the other 64
+                        const int at = (PAIR ? c : c & 1) ? o.at1 : o.at0, x = PAIR ? 128 * rank : 128 * (c >> 1);
+                        mbar_arrive_expect_tx(bar, at < 0 ? 2 * tree_bytes : (uint32_t)kChunkBytes);
+                        if (at < 0) {
+                            tma_load_3d(dst, &tm_vt, x, o.g, -1 - at, bar);
+                            tma_load_3d(dst + 8192, &tm_vt, x + 64, o.g, -1 - at, bar);
+                        } else {
+                            tma_load_3d_hint(dst, &tm_v, 0, at, x / 64, bar, o.pol);
+                        }
                     }
                 }
                 __syncwarp();
-                ++chunk;
                 ++vchunk;
-                if (++slot == (uint32_t)kNS) {
-                    slot = 0;
-                    ++turn;
-                }
-                if (++vslot == (uint32_t)kMaxSlots) vslot = 0;
+                advance();
             }
             return true;
         };
@@ -403,12 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = __all_sync(0xffffffffu, w))) break;
                     }
                     if (leader) {
-                        const int rows = (cur.pc.own ? d.NPGo : d.NPG) * d.G;
+                        const int nodes = d.half(cur.pc.own);
                         const CUtensorMap* tm = cur.pc.own ? &tm_qown : &tm_q;
-                        mbar_arrive_expect_tx(&ms->q_full, kChunks * rows * 128);
+                        mbar_arrive_expect_tx(&ms->q_full, D / 64 * nodes * d.G * 128);
 #pragma unroll 1
-                        for (int c = 0; c < kChunks; ++c)
-                            tma_load_3d(sQ + c * kChunkBytes, tm, 64 * c, cur.pc.g * d.G, blk.node0, &ms->q_full);
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(sQ + c * kChunkBytes, tm, 64 * c, cur.pc.g * d.G, blk.node0 + (int)rank * nodes,
+                                        &ms->q_full);
                     }
                     __syncwarp();
                     ++q_loads;
@@ -428,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // wait (bounded) for this CTA's own copies still in flight
             if (lane == 0) {
                 const uint32_t first = chunk > (uint32_t)kNS ? chunk - kNS : 0u;
-                for (uint32_t c = first; c < chunk; ++c) mbar_wait(&ms->full[c % kNS], (c / kNS) & 1, 200000000ll);
+                for (uint32_t c = first; c < chunk; ++c)
+                    mbar_wait(&ms->kfull[c % kMaxSlots], (c / kMaxSlots) & 1, 200000000ll);
                 const uint32_t vfirst = vchunk > (uint32_t)kNS ? vchunk - kNS : 0u;
                 for (uint32_t c = vfirst; c < vchunk; ++c)
                     mbar_wait(&ms->vfull[c % kMaxSlots], (c / kMaxSlots) & 1, 200000000ll);
@@ -440,95 +478,150 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The whole warp goes through the loop, one elected lane issues: addresses and descriptors
         // are then the warp's, in uniform registers (from one lane's registers an MMA took as long to
         // issue as to run twice).
-        constexpr uint32_t id_qk = idesc_f16(128, 128, BF16 ? 1u : 0u, 0, 0);
-        constexpr uint32_t id_pv = idesc_f16(128, 128, PV16 ? 1u : 0u, 0, 1);
-        constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
-        constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
-        const uint32_t aQ = smem_u32(sQ), aS = smem_u32(sSlots);
         const bool leader = elect_one();
-        uint32_t slot = 0, turn = 0, jq = 0;  // ring position and its pass; tiles whose QK is issued
-        uint32_t vslot = 0, vturn = 0;        // the same of V's barriers
-        uint32_t first_bits = 0;              // bit k: the k-th last QK issued opened a piece
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool w = mbar_wait(bar, parity);
             ok = __all_sync(0xffffffffu, w);
             return ok;
         };
-        Cursor qk;
-        qk.start(start);
-        // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
-        // (MMAs of one thread run in order).
-        auto next_qk = [&]() {
-            qk.step(W);
-            if (!qk.live) return;
-            if (qk.first() && !wait(&ms->q_full, qk.piece_no & 1)) return;
-            const uint32_t dS = tmem + (jq & 1) * 128;
+        if (rank != 0) {
+            // the pair's second CTA: tells the first one what has landed here
+            Cursor qk;
+            qk.start(start);
+            uint32_t n = 0;
+            while (ok) {
+                qk.step(W);
+                if (!qk.live) break;
+                if (qk.first()) {
+                    if (!wait(&ms->q_full, qk.piece_no & 1)) break;
+                    if (leader) mbar_arrive_at(cluster_addr(&ms->q_peer, 0));
+                }
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                if (!wait(&ms->full[slot], turn & 1)) return;
-                tc_fence_after();
-                if (leader) {
+                for (int c = 0; c < kChunks; ++c, ++n) {
+                    if (!wait(&ms->kfull[n % kMaxSlots], (n / kMaxSlots) & 1) || __any_sync(0xffffffffu, aborted(ms))) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_arrive_at(cluster_addr(&ms->kpeer[n % kMaxSlots], 0));
+                    __syncwarp();
+                }
+            }
+            if (!ok) set_abort(ms, a.status);
+        } else {
+            constexpr uint32_t M = PAIR ? 256 : 128, kNv = PAIR ? D : 128;  // PV's N
+            constexpr uint32_t id_qk = idesc_f16(M, 128, BF16 ? 1u : 0u, 0, 0);
+            constexpr uint32_t id_pv = idesc_f16(M, kNv, PV16 ? 1u : 0u, 0, 1);
+            constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
+            constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
+            const uint32_t aQ = smem_u32(sQ), aS = smem_u32(sSlots);
+            uint32_t slot = 0, jq = 0;      // ring position; tiles whose QK is issued
+            uint32_t kn = 0, vn = 0;        // chunks of K and of V so far
+            uint32_t first_bits = 0;        // bit k: the k-th last QK issued opened a piece
+            // barriers that the other CTA arrives on
+            auto wait_peer = [&](uint64_t* bar, uint32_t parity) {
+                const bool w = PAIR ? mbar_wait_cluster(bar, parity) : mbar_wait(bar, parity);
+                ok = __all_sync(0xffffffffu, w);
+                return ok;
+            };
+            auto commit = [&](uint64_t* bar) {
+                if constexpr (PAIR) mma_commit_pair(bar);
+                else mma_commit(bar);
+            };
+            auto advance = [&]() {
+                if (++slot == (uint32_t)kNS) slot = 0;
+            };
+            Cursor qk;
+            qk.start(start);
+            // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
+            // (MMAs of one thread run in order).
+            auto next_qk = [&]() {
+                qk.step(W);
+                if (!qk.live) return;
+                if (qk.first()) {
+                    if (!wait(&ms->q_full, qk.piece_no & 1)) return;
+                    if (PAIR && !wait_peer(&ms->q_peer, qk.piece_no & 1)) return;
+                }
+                const uint32_t dS = tmem + (jq & 1) * 128;
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    if (!wait(&ms->kfull[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
+                    if (PAIR && !wait_peer(&ms->kpeer[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t at = aS + slot * kChunkBytes;
+                        if constexpr (PAIR) {
 #pragma unroll
-                    for (int sub = 0; sub < 4; ++sub)
-                        mma_f16_ss(dS, make_desc(hi_k, aQ + c * kChunkBytes + sub * 32),
-                                   make_desc(hi_k, aS + slot * kChunkBytes + sub * 32), id_qk, (c | sub) != 0);
-                    mma_commit(&ms->empty[slot]);
+                            for (int k = 0; k < 8; ++k)
+                                mma_f16_ss_pair(dS, make_desc(hi_k, aQ + (2 * c + k / 4) * kChunkBytes + k % 4 * 32),
+                                                make_desc(hi_k, at + k / 4 * 8192 + k % 4 * 32), id_qk, (c | k) != 0);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ss(dS, make_desc(hi_k, aQ + c * kChunkBytes + k * 32), make_desc(hi_k, at + k * 32),
+                                           id_qk, (c | k) != 0);
+                        }
+                        commit(&ms->empty[slot]);
+                    }
+                    __syncwarp();
+                    ++kn;
+                    advance();
+                }
+                if (leader) {
+                    commit(&ms->s_full[jq & 1]);
+                    if (qk.last()) commit(&ms->q_empty);
                 }
                 __syncwarp();
-                if (++slot == (uint32_t)kNS) {
-                    slot = 0;
-                    ++turn;
-                }
-            }
-            if (leader) {
-                mma_commit(&ms->s_full[jq & 1]);
-                if (qk.last()) mma_commit(&ms->q_empty);
-            }
-            __syncwarp();
-            first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
-            ++jq;
-        };
-        next_qk();
-        if (ok && n_tiles > 1) next_qk();
-        for (uint32_t j = 0; ok && j < n_tiles; ++j) {
-            if (__any_sync(0xffffffffu, aborted(ms))) break;
-            // O += P(j) . V(j) once the softmax has written P(j)
-            if (!wait(&ms->p_full[j & 1], (j >> 1) & 1)) break;
-            const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
-            // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..; P's columns of a page
-            // begin where S's did
+                first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
+                ++jq;
+            };
+            next_qk();
+            if (ok && n_tiles > 1) next_qk();
+            for (uint32_t j = 0; ok && j < n_tiles; ++j) {
+                if (__any_sync(0xffffffffu, aborted(ms))) break;
+                // O += P(j) . V(j) once the softmax has written P(j); P's columns of a page begin
+                // where S's did
+                if (!wait_peer(&ms->p_full[j & 1], (j >> 1) & 1)) break;
+                const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                if (!wait(&ms->vready[vslot], vturn & 1)) break;
-                tc_fence_after();
-                if (leader) {
+                for (int c = 0; c < kChunks; ++c) {
+                    if (!wait_peer(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t at = aS + slot * kChunkBytes, dO = tmem + L::kColO;
+                        if constexpr (PAIR && D == 128) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_f16_ts(tmem + L::kColO + 128 * (c >> 1), aP + 64 * (c & 1) + 8 * ks,
-                                   make_desc(hi_v, aS + slot * kChunkBytes + ks * 2048), id_pv,
-                                   (c & 1) == 0 && ks == 0 ? more : 1u);
-                    mma_commit(&ms->empty[slot]);
+                            for (int k = 0; k < 8; ++k)
+                                mma_f16_ts_pair(dO, aP + 64 * (k / 4) + 8 * (k % 4),
+                                                make_desc(hi_v, at + k / 4 * 8192 + k % 4 * 2048), id_pv, k == 0 ? more : 1u);
+                        } else if constexpr (PAIR) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ts_pair(dO, aP + 64 * c + 8 * k, make_desc(hi_v, at + k * 2048), id_pv,
+                                                (c | k) == 0 ? more : 1u);
+                        } else {
+                            // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f16_ts(dO + 128 * (c >> 1), aP + 64 * (c & 1) + 8 * k, make_desc(hi_v, at + k * 2048),
+                                           id_pv, (c & 1) == 0 && k == 0 ? more : 1u);
+                        }
+                        commit(&ms->empty[slot]);
+                    }
+                    __syncwarp();
+                    ++vn;
+                    advance();
                 }
+                if (!ok) break;
+                if (leader) commit(&ms->pv_done[j & 1]);
                 __syncwarp();
-                if (++slot == (uint32_t)kNS) {
-                    slot = 0;
-                    ++turn;
-                }
-                if (++vslot == (uint32_t)kMaxSlots) {
-                    vslot = 0;
-                    ++vturn;
-                }
+                if (j + 2 < n_tiles) next_qk();
             }
-            if (!ok) break;
-            if (leader) mma_commit(&ms->pv_done[j & 1]);
-            __syncwarp();
-            if (j + 2 < n_tiles) next_qk();
-        }
-        if (!ok || __any_sync(0xffffffffu, aborted(ms))) {
-            set_abort(ms, a.status);
-            if (leader) mma_commit(&ms->drain);  // every MMA issued so far has finished before TMEM is freed
-            mbar_wait(&ms->drain, 0, 200000000ll);
+            if (!ok || __any_sync(0xffffffffu, aborted(ms))) {
+                set_abort(ms, a.status);
+                if (leader) commit(&ms->drain);  // every MMA issued so far has finished before TMEM is freed
+                mbar_wait(&ms->drain, 0, 200000000ll);
+            }
         }
         __syncwarp();
     } else if (warp < 4) {
@@ -563,20 +656,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
                 const uint32_t vn = j * kChunks + c;
-                const int word = __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + (c & 1));
+                // the pages in the chunk's two 8 KB boxes: one page twice, or both
+                constexpr bool kBoth = PAIR && D == 128;
+                const int page = kBoth ? 0 : PAIR ? c : c & 1;
+                const int word0 = __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + page);
+                const int word1 = kBoth ? __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + 1) : word0;
                 const bool landed = mbar_wait(&ms->vfull[vn % kMaxSlots], (vn / kMaxSlots) & 1);
                 if (!__all_sync(0xffffffffu, landed) || aborted(ms)) {
                     ok = false;
                     break;
                 }
                 uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
-                const int keys = word & 0x7f;
-                const bool tree = word & 0x80, whole = keys == kPage && !tree;
+                // (a page of 64 keys that is no tree: nothing to change)
+                const bool whole = (word0 & 0xff) == kPage && (word1 & 0xff) == kPage;
                 constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
                 constexpr int kBatch = 4;                                      // loads in flight
                 if (kConvert || !whole) {
 #pragma unroll 1
                     for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
+                        // (a batch lies in one box)
+                        const int word = u0 < kUnits / 2 ? word0 : word1, keys = word & 0x7f;
                         uint4 x[kBatch];
                         bool on[kBatch];
 #pragma unroll
@@ -588,9 +687,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kBatch; ++k) {
                             const int u = ct + 32 * kConvWarps * (u0 + k);
-                            if (tree && not_finite<BF16, kConvert>(x[k])) {
+                            if ((word & 0x80) && not_finite<BF16, kConvert>(x[k])) {
                                 const int node = ((word >> 8) - 1) * d.N + ((u & 511) >> 3);
-                                atomicOr(&ms->vbad[cur.piece_no % kBadSets][node >> 5], 1u << (node & 31));
+                                uint32_t* to = &ms->vbad[cur.piece_no % kBadSets][node >> 5];
+                                if constexpr (PAIR) {  // its other dims, and other rows, are the other CTA's
+                                    or_at(cluster_addr(to, 0), 1u << (node & 31));
+                                    or_at(cluster_addr(to, 1), 1u << (node & 31));
+                                    fence_cluster();
+                                } else {
+                                    atomicOr(to, 1u << (node & 31));
+                                }
                                 x[k] = make_uint4(0, 0, 0, 0);
                                 on[k] = false;
                             }
@@ -606,7 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms->vready[vn % kMaxSlots]);
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_at(cluster_addr(&ms->vready[vn % kMaxSlots], 0));
+                    else mbar_arrive(&ms->vready[vn % kMaxSlots]);
+                }
             }
             ++j;
         }
@@ -631,8 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur.next_piece(W);
             if (!cur.live) break;
             const Block blk = load_block(W, cur.pc.block);
-            const bool mine = row < blk.nodes * d.G;
-            const int node = blk.node0 + (mine ? row / d.G : 0);
+            const int before = (int)rank * d.half(cur.pc.own);  // the block's nodes in the pair's first CTA
+            const bool mine = row < min(d.half(cur.pc.own), blk.nodes - before) * d.G;
+            const int node = blk.node0 + (mine ? before + row / d.G : 0);
             const int b = node / d.N, i = node - b * d.N;
             // (rows past the block's own go along with what all rows see, so that their warp needs no masks)
             const int seq = mine || blk.seqs == 1 ? b - blk.b0 : -2;
@@ -749,7 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms->p_full[j & 1]);
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_at(cluster_addr(&ms->p_full[j & 1], 0));
+                    else mbar_arrive(&ms->p_full[j & 1]);
+                }
                 ++j;
             }
             if (bad) break;
@@ -776,10 +889,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((bits & anc) != 0) l = __int_as_float(0x7FC00000);
             }
             const bool whole = cur.pc.slot < 0;
+            const int at_row = cur.pc.slot + before * d.G + row;
             const float inv = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN stays, and is flagged)
             if (mine && half == 0) {
                 if (!whole) {
-                    float* s = W.ws + partial_rows(d) * D + cur.pc.slot + row;
+                    float* s = W.ws + partial_rows(d) * D + at_row;
                     s[0] = -neg_m;
                     s[partial_rows(d)] = l;
                 } else if (a.lse) {
@@ -795,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_ld_regs16(r);
                 if (!mine) continue;
                 if (!whole) {
-                    float4* o = reinterpret_cast<float4*>(W.ws + (size_t)(cur.pc.slot + row) * D + x);
+                    float4* o = reinterpret_cast<float4*>(W.ws + (size_t)at_row * D + x);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         o[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
@@ -835,20 +949,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    teardown();
 }
 
 struct Maps {
     CUtensorMap k, v, q, qown, kt, vt;
 };
 
+template <int D, bool BF16, bool PV16, bool PAIR>
+cudaError_t launch_pairs(const Maps& m, const Launch& W, cudaStream_t stream) {
+    auto kern = shared_tc_kernel<D, BF16, PV16, PAIR>;
+    constexpr int bytes = Lay<D, PAIR>::kBytes;
+    static SmemLimitSeen seen;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), bytes, seen);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(W.d.C * W.d.pair);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, m.k, m.v, m.q, m.qown, m.kt, m.vt, W);
+}
+
 template <int D, bool BF16, bool PV16>
 cudaError_t launch_one(const Maps& m, const Launch& W, cudaStream_t stream) {
-    auto kern = shared_tc_kernel<D, BF16, PV16>;
-    static SmemLimitSeen seen;
-    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), Lay<D>::kBytes, seen);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(W.d.C), dim3(kThreads), Lay<D>::kBytes, stream, m.k, m.v, m.q, m.qown, m.kt, m.vt, W);
+    return W.d.pair == 2 ? launch_pairs<D, BF16, PV16, true>(m, W, stream) : launch_pairs<D, BF16, PV16, false>(m, W, stream);
 }
 
 cudaError_t launch_bf16_256(const Maps&, const Launch&, cudaStream_t);

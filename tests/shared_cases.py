@@ -5,7 +5,7 @@ import torch
 
 PAGE = 64
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
-BLOCK_ROWS = 128
+ROWS = 128
 
 
 def batch(groups, N, seed=0, spare=3, reserve=0):
@@ -55,13 +55,15 @@ def read_plan(plan, B, N, Hq, Hkv, D, groups):
     """A plan's parts as arrays of 32-bit words."""
     raw = plan.cpu().numpy().tobytes()
     head = np.frombuffer(raw, np.int32, 16)
-    C, cap = int(head[7]), BLOCK_ROWS // (Hq // Hkv)
+    G = Hq // Hkv
+    pair = 2 if -(-B // groups) * N * G > ROWS else 1
+    C, cap = int(head[7]), ROWS // G * pair
     NG = -(-N // cap)
     NPGo = -(-N // NG)
     NG = -(-N // NPGo)
     sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups + 1, 5), seq=(B + 1, 6), blk=(B * NG + 1, 8), seg=(B * NG * Hkv, 2),
                  piece=(C + B * NG * Hkv, 8))
-    at, out = 0, dict(NG=NG, NPGo=NPGo, NPG=block_nodes(-(-B // groups) * N, N, cap), C=C)
+    at, out = 0, dict(NG=NG, NPGo=NPGo, NPG=block_nodes(-(-B // groups) * N, N, cap), C=C, rows=ROWS * pair)
     for name, (n, w) in sizes.items():
         out[name] = np.frombuffer(raw, np.int32, n * w, at).reshape(n, w)
         at += -(-4 * n * w // 16) * 16
@@ -75,7 +77,7 @@ def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
     B, groups, G = len(ctx), len(start) - 1, Hq // Hkv
     p = read_plan(plan, B, N, Hq, Hkv, D, groups)
     C, NG, NPGo, NPG = p["C"], p["NG"], p["NPGo"], p["NPG"]
-    assert max(NPG, NPGo) * G <= BLOCK_ROWS
+    assert max(NPG, NPGo) * G <= p["rows"]
     assert list(p["head"][0, 1:10]) == [B, N, Hq, Hkv, D, groups, C, table.shape[1], pages]
     blocks = int(p["head"][0, 10])
     assert blocks <= B * NG
@@ -121,7 +123,7 @@ def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
     for slot, n in sorted(rows):
         assert slot >= at
         at = slot + n
-    assert at <= B * N * Hq + BLOCK_ROWS * C
+    assert at <= B * N * Hq + p["rows"] * C
     return p
 
 
