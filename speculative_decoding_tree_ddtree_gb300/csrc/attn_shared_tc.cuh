@@ -518,12 +518,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t slot = 0, jq = 0;      // ring position; tiles whose QK is issued
             uint32_t kn = 0, vn = 0;        // chunks of K and of V so far
             uint32_t first_bits = 0;        // bit k: the k-th last QK issued opened a piece
-            // barriers that the other CTA arrives on
-            auto wait_peer = [&](uint64_t* bar, uint32_t parity) {
-                const bool w = PAIR ? mbar_wait_cluster(bar, parity) : mbar_wait(bar, parity);
-                ok = __all_sync(0xffffffffu, w);
-                return ok;
-            };
             auto commit = [&](uint64_t* bar) {
                 if constexpr (PAIR) mma_commit_pair(bar);
                 else mma_commit(bar);
@@ -540,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!qk.live) return;
                 if (qk.first()) {
                     if (!wait(&ms->q_full, qk.piece_no & 1)) return;
-                    if (PAIR && !wait_peer(&ms->q_peer, qk.piece_no & 1)) return;
+                    if (PAIR && !wait(&ms->q_peer, qk.piece_no & 1)) return;
                 }
                 const uint32_t dS = tmem + (jq & 1) * 128;
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     if (!wait(&ms->kfull[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
-                    if (PAIR && !wait_peer(&ms->kpeer[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
+                    if (PAIR && !wait(&ms->kpeer[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
                     tc_fence_after();
                     if (leader) {
                         const uint32_t at = aS + slot * kChunkBytes;
@@ -581,11 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, aborted(ms))) break;
                 // O += P(j) . V(j) once the softmax has written P(j); P's columns of a page begin
                 // where S's did
-                if (!wait_peer(&ms->p_full[j & 1], (j >> 1) & 1)) break;
+                if (!wait(&ms->p_full[j & 1], (j >> 1) & 1)) break;
                 const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
-                    if (!wait_peer(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) break;
+                    if (!wait(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) break;
                     tc_fence_after();
                     if (leader) {
                         const uint32_t at = aS + slot * kChunkBytes, dO = tmem + L::kColO;
