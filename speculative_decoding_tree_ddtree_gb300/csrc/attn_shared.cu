@@ -60,9 +60,9 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
     // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x a CTA's nodes of a block of either kind
     const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.N}, q_strides[2] = {row, (cuuint64_t)a.Hq * row};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(false)}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(true)};
-    // tree K/V as [B*N nodes][Hkv][D]; box = 64 dims of one head of a sequence's N nodes
+    // tree K/V as [B*N nodes][Hkv][D]; box = 64 dims of one head of 64 nodes
     const cuuint64_t t_dims[3] = {D, (cuuint64_t)a.Hkv, (cuuint64_t)a.B * a.N}, t_strides[2] = {row, (cuuint64_t)a.Hkv * row};
-    const cuuint32_t t_box[3] = {64, 1, (cuuint32_t)a.N};
+    const cuuint32_t t_box[3] = {64, 1, (cuuint32_t)kPage};
     const bool k_ok = p.pair == 2 ? map(&m.k, 3, a.k_pool, v_dims, v_strides, w_box)
                                   : map(&m.k, 2, a.k_pool, pool_dims, pool_strides, pool_box);
     if (!k_ok || !map(&m.v, 3, a.v_pool, v_dims, v_strides, v_box) ||

@@ -3,8 +3,8 @@
 // Rows (nodes of consecutive sequences of a group, times the query heads of a KV head)
 // are taken in blocks of at most 128, or of 256 for a pair of CTAs.  A block's key list is made of 64-key
 // pages: the group's common pages, which all of its rows see, then for each of its
-// sequences the pages that it has for itself and a page with its tree's nodes, which
-// that sequence's rows see.  Two pages make a key tile.  In a group without common
+// sequences the pages that it has for itself, which that sequence's rows see, and last
+// the tree nodes of all its sequences (they follow each other in memory), 64 to a page.  Two pages make a key tile.  In a group without common
 // pages to read once, a block holds rows of one sequence.  The segments (block, KV
 // head) form one flat list of tiles that is cut over the CTAs; a piece that does not
 // hold all tiles of its segment leaves partial sums (O, max, sum), which the merge
@@ -18,7 +18,7 @@ namespace shr {
 
 constexpr int kMagic = 0x6c745370;
 constexpr int kRows = 128;  // of a CTA: the MMA's M
-constexpr int kMaxCtas = 1024;
+constexpr int kMaxCtas = 512;
 
 struct Dims {
     int B, N, Hq, Hkv, G, D, groups;
@@ -32,7 +32,6 @@ struct Dims {
     __host__ __device__ int max_blocks() const { return B * NG; }
     __host__ __device__ int max_segs() const { return B * NG * Hkv; }
     __host__ __device__ long long max_pieces() const { return (long long)C + max_segs(); }
-    __host__ __device__ int max_nodes() const { return half(false) > half(true) ? half(false) : half(true); }
 };
 
 // Nodes of a block: as few blocks as hold `nodes`, of equal size; whole sequences of N
@@ -75,14 +74,25 @@ static_assert(sizeof(Block) == 32, "two 16-byte words");
 
 // What a CTA does at a time: tiles [ta, te) of a segment.
 struct Piece {
-    int block, g;
+    int b0, seqs, node0, nodes;  // of its block
+    int used, vp;
     int ta, te;
-    int slot;  // row of the partial sums, -1: all tiles
-    int own;   // rows of a sequence without common pages
+    int g;
+    int slot;    // row of the partial sums, -1: all tiles
+    int own;     // rows of a sequence without common pages
     int reread;  // other blocks read most of its pages too
-    int pad;
 };
-static_assert(sizeof(Piece) == 32, "two 16-byte words");
+static_assert(sizeof(Piece) == 48, "three 16-byte words");
+
+// A segment that several CTAs have tiles of, in the place of the first of them.
+struct Split {
+    int count;         // CTAs, 0: none begins here
+    int row;           // the first one's partial sums; the others' follow block_rows() apart
+    int node0, rows;   // its rows: those of nodes from node0 on ...
+    int g;             // ... and of this KV head
+    int pad[3];
+};
+static_assert(sizeof(Split) == 32, "two 16-byte words");
 
 struct Cta {
     int first, pieces, tiles, pad;
@@ -98,12 +108,8 @@ struct Group {
 struct Seq {
     int group, first;  // its group and that one's first sequence
     int L, used;
-    int off;           // pages of the sequences before it, without those that are read with their groups, with their trees
+    int off;           // pages of the sequences before it, without those that are read with their groups
     int pad;
-};
-
-struct Seg {
-    int first, count;  // CTAs that have its tiles; count 1: no partial sums
 };
 
 struct Head {
@@ -118,7 +124,7 @@ struct Plan {  // a plan's parts in its buffer
     Group* grp;    // [groups + 1]
     Seq* seq;      // [B + 1]
     Block* blk;    // [blocks + 1]
-    Seg* seg;      // [segments], in the order of the flat list: group, KV head, block
+    Split* split;  // [C]
     Piece* piece;  // [CTA + segment]
 };
 
@@ -138,7 +144,7 @@ __host__ __device__ inline size_t plan_bytes(const Dims& d, Plan* p, void* at) {
     q.grp = reinterpret_cast<Group*>(take(sizeof(Group) * ((size_t)d.groups + 1)));
     q.seq = reinterpret_cast<Seq*>(take(sizeof(Seq) * ((size_t)d.B + 1)));
     q.blk = reinterpret_cast<Block*>(take(sizeof(Block) * ((size_t)d.max_blocks() + 1)));
-    q.seg = reinterpret_cast<Seg*>(take(sizeof(Seg) * (size_t)d.max_segs()));
+    q.split = reinterpret_cast<Split*>(take(sizeof(Split) * (size_t)d.C));
     q.piece = reinterpret_cast<Piece*>(take(sizeof(Piece) * (size_t)d.max_pieces()));
     if (p) *p = q;
     return n;

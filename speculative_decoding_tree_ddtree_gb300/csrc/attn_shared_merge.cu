@@ -50,32 +50,78 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
     constexpr int kU = 32 / kV;  // partials in flight
     __shared__ float s_o[kMergeWarps][D];
     __shared__ float2 s_ml[kMergeWarps];
+    __shared__ int s_warp[kMergeWarps];
+    __shared__ Split s_split[kMaxCtas];
+    __shared__ int s_row[kMaxCtas + 1];  // rows of the split segments before each
     const lucetree_attn_args& a = W.a;
     const Dims& d = W.d;
     if (threadIdx.x == 0) pdl_trigger();
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    // ---- the split segments.  This reads the plan before the wait below: the attention
+    // kernel lets this one start only after its own wait, so the plan is final.
+    if (!plan_fits(W)) {
+        pdl_wait();  // (no launch completes before the one it follows)
+        return;
+    }
+    int n = 0, total = 0;
+    for (int c0 = 0; c0 < d.C; c0 += kMergeThreads) {
+        const int c = c0 + t;
+        Split sp = {};
+        if (c < d.C) {
+            const int4* x = reinterpret_cast<const int4*>(W.plan.split + c);
+            int4* y = reinterpret_cast<int4*>(&sp);
+            y[0] = x[0];
+            y[1] = x[1];
+        }
+        // how many come before it, and their rows (in the low 20 bits), by one scan
+        const int mine = sp.count > 0 ? 1 << 20 | sp.rows : 0;
+        int incl = mine;
+#pragma unroll
+        for (int y = 1; y < 32; y <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, y);
+            if (lane >= y) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        int all = 0, pre = incl - mine;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            pre += w < warp ? s_warp[w] : 0;
+            all += s_warp[w];
+        }
+        if (mine) {
+            s_split[n + (pre >> 20)] = sp;
+            s_row[n + (pre >> 20)] = total + (pre & 0xFFFFF);
+        }
+        n += all >> 20;
+        total += all & 0xFFFFF;
+    }
+    if (t == 0) s_row[n] = total;
+    __syncthreads();
     pdl_wait();  // the partial sums
-    if (!plan_fits(W)) return;
     const size_t pr = partial_rows(d);
-    const long long rows = (long long)d.B * d.N * d.Hq, warps = (long long)gridDim.x * kMergeWarps;
+    const long long rows = total, warps = (long long)gridDim.x * kMergeWarps;
     // warps to a row: as many as keep every row in flight
     int G = kMergeWarps;
     while (G > 1 && rows * G > warps) G >>= 1;
     const int member = warp % G;
     for (long long x0 = (long long)blockIdx.x * (kMergeWarps / G); x0 < rows; x0 += warps / G) {
         const long long x = x0 + warp / G;
-        const int node = (int)((x < rows ? x : 0) / d.Hq), h = (int)(x % d.Hq), g = h / d.G;
-        // the row's segment, and where its partial sums lie
-        const int b = node / d.N;
-        const Seq q = W.plan.seq[b];
-        const Group grp = W.plan.grp[q.group];
-        const int k = grp.used > 0 ? (node - grp.seq0 * d.N) / d.NPG : (b - grp.seq0) * d.NG + (node - b * d.N) / d.NPGo;
-        const int node0 = grp.used > 0 ? grp.seq0 * d.N + k * d.NPG : b * d.N + (node - b * d.N) / d.NPGo * d.NPGo;
-        const Seg seg = W.plan.seg[(size_t)grp.block0 * d.Hkv + (size_t)g * grp.blocks + k];
-        const bool has_row = x < rows && seg.count > 1;
-        const int count = has_row ? seg.count : 0;
-        const size_t first = (size_t)row0_of(d, grp.seq0, grp.n, g, node0) + (size_t)d.block_rows() * seg.first +
-                             (node - node0) * d.G + h % d.G;
+        const bool has_row = x < rows;
+        int at = 0;
+        if (has_row) {
+            int hi = n - 1;
+            while (at < hi) {
+                const int mid = (at + hi + 1) / 2;
+                if (s_row[mid] <= x) at = mid;
+                else hi = mid - 1;
+            }
+        }
+        const Split& sp = s_split[at];
+        const int r = has_row ? (int)x - s_row[at] : 0;
+        const int count = has_row ? sp.count : 0;
+        const size_t first = has_row ? (size_t)sp.row + r : 0;
         // partial j's O row
         auto o_at = [&](int j) { return W.ws + (first + (size_t)d.block_rows() * j) * D; };
         float m = -INFINITY, l = 0.f, o[kV] = {};
@@ -155,9 +201,10 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             o[y] *= inv;
             finite = finite && isfinite(o[y]);
         }
-        store_row<kV>(reinterpret_cast<TO*>(W.out) + x * D + lane * kV, o);
+        const size_t row = (size_t)(sp.node0 + r / d.G) * d.Hq + sp.g * d.G + r % d.G;
+        store_row<kV>(reinterpret_cast<TO*>(W.out) + row * D + lane * kV, o);
         if (!finite) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
-        if (a.lse && lane == 0) a.lse[x] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
@@ -165,7 +212,9 @@ template <typename TO>
 cudaError_t launch(const Launch& W, cudaStream_t stream) {
     int dev = 0;
     cudaGetDevice(&dev);
-    const long long rows = (long long)W.d.B * W.d.N * W.d.Hq, cap = (long long)kCtasPerSm * device_sm_count(dev);
+    // a CTA for every row that may have to be joined, as long as all run at once
+    const long long all = (long long)W.d.B * W.d.N * W.d.Hq, most = (long long)W.d.C * W.d.block_rows();
+    const long long rows = all < most ? all : most, cap = (long long)kCtasPerSm * device_sm_count(dev);
     const dim3 grid((unsigned)(rows < cap ? rows : cap)), block(kMergeThreads);
     if (W.d.D == 256) return launch_pdl(merge_kernel<TO, 256>, grid, block, 0, stream, W);
     return launch_pdl(merge_kernel<TO, 128>, grid, block, 0, stream, W);

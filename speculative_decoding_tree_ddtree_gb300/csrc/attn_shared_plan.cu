@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
         int n = 0, before, used = 0;
         if (b < d.B) {
             used = grps[seqs[b].group].used;
-            n = pages_of(seqs[b].L) - used + 1;
+            n = pages_of(seqs[b].L) - used;
         }
         const int all = block_scan(n, s_warp, &before);
         if (b < d.B) {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
             }
             k.b0 = div_mod(k.node0, d.N).x;
             k.seqs = div_mod(k.node0 + k.nodes - 1, d.N).x - k.b0 + 1;
-            k.vp = k.used + seqs[k.b0 + k.seqs].off - seqs[k.b0].off;
+            k.vp = k.used + seqs[k.b0 + k.seqs].off - seqs[k.b0].off + pages_of(k.seqs * d.N);
             n = tiles_of(k) + kPieceCost;
         }
         const int all = block_scan(n, s_warp, &before);
@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
             c.pieces = s_seg[r + 1] - s_seg[r] + (s_tile[r + 1] > 0);
         }
         P.cta[r] = c;
+        P.split[r] = Split{};
     }
     __syncthreads();
 #pragma unroll 1
@@ -304,17 +305,23 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanLaunch A) {
         const Group q = grps[last_at_most(&grps[0].block0, sizeof(Group) / 4, groups, div_mod(s, d.Hkv).x)];
         const int2 at = div_mod(s - q.block0 * d.Hkv, q.blocks);
         const int k = q.block0 + at.y, tiles = tiles_of(blks[k]);
+        const Block& b = blks[k];
         Piece p;
-        p.block = k;
-        p.g = at.x;
+        p.b0 = b.b0;
+        p.seqs = b.seqs;
+        p.node0 = b.node0;
+        p.nodes = b.nodes;
+        p.used = b.used;
+        p.vp = b.vp;
         p.ta = s == s_seg[r] ? s_tile[r] : 0;
         p.te = s == s_seg[r + 1] ? s_tile[r + 1] : tiles;
-        p.slot = p.ta == 0 && p.te == tiles ? -1 : row0_of(d, q.seq0, q.n, at.x, blks[k].node0) + d.block_rows() * r;
+        p.g = at.x;
+        p.slot = p.ta == 0 && p.te == tiles ? -1 : row0_of(d, q.seq0, q.n, at.x, b.node0) + d.block_rows() * r;
         p.own = q.used == 0;
         p.reread = (q.used > 0 ? q.blocks : d.NG) > 1;
-        p.pad = 0;
         P.piece[x] = p;
-        if (p.ta == 0) P.seg[s] = Seg{r, last_at_most(s_seg, 1, n, s) - r + 1};
+        if (p.ta == 0 && p.te < tiles)
+            P.split[r] = Split{last_at_most(s_seg, 1, n, s) - r + 1, p.slot, b.node0, b.nodes * d.G, at.x, {}};
         atomicAdd(&P.cta[r].tiles, p.te - p.ta);
     }
     // what was laid out in shared memory

@@ -159,6 +159,7 @@ struct Cursor {
         int4* w = reinterpret_cast<int4*>(&pc);
         w[0] = __ldg(x);
         w[1] = __ldg(x + 1);
+        w[2] = __ldg(x + 2);
         t = pc.ta;
     }
     __device__ bool first() const { return t == pc.ta; }
@@ -168,53 +169,46 @@ struct Cursor {
     }
 };
 
-__device__ __forceinline__ Block load_block(const Launch& W, int k) {
-    Block b;
-    const int4* x = reinterpret_cast<const int4*>(W.plan.blk + k);
-    int4* w = reinterpret_cast<int4*>(&b);
-    w[0] = __ldg(x);
-    w[1] = __ldg(x + 1);
-    return b;
-}
-
 // A page of a block's key list.
 struct Page {
-    int id;    // pool page, -1: none
-    int seq;   // its sequence of the block, -1: all
+    int id;    // pool page, -1: none; a tree page: its first node
+    int seq;   // a sequence's own page: which of the block's; a tree page: its number; -1: all see it
     int keys;  // keys of it that exist (0: a page that is missing)
     bool tree;
 };
-__device__ __forceinline__ Page page_at(const Launch& W, const Block& b, int v) {
-    Page p = {-1, -1, 0, false};
-    if (v >= b.vp) return p;
+__device__ __forceinline__ Page page_at(const Launch& W, const Piece& p, int v) {
+    Page r = {-1, -1, 0, false};
+    if (v >= p.vp) return r;
     int col = v;
-    long long row = b.b0;
-    p.keys = kPage;
-    if (v >= b.used) {
-        const int x = __ldg(&W.plan.seq[b.b0].off) + v - b.used;
-        int lo = b.b0, hi = b.b0 + b.seqs - 1;
+    long long row = p.b0;
+    r.keys = kPage;
+    if (v >= p.used) {
+        const int x = __ldg(&W.plan.seq[p.b0].off) + v - p.used;
+        const int past = x - __ldg(&W.plan.seq[p.b0 + p.seqs].off);
+        if (past >= 0) {
+            r.tree = true;
+            r.seq = past;
+            r.id = p.b0 * W.d.N + past * kPage;
+            r.keys = min(kPage, p.seqs * W.d.N - past * kPage);
+            return r;
+        }
+        int lo = p.b0, hi = p.b0 + p.seqs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (__ldg(&W.plan.seq[mid].off) <= x) lo = mid;
             else hi = mid - 1;
         }
         row = lo;
-        p.seq = lo - b.b0;
-        const int i = x - __ldg(&W.plan.seq[lo].off);
-        if (x == __ldg(&W.plan.seq[lo + 1].off) - 1) {
-            p.tree = true;
-            p.keys = W.d.N;
-            return p;
-        }
-        col = b.used + i;
-        p.keys = min(kPage, __ldg(&W.plan.seq[lo].L) - col * kPage);
+        r.seq = lo - p.b0;
+        col = p.used + x - __ldg(&W.plan.seq[lo].off);
+        r.keys = min(kPage, __ldg(&W.plan.seq[lo].L) - col * kPage);
     }
     const int id = __ldg(W.a.page_table + row * W.a.max_pages_per_seq + col);
-    if (id >= 0 && id < W.a.num_pages) p.id = id;
-    else p.keys = 0;
-    return p;
+    if (id >= 0 && id < W.a.num_pages) r.id = id;
+    else r.keys = 0;
+    return r;
 }
-// In one word: keys, tree, sequence + 1.
+// In one word: keys, tree, seq + 1.
 __device__ __forceinline__ int page_word(const Page& p) { return p.keys | (p.tree ? 0x80 : 0) | (p.seq + 1) << 8; }
 
 template <int D, bool BF16, bool PV16, bool PAIR>
@@ -264,11 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 2)
         for (int i = lane; i < kBadSets * kBadWords; i += 32) ms->vbad[i / kBadWords][i % kBadWords] = 0;
-    // rows of Q that no piece loads: their rows of S and O are never used, but finite
-    for (int i = d.max_nodes() * d.G * 8 + threadIdx.x; i < kRows * 8; i += kThreads)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) reinterpret_cast<uint4*>(sQ + c * kChunkBytes)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
+    // (rows of Q past a block's own are whatever lies there: their rows of S and O are never used)
     if (warp == 1) {
         if constexpr (PAIR) {
             tmem_alloc_pair(&ms->tmem_base, kTmemCols);
@@ -302,8 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // inputs may come from the previous kernel on the stream
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
+    Cta start = W.plan.cta[blockIdx.x / d.pair];  // (loaded with the head, not after it)
     const bool fits = plan_fits(W);
-    const Cta start = fits ? W.plan.cta[blockIdx.x / d.pair] : Cta{0, 0, 0, 0};
+    if (!fits) start.tiles = 0;
     if (start.tiles == 0) {  // uniform across the CTA: nothing to do but give TMEM back
         if (!fits && threadIdx.x == 0) atomicOr(a.status, LUCETREE_DEV_BAD_ROW);
         teardown();
@@ -315,11 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================================================ TMA producer
         const int oob_row = a.num_pages * d.Hkv * kPage;  // first row past the pool: zero fill
         const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
-        const uint32_t tree_bytes = (uint32_t)d.N * 128u;  // one 64-dim box of the tree's nodes
-        uint32_t chunk = 0, vchunk = 0;  // of K, of V
+                uint32_t chunk = 0, vchunk = 0;  // of K, of V
         int q_loads = 0;
         bool ok = true;
-        // A tile's pages: pool row, or for a tree's page -1 - (first node)
+        // A tile's pages: pool row, or for a tree page -1 - (first node)
         struct Operand {
             int at0, at1;
             int g;
@@ -348,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (PAIR) {
                         // [64 keys of page `rank`][dims 128 * c .. +127], 64 dims after the other 64
                         const int at = rank ? o.at1 : o.at0;
-                        mbar_arrive_expect_tx(bar, at < 0 ? 2 * tree_bytes : (uint32_t)kChunkBytes);
+                        mbar_arrive_expect_tx(bar, kChunkBytes);
                         if (at < 0) {
                             tma_load_3d(dst, &tm_kt, 128 * c, o.g, -1 - at, bar);
                             tma_load_3d(dst + 8192, &tm_kt, 128 * c + 64, o.g, -1 - at, bar);
@@ -357,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         // [128 keys: page 0 then page 1][dims 64 * c .. +63]
-                        mbar_arrive_expect_tx(bar, (tree0 ? tree_bytes : 8192u) + (tree1 ? tree_bytes : 8192u));
+                        mbar_arrive_expect_tx(bar, kChunkBytes);
                         if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
                         else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
                         if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
@@ -379,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint64_t* bar = &ms->vfull[vchunk % kMaxSlots];
                     if constexpr (PAIR && D == 128) {
                         // [128 keys: page 0 then page 1][dims 64 * rank .. +63]
-                        mbar_arrive_expect_tx(bar, (o.at0 < 0 ? tree_bytes : 8192u) + (o.at1 < 0 ? tree_bytes : 8192u));
+                        mbar_arrive_expect_tx(bar, kChunkBytes);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int at = h ? o.at1 : o.at0;
@@ -389,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         // [64 keys of a page][128 dims], 64 dims after the other 64
                         const int at = (PAIR ? c : c & 1) ? o.at1 : o.at0, x = PAIR ? 128 * rank : 128 * (c >> 1);
-                        mbar_arrive_expect_tx(bar, at < 0 ? 2 * tree_bytes : (uint32_t)kChunkBytes);
+                        mbar_arrive_expect_tx(bar, kChunkBytes);
                         if (at < 0) {
                             tma_load_3d(dst, &tm_vt, x, o.g, -1 - at, bar);
                             tma_load_3d(dst + 8192, &tm_vt, x + 64, o.g, -1 - at, bar);
@@ -406,14 +396,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         Cursor cur;
         cur.start(start);
-        Block blk = {};
         // the operands of 16 tiles, a page to a lane, one batch ahead
         auto load_batch = [&](int tb) {
             const int v = 2 * tb + lane;
             if (v >= 2 * cur.pc.te) return oob_row;
-            const Page p = page_at(W, blk, v);
-            if (p.tree) return -1 - (blk.b0 + p.seq) * d.N;
-            if (p.id < 0 && v < blk.vp) atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
+            const Page p = page_at(W, cur.pc, v);
+            if (p.tree) return -1 - p.id;
+            if (p.id < 0 && v < cur.pc.vp) atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
             return p.id >= 0 ? (p.id * d.Hkv + cur.pc.g) * kPage : oob_row;
         };
         int at_cur = 0, at_next = 0;
@@ -426,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool have_k = cur.live;
             if (have_k) {
                 const int rel = cur.t - cur.pc.ta;
-                if (rel == 0) blk = load_block(W, cur.pc.block);
                 if ((rel & 15) == 0) at_cur = at_next;
                 if (rel == 0 || (rel & 15) == 8) {
                     at_next = load_batch(cur.t + (rel == 0 ? 0 : 8));
@@ -444,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(&ms->q_full, D / 64 * nodes * d.G * 128);
 #pragma unroll 1
                         for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(sQ + c * kChunkBytes, tm, 64 * c, cur.pc.g * d.G, blk.node0 + (int)rank * nodes,
+                            tma_load_3d(sQ + c * kChunkBytes, tm, 64 * c, cur.pc.g * d.G, cur.pc.node0 + (int)rank * nodes,
                                         &ms->q_full);
                     }
                     __syncwarp();
@@ -630,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ct = threadIdx.x - 64;  // 0 .. 63
         Cursor cur;
         cur.start(start);
-        Block blk = {};
         int word_cur = 0, word_next = 0;  // pages of 16 tiles, one to a lane
         uint32_t j = 0;
         bool ok = true;
@@ -638,10 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur.step(W);
             if (!cur.live) break;
             const int rel = cur.t - cur.pc.ta;
-            if (rel == 0) blk = load_block(W, cur.pc.block);
             if ((rel & 15) == 0) word_cur = word_next;
             if (rel == 0 || (rel & 15) == 8) {
-                word_next = page_word(page_at(W, blk, 2 * (cur.t + (rel == 0 ? 0 : 8)) + lane));
+                word_next = page_word(page_at(W, cur.pc, 2 * (cur.t + (rel == 0 ? 0 : 8)) + lane));
                 if (rel == 0) word_cur = word_next;
             }
             // ring position of V(j)'s first chunk: the K operands before it
@@ -682,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < kBatch; ++k) {
                             const int u = ct + 32 * kConvWarps * (u0 + k);
                             if ((word & 0x80) && not_finite<BF16, kConvert>(x[k])) {
-                                const int node = ((word >> 8) - 1) * d.N + ((u & 511) >> 3);
+                                const int node = ((word >> 8) - 1) * kPage + ((u & 511) >> 3);  // of the block's trees
                                 uint32_t* to = &ms->vbad[cur.piece_no % kBadSets][node >> 5];
                                 if constexpr (PAIR) {  // its other dims, and other rows, are the other CTA's
                                     or_at(cluster_addr(to, 0), 1u << (node & 31));
@@ -733,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (!bad) {
             cur.next_piece(W);
             if (!cur.live) break;
-            const Block blk = load_block(W, cur.pc.block);
+            const Piece& blk = cur.pc;
             const int before = (int)rank * d.half(cur.pc.own);  // the block's nodes in the pair's first CTA
             const bool mine = row < min(d.half(cur.pc.own), blk.nodes - before) * d.G;
             const int node = blk.node0 + (mine ? before + row / d.G : 0);
@@ -752,13 +738,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool first = rel == 0;
                 if ((rel & 31) == 0) word_cur = word_next;
                 if (first || (rel & 31) == 16) {
-                    word_next = page_word(page_at(W, blk, 2 * (t + (first ? 0 : 16) + lane) + half));
+                    word_next = page_word(page_at(W, cur.pc, 2 * (t + (first ? 0 : 16) + lane) + half));
                     if (first) word_cur = word_next;
                 }
                 const int word = __shfl_sync(0xffffffffu, word_cur, rel & 31);
                 const int owner = (word >> 8) - 1;
-                uint64_t vis = word & 0x80 ? anc : low_bits(word & 0x7f);
-                if (owner >= 0 && owner != seq) vis = 0;
+                uint64_t vis = low_bits(word & 0x7f);
+                if (word & 0x80) {
+                    const int at = seq * d.N - owner * kPage;  // my tree's first node in the page
+                    vis = at >= kPage || at <= -kPage ? 0 : at >= 0 ? anc << at : anc >> -at;
+                } else if (owner >= 0 && owner != seq) {
+                    vis = 0;
+                }
                 const bool plain = __all_sync(0xffffffffu, vis == ~0ull);
                 const bool none = __all_sync(0xffffffffu, vis == 0);
 
@@ -789,9 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x[k]));
                     top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
-                // one barrier decides whether shifts have to move (a row without one has neg_m = infinity)
+                // one barrier decides whether shifts have to move (a row without one has neg_m = infinity);
+                // rows past the block's own have no say, or what lies there would decide the others' roundings
                 const bool bad_now = bad || aborted(ms);
-                if (bar_sync_or(1, kSoftmaxThreads, bad_now || first || top + neg_m > kTau)) {
+                if (bar_sync_or(1, kSoftmaxThreads, bad_now || first || (mine && top + neg_m > kTau))) {
                     ms->xchg[half][row] = top;  // for the row's other page
                     if (bar_sync_or(1, kSoftmaxThreads, bad_now)) {
                         bad = true;

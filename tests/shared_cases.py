@@ -61,8 +61,7 @@ def read_plan(plan, B, N, Hq, Hkv, D, groups):
     NG = -(-N // cap)
     NPGo = -(-N // NG)
     NG = -(-N // NPGo)
-    sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups + 1, 5), seq=(B + 1, 6), blk=(B * NG + 1, 8), seg=(B * NG * Hkv, 2),
-                 piece=(C + B * NG * Hkv, 8))
+    sizes = dict(head=(1, 16), cta=(C, 4), grp=(groups + 1, 5), seq=(B + 1, 6), blk=(B * NG + 1, 8), split=(C, 8), piece=(C + B * NG * Hkv, 12))
     at, out = 0, dict(NG=NG, NPGo=NPGo, NPG=block_nodes(-(-B // groups) * N, N, cap), C=C, rows=ROWS * pair)
     for name, (n, w) in sizes.items():
         out[name] = np.frombuffer(raw, np.int32, n * w, at).reshape(n, w)
@@ -84,14 +83,14 @@ def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
     both, of = common(ctx, start, table, pages), [max(g for g in range(groups) if start[g] <= b) for b in range(B)]
     used = p["grp"][:groups, 0]
     assert all(u in (0, n) for u, n in zip(used, both))
-    own = [-(-int(ctx[b]) // PAGE) - used[of[b]] + 1 for b in range(B)]
+    own = [-(-int(ctx[b]) // PAGE) - used[of[b]] for b in range(B)]
     assert list(p["seq"][:, 4]) == list(np.concatenate([[0], np.cumsum(own)]))
     node = 0
     for k in range(blocks):
         group, b0, seqs, node0, nodes, u, vp, _ = p["blk"][k]
         assert node0 == node and 1 <= nodes <= (NPG if u else NPGo)
         assert b0 == node0 // N and seqs == (node0 + nodes - 1) // N - b0 + 1 and (seqs == 1 or u)
-        assert group == of[b0] == of[b0 + seqs - 1] and u == used[group] and vp == u + sum(own[b0:b0 + seqs])
+        assert group == of[b0] == of[b0 + seqs - 1] and u == used[group] and vp == u + sum(own[b0:b0 + seqs]) + -(-seqs * N // PAGE)
         node += nodes
     assert node == B * N
     # segments in the flat order: group, KV head, block
@@ -99,26 +98,32 @@ def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
     for g in range(groups):
         mine = [k for k in range(blocks) if p["blk"][k, 0] == g]
         segs += [(k, h) for h in range(Hkv) for k in mine]
-    done, rows, total = {}, [], 0
+    done, rows, splits = {}, [], {}
     for c in range(C):
         first, n, tiles, _ = p["cta"][c]
         count = 0
         for i in range(first, first + n):
             assert 0 <= i < len(p["piece"])
-            block, g, ta, te, slot, alone, _, _ = p["piece"][i]
+            b0, seqs, node0, nodes, u, vp, ta, te, g, slot, alone, _ = p["piece"][i]
             s = i - c
-            assert segs[s] == (block, g) and 0 <= ta < te <= (p["blk"][block, 6] + 1) // 2
-            assert alone == (p["blk"][block, 5] == 0)
-            whole = (ta, te) == (0, (p["blk"][block, 6] + 1) // 2)
-            assert (slot < 0) == whole == (p["seg"][s, 1] == 1) and p["seg"][s, 0] <= c < p["seg"][s].sum()
+            block = segs[s][0]
+            assert list(p["blk"][block, 1:7]) == [b0, seqs, node0, nodes, u, vp] and segs[s][1] == g
+            assert 0 <= ta < te <= (vp + 1) // 2 and alone == (u == 0)
+            whole = (ta, te) == (0, (vp + 1) // 2)
+            assert (slot < 0) == whole
             if not whole:
-                rows.append((slot, p["blk"][block, 4] * G))
+                rows.append((slot, nodes * G))
+                k = c - len(done.get(s, []))  # the CTA that has its first tiles
+                n_split, row, n0, n_rows, head = p["split"][k, :5]
+                assert (n0, n_rows, head) == (node0, nodes * G, g) and slot == row + p["rows"] * (c - k)
+                splits[s] = (k, n_split)
             done.setdefault(s, []).append((ta, te))
             count += te - ta
         assert count == tiles
     for s, (k, _) in enumerate(segs):
         joins(done[s], (p["blk"][k, 6] + 1) // 2)
-        assert len(done[s]) == p["seg"][s, 1]
+        assert len(done[s]) == splits.get(s, (0, 1))[1]
+    assert sorted(k for k, _ in splits.values()) == list(np.nonzero(p["split"][:, 0])[0])
     at = 0
     for slot, n in sorted(rows):
         assert slot >= at
