@@ -14,7 +14,7 @@ namespace shr {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClusterMax = 8;
 // Batches that are laid out in shared memory (each trip to the plan in global memory costs its latency).

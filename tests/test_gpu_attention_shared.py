@@ -320,3 +320,162 @@ def test_pools_past_four_gigabytes(cuda_dev):
     out, lse, status = call(big, torch.bfloat16)
     assert status == 0
     near(out, lse, ref)
+
+
+# groups of more than 128 rows, which pairs of CTAs take together
+PAIRED = [([(10, [700, 650, 641, 720])], 12, 8, 2, 128, "bf16"), ([(10, [700, 650, 641, 720])], 12, 8, 2, 256, "f16"),
+          ([(7, [460, 470]), (0, [300]), (3, [200] * 9)], 16, 12, 2, 256, "bf16")]
+
+
+@pytest.mark.parametrize("i", range(len(PAIRED)))
+@pytest.mark.parametrize("out", ["f32", "same"])
+def test_pairs_and_nodes_that_are_not_finite(cuda_dev, i, out):
+    """Values that are not finite in one half of the dims, or of the keys, reach the rows of both CTAs that see them."""
+    LT = _lt()
+    s = make(*PAIRED[i], seed=20 + i)
+    t = s["q"].dtype if out == "same" else torch.float32
+    ref = reference(s, p_step=P_STEP[t])
+    out_, lse, status = call(s, t)
+    assert status == 0
+    near(out_, lse, ref)
+    B, N, D = s["q"].shape[0], s["q"].shape[1], s["q"].shape[3]
+    for b, node, dim, name in ((0, 3, 1, "v_tree"), (1, N - 1, D - 1, "v_tree"), (B - 1, 0, D // 2, "v_tree"), (1, 2, 5, "k_tree")):
+        x = dict(s)
+        x[name] = s[name].clone()
+        x[name][b, node, 0, dim] = float("inf") if name == "v_tree" else float("nan")
+        got, lse, status = call(x, t)
+        assert status == LT.DEV_NONFINITE
+        Hq, Hkv = s["q"].shape[2], s["k_tree"].shape[2]
+        good = torch.ones(B, N, Hq, dtype=torch.bool)
+        good[b, :, :Hq // Hkv] = ~s["sees"][b, :, node][:, None]  # (query heads of KV head 0)
+        near(got, lse, ref, good)
+        assert bool(torch.isnan(got[~good]).all()) and bool(torch.isnan(lse[~good]).all())
+
+
+def test_pairs_rows_without_keys_and_missing_pages(cuda_dev):
+    LT = _lt()
+    s = make([(0, [0, 0, 0]), (4, [260, 300, 280])], 16, 8, 2, 128, "f16", seed=3)
+    anc = s["anc_mask"].cuda().clone()
+    anc[1, 9] = 0
+    out, lse, status = call(s, torch.float32, anc=anc)
+    assert status == LT.DEV_BAD_NODE
+    assert bool((out[1, 9] == 0).all()) and bool(torch.isneginf(lse[1, 9]).all())
+    good = torch.ones(6, 16, dtype=torch.bool)
+    good[1, 9] = False
+    near(out, lse, reference(s), good)
+    table = s["page_table"].cuda()
+    bad = table.clone()
+    bad[4, 4] = -1  # positions 256 .. of sequence 4
+    out, lse, status = call(s, torch.float32, table=bad, plan_table=table)
+    assert status == LT.DEV_BAD_PAGE
+    t = dict(s, ctx_len=torch.tensor([0, 0, 0, 260, 256, 280], dtype=torch.int32))
+    near(out, lse, reference(t))
+
+
+def test_pairs_growing_and_steep_scores(cuda_dev):
+    s = make([(20, [1300, 1400, 1350])], 24, 4, 1, 256, "bf16", seed=9, junk=0.0)
+    s["q"] = torch.full_like(s["q"], 0.25)
+    for b in range(3):
+        for p in range(0 if b == 0 else 1280, int(s["ctx_len"][b])):
+            at = int(s["page_table"][b, p // PAGE]), slice(None), p % PAGE
+            s["k_pool"][at] = s["k_pool"][at] * 0.1 + p / 100
+    check(s, torch.float32)
+    check(s, torch.bfloat16)
+    s = make([(16, [1024, 1100, 1050])], 20, 4, 1, 128, "f16", seed=2, junk=0.0)
+    for j in range(16):
+        s["k_pool"][int(s["page_table"][0, j])] *= 40.0 if j % 4 == 1 else 0.01
+    check(s, torch.float32, scale=1.0)
+
+
+def test_pairs_are_identical_from_call_to_call(cuda_dev):
+    for D, t in ((256, "bf16"), (128, "f16")):
+        s = make([(40, [2600 + i for i in range(9)]), (0, [5000]), (33, [2200, 2300])], 22, 12, 2, D, t, seed=6)
+        first = call(s, s["q"].dtype)
+        for _ in range(4):
+            again = call(s, s["q"].dtype)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_a_forked_prompt_decodes_with_shared_pages(cuda_dev):
+    """A prompt appended, forked into beams, and decoded for some steps: rotation, plan, attention of two layers and
+    commit on the library's calls, against a cache kept token by token."""
+    LT = _lt()
+    B, N, Hq, Hkv, D, layers, prompt = 6, 3, 8, 2, 128, 2, 200
+    g, maxp, pages = torch.Generator().manual_seed(1), 8, 60
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    e = lambda *s, t=torch.int32: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    steps, _ = LT.lucetree_rope_steps(64, 1e4)
+    freq = 1e4 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64)
+    steps, status = steps.cuda(), i32(0)
+    pools = [(r(pages, Hkv, PAGE, D), r(pages, Hkv, PAGE, D)) for _ in range(layers)]
+
+    def turned(x, pos):  # x [n][H][D] at pos [n], as the cache holds it
+        a = (pos[:, None].double() * freq)[:, None]
+        x = x.double().cpu()
+        y = x.clone()
+        y[..., :32] = x[..., :32] * a.cos() - x[..., 32:64] * a.sin()
+        y[..., 32:64] = x[..., :32] * a.sin() + x[..., 32:64] * a.cos()
+        return y.to(torch.bfloat16).double()
+
+    # the prompt
+    table = torch.full((1, maxp), -1, dtype=torch.int32, device="cuda")
+    table[0, :4] = i32(40, 3, 17, 5)
+    ref = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    ref[table[0, :4].long()] = 1
+    cache = []
+    for k_pool, v_pool in pools:
+        k, v = r(prompt, Hkv, D), r(prompt, Hkv, D)
+        ctx = e(1)
+        LT.lucetree_append_kv(k, v, i32(0, prompt), table, i32(0), ctx, k_pool, v_pool, status, steps=steps)
+        cache.append([(turned(k, torch.arange(prompt)), v.double().cpu()) for _ in range(B)])
+    # six beams of it
+    src, out_t, ctx_b, ref_b, cs, cd = i32(*[0] * B), e(B, maxp), e(B), e(pages), e(B), e(B)
+    ws = e(LT.lucetree_reorder_pages_workspace(1, B, pages), t=torch.uint8)
+    LT.lucetree_reorder_pages(table, ctx, src, 2 * N * 4, ref, out_t, ctx_b, ref_b, cs, cd, status, ws)
+    for pool in pools:
+        LT.lucetree_copy_pages(cs, cd, *pool, status)
+    plan = e(LT.lucetree_shared_plan_bytes(B, N, Hq, Hkv, D, 1), t=torch.uint8)
+    aws = e(LT.lucetree_verify_attn_shared_workspace(B, N, Hq, Hkv, D, 1), t=torch.uint8)
+    shared, anc = e(1), e(B, N, t=torch.int64)
+    for step in range(4):
+        parent = i32(-1, 0, 0).expand(B, N).contiguous()  # two continuations of node 0
+        LT.lucetree_build_anc_mask(parent, anc, status)
+        LT.lucetree_shared_plan(out_t, ctx_b, i32(0, B), N, Hq, Hkv, D, pages, shared, plan, status)
+        assert int(shared.item()) == prompt // PAGE
+        take = torch.tensor([(b + step) % 3 for b in range(B)])  # 0: node 0; 1, 2: that child too
+        acc = torch.full((B, N), -1, dtype=torch.int32)
+        acc[:, 0] = 0
+        acc[take > 0, 1] = take[take > 0].int()
+        n_acc = 1 + (take > 0).int()
+        L = ctx_b.cpu()
+        new_ctx = e(B)
+        for layer, (k_pool, v_pool) in enumerate(pools):
+            qkv = r(B, N, (Hq + 2 * Hkv) * D)
+            q, k, v = (x.unflatten(-1, (-1, D)) for x in qkv.split([Hq * D, Hkv * D, Hkv * D], -1))
+            qr, kt, vt = e(*q.shape, t=q.dtype), e(*k.shape, t=q.dtype), e(*v.shape, t=q.dtype)
+            LT.lucetree_rope(q, k, steps, 0, qr, kt, status, ctx_len=ctx_b, anc_mask=anc, v=v, v_out=vt)
+            out = e(B, N, Hq, D, t=torch.float32)
+            LT.lucetree_verify_attn_shared(qr, k_pool, v_pool, out_t, ctx_b, kt, vt, anc, 1, plan, out, status, aws)
+            LT.lucetree_commit(kt, vt, acc.cuda(), n_acc.int().cuda(), out_t, ctx_b, new_ctx, k_pool, v_pool, status)
+            for b in range(B):
+                pos = torch.tensor([L[b], L[b] + 1, L[b] + 1])
+                kb, vb = turned(k[b], pos), v[b].double().cpu()
+                qb = turned(q[b], pos)
+                kc, vc = cache[layer][b]
+                for i in range(N):
+                    path = [0] if i == 0 else [0, i]
+                    K, V = torch.cat([kc, kb[path]]), torch.cat([vc, vb[path]])
+                    for h in range(Hq):
+                        x = K[:, h // 4] @ qb[i, h] * D ** -0.5
+                        p = torch.softmax(x, 0)
+                        want = p @ V[:, h // 4]
+                        # P in fp16: 2^-11 of a term, and 2^-25 of the largest; 2^-12 for a rotated value that lies next
+                        # to the border of two bf16 values, where 32 and 64 bits may round apart (2^-8 of one of a
+                        # score's 128 products, D^-0.5 of which the score has, for few keys)
+                        room = (2.0 ** -11 + 2.0 ** -12) * (p @ V[:, h // 4].abs()) + 2.0 ** -25 * V[:, h // 4].abs().sum(0)
+                        assert bool(((out[b, i, h].double().cpu() - want).abs() <= room).all())
+                keep = acc[b][:int(n_acc[b])].long()
+                cache[layer][b] = (torch.cat([kc, kb[keep]]), torch.cat([vc, vb[keep]]))
+        ctx_b = new_ctx
+        assert int(status.item()) == 0 and torch.equal(ctx_b.cpu(), L + n_acc)
