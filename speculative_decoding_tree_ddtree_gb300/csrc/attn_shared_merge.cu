@@ -59,13 +59,7 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     // ---- the split segments.  This reads the plan before the wait below: the attention
     // kernel lets this one start only after its own wait, so the plan is final.
-    if (!plan_fits(W)) {
-        pdl_wait();  // (no launch completes before the one it follows)
-        return;
-    }
-    int n = 0, total = 0;
-    for (int c0 = 0; c0 < d.C; c0 += kMergeThreads) {
-        const int c = c0 + t;
+    auto split_of = [&](int c) {
         Split sp = {};
         if (c < d.C) {
             const int4* x = reinterpret_cast<const int4*>(W.plan.split + c);
@@ -73,6 +67,17 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             y[0] = x[0];
             y[1] = x[1];
         }
+        return sp;
+    };
+    Split sp = split_of(t);  // (with the head, not after it)
+    if (!plan_fits(W)) {
+        pdl_wait();  // (no launch completes before the one it follows)
+        return;
+    }
+    int n = 0, total = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < d.C; c0 += kMergeThreads) {
+        if (c0 > 0) sp = split_of(c0 + t);
         // how many come before it, and their rows (in the low 20 bits), by one scan
         const int mine = sp.count > 0 ? 1 << 20 | sp.rows : 0;
         int incl = mine;
@@ -101,17 +106,21 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
     __syncthreads();
     pdl_wait();  // the partial sums
     const size_t pr = partial_rows(d);
-    const long long rows = total, warps = (long long)gridDim.x * kMergeWarps;
-    // warps to a row: as many as keep every row in flight
-    int G = kMergeWarps;
-    while (G > 1 && rows * G > warps) G >>= 1;
-    const int member = warp % G;
-    for (long long x0 = (long long)blockIdx.x * (kMergeWarps / G); x0 < rows; x0 += warps / G) {
-        const long long x = x0 + warp / G;
+    const int rows = total, warps = (int)gridDim.x * kMergeWarps;  // (rows: at most 512 segments' 256)
+    // warps to a row: as many as keep every row in flight, a power of two
+    int bits = 3;
+#pragma unroll 1
+    while (bits > 0 && rows > warps >> bits) --bits;
+    static_assert(kMergeWarps == 8, "2^3");
+    const int G = 1 << bits, member = warp & (G - 1);
+#pragma unroll 1
+    for (int x0 = (int)blockIdx.x << (3 - bits); x0 < rows; x0 += warps >> bits) {
+        const int x = x0 + (warp >> bits);
         const bool has_row = x < rows;
         int at = 0;
         if (has_row) {
             int hi = n - 1;
+#pragma unroll 1
             while (at < hi) {
                 const int mid = (at + hi + 1) / 2;
                 if (s_row[mid] <= x) at = mid;
@@ -119,18 +128,26 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             }
         }
         const Split& sp = s_split[at];
-        const int r = has_row ? (int)x - s_row[at] : 0;
+        const int r = has_row ? x - s_row[at] : 0;
         const int count = has_row ? sp.count : 0;
         const size_t first = has_row ? (size_t)sp.row + r : 0;
         // partial j's O row
         auto o_at = [&](int j) { return W.ws + (first + (size_t)d.block_rows() * j) * D; };
         float m = -INFINITY, l = 0.f, o[kV] = {};
         // this warp's partials are member, member + G, ..
-        const int mine = has_row ? (count - member + G - 1) / G : 0;
+        const int mine = has_row ? (count - member + G - 1) >> bits : 0;
+#pragma unroll 1
         for (int k0 = 0; k0 < mine; k0 += 32) {
             const int n = min(32, mine - k0);
-            float v[kU][kV];
-            auto load = [&](int u0) {
+            float mk = -INFINITY, lk = 0.f, w = 0.f;
+            if (lane < n) {
+                const float* s = W.ws + pr * D + first + (size_t)d.block_rows() * (member + (k0 + lane) * G);
+                mk = s[0];
+                lk = s[pr];
+            }
+#pragma unroll 1
+            for (int u0 = 0; u0 < n; u0 += kU) {
+                float v[kU][kV];
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     if (u0 + u < n) {
@@ -140,28 +157,20 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
                         for (int y = 0; y < kV; ++y) v[u][y] = 0.f;
                     }
                 }
-            };
-            load(0);  // with the maxima and sums, not after them
-            float mk = -INFINITY, lk = 0.f;
-            if (lane < n) {
-                const float* s = W.ws + pr * D + first + (size_t)d.block_rows() * (member + (k0 + lane) * G);
-                mk = s[0];
-                lk = s[pr];
-            }
-            float top = fmaxf(m, mk);
+                if (u0 == 0) {  // (the maxima and sums come with the first rows, not before them)
+                    float top = fmaxf(m, mk);
+#pragma unroll 1
+                    for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+                    w = mk > -INFINITY ? exp2f(mk - top) : 0.f;  // (0 past n)
+                    float sum = w * lk;
+#pragma unroll 1
+                    for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+                    const float keep = m > -INFINITY ? exp2f(m - top) : 0.f;
+                    l = fmaf(l, keep, sum);
+                    m = top;
 #pragma unroll
-            for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
-            const float w = mk > -INFINITY ? exp2f(mk - top) : 0.f;  // (0 past n)
-            float sum = w * lk;
-#pragma unroll
-            for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
-            const float keep = m > -INFINITY ? exp2f(m - top) : 0.f;
-            l = fmaf(l, keep, sum);
-            m = top;
-#pragma unroll
-            for (int y = 0; y < kV; ++y) o[y] *= keep;
-            for (int u0 = 0; u0 < n; u0 += kU) {
-                if (u0 > 0) load(u0);
+                    for (int y = 0; y < kV; ++y) o[y] *= keep;
+                }
 #pragma unroll
                 for (int u = 0; u < kU; ++u) {
                     const float wu = __shfl_sync(0xffffffffu, w, u0 + u);
@@ -179,11 +188,13 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             __syncthreads();
             if (member != 0) continue;
             float top = m;
+#pragma unroll 1
             for (int w = 1; w < G; ++w) top = fmaxf(top, s_ml[warp + w].x);
             const float keep = m > -INFINITY ? exp2f(m - top) : 0.f;
             l *= keep;
 #pragma unroll
             for (int y = 0; y < kV; ++y) o[y] *= keep;
+#pragma unroll 1
             for (int w = 1; w < G; ++w) {
                 const float2 ml = s_ml[warp + w];
                 const float wt = ml.x > -INFINITY ? exp2f(ml.x - top) : 0.f;
