@@ -9,6 +9,10 @@
 // shared memory once each (192 KB with D = 256); with the keys on M, as the windowed
 // attention has them for its few rows, it is V^T and P^T instead of V (272 KB for 144 rows),
 // and shared memory's bandwidth is what bounds many rows.
+//   - Pairs of CTAs (cta_group::2, M = 256) where the mean group has more than 128 rows: each CTA has
+//     half of the block's nodes and loads half of the keys (K) and of the dims (V), so a tile costs
+//     half of the loads and of shared memory's reads for a row.  Without them 16 sequences at budget
+//     22 under 16,384 tokens took 148 us instead of 113.
 //   - Two S buffers: QK of the next tile runs while a tile's softmax does.  D = 256 uses all
 //     512 columns (S 2 x 128, O 256).
 //   - Eight softmax warps: a tile's first page belongs to one warpgroup, the second to
@@ -23,6 +27,14 @@
 //     output's own rounding, and the terms' roundings average out) and V is multiplied
 //     as it lands; otherwise P is fp16 (2^-11) and bf16 V is converted in shared memory
 //     (exact from 2^-17 to below 65536).
+//
+// Measured with 24 query and 4 KV heads of 256 dims, bf16 in and out, the merge included: 96
+// sequences at budget 22 under 16,384 tokens 507 to 535 us (1.52 to 1.60 PFLOP/s; a tile of the pair 2,700
+// cycles, its MMAs 2,048); 16 such sequences 114; one token each of 192 72, of 96 48, of 8
+// 22.7 (67 MB of keys and values, 10 us at HBM's rate; four tiles in most CTAs where the mean is
+// 3.4 are 1.8 of the rest, the others the chain of plan, page table and first tile, the last tile
+// and the merge).  With one CTA a tile of 128 KB takes 2.9 us where every page is read once
+// (24 groups of 8 beams: 86 us), which is HBM's rate.
 #pragma once
 
 #include "attn_prefix_tc.cuh"
@@ -46,7 +58,8 @@ constexpr int kSoftmaxThreads = 32 * kSmWarps;
 constexpr int kThreads = 128 + kSoftmaxThreads;
 constexpr int kMaxSlots = 12;
 constexpr int kBadSets = 8;    // pieces whose V may be in the ring at once, and more
-constexpr int kBadWords = 12;  // tree nodes of a block's sequences: at most 254 + 2 N
+constexpr int kNodeWords = 12;  // tree nodes of a block's sequences: at most 254 + 2 N
+constexpr int kBadWords = kNodeWords + 8;  // ... and the sequences
 
 struct Misc {
     float xchg[2][kRows];        // a row's values for the other warpgroup's half
@@ -58,9 +71,12 @@ struct Misc {
     uint64_t s_full[2], p_full[2];  // of tiles j, at [j & 1]
     uint64_t pv_done[2];            // (PV(j - 2) is done once S(j) is there: two of them tell PV(j) from it)
     uint64_t q_full, q_peer, q_empty, drain;
-    uint32_t vbad[kBadSets][kBadWords];  // piece n at [n % kBadSets]: tree nodes whose V is not finite
+    // piece n at [n % kBadSets]: tree nodes, and sequences with own pages, whose V is not finite
+    uint32_t vbad[kBadSets][kBadWords];
     uint32_t tmem_base;
     int abort_flag;
+    int pass;   // 1: the second one, with all values looked at ...
+    int again;  // ... which comes if this is 1
 };
 
 template <int D, bool PAIR>
@@ -139,23 +155,25 @@ __device__ __forceinline__ bool not_finite(const uint4& u) {
 
 // The CTA's tiles in order: piece and tile within its segment.
 struct Cursor {
-    Cta me;
-    int piece_no;  // -1 before the first
+    int next, left;  // the next piece's place in the plan, and how many come from there on
+    int serial;      // number of the current one, counted over both passes
     int t;
     bool live;
     Piece pc;
-    __device__ void start(const Cta& c) {
-        me = c;
-        piece_no = -1;
+    __device__ void start(const Cta& c, int pass) {
+        next = c.first;
+        left = c.pieces;
+        serial = pass * c.pieces - 1;
         t = -1;
         pc.te = 0;
         live = true;
     }
     __device__ void next_piece(const Launch& W) {
-        ++piece_no;
-        live = piece_no < me.pieces;
+        live = left > 0;
         if (!live) return;
-        const int4* x = reinterpret_cast<const int4*>(W.plan.piece + me.first + piece_no);
+        --left;
+        ++serial;
+        const int4* x = reinterpret_cast<const int4*>(W.plan.piece + next++);
         int4* w = reinterpret_cast<int4*>(&pc);
         w[0] = __ldg(x);
         w[1] = __ldg(x + 1);
@@ -224,10 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kNS = L::kNS;
 
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sQ = smem;
-    uint8_t* sSlots = smem + L::kSlotOff;
-    Misc* ms = reinterpret_cast<Misc*>(smem + L::kMiscOff);
+    uint8_t* const base0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Misc* ms = reinterpret_cast<Misc*>(base0 + L::kMiscOff);
 
     const lucetree_attn_args& a = W.a;
     const Dims& d = W.d;
@@ -254,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&ms->q_empty, 1);
         mbar_init(&ms->drain, 1);
         ms->abort_flag = 0;
+        ms->pass = ms->again = 0;
         mbar_fence_init();
     }
     if (warp == 2)
@@ -280,10 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are there
     tc_fence_after();
-    const uint32_t tmem = ms->tmem_base;
     auto teardown = [&]() {
-        if constexpr (PAIR) cluster_sync();  // the other CTA's arrivals and MMAs have come
-        if (warp == 1) {
+        const uint32_t tmem = ms->tmem_base;
+        if (threadIdx.x >> 5 == 1) {
             if constexpr (PAIR) tmem_dealloc_pair(tmem, kTmemCols);
             else tmem_dealloc(tmem, kTmemCols);
         }
@@ -297,644 +313,700 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!fits) start.tiles = 0;
     if (start.tiles == 0) {  // uniform across the CTA: nothing to do but give TMEM back
         if (!fits && threadIdx.x == 0) atomicOr(a.status, LUCETREE_DEV_BAD_ROW);
+        if constexpr (PAIR) cluster_sync();
         teardown();
         return;
     }
-    const uint32_t n_tiles = (uint32_t)start.tiles;
 
-    if (warp == 0) {
-        // ============================================================ TMA producer
-        const int oob_row = a.num_pages * d.Hkv * kPage;  // first row past the pool: zero fill
-        const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
-                uint32_t chunk = 0, vchunk = 0;  // of K, of V
-        int q_loads = 0;
-        bool ok = true;
-        // A tile's pages: pool row, or for a tree page -1 - (first node)
-        struct Operand {
-            int at0, at1;
-            int g;
-            uint64_t pol;
-        };
-        const bool leader = elect_one();
-        uint32_t slot = 0, turn = 0;  // ring position and its pass
-        auto next_slot = [&]() {
-            const bool w = mbar_wait(&ms->empty[slot], (turn & 1) ^ 1);
-            return __all_sync(0xffffffffu, w);  // lanes agree on a timeout
-        };
-        auto advance = [&]() {
-            if (++slot == (uint32_t)kNS) {
-                slot = 0;
-                ++turn;
-            }
-        };
-        auto issue_k = [&](const Operand& o) -> bool {
-            const bool tree0 = o.at0 < 0, tree1 = o.at1 < 0;
+    // A value of a sequence's own pages that is not finite spoils the rows of the block's other sequences
+    // too (0 x it is NaN).  Looking for those in every page takes the V warps longer than the
+    // products do (32 sequences under 32,768 tokens: 50 -> 70 us); so the rows are looked at
+    // instead, once a piece is done, and if one is not finite the CTA goes through its pieces
+    // again and looks at all values.  Numbers of tiles, chunks and pieces go on.
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                if (!next_slot()) return false;
-                if (leader) {
-                    uint8_t* dst = sSlots + slot * kChunkBytes;
-                    uint64_t* bar = &ms->kfull[chunk % kMaxSlots];
-                    if constexpr (PAIR) {
-                        // [64 keys of page `rank`][dims 128 * c .. +127], 64 dims after the other 64
-                        const int at = rank ? o.at1 : o.at0;
-                        mbar_arrive_expect_tx(bar, kChunkBytes);
-                        if (at < 0) {
-                            tma_load_3d(dst, &tm_kt, 128 * c, o.g, -1 - at, bar);
-                            tma_load_3d(dst + 8192, &tm_kt, 128 * c + 64, o.g, -1 - at, bar);
-                        } else {
-                            tma_load_3d_hint(dst, &tm_k, 0, at, 2 * c, bar, o.pol);
-                        }
-                    } else {
-                        // [128 keys: page 0 then page 1][dims 64 * c .. +63]
-                        mbar_arrive_expect_tx(bar, kChunkBytes);
-                        if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
-                        else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
-                        if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
-                        else tma_load_2d_hint(dst + 8192, &tm_k, 64 * c, o.at1, bar, o.pol);
-                    }
+    for (;;) {
+        // (what a pass finds out anew is kept in no register for the next one)
+        uint32_t zero, tid;
+        asm volatile("mov.u32 %0, 0;\n\tmov.u32 %1, %%tid.x;" : "=r"(zero), "=r"(tid));
+        const int warp = tid >> 5, lane = tid & 31;
+        const uint32_t rank = PAIR ? cluster_rank() : 0u;
+        uint8_t* const smem =
+            reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + zero + 1023) & ~uintptr_t(1023));
+        uint8_t* const sQ = smem;
+        uint8_t* const sSlots = smem + L::kSlotOff;
+        Misc* const ms = reinterpret_cast<Misc*>(smem + L::kMiscOff);
+        const uint32_t tmem = *(volatile uint32_t*)&ms->tmem_base;
+        const int pass = *(volatile int*)&ms->pass;
+        const uint32_t n_tiles = (uint32_t)start.tiles;
+        const uint32_t tiles0 = pass * n_tiles, chunks0 = tiles0 * kChunks, ring0 = 2 * chunks0;
+        if (warp == 0) {
+            // ============================================================ TMA producer
+            const int oob_row = a.num_pages * d.Hkv * kPage;  // first row past the pool: zero fill
+            const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
+            uint32_t chunk = chunks0, vchunk = chunks0;  // of K, of V
+            int q_loads = pass * start.pieces;
+            bool ok = true;
+            // A tile's pages: pool row, or for a tree page -1 - (first node)
+            struct Operand {
+                int at0, at1;
+                int g;
+                uint64_t pol;
+            };
+            const bool leader = elect_one();
+            uint32_t slot = ring0 % kNS, turn = ring0 / kNS;  // ring position and its turn
+            auto next_slot = [&]() {
+                const bool w = mbar_wait(&ms->empty[slot], (turn & 1) ^ 1);
+                return __all_sync(0xffffffffu, w);  // lanes agree on a timeout
+            };
+            auto advance = [&]() {
+                if (++slot == (uint32_t)kNS) {
+                    slot = 0;
+                    ++turn;
                 }
-                __syncwarp();
-                ++chunk;
-                advance();
-            }
-            return true;
-        };
-        auto issue_v = [&](const Operand& o) -> bool {
+            };
+            auto issue_k = [&](const Operand& o) -> bool {
+                const bool tree0 = o.at0 < 0, tree1 = o.at1 < 0;
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                if (!next_slot()) return false;
-                if (leader) {
-                    uint8_t* dst = sSlots + slot * kChunkBytes;
-                    uint64_t* bar = &ms->vfull[vchunk % kMaxSlots];
-                    if constexpr (PAIR && D == 128) {
-                        // [128 keys: page 0 then page 1][dims 64 * rank .. +63]
-                        mbar_arrive_expect_tx(bar, kChunkBytes);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int at = h ? o.at1 : o.at0;
-                            if (at < 0) tma_load_3d(dst + 8192 * h, &tm_vt, 64 * rank, o.g, -1 - at, bar);
-                            else tma_load_3d_hint(dst + 8192 * h, &tm_v, 0, at, rank, bar, o.pol);
-                        }
-                    } else {
-                        // [64 keys of a page][128 dims], 64 dims after the other 64
-                        const int at = (PAIR ? c : c & 1) ? o.at1 : o.at0, x = PAIR ? 128 * rank : 128 * (c >> 1);
-                        mbar_arrive_expect_tx(bar, kChunkBytes);
-                        if (at < 0) {
-                            tma_load_3d(dst, &tm_vt, x, o.g, -1 - at, bar);
-                            tma_load_3d(dst + 8192, &tm_vt, x + 64, o.g, -1 - at, bar);
-                        } else {
-                            tma_load_3d_hint(dst, &tm_v, 0, at, x / 64, bar, o.pol);
-                        }
-                    }
-                }
-                __syncwarp();
-                ++vchunk;
-                advance();
-            }
-            return true;
-        };
-        Cursor cur;
-        cur.start(start);
-        // the operands of 16 tiles, a page to a lane, one batch ahead
-        auto load_batch = [&](int tb) {
-            const int v = 2 * tb + lane;
-            if (v >= 2 * cur.pc.te) return oob_row;
-            const Page p = page_at(W, cur.pc, v);
-            if (p.tree) return -1 - p.id;
-            if (p.id < 0 && v < cur.pc.vp) atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
-            return p.id >= 0 ? (p.id * d.Hkv + cur.pc.g) * kPage : oob_row;
-        };
-        int at_cur = 0, at_next = 0;
-        Operand v_op = {0, 0, 0, pol_once};  // of the tile whose V is still to be loaded
-        bool have_v = false;
-        // K(t), then V(t-1); after the last tile its V alone
-        while (ok && cur.live) {
-            cur.step(W);
-            Operand op = v_op;
-            const bool have_k = cur.live;
-            if (have_k) {
-                const int rel = cur.t - cur.pc.ta;
-                if ((rel & 15) == 0) at_cur = at_next;
-                if (rel == 0 || (rel & 15) == 8) {
-                    at_next = load_batch(cur.t + (rel == 0 ? 0 : 8));
-                    if (rel == 0) at_cur = at_next;
-                }
-                if (rel == 0) {
-                    // a new segment: its queries replace the previous ones once their last QK is done
-                    if (cur.piece_no > 0) {
-                        const bool w = mbar_wait(&ms->q_empty, (cur.piece_no - 1) & 1);
-                        if (!(ok = __all_sync(0xffffffffu, w))) break;
-                    }
+                for (int c = 0; c < kChunks; ++c) {
+                    if (!next_slot()) return false;
                     if (leader) {
-                        const int nodes = d.half(cur.pc.own);
-                        const CUtensorMap* tm = cur.pc.own ? &tm_qown : &tm_q;
-                        mbar_arrive_expect_tx(&ms->q_full, D / 64 * nodes * d.G * 128);
-#pragma unroll 1
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(sQ + c * kChunkBytes, tm, 64 * c, cur.pc.g * d.G, cur.pc.node0 + (int)rank * nodes,
-                                        &ms->q_full);
+                        uint8_t* dst = sSlots + slot * kChunkBytes;
+                        uint64_t* bar = &ms->kfull[chunk % kMaxSlots];
+                        if constexpr (PAIR) {
+                            // [64 keys of page `rank`][dims 128 * c .. +127], 64 dims after the other 64
+                            const int at = rank ? o.at1 : o.at0;
+                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                            if (at < 0) {
+                                tma_load_3d(dst, &tm_kt, 128 * c, o.g, -1 - at, bar);
+                                tma_load_3d(dst + 8192, &tm_kt, 128 * c + 64, o.g, -1 - at, bar);
+                            } else {
+                                tma_load_3d_hint(dst, &tm_k, 0, at, 2 * c, bar, o.pol);
+                            }
+                        } else {
+                            // [128 keys: page 0 then page 1][dims 64 * c .. +63]
+                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                            if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
+                            else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
+                            if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
+                            else tma_load_2d_hint(dst + 8192, &tm_k, 64 * c, o.at1, bar, o.pol);
+                        }
                     }
                     __syncwarp();
-                    ++q_loads;
+                    ++chunk;
+                    advance();
                 }
-                op.at0 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15));
-                op.at1 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15) + 1);
-                op.g = cur.pc.g;
-                op.pol = cur.pc.reread ? pol_again : pol_once;
-            }
-            if (have_k) ok = issue_k(op);
-            if (ok && have_v) ok = issue_v(v_op);
-            v_op = op;
-            have_v = have_k;
-        }
-        if (!ok || aborted(ms)) {
-            set_abort(ms, a.status);
-            // wait (bounded) for this CTA's own copies still in flight
-            if (lane == 0) {
-                const uint32_t first = chunk > (uint32_t)kNS ? chunk - kNS : 0u;
-                for (uint32_t c = first; c < chunk; ++c)
-                    mbar_wait(&ms->kfull[c % kMaxSlots], (c / kMaxSlots) & 1, 200000000ll);
-                const uint32_t vfirst = vchunk > (uint32_t)kNS ? vchunk - kNS : 0u;
-                for (uint32_t c = vfirst; c < vchunk; ++c)
-                    mbar_wait(&ms->vfull[c % kMaxSlots], (c / kMaxSlots) & 1, 200000000ll);
-                if (q_loads > 0) mbar_wait(&ms->q_full, (q_loads - 1) & 1, 200000000ll);
-            }
-        }
-    } else if (warp == 1) {
-        // ============================================================ MMA issuer
-        // The whole warp goes through the loop, one elected lane issues: addresses and descriptors
-        // are then the warp's, in uniform registers (from one lane's registers an MMA took as long to
-        // issue as to run twice).
-        const bool leader = elect_one();
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            const bool w = mbar_wait(bar, parity);
-            ok = __all_sync(0xffffffffu, w);
-            return ok;
-        };
-        if (rank != 0) {
-            // the pair's second CTA: tells the first one what has landed here
-            Cursor qk;
-            qk.start(start);
-            uint32_t n = 0;
-            while (ok) {
-                qk.step(W);
-                if (!qk.live) break;
-                if (qk.first()) {
-                    if (!wait(&ms->q_full, qk.piece_no & 1)) break;
-                    if (leader) mbar_arrive_at(cluster_addr(&ms->q_peer, 0));
-                }
+                return true;
+            };
+            auto issue_v = [&](const Operand& o) -> bool {
 #pragma unroll 1
-                for (int c = 0; c < kChunks; ++c, ++n) {
-                    if (!wait(&ms->kfull[n % kMaxSlots], (n / kMaxSlots) & 1) || __any_sync(0xffffffffu, aborted(ms))) {
+                for (int c = 0; c < kChunks; ++c) {
+                    if (!next_slot()) return false;
+                    if (leader) {
+                        uint8_t* dst = sSlots + slot * kChunkBytes;
+                        uint64_t* bar = &ms->vfull[vchunk % kMaxSlots];
+                        if constexpr (PAIR && D == 128) {
+                            // [128 keys: page 0 then page 1][dims 64 * rank .. +63]
+                            mbar_arrive_expect_tx(bar, kChunkBytes);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int at = h ? o.at1 : o.at0;
+                                if (at < 0) tma_load_3d(dst + 8192 * h, &tm_vt, 64 * rank, o.g, -1 - at, bar);
+                                else tma_load_3d_hint(dst + 8192 * h, &tm_v, 0, at, rank, bar, o.pol);
+                            }
+                        } else {
+                            // [64 keys of a page][128 dims], 64 dims after the other 64
+                            const int at = (PAIR ? c : c & 1) ? o.at1 : o.at0, x = PAIR ? 128 * rank : 128 * (c >> 1);
+                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                            if (at < 0) {
+                                tma_load_3d(dst, &tm_vt, x, o.g, -1 - at, bar);
+                                tma_load_3d(dst + 8192, &tm_vt, x + 64, o.g, -1 - at, bar);
+                            } else {
+                                tma_load_3d_hint(dst, &tm_v, 0, at, x / 64, bar, o.pol);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    ++vchunk;
+                    advance();
+                }
+                return true;
+            };
+            Cursor cur;
+            cur.start(start, pass);
+            // the operands of 16 tiles, a page to a lane, one batch ahead
+            auto load_batch = [&](int tb) {
+                const int v = 2 * tb + lane;
+                if (v >= 2 * cur.pc.te) return oob_row;
+                const Page p = page_at(W, cur.pc, v);
+                if (p.tree) return -1 - p.id;
+                if (p.id < 0 && v < cur.pc.vp) atomicOr(a.status, LUCETREE_DEV_BAD_PAGE);
+                return p.id >= 0 ? (p.id * d.Hkv + cur.pc.g) * kPage : oob_row;
+            };
+            int at_cur = 0, at_next = 0;
+            Operand v_op = {0, 0, 0, pol_once};  // of the tile whose V is still to be loaded
+            bool have_v = false;
+            // K(t), then V(t-1); after the last tile its V alone
+            while (ok && cur.live) {
+                cur.step(W);
+                Operand op = v_op;
+                const bool have_k = cur.live;
+                if (have_k) {
+                    const int rel = cur.t - cur.pc.ta;
+                    if ((rel & 15) == 0) at_cur = at_next;
+                    if (rel == 0 || (rel & 15) == 8) {
+                        at_next = load_batch(cur.t + (rel == 0 ? 0 : 8));
+                        if (rel == 0) at_cur = at_next;
+                    }
+                    if (rel == 0) {
+                        // a new segment: its queries replace the previous ones once their last QK is done
+                        if (cur.serial > 0) {
+                            const bool w = mbar_wait(&ms->q_empty, (cur.serial - 1) & 1);
+                            if (!(ok = __all_sync(0xffffffffu, w))) break;
+                        }
+                        if (leader) {
+                            const int nodes = d.half(cur.pc.own);
+                            const CUtensorMap* tm = cur.pc.own ? &tm_qown : &tm_q;
+                            mbar_arrive_expect_tx(&ms->q_full, D / 64 * nodes * d.G * 128);
+#pragma unroll 1
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_3d(sQ + c * kChunkBytes, tm, 64 * c, cur.pc.g * d.G, cur.pc.node0 + (int)rank * nodes,
+                                            &ms->q_full);
+                        }
+                        __syncwarp();
+                        ++q_loads;
+                    }
+                    op.at0 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15));
+                    op.at1 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15) + 1);
+                    op.g = cur.pc.g;
+                    op.pol = cur.pc.reread ? pol_again : pol_once;
+                }
+                if (have_k) ok = issue_k(op);
+                if (ok && have_v) ok = issue_v(v_op);
+                v_op = op;
+                have_v = have_k;
+            }
+            if (!ok || aborted(ms)) {
+                set_abort(ms, a.status);
+                // wait (bounded) for this CTA's own copies still in flight
+                if (lane == 0) {
+                    const uint32_t first = chunk > (uint32_t)kNS ? chunk - kNS : 0u;
+                    for (uint32_t c = first; c < chunk; ++c)
+                        mbar_wait(&ms->kfull[c % kMaxSlots], (c / kMaxSlots) & 1, 200000000ll);
+                    const uint32_t vfirst = vchunk > (uint32_t)kNS ? vchunk - kNS : 0u;
+                    for (uint32_t c = vfirst; c < vchunk; ++c)
+                        mbar_wait(&ms->vfull[c % kMaxSlots], (c / kMaxSlots) & 1, 200000000ll);
+                    if (q_loads > 0) mbar_wait(&ms->q_full, (q_loads - 1) & 1, 200000000ll);
+                }
+            }
+        } else if (warp == 1) {
+            // ============================================================ MMA issuer
+            // The whole warp goes through the loop, one elected lane issues: addresses and descriptors
+            // are then the warp's, in uniform registers (from one lane's registers an MMA took as long to
+            // issue as to run twice).
+            const bool leader = elect_one();
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                const bool w = mbar_wait(bar, parity);
+                ok = __all_sync(0xffffffffu, w);
+                return ok;
+            };
+            if (rank != 0) {
+                // the pair's second CTA: tells the first one what has landed here
+                Cursor qk;
+                qk.start(start, pass);
+                uint32_t n = chunks0;
+                while (ok) {
+                    qk.step(W);
+                    if (!qk.live) break;
+                    if (qk.first()) {
+                        if (!wait(&ms->q_full, qk.serial & 1)) break;
+                        if (leader) mbar_arrive_at(cluster_addr(&ms->q_peer, 0));
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c, ++n) {
+                        if (!wait(&ms->kfull[n % kMaxSlots], (n / kMaxSlots) & 1) || __any_sync(0xffffffffu, aborted(ms))) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) mbar_arrive_at(cluster_addr(&ms->kpeer[n % kMaxSlots], 0));
+                        __syncwarp();
+                    }
+                }
+                if (!ok) set_abort(ms, a.status);
+            } else {
+                constexpr uint32_t M = PAIR ? 256 : 128, kNv = PAIR ? D : 128;  // PV's N
+                constexpr uint32_t id_qk = idesc_f16(M, 128, BF16 ? 1u : 0u, 0, 0);
+                constexpr uint32_t id_pv = idesc_f16(M, kNv, PV16 ? 1u : 0u, 0, 1);
+                constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
+                constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
+                const uint32_t aQ = smem_u32(sQ), aS = smem_u32(sSlots);
+                uint32_t slot = ring0 % kNS, jq = tiles0;   // ring position; tiles whose QK is issued
+                uint32_t kn = chunks0, vn = chunks0;        // chunks of K and of V so far
+                uint32_t first_bits = 0;        // bit k: the k-th last QK issued opened a piece
+                auto commit = [&](uint64_t* bar) {
+                    if constexpr (PAIR) mma_commit_pair(bar);
+                    else mma_commit(bar);
+                };
+                auto advance = [&]() {
+                    if (++slot == (uint32_t)kNS) slot = 0;
+                };
+                Cursor qk;
+                qk.start(start, pass);
+                // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
+                // (MMAs of one thread run in order).
+                auto next_qk = [&]() {
+                    qk.step(W);
+                    if (!qk.live) return;
+                    if (qk.first()) {
+                        if (!wait(&ms->q_full, qk.serial & 1)) return;
+                        if (PAIR && !wait(&ms->q_peer, qk.serial & 1)) return;
+                    }
+                    const uint32_t dS = tmem + (jq & 1) * 128;
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (!wait(&ms->kfull[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
+                        if (PAIR && !wait(&ms->kpeer[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint32_t at = aS + slot * kChunkBytes;
+                            if constexpr (PAIR) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_f16_ss_pair(dS, make_desc(hi_k, aQ + (2 * c + k / 4) * kChunkBytes + k % 4 * 32),
+                                                    make_desc(hi_k, at + k / 4 * 8192 + k % 4 * 32), id_qk, (c | k) != 0);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_f16_ss(dS, make_desc(hi_k, aQ + c * kChunkBytes + k * 32), make_desc(hi_k, at + k * 32),
+                                               id_qk, (c | k) != 0);
+                            }
+                            commit(&ms->empty[slot]);
+                        }
+                        __syncwarp();
+                        ++kn;
+                        advance();
+                    }
+                    if (leader) {
+                        commit(&ms->s_full[jq & 1]);
+                        if (qk.last()) commit(&ms->q_empty);
+                    }
+                    __syncwarp();
+                    first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
+                    ++jq;
+                };
+                next_qk();
+                if (ok && n_tiles > 1) next_qk();
+                for (uint32_t j = tiles0; ok && j < tiles0 + n_tiles; ++j) {
+                    if (__any_sync(0xffffffffu, aborted(ms))) break;
+                    // O += P(j) . V(j) once the softmax has written P(j); P's columns of a page begin
+                    // where S's did
+                    if (!wait(&ms->p_full[j & 1], (j >> 1) & 1)) break;
+                    const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (!wait(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) break;
+                        tc_fence_after();
+                        if (leader) {
+                            const uint32_t at = aS + slot * kChunkBytes, dO = tmem + L::kColO;
+                            if constexpr (PAIR && D == 128) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_f16_ts_pair(dO, aP + 64 * (k / 4) + 8 * (k % 4),
+                                                    make_desc(hi_v, at + k / 4 * 8192 + k % 4 * 2048), id_pv, k == 0 ? more : 1u);
+                            } else if constexpr (PAIR) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_f16_ts_pair(dO, aP + 64 * c + 8 * k, make_desc(hi_v, at + k * 2048), id_pv,
+                                                    (c | k) == 0 ? more : 1u);
+                            } else {
+                                // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_f16_ts(dO + 128 * (c >> 1), aP + 64 * (c & 1) + 8 * k, make_desc(hi_v, at + k * 2048),
+                                               id_pv, (c & 1) == 0 && k == 0 ? more : 1u);
+                            }
+                            commit(&ms->empty[slot]);
+                        }
+                        __syncwarp();
+                        ++vn;
+                        advance();
+                    }
+                    if (!ok) break;
+                    if (leader) commit(&ms->pv_done[j & 1]);
+                    __syncwarp();
+                    if (j + 2 < tiles0 + n_tiles) next_qk();
+                }
+                if (!ok || __any_sync(0xffffffffu, aborted(ms))) {
+                    set_abort(ms, a.status);
+                    if (leader) commit(&ms->drain);  // every MMA issued so far has finished before TMEM is freed
+                    mbar_wait(&ms->drain, 0, 200000000ll);
+                }
+            }
+            __syncwarp();
+        } else if (warp < 4) {
+            // ============================================================ V operand (warps 2, 3)
+            // Each V chunk, once landed: bf16 -> fp16 in place where PV runs on fp16, zeros in the
+            // rows of keys that no row sees (past a sequence's end, past the tree's nodes: arbitrary
+            // data, and 0 * NaN would poison every row), and zeros in place of values that are not finite
+            // in pages that some rows see and others do not: trees, and own pages of a block of several
+            // sequences.  Their nodes and sequences are noted, and the epilogue makes the rows that see
+            // them NaN.  Then vready.  Thread ct owns 16-byte units ct + 64 i of a chunk; unit u
+            // holds 8 dims of key (u % 512) / 8 (each 8 KB box is [64 keys][128 B]; the swizzle
+            // permutes units only within a key's row).
+            const int ct = tid - 64;  // 0 .. 63
+            Cursor cur;
+            cur.start(start, pass);
+            int word_cur = 0, word_next = 0;  // pages of 16 tiles, one to a lane
+            uint32_t j = 0;  // of this pass
+            bool ok = true;
+            while (ok) {
+                cur.step(W);
+                if (!cur.live) break;
+                const int rel = cur.t - cur.pc.ta;
+                if ((rel & 15) == 0) word_cur = word_next;
+                if (rel == 0 || (rel & 15) == 8) {
+                    word_next = page_word(page_at(W, cur.pc, 2 * (cur.t + (rel == 0 ? 0 : 8)) + lane));
+                    if (rel == 0) word_cur = word_next;
+                }
+                // ring position of V(j)'s first chunk: the K operands before it
+                // (K(0) .. K(j+1), or .. K(j) for the last tile) and V(0) .. V(j-1)
+                const uint32_t vbase = ring0 + ((j + 1 < n_tiles ? j + 2 : j + 1) + j) * kChunks;
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    const uint32_t vn = chunks0 + j * kChunks + c;
+                    // the pages in the chunk's two 8 KB boxes: one page twice, or both
+                    constexpr bool kBoth = PAIR && D == 128;
+                    const int page = kBoth ? 0 : PAIR ? c : c & 1;
+                    const int word0 = __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + page);
+                    const int word1 = kBoth ? __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + 1) : word0;
+                    const bool landed = mbar_wait(&ms->vfull[vn % kMaxSlots], (vn / kMaxSlots) & 1);
+                    if (!__all_sync(0xffffffffu, landed) || aborted(ms)) {
                         ok = false;
                         break;
                     }
-                    if (leader) mbar_arrive_at(cluster_addr(&ms->kpeer[n % kMaxSlots], 0));
-                    __syncwarp();
-                }
-            }
-            if (!ok) set_abort(ms, a.status);
-        } else {
-            constexpr uint32_t M = PAIR ? 256 : 128, kNv = PAIR ? D : 128;  // PV's N
-            constexpr uint32_t id_qk = idesc_f16(M, 128, BF16 ? 1u : 0u, 0, 0);
-            constexpr uint32_t id_pv = idesc_f16(M, kNv, PV16 ? 1u : 0u, 0, 1);
-            constexpr uint64_t hi_k = desc_hi(16, 1024, kLayoutSwizzle128);
-            constexpr uint64_t hi_v = desc_hi(8192, 1024, kLayoutSwizzle128);  // 2nd 64-dim box at +8 KB
-            const uint32_t aQ = smem_u32(sQ), aS = smem_u32(sSlots);
-            uint32_t slot = 0, jq = 0;      // ring position; tiles whose QK is issued
-            uint32_t kn = 0, vn = 0;        // chunks of K and of V so far
-            uint32_t first_bits = 0;        // bit k: the k-th last QK issued opened a piece
-            auto commit = [&](uint64_t* bar) {
-                if constexpr (PAIR) mma_commit_pair(bar);
-                else mma_commit(bar);
-            };
-            auto advance = [&]() {
-                if (++slot == (uint32_t)kNS) slot = 0;
-            };
-            Cursor qk;
-            qk.start(start);
-            // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
-            // (MMAs of one thread run in order).
-            auto next_qk = [&]() {
-                qk.step(W);
-                if (!qk.live) return;
-                if (qk.first()) {
-                    if (!wait(&ms->q_full, qk.piece_no & 1)) return;
-                    if (PAIR && !wait(&ms->q_peer, qk.piece_no & 1)) return;
-                }
-                const uint32_t dS = tmem + (jq & 1) * 128;
+                    uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
+                    // pages that not all rows see
+                    auto look = [&](int word) { return (word & 0x80) || (pass > 0 && (word >> 8) > 0 && cur.pc.seqs > 1); };
+                    // (nothing to change)
+                    const bool whole = (word0 & 0xff) == kPage && (word1 & 0xff) == kPage && !look(word0) && !look(word1);
+                    constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
+                    constexpr int kBatch = 4;                                      // loads in flight
+                    if (kConvert || !whole) {
 #pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    if (!wait(&ms->kfull[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
-                    if (PAIR && !wait(&ms->kpeer[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint32_t at = aS + slot * kChunkBytes;
-                        if constexpr (PAIR) {
+                        for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
+                            // (a batch lies in one box)
+                            const int word = u0 < kUnits / 2 ? word0 : word1, keys = word & 0x7f;
+                            const bool looked = look(word);
+                            uint4 x[kBatch];
+                            bool on[kBatch];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_f16_ss_pair(dS, make_desc(hi_k, aQ + (2 * c + k / 4) * kChunkBytes + k % 4 * 32),
-                                                make_desc(hi_k, at + k / 4 * 8192 + k % 4 * 32), id_qk, (c | k) != 0);
-                        } else {
+                            for (int k = 0; k < kBatch; ++k) {
+                                const int u = ct + 32 * kConvWarps * (u0 + k), key = (u & 511) >> 3;
+                                on[k] = key < keys;
+                                x[k] = on[k] ? base[u] : make_uint4(0, 0, 0, 0);
+                            }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16_ss(dS, make_desc(hi_k, aQ + c * kChunkBytes + k * 32), make_desc(hi_k, at + k * 32),
-                                           id_qk, (c | k) != 0);
-                        }
-                        commit(&ms->empty[slot]);
-                    }
-                    __syncwarp();
-                    ++kn;
-                    advance();
-                }
-                if (leader) {
-                    commit(&ms->s_full[jq & 1]);
-                    if (qk.last()) commit(&ms->q_empty);
-                }
-                __syncwarp();
-                first_bits = (first_bits << 1) | (qk.first() ? 1u : 0u);
-                ++jq;
-            };
-            next_qk();
-            if (ok && n_tiles > 1) next_qk();
-            for (uint32_t j = 0; ok && j < n_tiles; ++j) {
-                if (__any_sync(0xffffffffu, aborted(ms))) break;
-                // O += P(j) . V(j) once the softmax has written P(j); P's columns of a page begin
-                // where S's did
-                if (!wait(&ms->p_full[j & 1], (j >> 1) & 1)) break;
-                const uint32_t more = ((first_bits >> (jq - 1 - j)) & 1u) ^ 1u, aP = tmem + (j & 1) * 128;
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    if (!wait(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint32_t at = aS + slot * kChunkBytes, dO = tmem + L::kColO;
-                        if constexpr (PAIR && D == 128) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_f16_ts_pair(dO, aP + 64 * (k / 4) + 8 * (k % 4),
-                                                make_desc(hi_v, at + k / 4 * 8192 + k % 4 * 2048), id_pv, k == 0 ? more : 1u);
-                        } else if constexpr (PAIR) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16_ts_pair(dO, aP + 64 * c + 8 * k, make_desc(hi_v, at + k * 2048), id_pv,
-                                                (c | k) == 0 ? more : 1u);
-                        } else {
-                            // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f16_ts(dO + 128 * (c >> 1), aP + 64 * (c & 1) + 8 * k, make_desc(hi_v, at + k * 2048),
-                                           id_pv, (c & 1) == 0 && k == 0 ? more : 1u);
-                        }
-                        commit(&ms->empty[slot]);
-                    }
-                    __syncwarp();
-                    ++vn;
-                    advance();
-                }
-                if (!ok) break;
-                if (leader) commit(&ms->pv_done[j & 1]);
-                __syncwarp();
-                if (j + 2 < n_tiles) next_qk();
-            }
-            if (!ok || __any_sync(0xffffffffu, aborted(ms))) {
-                set_abort(ms, a.status);
-                if (leader) commit(&ms->drain);  // every MMA issued so far has finished before TMEM is freed
-                mbar_wait(&ms->drain, 0, 200000000ll);
-            }
-        }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ============================================================ V operand (warps 2, 3)
-        // Each V chunk, once landed: bf16 -> fp16 in place where PV runs on fp16, zeros in the
-        // rows of keys that no row sees (past a sequence's end, past the tree's nodes: arbitrary
-        // data, and 0 * NaN would poison every row), and zeros in place of tree values that are not
-        // finite, whose nodes are noted: some rows see them, others do not, and the epilogue makes
-        // the former NaN.  Then vready.  Thread ct owns 16-byte units ct + 64 i of a chunk; unit u
-        // holds 8 dims of key (u % 512) / 8 (each 8 KB box is [64 keys][128 B]; the swizzle
-        // permutes units only within a key's row).
-        const int ct = threadIdx.x - 64;  // 0 .. 63
-        Cursor cur;
-        cur.start(start);
-        int word_cur = 0, word_next = 0;  // pages of 16 tiles, one to a lane
-        uint32_t j = 0;
-        bool ok = true;
-        while (ok) {
-            cur.step(W);
-            if (!cur.live) break;
-            const int rel = cur.t - cur.pc.ta;
-            if ((rel & 15) == 0) word_cur = word_next;
-            if (rel == 0 || (rel & 15) == 8) {
-                word_next = page_word(page_at(W, cur.pc, 2 * (cur.t + (rel == 0 ? 0 : 8)) + lane));
-                if (rel == 0) word_cur = word_next;
-            }
-            // ring position of V(j)'s first chunk: the K operands before it
-            // (K(0) .. K(j+1), or .. K(j) for the last tile) and V(0) .. V(j-1)
-            const uint32_t vbase = ((j + 1 < n_tiles ? j + 2 : j + 1) + j) * kChunks;
-#pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                const uint32_t vn = j * kChunks + c;
-                // the pages in the chunk's two 8 KB boxes: one page twice, or both
-                constexpr bool kBoth = PAIR && D == 128;
-                const int page = kBoth ? 0 : PAIR ? c : c & 1;
-                const int word0 = __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + page);
-                const int word1 = kBoth ? __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + 1) : word0;
-                const bool landed = mbar_wait(&ms->vfull[vn % kMaxSlots], (vn / kMaxSlots) & 1);
-                if (!__all_sync(0xffffffffu, landed) || aborted(ms)) {
-                    ok = false;
-                    break;
-                }
-                uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
-                // (a page of 64 keys that is no tree: nothing to change)
-                const bool whole = (word0 & 0xff) == kPage && (word1 & 0xff) == kPage;
-                constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
-                constexpr int kBatch = 4;                                      // loads in flight
-                if (kConvert || !whole) {
-#pragma unroll 1
-                    for (int u0 = 0; u0 < kUnits; u0 += kBatch) {
-                        // (a batch lies in one box)
-                        const int word = u0 < kUnits / 2 ? word0 : word1, keys = word & 0x7f;
-                        uint4 x[kBatch];
-                        bool on[kBatch];
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int u = ct + 32 * kConvWarps * (u0 + k), key = (u & 511) >> 3;
-                            on[k] = key < keys;
-                            x[k] = on[k] ? base[u] : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            const int u = ct + 32 * kConvWarps * (u0 + k);
-                            if ((word & 0x80) && not_finite<BF16, kConvert>(x[k])) {
-                                const int node = ((word >> 8) - 1) * kPage + ((u & 511) >> 3);  // of the block's trees
-                                uint32_t* to = &ms->vbad[cur.piece_no % kBadSets][node >> 5];
-                                if constexpr (PAIR) {  // its other dims, and other rows, are the other CTA's
-                                    or_at(cluster_addr(to, 0), 1u << (node & 31));
-                                    or_at(cluster_addr(to, 1), 1u << (node & 31));
-                                    fence_cluster();
-                                } else {
-                                    atomicOr(to, 1u << (node & 31));
+                            for (int k = 0; k < kBatch; ++k) {
+                                const int u = ct + 32 * kConvWarps * (u0 + k);
+                                if (looked && not_finite<BF16, kConvert>(x[k])) {
+                                    const int owner = (word >> 8) - 1;
+                                    const int at = word & 0x80 ? owner * kPage + ((u & 511) >> 3) : kNodeWords * 32 + owner;
+                                    uint32_t* to = &ms->vbad[cur.serial % kBadSets][at >> 5];
+                                    const uint32_t bit = 1u << (at & 31);
+                                    if (*reinterpret_cast<volatile uint32_t*>(to) & bit) {
+                                        // (noted, in a pair by someone who tells the other CTA too)
+                                    } else if constexpr (PAIR) {  // its other dims, and other rows, are the other CTA's
+                                        or_at(cluster_addr(to, 0), bit);
+                                        or_at(cluster_addr(to, 1), bit);
+                                        fence_cluster();
+                                    } else {
+                                        atomicOr(to, bit);
+                                    }
+                                    x[k] = make_uint4(0, 0, 0, 0);
+                                    on[k] = false;
                                 }
-                                x[k] = make_uint4(0, 0, 0, 0);
-                                on[k] = false;
+                                if constexpr (kConvert) {
+                                    x[k].x = bf16x2_to_f16x2(x[k].x);
+                                    x[k].y = bf16x2_to_f16x2(x[k].y);
+                                    x[k].z = bf16x2_to_f16x2(x[k].z);
+                                    x[k].w = bf16x2_to_f16x2(x[k].w);
+                                }
+                                if (kConvert || !on[k]) base[u] = x[k];
                             }
-                            if constexpr (kConvert) {
-                                x[k].x = bf16x2_to_f16x2(x[k].x);
-                                x[k].y = bf16x2_to_f16x2(x[k].y);
-                                x[k].z = bf16x2_to_f16x2(x[k].z);
-                                x[k].w = bf16x2_to_f16x2(x[k].w);
-                            }
-                            if (kConvert || !on[k]) base[u] = x[k];
                         }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_at(cluster_addr(&ms->vready[vn % kMaxSlots], 0));
-                    else mbar_arrive(&ms->vready[vn % kMaxSlots]);
-                }
-            }
-            ++j;
-        }
-        if (!ok) set_abort(ms, a.status);
-    } else {
-        // ============================================================ softmax + epilogue
-        // Thread: row `row` (its TMEM lane), page `half` of every tile.
-        const int half = (warp - 4) >> 2;
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // the warp's lanes
-        const float sl2 = W.scale_log2;
-        uint32_t j = 0;
-        bool bad = false;  // warp-uniform at every tcgen05 load / store below
-        // bounded wait whose outcome all lanes of the warp agree on
-        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-            const bool w = mbar_wait(bar, parity);
-            return __all_sync(0xffffffffu, w);
-        };
-        Cursor cur;
-        cur.start(start);
-        while (!bad) {
-            cur.next_piece(W);
-            if (!cur.live) break;
-            const Piece& blk = cur.pc;
-            const int before = (int)rank * d.half(cur.pc.own);  // the block's nodes in the pair's first CTA
-            const bool mine = row < min(d.half(cur.pc.own), blk.nodes - before) * d.G;
-            const int node = blk.node0 + (mine ? before + row / d.G : 0);
-            const int b = node / d.N, i = node - b * d.N;
-            // (rows past the block's own go along with what all rows see, so that their warp needs no masks)
-            const int seq = mine || blk.seqs == 1 ? b - blk.b0 : -2;
-            const uint64_t anc = __ldg(a.anc_mask + node) & low_bits(d.N);
-            const long long out_row = (long long)node * d.Hq + cur.pc.g * d.G + row % d.G;
-            if (mine && half == 0 && !((anc >> i) & 1u)) atomicOr(a.status, LUCETREE_DEV_BAD_NODE);
-            float neg_m = INFINITY;  // the shift, negated: none yet
-            float l = 0.f;           // my page's part of the row's sum
-            int word_cur = 0, word_next = 0;  // my page of 32 tiles, one to a lane
-#pragma unroll 1
-            for (int t = cur.pc.ta; t < cur.pc.te; ++t) {
-                const int rel = t - cur.pc.ta;
-                const bool first = rel == 0;
-                if ((rel & 31) == 0) word_cur = word_next;
-                if (first || (rel & 31) == 16) {
-                    word_next = page_word(page_at(W, cur.pc, 2 * (t + (first ? 0 : 16) + lane) + half));
-                    if (first) word_cur = word_next;
-                }
-                const int word = __shfl_sync(0xffffffffu, word_cur, rel & 31);
-                const int owner = (word >> 8) - 1;
-                uint64_t vis = low_bits(word & 0x7f);
-                if (word & 0x80) {
-                    const int at = seq * d.N - owner * kPage;  // my tree's first node in the page
-                    vis = at >= kPage || at <= -kPage ? 0 : at >= 0 ? anc << at : anc >> -at;
-                } else if (owner >= 0 && owner != seq) {
-                    vis = 0;
-                }
-                const bool plain = __all_sync(0xffffffffu, vis == ~0ull);
-                const bool none = __all_sync(0xffffffffu, vis == 0);
-
-                if (!wait_all(&ms->s_full[j & 1], (j >> 1) & 1)) bad = true;
-                if (!bad) tc_fence_after();
-                const uint32_t ts = tl + (j & 1) * 128 + half * 64;
-                uint32_t x[64];  // scores in units of log2; masked ones -infinity
-                float top = -INFINITY;
-                if (!bad && !none) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld16(ts + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_wait_ld_regs16(*reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
-                    const uint64_t scale = pack2(sl2, sl2);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float2 y = unpack2(mul2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale));
-                        x[2 * k] = __float_as_uint(y.x);
-                        x[2 * k + 1] = __float_as_uint(y.y);
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) mbar_arrive_at(cluster_addr(&ms->vready[vn % kMaxSlots], 0));
+                        else mbar_arrive(&ms->vready[vn % kMaxSlots]);
                     }
-                    if (!plain) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (!((vis >> k) & 1u)) x[k] = 0xFF800000u;
-                    }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x[k]));
-                    top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                }
-                // one barrier decides whether shifts have to move (a row without one has neg_m = infinity);
-                // rows past the block's own have no say, or what lies there would decide the others' roundings
-                const bool bad_now = bad || aborted(ms);
-                if (bar_sync_or(1, kSoftmaxThreads, bad_now || first || (mine && top + neg_m > kTau))) {
-                    ms->xchg[half][row] = top;  // for the row's other page
-                    if (bar_sync_or(1, kSoftmaxThreads, bad_now)) {
-                        bad = true;
-                        break;
-                    }
-                    const float mo = -neg_m, mn = fmaxf(mo, fmaxf(top, ms->xchg[half ^ 1][row]));
-                    // (the shift of a row that has seen no key stays -infinity: its sum is 0)
-                    const float alpha = mn > mo ? ex2(mo - mn) : 1.f;
-                    neg_m = -mn;
-                    l = alpha > 0.f ? l * alpha : 0.f;
-                    if (!first) {
-                        // the O row so far moves with its shift, once PV(j-1) has finished adding to it:
-                        // each warpgroup half of the dims (a warp that timed out skips its TMEM
-                        // accesses but keeps to the barriers)
-                        if (!wait_all(&ms->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) bad = true;
-                        if (!bad) tc_fence_after();
-                        if (!bad && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t r[16];
-                                const uint32_t at = tl + L::kColO + half * (D / 2) + 16 * c;
-                                tmem_ld16(at, r);
-                                tmem_wait_ld_regs16(r);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
-                                tmem_st16(at, r);
-                            }
-                            tmem_wait_st();
-                        }
-                    }
-                    // (nobody overwrites the exchanged maxima before everybody has read them)
-                    if (bar_sync_or(1, kSoftmaxThreads, bad)) {
-                        bad = true;
-                        break;
-                    }
-                }
-                // P = 2^(x - m) as 16-bit pairs, over S: [row][32 columns of two keys each] where my
-                // page's S began
-                uint32_t ph[32];
-                if (none) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) ph[k] = 0;
-                } else {
-                    const float shift = neg_m == INFINITY ? 0.f : neg_m;  // (no key yet: every x is -infinity)
-                    const uint64_t m2 = pack2(shift, shift);
-                    uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float2 y = unpack2(add2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), m2));
-                        const float p0 = ex2(y.x), p1 = ex2(y.y);
-                        acc[k & 3] = add2(acc[k & 3], pack2(p0, p1));
-                        ph[k] = PV16 ? pack_bf162(p0, p1) : pack_half2(p0, p1);
-                    }
-                    const float2 s = unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
-                    l += s.x + s.y;
-                }
-                tmem_st16(ts, *reinterpret_cast<uint32_t(*)[16]>(&ph[0]));
-                tmem_st16(ts + 16, *reinterpret_cast<uint32_t(*)[16]>(&ph[16]));
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_at(cluster_addr(&ms->p_full[j & 1], 0));
-                    else mbar_arrive(&ms->p_full[j & 1]);
                 }
                 ++j;
             }
-            if (bad) break;
-
-            // ---------------------------------------------------------- epilogue
-            ms->xchg[half][row] = l;
-            const bool got = mbar_wait(&ms->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
-            if (bar_sync_or(1, kSoftmaxThreads, !got || aborted(ms))) {
-                bad = true;
-                break;
-            }
-            tc_fence_after();
-            l += ms->xchg[half ^ 1][row];
-            const uint32_t* vb = ms->vbad[cur.piece_no % kBadSets];
-            uint32_t any = 0;
-#pragma unroll
-            for (int k = 0; k < kBadWords; ++k) any |= vb[k];
-            if (__builtin_expect(any != 0, 0)) {
-                // bits seq * N .. + N - 1
-                const int at = seq * d.N, w = at >> 5, s = at & 31;
-                const uint64_t lo = (uint64_t)vb[w] | (uint64_t)(w + 1 < kBadWords ? vb[w + 1] : 0) << 32;
-                const uint64_t hi = w + 2 < kBadWords ? vb[w + 2] : 0;
-                const uint64_t bits = s ? lo >> s | hi << (64 - s) : lo;
-                if ((bits & anc) != 0) l = __int_as_float(0x7FC00000);
-            }
-            const bool whole = cur.pc.slot < 0;
-            const int at_row = cur.pc.slot + before * d.G + row;
-            const float inv = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN stays, and is flagged)
-            if (mine && half == 0) {
-                if (!whole) {
-                    float* s = W.ws + partial_rows(d) * D + at_row;
-                    s[0] = -neg_m;
-                    s[partial_rows(d)] = l;
-                } else if (a.lse) {
-                    a.lse[out_row] = l != 0.f ? (log2f(l) - neg_m) * kLn2 : -INFINITY;
-                }
-            }
-            bool finite = true;
+            if (!ok) set_abort(ms, a.status);
+        } else {
+            // ============================================================ softmax + epilogue
+            // Thread: row `row` (its TMEM lane), page `half` of every tile.
+            const int half = (warp - 4) >> 2;
+            const int row = (warp & 3) * 32 + lane;
+            const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);  // the warp's lanes
+            const float sl2 = W.scale_log2;
+            uint32_t j = tiles0;
+            bool bad = false;  // warp-uniform at every tcgen05 load / store below
+            // bounded wait whose outcome all lanes of the warp agree on
+            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+                const bool w = mbar_wait(bar, parity);
+                return __all_sync(0xffffffffu, w);
+            };
+            Cursor cur;
+            cur.start(start, pass);
+            while (!bad) {
+                cur.next_piece(W);
+                if (!cur.live) break;
+                const Piece& blk = cur.pc;
+                const int before = (int)rank * d.half(cur.pc.own);  // the block's nodes in the pair's first CTA
+                const bool mine = row < min(d.half(cur.pc.own), blk.nodes - before) * d.G;
+                const int node = blk.node0 + (mine ? before + row / d.G : 0);
+                const int b = node / d.N, i = node - b * d.N;
+                // (rows past the block's own go along with what all rows see, so that their warp needs no masks)
+                const int seq = mine || blk.seqs == 1 ? b - blk.b0 : -2;
+                const uint64_t anc = __ldg(a.anc_mask + node) & low_bits(d.N);
+                if (mine && half == 0 && !((anc >> i) & 1u)) atomicOr(a.status, LUCETREE_DEV_BAD_NODE);
+                float neg_m = INFINITY;  // the shift, negated: none yet
+                float l = 0.f;           // my page's part of the row's sum
+                int word_cur = 0, word_next = 0;  // my page of 32 tiles, one to a lane
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[16];
-                const int x = half * (D / 2) + 16 * c;
-                tmem_ld16(tl + L::kColO + x, r);
-                tmem_wait_ld_regs16(r);
-                if (!mine) continue;
-                if (!whole) {
-                    float4* o = reinterpret_cast<float4*>(W.ws + (size_t)at_row * D + x);
+                for (int t = cur.pc.ta; t < cur.pc.te; ++t) {
+                    const int rel = t - cur.pc.ta;
+                    const bool first = rel == 0;
+                    if ((rel & 31) == 0) word_cur = word_next;
+                    if (first || (rel & 31) == 16) {
+                        word_next = page_word(page_at(W, cur.pc, 2 * (t + (first ? 0 : 16) + lane) + half));
+                        if (first) word_cur = word_next;
+                    }
+                    const int word = __shfl_sync(0xffffffffu, word_cur, rel & 31);
+                    const int owner = (word >> 8) - 1;
+                    uint64_t vis = low_bits(word & 0x7f);
+                    if (word & 0x80) {
+                        const int at = seq * d.N - owner * kPage;  // my tree's first node in the page
+                        vis = at >= kPage || at <= -kPage ? 0 : at >= 0 ? anc << at : anc >> -at;
+                    } else if (owner >= 0 && owner != seq) {
+                        vis = 0;
+                    }
+                    const bool plain = __all_sync(0xffffffffu, vis == ~0ull);
+                    const bool none = __all_sync(0xffffffffu, vis == 0);
+
+                    if (!wait_all(&ms->s_full[j & 1], (j >> 1) & 1)) bad = true;
+                    if (!bad) tc_fence_after();
+                    const uint32_t ts = tl + (j & 1) * 128 + half * 64;
+                    uint32_t x[64];  // scores in units of log2; masked ones -infinity
+                    float top = -INFINITY;
+                    if (!bad && !none) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
-                                           __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-                    continue;
+                        for (int c = 0; c < 4; ++c) tmem_ld16(ts + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_wait_ld_regs16(*reinterpret_cast<uint32_t(*)[16]>(&x[16 * c]));
+                        const uint64_t scale = pack2(sl2, sl2);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float2 y = unpack2(mul2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale));
+                            x[2 * k] = __float_as_uint(y.x);
+                            x[2 * k + 1] = __float_as_uint(y.y);
+                        }
+                        if (!plain) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (!((vis >> k) & 1u)) x[k] = 0xFF800000u;
+                        }
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(x[k]));
+                        top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    }
+                    // one barrier decides whether shifts have to move (a row without one has neg_m = infinity);
+                    // rows past the block's own have no say, or what lies there would decide the others' roundings
+                    const bool bad_now = bad || aborted(ms);
+                    if (bar_sync_or(1, kSoftmaxThreads, bad_now || first || (mine && top + neg_m > kTau))) {
+                        ms->xchg[half][row] = top;  // for the row's other page
+                        if (bar_sync_or(1, kSoftmaxThreads, bad_now)) {
+                            bad = true;
+                            break;
+                        }
+                        const float mo = -neg_m, mn = fmaxf(mo, fmaxf(top, ms->xchg[half ^ 1][row]));
+                        // (the shift of a row that has seen no key stays -infinity: its sum is 0)
+                        const float alpha = mn > mo ? ex2(mo - mn) : 1.f;
+                        neg_m = -mn;
+                        l = alpha > 0.f ? l * alpha : 0.f;
+                        if (!first) {
+                            // the O row so far moves with its shift, once PV(j-1) has finished adding to it:
+                            // each warpgroup half of the dims (a warp that timed out skips its TMEM
+                            // accesses but keeps to the barriers)
+                            if (!wait_all(&ms->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) bad = true;
+                            if (!bad) tc_fence_after();
+                            if (!bad && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t r[16];
+                                    const uint32_t at = tl + L::kColO + half * (D / 2) + 16 * c;
+                                    tmem_ld16(at, r);
+                                    tmem_wait_ld_regs16(r);
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+                                    tmem_st16(at, r);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                        // (nobody overwrites the exchanged maxima before everybody has read them)
+                        if (bar_sync_or(1, kSoftmaxThreads, bad)) {
+                            bad = true;
+                            break;
+                        }
+                    }
+                    // P = 2^(x - m) as 16-bit pairs, over S: [row][32 columns of two keys each] where my
+                    // page's S began
+                    uint32_t ph[32];
+                    if (none) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ph[k] = 0;
+                    } else {
+                        const float shift = neg_m == INFINITY ? 0.f : neg_m;  // (no key yet: every x is -infinity)
+                        const uint64_t m2 = pack2(shift, shift);
+                        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float2 y = unpack2(add2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), m2));
+                            const float p0 = ex2(y.x), p1 = ex2(y.y);
+                            acc[k & 3] = add2(acc[k & 3], pack2(p0, p1));
+                            ph[k] = PV16 ? pack_bf162(p0, p1) : pack_half2(p0, p1);
+                        }
+                        const float2 s = unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+                        l += s.x + s.y;
+                    }
+                    tmem_st16(ts, *reinterpret_cast<uint32_t(*)[16]>(&ph[0]));
+                    tmem_st16(ts + 16, *reinterpret_cast<uint32_t(*)[16]>(&ph[16]));
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) mbar_arrive_at(cluster_addr(&ms->p_full[j & 1], 0));
+                        else mbar_arrive(&ms->p_full[j & 1]);
+                    }
+                    ++j;
                 }
-                float o[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    o[k] = __uint_as_float(r[k]) * inv;
-                    if (l != l) o[k] = l;
-                    finite = finite && isfinite(o[k]);
+                if (bad) break;
+
+                // ---------------------------------------------------------- epilogue
+                ms->xchg[half][row] = l;
+                const Piece& done = cur.pc;
+                const bool got = mbar_wait(&ms->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1);
+                if (bar_sync_or(1, kSoftmaxThreads, !got || aborted(ms))) {
+                    bad = true;
+                    break;
                 }
-                if (PV16 || W.out_dtype != LUCETREE_F32) {
-                    uint32_t w[8];
+                tc_fence_after();
+                l += ms->xchg[half ^ 1][row];
+                const uint32_t* vb = ms->vbad[cur.serial % kBadSets];
+                uint32_t any = 0;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        w[k] = PV16 ? pack_bf162(o[2 * k], o[2 * k + 1]) : pack_half2(o[2 * k], o[2 * k + 1]);
-                    uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(W.out) + out_row * D + x);
-                    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                } else {
-                    float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(W.out) + out_row * D + x);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                for (int k = 0; k < kBadWords; ++k) any |= vb[k];
+                if (__builtin_expect(any != 0, 0) && mine) {
+                    // bits seq * N .. + N - 1
+                    const int at = seq * d.N, w = at >> 5, s = at & 31;
+                    const uint64_t lo = (uint64_t)vb[w] | (uint64_t)(w + 1 < kNodeWords ? vb[w + 1] : 0) << 32;
+                    const uint64_t hi = w + 2 < kNodeWords ? vb[w + 2] : 0;
+                    const bool own = (vb[kNodeWords + (seq >> 5)] >> (seq & 31)) & 1u;
+                    const uint64_t bits = s ? lo >> s | hi << (64 - s) : lo;
+                    if ((bits & anc) != 0 || own) l = __int_as_float(0x7FC00000);
                 }
+                const bool whole = done.slot < 0;
+                const int at_row = done.slot + before * d.G + row;
+                const long long out_row = (long long)(done.node0 + before + row / d.G) * d.Hq + done.g * d.G + row % d.G;
+                const float inv = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN stays, and is flagged)
+                if (mine && half == 0) {
+                    if (!whole) {
+                        float* s = W.ws + partial_rows(d) * D + at_row;
+                        s[0] = -neg_m;
+                        s[partial_rows(d)] = l;
+                    } else if (a.lse) {
+                        a.lse[out_row] = l != 0.f ? (log2f(l) - neg_m) * kLn2 : -INFINITY;
+                    }
+                }
+                bool finite = true;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[16];
+                    const int x = half * (D / 2) + 16 * c;
+                    tmem_ld16(tl + L::kColO + x, r);
+                    tmem_wait_ld_regs16(r);
+                    if (!mine) continue;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) finite = finite && isfinite(__uint_as_float(r[k]));
+                    if (!whole) {
+                        float4* o = reinterpret_cast<float4*>(W.ws + (size_t)at_row * D + x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
+                                               __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
+                        continue;
+                    }
+                    float o[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        o[k] = __uint_as_float(r[k]) * inv;
+                        if (l != l) o[k] = l;
+                        finite = finite && isfinite(o[k]);
+                    }
+                    if (PV16 || W.out_dtype != LUCETREE_F32) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = PV16 ? pack_bf162(o[2 * k], o[2 * k + 1]) : pack_half2(o[2 * k], o[2 * k + 1]);
+                        uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(W.out) + out_row * D + x);
+                        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+                        float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(W.out) + out_row * D + x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+                if (!finite) {
+                    if (whole) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
+                    if (done.seqs > 1) {
+                        if constexpr (PAIR) {
+                            or_at(cluster_addr(&ms->again, 0), 1u);
+                            or_at(cluster_addr(&ms->again, 1), 1u);
+                        } else {
+                            ms->again = 1;
+                        }
+                    }
+                }
+                tc_fence_before();
+                bar_sync(1, kSoftmaxThreads);  // the piece's O and values in shared memory are no longer read
+                if (any && half == 0 && row < kBadWords) ms->vbad[cur.serial % kBadSets][row] = 0;
             }
-            if (!finite) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
-            tc_fence_before();
-            bar_sync(1, kSoftmaxThreads);  // the piece's O and values in shared memory are no longer read
-            if (any && half == 0 && row < kBadWords) ms->vbad[cur.piece_no % kBadSets][row] = 0;
+            if (bad) set_abort(ms, a.status);
         }
-        if (bad) set_abort(ms, a.status);
+
+        tc_fence_before();
+        __syncthreads();
+        if constexpr (PAIR) {
+            // (both CTAs go on, or neither)
+            if (tid < 2 && aborted(ms)) or_at(cluster_addr(&ms->again, tid), 2u);
+            __syncwarp();
+            cluster_sync();  // the other CTA's arrivals and MMAs have come
+        }
+        tc_fence_after();
+        if (*(volatile int*)&ms->pass > 0 || *(volatile int*)&ms->again != 1 || (!PAIR && aborted(ms))) break;
+        __syncthreads();
+        if (tid == 0) ms->pass = 1;
+        __syncthreads();
+        start = W.plan.cta[blockIdx.x / d.pair];  // (again, so that no thread has to keep it)
     }
 
     // ---------------------------------------------------------------- teardown
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     teardown();
 }
 

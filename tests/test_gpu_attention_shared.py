@@ -479,3 +479,33 @@ def test_a_forked_prompt_decodes_with_shared_pages(cuda_dev):
                 cache[layer][b] = (torch.cat([kc, kb[keep]]), torch.cat([vc, vb[keep]]))
         ctx_b = new_ctx
         assert int(status.item()) == 0 and torch.equal(ctx_b.cpu(), L + n_acc)
+
+
+@pytest.mark.parametrize("case", [
+    ([(10, [700, 650, 800])], 5, 4, 2, 128, "bf16"),             # one block of three sequences
+    ([(10, [700, 650, 641, 720])], 12, 8, 2, 256, "f16"),        # pairs
+    ([(6, [500, 450] * 20), (0, [300])], 1, 12, 2, 128, "f16"),  # forty sequences of one node, one alone
+    ([(6, [500, 450] * 20)], 6, 4, 4, 256, "bf16"),
+    ([(12, [1100] * 6)] * 40, 3, 8, 2, 128, "bf16"),            # several pieces to a CTA
+    ([(12, [1100] * 6)] * 40, 3, 24, 2, 256, "bf16"),           # ... and to a pair
+], ids=lambda c: "%d-%d-%d-%d-%s" % (len(c[0]), c[1], c[2] // c[3], c[4], c[5]))
+@pytest.mark.parametrize("out", ["f32", "same"])
+def test_committed_values_that_are_not_finite_stay_with_their_sequences(cuda_dev, case, out):
+    LT = _lt()
+    s = make(*case, seed=13)
+    B, N, Hq, D = s["q"].shape
+    Hkv = s["k_tree"].shape[2]
+    t = torch.float32 if out == "f32" else s["q"].dtype
+    ref = reference(s, p_step=P_STEP[t])
+    for b, pos, dim in ((1, int(s["ctx_len"][1]) - 1, 0), (B - 1, int(s["ctx_len"][B - 1]) - 2, D - 1), (0, 70, D // 2)):
+        for value in (float("nan"), float("inf")):
+            x = dict(s, v_pool=s["v_pool"].clone())
+            page = int(s["page_table"][b, pos // PAGE])
+            x["v_pool"][page, 1, pos % PAGE, dim] = value
+            got, lse, status = call(x, t)
+            assert status == LT.DEV_NONFINITE
+            with_it = torch.tensor([page in s["page_table"][c, :-(-int(s["ctx_len"][c]) // PAGE)].tolist() for c in range(B)])
+            good = torch.ones(B, N, Hq, dtype=torch.bool)
+            good[with_it, :, Hq // Hkv:2 * (Hq // Hkv)] = False
+            near(got, lse, ref, good)
+            assert not bool(torch.isfinite(got[~good][:, dim]).any())
