@@ -602,8 +602,10 @@ extern "C" lucetree_status lucetree_rope(const lucetree_rope_args* a, void* stre
     for (const void* p : {a->q, a->k, a->v, (const void*)a->q_out, (const void*)a->k_out, (const void*)a->v_out})
         if (!aligned(p, 16)) return LUCETREE_ERR_INVALID_ARG;
     const Span out[] = {{a->q_out, 2 * T * qe}, {a->k_out, 2 * T * ke}, {a->v_out, 2 * T * ke}};
+    const bool given = a->positions != nullptr;
     const Span in[] = {{a->q, span_bytes(T, a->q_stride, qe)}, {a->k, span_bytes(T, a->k_stride, ke)},
-                       {a->v, span_bytes(T, a->v_stride, ke)}};
+                       {a->v, span_bytes(T, a->v_stride, ke)}, {a->steps, 4ll * a->rot_dims}, {a->positions, 4 * T},
+                       {given ? nullptr : a->ctx_len, 4ll * a->B}, {given ? nullptr : a->anc_mask, 8 * T}};
     if (any_overlap(out, in)) return LUCETREE_ERR_INVALID_ARG;
     return launch_rope(*a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LUCETREE_OK : LUCETREE_ERR_CUDA;
 }
@@ -643,7 +645,8 @@ extern "C" lucetree_status lucetree_append_kv(const lucetree_append_args* a, voi
                         {a->ctx_len_out, 4ll * a->B}, {kq ? a->k_exp : nullptr, pool_rows}, {vq ? a->v_exp : nullptr, pool_rows}};
     const Span in[] = {{a->q, span_bytes(T, a->q_stride, qe)}, {a->k, span_bytes(T, a->k_stride, ke)},
                        {a->v, span_bytes(T, a->v_stride, ke)}, {a->start, 4ll * (a->B + 1ll)},
-                       {a->page_table, 4ll * a->B * a->max_pages_per_seq}, {a->ctx_len_in, 4ll * a->B}};
+                       {a->page_table, 4ll * a->B * a->max_pages_per_seq}, {a->ctx_len_in, 4ll * a->B},
+                       {a->steps, 4ll * a->rot_dims}};
     if (any_overlap(out, in)) return LUCETREE_ERR_INVALID_ARG;
     return launch_append_kv(*a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LUCETREE_OK : LUCETREE_ERR_CUDA;
 }

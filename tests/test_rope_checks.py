@@ -211,7 +211,8 @@ def test_rope_entry_refuses_before_any_launch():
                 dict(rot_dims=0), dict(magnitude=float("inf")), dict(ctx_len=None), dict(anc_mask=None),
                 dict(q_stride=511), dict(q_stride=516), dict(k_stride=255), dict(v_stride=0), dict(q=MB + 8),
                 dict(k_out=8 * MB + 2), dict(q_out=MB), dict(q_out=MB + 512), dict(k_out=3 * MB), dict(v_out=7 * MB + 16),
-                dict(k_out=7 * MB)):
+                dict(k_out=7 * MB), dict(q_out=4 * MB + 16), dict(k_out=5 * MB), dict(v_out=6 * MB + 32),
+                dict(v_out=6 * MB, positions=6 * MB + 16, ctx_len=None, anc_mask=None)):
         assert rc(**bad) == 1, bad
     for bad in (dict(dtype=LT.LUCETREE_F32), dict(D=120), dict(D=1040), dict(layout=2), dict(layout=-1), dict(N=65),
                 dict(B=1 << 20, N=1 << 11, positions=MB)):
@@ -235,7 +236,7 @@ def test_append_entry_refuses_before_any_launch():
                 dict(ctx_len_in=None), dict(ctx_len_out=None), dict(ctx_len_out=7 * MB), dict(ctx_len_out=7 * MB + 4),
                 dict(k_pool=None), dict(k_format=1), dict(v_format=1), dict(v_format=2), dict(rot_dims=258), dict(Hq=0),
                 dict(magnitude=float("nan")), dict(q_stride=1016), dict(k_stride=2052), dict(v=3 * MB + 8), dict(q_out=MB),
-                dict(v_pool=9 * MB), dict(k_pool=2 * MB), dict(k_format=1, k_exp=9 * MB), dict(v_pool=6 * MB)):
+                dict(v_pool=9 * MB), dict(k_pool=2 * MB), dict(k_format=1, k_exp=9 * MB), dict(v_pool=6 * MB), dict(q_out=5 * MB)):
         assert rc(**bad) == 1, bad
     for bad in (dict(dtype=LT.LUCETREE_F32), dict(page_size=16), dict(D=264), dict(layout=2), dict(k_format=2),
                 dict(v_format=3), dict(k_format=1, k_exp=13 * MB, dtype=LT.LUCETREE_F16),
