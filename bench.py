@@ -1080,6 +1080,73 @@ def measure_beam(args, dev, stream):
             "peak_kind": kind}
 
 
+def measure_shared(args, dev, stream):
+    """Attention over a shared prefix: 16 sequences under 16,384 common tokens with
+    1,024 more each, 24/4 heads of 256 dims in bf16, at budget 22 and as the
+    single-token decode step; the plan and the attention apart, back-to-back calls
+    between CUDA events."""
+    import torch
+    from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
+    B, both, own, Hq, Hkv, D = 16, 16384, 1024, 24, 4, 256
+    g = torch.Generator(device=dev).manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=g, device=dev, dtype=torch.bfloat16)  # noqa: E731
+    pages = both // 64 + B * (own // 64)
+    k_pool, v_pool = r(pages, Hkv, 64, D), r(pages, Hkv, 64, D)
+    perm = torch.randperm(pages, generator=g, device=dev).to(torch.int32)
+    table = torch.cat([perm[:both // 64].expand(B, -1), perm[both // 64:].view(B, -1)], 1).contiguous()
+    ctx = torch.full((B,), both + own, dtype=torch.int32, device=dev)
+    start = torch.tensor([0, B], dtype=torch.int32, device=dev)
+    st, common = torch.zeros(1, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev)
+    peak, kind = peak_hbm()
+    res = {}
+    for N in (22, 1):
+        q, kt, vt = r(B, N, Hq, D), r(B, N, Hkv, D), r(B, N, Hkv, D)
+        parent = torch.tensor([[max(-1, (i - 1) // 2) if i else -1 for i in range(N)]] * B, dtype=torch.int32, device=dev)
+        anc, out = torch.empty(B, N, dtype=torch.int64, device=dev), torch.empty_like(q)
+        plan = torch.empty(LT.lucetree_shared_plan_bytes(B, N, Hq, Hkv, D, 1), dtype=torch.uint8, device=dev)
+        ws = torch.empty(LT.lucetree_verify_attn_shared_workspace(B, N, Hq, Hkv, D, 1), dtype=torch.uint8, device=dev)
+        LT.lucetree_build_anc_mask(parent, anc, st)
+        stream.wait_stream(torch.cuda.current_stream(dev))
+        n = min(args.steps, 500)
+        ms_plan = time_spans(lambda: LT.lucetree_shared_plan(table, ctx, start, N, Hq, Hkv, D, pages, common, plan, st,
+                                                             stream=stream), stream, dev, n)
+        ms = time_spans(lambda: LT.lucetree_verify_attn_shared(q, k_pool, v_pool, table, ctx, kt, vt, anc, 1, plan, out, st,
+                                                               ws, stream=stream), stream, dev, n)
+        kv, flops = (both + B * own) * Hkv * D * 2 * 2, 4 * B * N * Hq * D * (both + own)
+        t = float(np.median(ms))
+        res["budget %d" % N] = {"ms": t, "plan_ms": float(np.median(ms_plan)), "kv_bytes": kv, "GBps": kv / t / 1e6,
+                                "frac_of_hbm_peak": kv / t / 1e6 / peak, "peak_kind": kind, "TFLOPs": flops / t / 1e9}
+    res["common_pages"], res["device_status"] = int(common.item()), int(st.item())
+    return res
+
+
+def measure_append(args, dev, stream):
+    """Prompts into the paged cache: 24,576 tokens of 8 sequences rotated on the way,
+    24/4 heads of 256 dims in bf16; back-to-back calls (805 MB each) between CUDA events."""
+    import torch
+    from speculative_decoding_tree_ddtree_gb300 import lucetree as LT
+    lens, Hq, Hkv, D = [4096 - 293 * i for i in range(8)], 24, 4, 256
+    lens[-1] += 24576 - sum(lens)
+    g = torch.Generator(device=dev).manual_seed(0)
+    rows, B, per = sum(lens), len(lens), (max(lens) + 63) // 64
+    x = torch.randn(rows, (Hq + 2 * Hkv) * D, generator=g, device=dev, dtype=torch.bfloat16)
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in x.split([Hq * D, Hkv * D, Hkv * D], -1))
+    k_pool, v_pool = (torch.empty(B * per, Hkv, 64, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    table = torch.randperm(B * per, generator=g, device=dev).to(torch.int32).view(B, per)
+    start = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=dev)
+    ctx, st = torch.zeros(B, dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    ctx_out, q_out = torch.empty_like(ctx), torch.empty(rows, Hq, D, dtype=torch.bfloat16, device=dev)
+    steps = LT.lucetree_rope_steps(D, 1e6)[0].to(dev)
+    stream.wait_stream(torch.cuda.current_stream(dev))
+    t = float(np.median(time_spans(lambda: LT.lucetree_append_kv(k, v, start, table, ctx, ctx_out, k_pool, v_pool, st, q=q,
+                                                                 q_out=q_out, steps=steps, stream=stream),
+                                   stream, dev, min(args.steps, 200))))
+    peak, kind = peak_hbm()
+    nbytes = 2 * x.numel() * 2
+    return {"ms": t, "bytes": nbytes, "GBps": nbytes / t / 1e6, "frac_of_hbm_peak": nbytes / t / 1e6 / peak, "peak_kind": kind,
+            "device_status": int(st.item())}
+
+
 def _run_measure(name, measure, args):
     import torch
     from speculative_decoding_tree_ddtree_gb300.build import build
@@ -1139,6 +1206,8 @@ def build_parser() -> argparse.ArgumentParser:
     ap.add_argument("--delta-only", action="store_true", help="time only the recurrent-state tree pass and commit")
     ap.add_argument("--window-only", action="store_true", help="time only the windowed attention")
     ap.add_argument("--beam-only", action="store_true", help="time only the beam selection")
+    ap.add_argument("--shared-only", action="store_true", help="time only the attention over a shared prefix")
+    ap.add_argument("--append-only", action="store_true", help="time only the append to the paged cache")
     ap.add_argument("--no-stage", action="store_true", help="skip the host-resident page staging measurement")
     ap.add_argument("--no-vq", action="store_true", help="skip the quantised-V attention measurement")
     ap.add_argument("--vq-only", action="store_true", help="time only the quantised-V attention calls")
@@ -1159,6 +1228,10 @@ def main(argv=None):
         return _run_measure("window", measure_window, args)
     if args.beam_only:
         return _run_measure("beam", measure_beam, args)
+    if args.shared_only:
+        return _run_measure("shared", measure_shared, args)
+    if args.append_only:
+        return _run_measure("append", measure_append, args)
     if args.stage_only:
         return run_stage_only(args)
     if args.vq_only:
