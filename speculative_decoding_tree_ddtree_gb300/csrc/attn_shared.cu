@@ -53,10 +53,10 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
     // pools as [num_pages * Hkv * 64 rows][D]; box = one 64-token page x 64 dims
     const cuuint64_t pool_dims[2] = {D, (cuuint64_t)a.num_pages * a.Hkv * kPage}, pool_strides[1] = {row};
     const cuuint32_t pool_box[2] = {64, (cuuint32_t)kPage};
-    // V (K of a pair): the same as [D / 64][rows][64], box = 128 dims, 64 after the other 64 (V of a pair
-    // with D = 128: half of the dims)
+    // V (K of a pair): the same as [D / 64][rows][64], box = 128 dims, 64 after the other 64 (K of a pair: all
+    // dims; V of a pair with D = 128: half of them)
     const cuuint64_t v_dims[3] = {64, pool_dims[1], D / 64}, v_strides[2] = {row, 128};
-    const cuuint32_t w_box[3] = {64, (cuuint32_t)kPage, 2}, v_box[3] = {64, (cuuint32_t)kPage, p.pair == 2 && D == 128 ? 1u : 2u};
+    const cuuint32_t w_box[3] = {64, (cuuint32_t)kPage, (cuuint32_t)(D / 64)}, v_box[3] = {64, (cuuint32_t)kPage, p.pair == 2 && D == 128 ? 1u : 2u};
     // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x a CTA's nodes of a block of either kind
     const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.N}, q_strides[2] = {row, (cuuint64_t)a.Hq * row};
     const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(false)}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(true)};

@@ -29,12 +29,11 @@
 //     (exact from 2^-17 to below 65536).
 //
 // Measured with 24 query and 4 KV heads of 256 dims, bf16 in and out, the merge included: 96
-// sequences at budget 22 under 16,384 tokens 507 to 535 us (1.52 to 1.60 PFLOP/s; a tile of the pair 2,700
-// cycles, its MMAs 2,048); 16 such sequences 114; one token each of 192 72, of 96 48, of 8
-// 22.7 (67 MB of keys and values, 10 us at HBM's rate; four tiles in most CTAs where the mean is
-// 3.4 are 1.8 of the rest, the others the chain of plan, page table and first tile, the last tile
-// and the merge).  With one CTA a tile of 128 KB takes 2.9 us where every page is read once
-// (24 groups of 8 beams: 86 us), which is HBM's rate.
+// sequences at budget 22 under 16,384 tokens 470 us (1.81 PFLOP/s); 16 such sequences 103; one
+// token each of 192 66, of 96 45, of 8 22.7 (67 MB of keys and values, 10 us at HBM's rate; four
+// tiles in most CTAs where the mean is 3.4 are 1.8 of the rest, the others the chain of plan, page
+// table and first tile, the last tile and the merge).  With one CTA a tile of 128 KB takes 2.9 us
+// where every page is read once (24 groups of 8 beams: 86 us), which is HBM's rate.
 #pragma once
 
 #include "attn_prefix_tc.cuh"
@@ -64,13 +63,12 @@ constexpr int kBadWords = kNodeWords + 8;  // ... and the sequences
 struct Misc {
     float xchg[2][kRows];        // a row's values for the other warpgroup's half
     uint64_t empty[kMaxSlots];   // of ring slots
-    uint64_t kfull[kMaxSlots];   // K chunk n at [n % kMaxSlots]: landed ...
-    uint64_t kpeer[kMaxSlots];   // ... in a pair's second CTA too
+    uint64_t kfull[kMaxSlots];   // K chunk n at [n % kMaxSlots]: landed, in the first CTA of a pair: in both
     uint64_t vfull[kMaxSlots];   // V chunk n at [n % kMaxSlots]: landed ...
     uint64_t vready[kMaxSlots];  // ... made the operand
     uint64_t s_full[2], p_full[2];  // of tiles j, at [j & 1]
     uint64_t pv_done[2];            // (PV(j - 2) is done once S(j) is there: two of them tell PV(j) from it)
-    uint64_t q_full, q_peer, q_empty, drain;
+    uint64_t q_full, q_empty, drain;
     // piece n at [n % kBadSets]: tree nodes, and sequences with own pages, whose V is not finite
     uint32_t vbad[kBadSets][kBadWords];
     uint32_t tmem_base;
@@ -81,16 +79,18 @@ struct Misc {
 
 template <int D, bool PAIR>
 struct Lay {
-    // Ring chunks per operand.  One CTA: K [128 keys][64 dims], V [64 keys][128 dims].  A pair, whose
-    // CTAs hold half of each operand: K [64 keys of its page][128 dims]; V its half of the dims,
-    // [64 keys][128 dims] or, with D = 128, [128 keys][64 dims].  16 KB each.
-    static constexpr int kChunks = PAIR ? D / 128 : D / 64;
+    // Ring chunks per operand.  One CTA: 16 KB each, K [128 keys][64 dims], V [64 keys][128 dims].  A
+    // pair, whose CTAs hold half of each operand: all of it, K [64 keys of its page][D dims], V
+    // [128 keys][D / 2 dims] (in chunks of 16 KB with D = 256, 96 sequences at budget 22 took
+    // 531 us instead of 470: the waits and commits of the warp that issues the MMAs count).
+    static constexpr int kChunks = PAIR ? 1 : D / 64;
+    static constexpr int kSlotBytes = PAIR ? D / 128 * kChunkBytes : kChunkBytes;
     static constexpr int kQBytes = D / 64 * kChunkBytes;
     static constexpr int kMiscBytes = (sizeof(Misc) + 127) / 128 * 128;
-    static constexpr int kRaw = (kSmemLimit - 1024 - kQBytes - kMiscBytes) / kChunkBytes;
+    static constexpr int kRaw = (kSmemLimit - 1024 - kQBytes - kMiscBytes) / kSlotBytes;
     static constexpr int kNS = kRaw > kMaxSlots ? kMaxSlots : kRaw;
     static constexpr int kSlotOff = kQBytes;
-    static constexpr int kMiscOff = kSlotOff + kNS * kChunkBytes;
+    static constexpr int kMiscOff = kSlotOff + kNS * kSlotBytes;
     static constexpr int kBytes = kMiscOff + kMiscBytes + 1024;
     static constexpr uint32_t kColO = 256;  // after S 0 and S 1
     static_assert(kNS >= 2 * kChunks, "the ring holds a K and a V operand");
@@ -240,6 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kConvert = BF16 && !PV16;  // V to fp16 on chip
     constexpr int kChunks = L::kChunks;
     constexpr int kNS = L::kNS;
+    constexpr int kSlotBytes = L::kSlotBytes;
+    constexpr int kPageBytes = kSlotBytes / 2;  // of V in a pair
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const base0 = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -253,10 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- set-up
     // (reads no global memory: it overlaps the previous kernel's tail)
     if (threadIdx.x == 0) {
+        const int firsts = PAIR && rank == 0 ? 2 : 1;  // a pair's second CTA tells the first one
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(&ms->empty[i], 1);
-            mbar_init(&ms->kfull[i], 1);
-            mbar_init(&ms->kpeer[i], 1);
+            mbar_init(&ms->kfull[i], firsts);
             mbar_init(&ms->vfull[i], 1);
             mbar_init(&ms->vready[i], PAIR ? 2 * kConvWarps : kConvWarps);
         }
@@ -265,8 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ms->p_full[i], PAIR ? 2 * kSmWarps : kSmWarps);
             mbar_init(&ms->pv_done[i], 1);
         }
-        mbar_init(&ms->q_full, 1);
-        mbar_init(&ms->q_peer, 1);
+        mbar_init(&ms->q_full, firsts);
         mbar_init(&ms->q_empty, 1);
         mbar_init(&ms->drain, 1);
         ms->abort_flag = 0;
@@ -370,21 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kChunks; ++c) {
                     if (!next_slot()) return false;
                     if (leader) {
-                        uint8_t* dst = sSlots + slot * kChunkBytes;
+                        uint8_t* dst = sSlots + slot * kSlotBytes;
                         uint64_t* bar = &ms->kfull[chunk % kMaxSlots];
                         if constexpr (PAIR) {
-                            // [64 keys of page `rank`][dims 128 * c .. +127], 64 dims after the other 64
+                            // [64 keys of page `rank`][dims], 64 dims after the other 64
                             const int at = rank ? o.at1 : o.at0;
-                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                            mbar_arrive_expect_tx(bar, kSlotBytes);
                             if (at < 0) {
-                                tma_load_3d(dst, &tm_kt, 128 * c, o.g, -1 - at, bar);
-                                tma_load_3d(dst + 8192, &tm_kt, 128 * c + 64, o.g, -1 - at, bar);
+#pragma unroll 1
+                                for (int x = 0; x < D / 64; ++x) tma_load_3d(dst + 8192 * x, &tm_kt, 64 * x, o.g, -1 - at, bar);
                             } else {
-                                tma_load_3d_hint(dst, &tm_k, 0, at, 2 * c, bar, o.pol);
+                                tma_load_3d_hint(dst, &tm_k, 0, at, 0, bar, o.pol);
                             }
                         } else {
                             // [128 keys: page 0 then page 1][dims 64 * c .. +63]
-                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                            mbar_arrive_expect_tx(bar, kSlotBytes);
                             if (tree0) tma_load_3d(dst, &tm_kt, 64 * c, o.g, -1 - o.at0, bar);
                             else tma_load_2d_hint(dst, &tm_k, 64 * c, o.at0, bar, o.pol);
                             if (tree1) tma_load_3d(dst + 8192, &tm_kt, 64 * c, o.g, -1 - o.at1, bar);
@@ -402,21 +403,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kChunks; ++c) {
                     if (!next_slot()) return false;
                     if (leader) {
-                        uint8_t* dst = sSlots + slot * kChunkBytes;
+                        uint8_t* dst = sSlots + slot * kSlotBytes;
                         uint64_t* bar = &ms->vfull[vchunk % kMaxSlots];
-                        if constexpr (PAIR && D == 128) {
-                            // [128 keys: page 0 then page 1][dims 64 * rank .. +63]
-                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                        if constexpr (PAIR) {
+                            // [64 keys][D / 2 dims, 64 after the other 64] of page 0, then page 1
+                            mbar_arrive_expect_tx(bar, kSlotBytes);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int at = h ? o.at1 : o.at0;
-                                if (at < 0) tma_load_3d(dst + 8192 * h, &tm_vt, 64 * rank, o.g, -1 - at, bar);
-                                else tma_load_3d_hint(dst + 8192 * h, &tm_v, 0, at, rank, bar, o.pol);
+                                if (at < 0) {
+#pragma unroll 1
+                                    for (int x = 0; x < D / 128; ++x)
+                                        tma_load_3d(dst + kPageBytes * h + 8192 * x, &tm_vt, 64 * (D / 128 * rank + x), o.g,
+                                                    -1 - at, bar);
+                                } else {
+                                    tma_load_3d_hint(dst + kPageBytes * h, &tm_v, 0, at, D / 128 * rank, bar, o.pol);
+                                }
                             }
                         } else {
                             // [64 keys of a page][128 dims], 64 dims after the other 64
-                            const int at = (PAIR ? c : c & 1) ? o.at1 : o.at0, x = PAIR ? 128 * rank : 128 * (c >> 1);
-                            mbar_arrive_expect_tx(bar, kChunkBytes);
+                            const int at = c & 1 ? o.at1 : o.at0, x = 128 * (c >> 1);
+                            mbar_arrive_expect_tx(bar, kSlotBytes);
                             if (at < 0) {
                                 tma_load_3d(dst, &tm_vt, x, o.g, -1 - at, bar);
                                 tma_load_3d(dst + 8192, &tm_vt, x + 64, o.g, -1 - at, bar);
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!qk.live) break;
                     if (qk.first()) {
                         if (!wait(&ms->q_full, qk.serial & 1)) break;
-                        if (leader) mbar_arrive_at(cluster_addr(&ms->q_peer, 0));
+                        if (leader) mbar_arrive_at(cluster_addr(&ms->q_full, 0));
                     }
 #pragma unroll 1
                     for (int c = 0; c < kChunks; ++c, ++n) {
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = false;
                             break;
                         }
-                        if (leader) mbar_arrive_at(cluster_addr(&ms->kpeer[n % kMaxSlots], 0));
+                        if (leader) mbar_arrive_at(cluster_addr(&ms->kfull[n % kMaxSlots], 0));
                         __syncwarp();
                     }
                 }
@@ -559,21 +566,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!qk.live) return;
                     if (qk.first()) {
                         if (!wait(&ms->q_full, qk.serial & 1)) return;
-                        if (PAIR && !wait(&ms->q_peer, qk.serial & 1)) return;
                     }
                     const uint32_t dS = tmem + (jq & 1) * 128;
 #pragma unroll 1
                     for (int c = 0; c < kChunks; ++c) {
                         if (!wait(&ms->kfull[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
-                        if (PAIR && !wait(&ms->kpeer[kn % kMaxSlots], (kn / kMaxSlots) & 1)) return;
                         tc_fence_after();
                         if (leader) {
-                            const uint32_t at = aS + slot * kChunkBytes;
+                            const uint32_t at = aS + slot * kSlotBytes;
                             if constexpr (PAIR) {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_f16_ss_pair(dS, make_desc(hi_k, aQ + (2 * c + k / 4) * kChunkBytes + k % 4 * 32),
-                                                    make_desc(hi_k, at + k / 4 * 8192 + k % 4 * 32), id_qk, (c | k) != 0);
+                                for (int k = 0; k < D / 16; ++k)
+                                    mma_f16_ss_pair(dS, make_desc(hi_k, aQ + k / 4 * kChunkBytes + k % 4 * 32),
+                                                    make_desc(hi_k, at + k / 4 * 8192 + k % 4 * 32), id_qk, k != 0);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
@@ -607,17 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!wait(&ms->vready[vn % kMaxSlots], (vn / kMaxSlots) & 1)) break;
                         tc_fence_after();
                         if (leader) {
-                            const uint32_t at = aS + slot * kChunkBytes, dO = tmem + L::kColO;
-                            if constexpr (PAIR && D == 128) {
+                            const uint32_t at = aS + slot * kSlotBytes, dO = tmem + L::kColO;
+                            if constexpr (PAIR) {
 #pragma unroll
                                 for (int k = 0; k < 8; ++k)
                                     mma_f16_ts_pair(dO, aP + 64 * (k / 4) + 8 * (k % 4),
-                                                    make_desc(hi_v, at + k / 4 * 8192 + k % 4 * 2048), id_pv, k == 0 ? more : 1u);
-                            } else if constexpr (PAIR) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_f16_ts_pair(dO, aP + 64 * c + 8 * k, make_desc(hi_v, at + k * 2048), id_pv,
-                                                    (c | k) == 0 ? more : 1u);
+                                                    make_desc(hi_v, at + k / 4 * kPageBytes + k % 4 * 2048), id_pv,
+                                                    k == 0 ? more : 1u);
                             } else {
                                 // chunk c: output dims 128 (c >> 1) .., keys 64 (c & 1) ..
 #pragma unroll
@@ -675,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < kChunks; ++c) {
                     const uint32_t vn = chunks0 + j * kChunks + c;
                     // the pages in the chunk's two 8 KB boxes: one page twice, or both
-                    constexpr bool kBoth = PAIR && D == 128;
-                    const int page = kBoth ? 0 : PAIR ? c : c & 1;
+                    constexpr bool kBoth = PAIR;
+                    const int page = kBoth ? 0 : c & 1;
                     const int word0 = __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + page);
                     const int word1 = kBoth ? __shfl_sync(0xffffffffu, word_cur, 2 * (rel & 15) + 1) : word0;
                     const bool landed = mbar_wait(&ms->vfull[vn % kMaxSlots], (vn / kMaxSlots) & 1);
@@ -684,12 +685,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kChunkBytes);
+                    uint4* base = reinterpret_cast<uint4*>(sSlots + ((vbase + c) % kNS) * kSlotBytes);
                     // pages that not all rows see
                     auto look = [&](int word) { return (word & 0x80) || (pass > 0 && (word >> 8) > 0 && cur.pc.seqs > 1); };
                     // (nothing to change)
                     const bool whole = (word0 & 0xff) == kPage && (word1 & 0xff) == kPage && !look(word0) && !look(word1);
-                    constexpr int kUnits = kChunkBytes / 16 / (32 * kConvWarps);  // 16 per thread
+                    constexpr int kUnits = kSlotBytes / 16 / (32 * kConvWarps);  // of a thread
                     constexpr int kBatch = 4;                                      // loads in flight
                     if (kConvert || !whole) {
 #pragma unroll 1
