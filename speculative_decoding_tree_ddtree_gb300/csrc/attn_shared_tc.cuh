@@ -56,7 +56,6 @@ constexpr int kSmWarps = 8;                        // warps 4 .. 11: two warpgro
 constexpr int kSoftmaxThreads = 32 * kSmWarps;
 constexpr int kThreads = 128 + kSoftmaxThreads;
 constexpr int kMaxSlots = 12;
-constexpr int kBadSets = 8;    // pieces whose V may be in the ring at once, and more
 constexpr int kNodeWords = 12;  // tree nodes of a block's sequences: at most 254 + 2 N
 constexpr int kBadWords = kNodeWords + 8;  // ... and the sequences
 
@@ -69,12 +68,12 @@ struct Misc {
     uint64_t s_full[2], p_full[2];  // of tiles j, at [j & 1]
     uint64_t pv_done[2];            // (PV(j - 2) is done once S(j) is there: two of them tell PV(j) from it)
     uint64_t q_full, q_empty, drain;
-    // piece n at [n % kBadSets]: tree nodes, and sequences with own pages, whose V is not finite
-    uint32_t vbad[kBadSets][kBadWords];
     uint32_t tmem_base;
     int abort_flag;
     int pass;   // 1: the second one, with all values looked at ...
     int again;  // ... which comes if this is 1
+    // piece n at [n % Lay::kBadSets]: tree nodes, and sequences with own pages, whose V is not finite
+    uint32_t vbad[][kBadWords];
 };
 
 template <int D, bool PAIR>
@@ -86,7 +85,10 @@ struct Lay {
     static constexpr int kChunks = PAIR ? 1 : D / 64;
     static constexpr int kSlotBytes = PAIR ? D / 128 * kChunkBytes : kChunkBytes;
     static constexpr int kQBytes = D / 64 * kChunkBytes;
-    static constexpr int kMiscBytes = (sizeof(Misc) + 127) / 128 * 128;
+    // Pieces from the one whose rows are being finished to the last one with V in the ring: its next
+    // six (12 slots of K and V in turn), three or fewer.
+    static constexpr int kBadSets = PAIR && D == 128 ? 8 : 4;
+    static constexpr int kMiscBytes = (sizeof(Misc) + 4 * kBadSets * kBadWords + 127) / 128 * 128;
     static constexpr int kRaw = (kSmemLimit - 1024 - kQBytes - kMiscBytes) / kSlotBytes;
     static constexpr int kNS = kRaw > kMaxSlots ? kMaxSlots : kRaw;
     static constexpr int kSlotOff = kQBytes;
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kConvert = BF16 && !PV16;  // V to fp16 on chip
     constexpr int kChunks = L::kChunks;
     constexpr int kNS = L::kNS;
+    constexpr int kBadSets = L::kBadSets;
     constexpr int kSlotBytes = L::kSlotBytes;
     constexpr int kPageBytes = kSlotBytes / 2;  // of V in a pair
 
