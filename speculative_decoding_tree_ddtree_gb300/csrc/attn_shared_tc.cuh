@@ -29,10 +29,10 @@
 //     (exact from 2^-17 to below 65536).
 //
 // Measured with 24 query and 4 KV heads of 256 dims, bf16 in and out, the merge included: 96
-// sequences at budget 22 under 16,384 tokens 470 us (1.81 PFLOP/s); 16 such sequences 103; one
-// token each of 192 66, of 96 45, of 8 22.7 (67 MB of keys and values, 10 us at HBM's rate; four
-// tiles in most CTAs where the mean is 3.4 are 1.8 of the rest, the others the chain of plan, page
-// table and first tile, the last tile and the merge).  With one CTA a tile of 128 KB takes 2.9 us
+// sequences at budget 22 under 16,384 tokens 463 to 474 us (1.81 PFLOP/s); 16 such sequences 99; one
+// token each of 192 62, of 96 42.5, of 8 22.8 (67 MB of keys and values, 10 us at HBM's rate;
+// four tiles in most CTAs where the mean is 3.4 are 1.8 of the rest, the others the chain of plan,
+// page table and first tile, the last tile and the merge).  With one CTA a tile of 128 KB takes 2.9 us
 // where every page is read once (24 groups of 8 beams: 86 us), which is HBM's rate.
 #pragma once
 
@@ -129,6 +129,26 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// Four lanes with four units of U words each: unit k of lane i becomes unit i of lane k.
+template <int U>
+__device__ __forceinline__ void turn4(uint32_t (&v)[4 * U], int lane) {
+#pragma unroll
+    for (int s = 1; s < 4; s <<= 1) {
+        const bool odd = (lane & s) != 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & s) continue;
+#pragma unroll
+            for (int y = 0; y < U; ++y) {
+                uint32_t &lo = v[k * U + y], &hi = v[(k + s) * U + y];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, s);
+                if (odd) lo = got;
+                else hi = got;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n > 0 ? ~0ull >> (64 - n) : 0ull; }  // n <= 64
@@ -925,60 +945,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if ((bits & anc) != 0 || own) l = __int_as_float(0x7FC00000);
                 }
                 const bool whole = done.slot < 0;
-                const int at_row = done.slot + before * d.G + row;
-                const long long out_row = (long long)(done.node0 + before + row / d.G) * d.Hq + done.g * d.G + row % d.G;
-                const float inv = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN stays, and is flagged)
+                // rows of the output, or of the partial sums: mine, and the four of my lane's group of four
+                const int my_row = whole ? node * d.Hq + done.g * d.G + row % d.G : done.slot + before * d.G + row;
+                const int row4 = row & ~3, rows = min(d.half(done.own), done.nodes - before) * d.G;
+                int to_row[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) to_row[k] = __shfl_sync(0xffffffffu, my_row, (lane & 28) + k);
+                const float inv = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (0: no key; NaN makes the row NaN)
                 if (mine && half == 0) {
                     if (!whole) {
-                        float* s = W.ws + partial_rows(d) * D + at_row;
+                        float* s = W.ws + partial_rows(d) * D + my_row;
                         s[0] = -neg_m;
                         s[partial_rows(d)] = l;
                     } else if (a.lse) {
-                        a.lse[out_row] = l != 0.f ? (log2f(l) - neg_m) * kLn2 : -INFINITY;
+                        a.lse[my_row] = l != 0.f ? (log2f(l) - neg_m) * kLn2 : -INFINITY;
                     }
                 }
-                bool finite = true;
+                const bool out16 = whole && (PV16 || W.out_dtype != LUCETREE_F32);
+                float zero = 0.f;  // NaN: my row holds a value that is not finite
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t r[16];
                     const int x = half * (D / 2) + 16 * c;
                     tmem_ld16(tl + L::kColO + x, r);
                     tmem_wait_ld_regs16(r);
-                    if (!mine) continue;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) finite = finite && isfinite(__uint_as_float(r[k]));
-                    if (!whole) {
-                        float4* o = reinterpret_cast<float4*>(W.ws + (size_t)at_row * D + x);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o[k] = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]),
-                                               __uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3]));
-                        continue;
-                    }
-                    float o[16];
+                    if ((warp & 3) * 32 >= rows) continue;  // (the whole warp)
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        o[k] = __uint_as_float(r[k]) * inv;
-                        if (l != l) o[k] = l;
-                        finite = finite && isfinite(o[k]);
+                        zero = fmaf(__uint_as_float(r[k]), 0.f, zero);
+                        r[k] = __float_as_uint(__uint_as_float(r[k]) * inv);
                     }
-                    if (PV16 || W.out_dtype != LUCETREE_F32) {
+                    // Lanes of a group of four exchange their columns, so that each of them has a quarter of
+                    // all four rows and a store covers 64 bytes of a row (a lane to a row, its 16 bytes apart
+                    // from all others, a piece's rows took 6,000 to 14,000 cycles; 16 sequences at budget
+                    // 22 under 4,096 tokens 46 us instead of 41.5, four sequences 12.2 instead of 12.8).
+                    if (out16) {
                         uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            w[k] = PV16 ? pack_bf162(o[2 * k], o[2 * k + 1]) : pack_half2(o[2 * k], o[2 * k + 1]);
-                        uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(W.out) + out_row * D + x);
-                        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    } else {
-                        float4* to = reinterpret_cast<float4*>(reinterpret_cast<float*>(W.out) + out_row * D + x);
+                        for (int k = 0; k < 8; ++k) {
+                            const float o0 = __uint_as_float(r[2 * k]), o1 = __uint_as_float(r[2 * k + 1]);
+                            w[k] = PV16 ? pack_bf162(o0, o1) : pack_half2(o0, o1);
+                        }
+                        turn4<2>(w, lane);
+                        uint16_t* const to = reinterpret_cast<uint16_t*>(W.out) + x + 4 * (lane & 3);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        for (int k = 0; k < 4; ++k)
+                            if (row4 + k < rows)
+                                *reinterpret_cast<uint2*>(to + (size_t)to_row[k] * D) = make_uint2(w[2 * k], w[2 * k + 1]);
+                    } else {
+                        turn4<4>(r, lane);
+                        float* const to = (whole ? reinterpret_cast<float*>(W.out) : W.ws) + x + 4 * (lane & 3);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (row4 + k < rows)
+                                *reinterpret_cast<uint4*>(to + (size_t)to_row[k] * D) =
+                                    make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
                     }
                 }
-                if (!finite) {
+                if (mine && !(zero + l == l)) {
                     if (whole) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
-                    if (done.seqs > 1) {
+                    if (done.seqs > 1 && zero != zero) {
                         if constexpr (PAIR) {
                             or_at(cluster_addr(&ms->again, 0), 1u);
                             or_at(cluster_addr(&ms->again, 1), 1u);
