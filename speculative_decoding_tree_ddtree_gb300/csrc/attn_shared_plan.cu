@@ -8,8 +8,8 @@
 // by searches in the running sums and goes through that CTA's pieces one after the other: no
 // search and no division for each piece, and no counting of them.  Bound by its chain of
 // dependent steps, 900 to 2,000 cycles each, most of that the fetch of instructions which run
-// once (20 KB), and for long rows by the trips to the page table: 4.7 us for 4 sequences, 5.1
-// for 8 under 16,384 tokens, 6.9 for 32 under 32,768, 9.0 for 24 groups of 8.  It runs once for
+// once (20 KB), and for long rows by the trips to the page table: 4.7 us for 4 sequences, 5.0
+// for 8 under 16,384 tokens, 7.2 for 32 under 32,768, 8.0 for 24 groups of 8.  It runs once for
 // all layers of a decoding step.
 #include "attn_shared.cuh"
 #include "tc_ptx.cuh"
@@ -24,6 +24,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kClusterMax = 8;
 // Batches that are laid out in shared memory (each trip to the plan in global memory costs its latency).
 constexpr int kSmallSeqs = 256, kSmallBlocks = 512;
+constexpr int kLoads = 8;      // table entries of a lane in flight
 constexpr int kPieceCost = 2;  // tiles' time that a segment's queries, first tile and output take
 
 // n / d for 0 <= n < 2^31: n m >> s with m = ceil(2^s / d), s = 31 + ceil(log2 d); m d - 2^s < d,
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         if (first != b) {
             const int32_t* x = A.table + (size_t)b * A.max_pages;
             const int32_t* y = A.table + (size_t)first * A.max_pages;
-            constexpr int kU = 8;
+            constexpr int kU = kLoads;
 #pragma unroll 1
             for (int c0 = in_row; c0 - in_row < n; c0 += lanes * kU) {
                 int v[kU], w[kU], mine = 0x7fffffff;
@@ -389,11 +390,20 @@ cudaError_t launch_shared_plan(const lucetree_shared_plan_args& a, const Dims& d
     A.NPG = quick(d.NPG);
     A.NG = quick(d.NG);
     A.Hkv = quick(d.Hkv);
-    // a CTA for every 8 rows to compare, as far as a cluster goes, then fewer lanes to a row
+    // One CTA where it compares all rows at once, with eight lanes or more to a row that go through
+    // the table's columns in four turns at most: no barrier of a cluster, whose results come through
+    // memory (21 rows of 55 pages 6.2 us instead of 7.1, 24 4.9 instead of 5.7; but 32 of 530, nine
+    // turns, 10.0 instead of 7.2, and 64 of 36 in two turns of rows 7.2 instead of 6.8).  Otherwise a
+    // CTA for every 8 rows, as far as a cluster goes, then fewer lanes to a row.
     int ctas = 1;
-    while (ctas < kClusterMax && ctas * kWarps < a.B) ctas *= 2;
     A.lane_bits = 5;
-    while (A.lane_bits > 3 && ctas * (kThreads >> A.lane_bits) < a.B) --A.lane_bits;
+    while (A.lane_bits > 3 && (kThreads >> A.lane_bits) < a.B) --A.lane_bits;
+    const int cols = kLoads << A.lane_bits;
+    if (a.B > kWarps && (a.B > (kThreads >> A.lane_bits) || (a.max_pages_per_seq + cols - 1) / cols > 4)) {
+        while (ctas < kClusterMax && ctas * kWarps < a.B) ctas *= 2;
+        A.lane_bits = 5;
+        while (A.lane_bits > 3 && ctas * (kThreads >> A.lane_bits) < a.B) --A.lane_bits;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
