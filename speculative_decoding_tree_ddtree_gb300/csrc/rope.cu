@@ -4,20 +4,24 @@
 //
 // A pair (x, y) of rotated dims at position p becomes m (x cos a - y sin a,
 // x sin a + y cos a), a = p f_i.  A step is f_i / 2 pi in units of 2^-64 turns, so
-// p * step mod 2^64 is the angle's fraction of a turn, exact to 2^-32 of it for
-// any position (in fp32, p f_i is off by 2^-24 p f_i: 0.008 at p = 131,072), and
-// sincospi needs no range reduction.
+// p * step mod 2^64 is the angle's fraction of a turn, taken to 2^-32 of it, for any
+// position (in fp32, p f_i is off by 2^-24 p f_i: 0.008 at p = 131,072), and what is left
+// of it after the nearest quarter turn is an integer too.  The cosine and sine are off by
+// less than a step of fp32 (turn), which decides how many of the keys that are stored as
+// codes land on the other side of a border: of 16.8 million E4M3 codes 13 differ from those
+// of 64 bits (18 with cosines that are rounded from 64 bits and no fused products; 31 with
+// sincospi of the fraction in fp32, which took 1 % less time).
 //
 // Bound by HBM: every element is read once and written once.  A block takes a few
-// tokens: their positions and cosines go to shared memory once (one sincospi a thread
-// and token instead of eight in each thread that rotates), and the threads go through
+// tokens: their positions and cosines go to shared memory once (one a thread and
+// token instead of eight in each thread that rotates), and the threads go through
 // the tokens' heads, 16 dims to a thread (two 16-byte vectors, which hold both parts of
 // its 8 pairs), the next two heads' vectors in flight.  The first ones are asked for
 // before the positions are known, so that a single token waits for three loads in a row
 // (start, page, row) and not for four.  Measured with 24 query and 4 KV heads of 256
 // dims in bf16: 24,576 prompt tokens into the cache 132 to 137 us (5.9 to 6.1 TB/s, 88 to
 // 91 % of a copy's rate), 6,144 into E4M3 / int8 pools 37 us (5.1 TB/s), 704 tree nodes
-// 7.2 us (3.2 TB/s; the launch and the chain of loads are 2 us of it: 8 nodes take 2.1).
+// 7.4 us (3.2 TB/s; the launch and the chain of loads are 2 us of it: 8 nodes take 2.1).
 #include <math.h>
 
 #include "e4m3.cuh"
@@ -82,12 +86,40 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
     return make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()), pack2(f[6], f[7], T()));
 }
 
-// Cosine and sine of pair i at position p, times the magnitude.
-__device__ __forceinline__ void turn(const RopeLaunch& R, long long p, int i, float& c, float& s) {
-    const uint64_t part = (uint64_t)p * __ldg(R.steps + i);
-    sincospif((float)(int32_t)(part >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-    c *= R.magnitude;
-    s *= R.magnitude;
+// Cosine and sine of `part` 2^-64 turns, times m.  After the nearest quarter turn |x| <= pi / 4, and the Taylor series
+// to x^9 and x^10 are off by less than 2^-28; the leading terms (2 pi r, and 1 - (2 pi r)^2 / 2) are kept as sums of
+// two floats: cosines are off by 0.58 steps at most, sines by 0.91 (two million angles, on the CPU).
+__device__ __forceinline__ void turn(uint64_t part, float m, float& c, float& s) {
+    const uint32_t q = (uint32_t)((part + (1ull << 61)) >> 62);
+    const int rest = (int)((uint32_t)(part >> 32) - (q << 30));  // 2^-32 turns, [-2^29, 2^29]
+    const float top = (float)rest;
+    const float r = top * 0x1p-32f, rl = (float)(rest - (int)top) * 0x1p-32f;  // turns, in two parts
+    // (products whose rounding is made good are kept from being fused into a sum)
+    const float t = __fmul_rn(r, r), tl = fmaf(2.f * r, rl, fmaf(r, r, -t));
+    // sin: (2 pi)^k / k!
+    const float sh = __fmul_rn(r, 6.2831855f);
+    float sl = fmaf(r, 6.2831855f, -sh);
+    sl = fmaf(r, -1.7484556e-7f, sl);
+    sl = fmaf(rl, 6.2831855f, sl);
+    sl = fmaf(r * t, fmaf(t, fmaf(t, fmaf(t, 42.058693f, -76.70586f), 81.60525f), -41.341702f), sl);
+    // cos
+    const float u = __fmul_rn(t, -19.739208f);
+    float cl = fmaf(t, -19.739208f, -u);
+    cl = fmaf(t, -5.8074317e-7f, cl);
+    cl = fmaf(tl, -19.739208f, cl);
+    cl = fmaf(t * t, fmaf(t, fmaf(t, fmaf(t, -26.426256f, 60.24464f), -85.45682f), 64.93939f), cl);
+    const float ch = __fadd_rn(1.f, u);
+    cl += __fadd_rn(__fsub_rn(1.f, ch), u);
+    // a sum of two floats times m, rounded once
+    auto times_m = [&](float hi, float lo) {
+        const float x = __fmul_rn(hi, m);
+        return x + fmaf(lo, m, fmaf(hi, m, -x));
+    };
+    const float cx = times_m(ch, cl), sx = times_m(sh, sl);
+    c = q & 1 ? sx : cx;
+    s = q & 1 ? cx : sx;
+    if (q == 1 || q == 2) c = -c;
+    if (q & 2) s = -s;
 }
 
 // x such that max 2^x is at most `top` 2^e and above half of it (top in [0.5, 1); 0 for max = 0).
@@ -278,10 +310,7 @@ __global__ void __launch_bounds__(kBlock, 4) rope_kernel(const RopeLaunch R) {
             const int p = i % per;
             if (p >= h2) continue;
             const uint64_t part = (uint64_t)s_pos[i / per] * (p == tp ? step : __ldg(R.steps + p));
-            float c, s;
-            sincospif((float)(int32_t)(part >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-            s_cos[i] = c * R.magnitude;
-            s_sin[i] = s * R.magnitude;
+            turn(part, R.magnitude, s_cos[i], s_sin[i]);
         }
     __syncthreads();
 

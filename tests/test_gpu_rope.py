@@ -108,6 +108,24 @@ def test_any_position(cuda_dev):
         near(out[1][0], *rotated(k[0], p[0], 128, layout))
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("magnitude", [1.0, 1.1386294])
+def test_cosines_within_a_step(cuda_dev, layout, magnitude):
+    """A cosine is off by less than a step of fp32 (2^-23 m), the product that is rounded apart and the sum by half a
+    step each: less than 2^-22 of m (|x| + |y|) together."""
+    LT, N = _lt(), 3000
+    q, k, _ = projection((1, N), 2, 1, 256, "f16", 8)
+    pos = torch.randint(0, 2 ** 20, (1, N), generator=torch.Generator().manual_seed(4), dtype=torch.int32)
+    pos[0, :5] = torch.tensor([0, 1, 2, 2 ** 20, 2 ** 31 - 1])
+    steps, _ = LT.lucetree_rope_steps(256, 10000.0)
+    out, status = [torch.empty(t.shape, dtype=t.dtype, device="cuda") for t in (q, k)], _status()
+    LT.lucetree_rope(q, k, steps.cuda(), layout, *out, status, positions=pos.cuda(), magnitude=magnitude)
+    m = float(np.float32(magnitude))
+    for x, y in zip((q, k), out):
+        want, err = rotated(x[0], pos[0], 256, layout, magnitude=m)
+        near(y[0], want, err * (2.0 ** -22 / 2.0 ** -21))
+
+
 def test_scores_depend_on_distance_alone(cuda_dev):
     """q at p + d and k at p have the same product for every p: the angles of far positions are as exact as near ones."""
     LT = _lt()
