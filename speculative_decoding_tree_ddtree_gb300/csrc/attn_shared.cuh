@@ -94,8 +94,10 @@ struct Split {
 };
 static_assert(sizeof(Split) == 32, "two 16-byte words");
 
+// A CTA's pieces: its first one stands in its own place r, where it can be fetched with this record,
+// the others from `next` on (each begins its segment s, and stands in place C + s).
 struct Cta {
-    int first, pieces, tiles, pad;
+    int next, pieces, tiles, pad;
 };
 
 struct Group {
@@ -125,7 +127,7 @@ struct Plan {  // a plan's parts in its buffer
     Seq* seq;      // [B + 1]
     Block* blk;    // [blocks + 1]
     Split* split;  // [C]
-    Piece* piece;  // [CTA + segment]
+    Piece* piece;  // [CTA, then segment]
 };
 
 __host__ __device__ inline size_t up16(size_t n) { return (n + 15) / 16 * 16; }

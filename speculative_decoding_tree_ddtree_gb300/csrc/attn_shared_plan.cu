@@ -314,7 +314,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     __syncthreads();
 
     // ---------------------------------------------------- pieces, by the first warps
-    // Piece x = r + s is CTA r's of segment s.
     constexpr int kCopyWarps = 3;
     constexpr int kPieceThreads = kThreads - 32 * kCopyWarps;
     if (t < kPieceThreads) {
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         for (int r = t; r < d.C; r += kPieceThreads) {
             const int s0 = s_seg[r], s1 = s_seg[r + 1], t1 = s_tile[r + 1];
             const int n = s1 - s0 + (t1 > 0);
-            *reinterpret_cast<int4*>(P.cta + r) = make_int4(r + s0, n, s_done[r + 1] - s_done[r], 0);
+            *reinterpret_cast<int4*>(P.cta + r) = make_int4(d.C + s0 + 1, n, s_done[r + 1] - s_done[r], 0);
             int kk = s_blk_no[r], hd = s_head[r], ta = s_tile[r];
             int4 split[2] = {};
 #pragma unroll 1
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
                 const int tiles = tiles_of(b.vp), te = s == s1 ? t1 : tiles;
                 const bool whole = ta == 0 && te == tiles;
                 const int slot = whole ? -1 : row0_of(d, q.seq0, q.n, hd, b.node0) + d.block_rows() * r;
-                int4* const p = reinterpret_cast<int4*>(P.piece + r + s);
+                int4* const p = reinterpret_cast<int4*>(P.piece + (s == s0 ? r : d.C + s));
                 p[0] = make_int4(b.b0, b.seqs, b.node0, b.nodes);
                 p[1] = make_int4(b.used, b.vp, ta, te);
                 p[2] = make_int4(hd, slot, q.used == 0, (q.used > 0 ? q.blocks : d.NG) > 1);

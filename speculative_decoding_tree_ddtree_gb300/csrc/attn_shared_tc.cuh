@@ -29,8 +29,8 @@
 //     (exact from 2^-17 to below 65536).
 //
 // Measured with 24 query and 4 KV heads of 256 dims, bf16 in and out, the merge included: 96
-// sequences at budget 22 under 16,384 tokens 463 to 474 us (1.81 PFLOP/s); 16 such sequences 99; one
-// token each of 192 62, of 96 42.5, of 8 22.8 (67 MB of keys and values, 10 us at HBM's rate;
+// sequences at budget 22 under 16,384 tokens 460 to 474 us (1.79 to 1.85 PFLOP/s); 16 such sequences
+// 99; one token each of 192 60, of 96 42, of 8 23 (67 MB of keys and values, 10 us at HBM's rate;
 // four tiles in most CTAs where the mean is 3.4 are 1.8 of the rest, the others the chain of plan,
 // page table and first tile, the last tile and the merge).  With one CTA a tile of 128 KB takes 2.9 us
 // where every page is read once (24 groups of 8 beams: 86 us), which is HBM's rate.
@@ -177,13 +177,14 @@ __device__ __forceinline__ bool not_finite(const uint4& u) {
 
 // The CTA's tiles in order: piece and tile within its segment.
 struct Cursor {
-    int next, left;  // the next piece's place in the plan, and how many come from there on
+    int next, then, left;  // the places of the next two pieces in the plan, and how many come
     int serial;      // number of the current one, counted over both passes
     int t;
     bool live;
     Piece pc;
-    __device__ void start(const Cta& c, int pass) {
-        next = c.first;
+    __device__ void start(const Launch& W, const Cta& c, int pass) {
+        next = (int)blockIdx.x / W.d.pair;
+        then = c.next;
         left = c.pieces;
         serial = pass * c.pieces - 1;
         t = -1;
@@ -195,7 +196,8 @@ struct Cursor {
         if (!live) return;
         --left;
         ++serial;
-        const int4* x = reinterpret_cast<const int4*>(W.plan.piece + next++);
+        const int4* x = reinterpret_cast<const int4*>(W.plan.piece + next);
+        next = then++;
         int4* w = reinterpret_cast<int4*>(&pc);
         w[0] = __ldg(x);
         w[1] = __ldg(x + 1);
@@ -332,7 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // inputs may come from the previous kernel on the stream
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
-    Cta start = W.plan.cta[blockIdx.x / d.pair];  // (loaded with the head, not after it)
+    // (the record is loaded with the head, not after it, and the first piece on its way)
+    if (threadIdx.x < 3)
+        prefetch_l1(reinterpret_cast<const char*>(W.plan.piece + blockIdx.x / d.pair) + min(32 * threadIdx.x, 47u));
+    Cta start = W.plan.cta[blockIdx.x / d.pair];
     const bool fits = plan_fits(W);
     if (!fits) start.tiles = 0;
     if (start.tiles == 0) {  // uniform across the CTA: nothing to do but give TMEM back
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             Cursor cur;
-            cur.start(start, pass);
+            cur.start(W, start, pass);
             // the operands of 16 tiles, a page to a lane, one batch ahead
             auto load_batch = [&](int tb) {
                 const int v = 2 * tb + lane;
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (rank != 0) {
                 // the pair's second CTA: tells the first one what has landed here
                 Cursor qk;
-                qk.start(start, pass);
+                qk.start(W, start, pass);
                 uint32_t n = chunks0;
                 while (ok) {
                     qk.step(W);
@@ -581,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++slot == (uint32_t)kNS) slot = 0;
                 };
                 Cursor qk;
-                qk.start(start, pass);
+                qk.start(W, start, pass);
                 // S(jq) = Q . K(jq)^T.  Its buffer held P(jq - 2), whose PV has been issued before
                 // (MMAs of one thread run in order).
                 auto next_qk = [&]() {
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // permutes units only within a key's row).
             const int ct = tid - 64;  // 0 .. 63
             Cursor cur;
-            cur.start(start, pass);
+            cur.start(W, start, pass);
             int word_cur = 0, word_next = 0;  // pages of 16 tiles, one to a lane
             uint32_t j = 0;  // of this pass
             bool ok = true;
@@ -784,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return __all_sync(0xffffffffu, w);
             };
             Cursor cur;
-            cur.start(start, pass);
+            cur.start(W, start, pass);
             while (!bad) {
                 cur.next_piece(W);
                 if (!cur.live) break;

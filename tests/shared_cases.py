@@ -100,12 +100,12 @@ def check_plan(plan, ctx, start, table, pages, N, Hq, Hkv, D):
         segs += [(k, h) for h in range(Hkv) for k in mine]
     done, rows, splits = {}, [], {}
     for c in range(C):
-        first, n, tiles, _ = p["cta"][c]
+        then, n, tiles, _ = p["cta"][c]
         count = 0
-        for i in range(first, first + n):
+        for s in range(then - 1 - C, then - 1 - C + n):
+            i = c if s == then - 1 - C else C + s
             assert 0 <= i < len(p["piece"])
             b0, seqs, node0, nodes, u, vp, ta, te, g, slot, alone, _ = p["piece"][i]
-            s = i - c
             block = segs[s][0]
             assert list(p["blk"][block, 1:7]) == [b0, seqs, node0, nodes, u, vp] and segs[s][1] == g
             assert 0 <= ta < te <= (vp + 1) // 2 and alone == (u == 0)
