@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // (the shift of a row that has seen no key stays -infinity: its sum is 0)
                         const float alpha = mn > mo ? ex2(mo - mn) : 1.f;
                         neg_m = -mn;
-                        l = alpha > 0.f ? l * alpha : 0.f;
+                        l = alpha > 0.f || l != l ? l * alpha : 0.f;  // (NaN stays: a score was NaN, though no shift tells)
                         if (!first) {
                             // the O row so far moves with its shift, once PV(j-1) has finished adding to it:
                             // each warpgroup half of the dims (a warp that timed out skips its TMEM

@@ -509,3 +509,69 @@ def test_committed_values_that_are_not_finite_stay_with_their_sequences(cuda_dev
             good[with_it, :, Hq // Hkv:2 * (Hq // Hkv)] = False
             near(got, lse, ref, good)
             assert not bool(torch.isfinite(got[~good][:, dim]).any())
+
+
+@pytest.mark.parametrize("case", [([(10, [700, 650, 800])], 5, 4, 2, 128, "bf16"),
+                                  ([(10, [700, 650, 641, 720])], 12, 8, 2, 256, "f16")], ids=["one", "pair"])
+def test_queries_and_committed_keys_that_are_not_finite_stay_with_their_rows(cuda_dev, case):
+    LT = _lt()
+    s = make(*case, seed=14)
+    B, N, Hq, D = s["q"].shape
+    G = Hq // s["k_tree"].shape[2]
+    ref = reference(s)
+    x = dict(s, q=s["q"].clone())
+    x["q"][1, 2, G, 3] = float("nan")
+    got, lse, status = call(x, torch.float32)
+    good = torch.ones(B, N, Hq, dtype=torch.bool)
+    good[1, 2, G] = False
+    near(got, lse, ref, good)
+    assert status == LT.DEV_NONFINITE and bool(torch.isnan(got[~good]).all()) and bool(torch.isnan(lse[~good]).all())
+    x = dict(s, k_pool=s["k_pool"].clone())
+    pos = int(s["ctx_len"][2]) - 1
+    x["k_pool"][int(s["page_table"][2, pos // PAGE]), 0, pos % PAGE, D - 1] = float("nan")
+    got, lse, status = call(x, torch.float32)
+    good = torch.ones(B, N, Hq, dtype=torch.bool)
+    good[2, :, :G] = False
+    near(got, lse, ref, good)
+    assert status == LT.DEV_NONFINITE and bool(torch.isnan(got[~good]).all()) and bool(torch.isnan(lse[~good]).all())
+
+
+def test_a_broken_sequence_in_a_captured_call(cuda_dev):
+    """A captured call with values that are not finite, replayed once they are mended."""
+    LT = _lt()
+    s = make([(10, [700, 650, 641, 720])], 12, 8, 2, 256, "bf16", seed=15)
+    ref = reference(s)
+    d = {k: v.cuda() for k, v in s.items()}
+    B, N, Hq, D = s["q"].shape
+    out, lse = torch.empty(B, N, Hq, D, device="cuda"), torch.empty(B, N, Hq, device="cuda")
+    status, shared = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    plan = torch.empty(LT.lucetree_shared_plan_bytes(B, N, Hq, 2, D, 1), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(LT.lucetree_verify_attn_shared_workspace(B, N, Hq, 2, D, 1), dtype=torch.uint8, device="cuda")
+
+    def run():
+        LT.lucetree_shared_plan(d["page_table"], d["ctx_len"], d["group_start"], N, Hq, 2, D, d["k_pool"].shape[0], shared,
+                                plan, status)
+        LT.lucetree_verify_attn_shared(d["q"], d["k_pool"], d["v_pool"], d["page_table"], d["ctx_len"], d["k_tree"],
+                                       d["v_tree"], d["anc_mask"], 1, plan, out, status, ws, lse=lse)
+
+    page, slot = int(s["page_table"][3, 718 // PAGE]), 718 % PAGE
+    was = d["v_pool"][page, 0, slot].clone()
+    d["v_pool"][page, 0, slot] = float("nan")
+    run()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        run()
+    good = torch.ones(B, N, Hq, dtype=torch.bool)
+    good[3, :, :4] = False
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        near(out.cpu(), lse.cpu(), ref, good)
+        assert bool(torch.isnan(out.cpu()[~good]).all())
+    d["v_pool"][page, 0, slot] = was
+    status.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    near(out.cpu(), lse.cpu(), ref)
+    assert int(status.item()) == 0
