@@ -520,6 +520,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v_op = op;
                 have_v = have_k;
             }
+            // Arrivals that follow MMAs come on their own, in no order that is promised, in a pair at
+            // both CTAs; none may find its CTA gone.  Those of S are all waited for by the softmax; here
+            // the last ones of every slot, of the queries and of the two O accumulations.
+            auto arrived = [&](uint64_t* bar, uint32_t parity) {
+                const bool w = mbar_wait(bar, parity);
+                return __all_sync(0xffffffffu, w);
+            };
+            if (ok) {
+                const uint32_t end = tiles0 + n_tiles;
+#pragma unroll 1
+                for (int c = 0; c < kNS && ok; ++c) {
+                    ok = next_slot();
+                    advance();
+                }
+                ok = ok && arrived(&ms->q_empty, cur.serial & 1);
+#pragma unroll 1
+                for (uint32_t j = end > 1 ? end - 2 : 0u; j < end && ok; ++j) ok = arrived(&ms->pv_done[j & 1], (j >> 1) & 1);
+            }
             if (!ok || aborted(ms)) {
                 set_abort(ms, a.status);
                 // wait (bounded) for this CTA's own copies still in flight
@@ -1031,7 +1049,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (both CTAs go on, or neither)
             if (tid < 2 && aborted(ms)) or_at(cluster_addr(&ms->again, tid), 2u);
             __syncwarp();
-            cluster_sync();  // the other CTA's arrivals and MMAs have come
+            cluster_sync();  // the other CTA's waits are over
+            // (after an abort the first CTA's MMAs are drained, see above: the second one's notice of it)
+            if (tid < 32 && rank != 0 && (*(volatile int*)&ms->again & 2)) mbar_wait(&ms->drain, 0, 200000000ll);
         }
         tc_fence_after();
         if (*(volatile int*)&ms->pass > 0 || *(volatile int*)&ms->again != 1 || (!PAIR && aborted(ms))) break;
