@@ -252,7 +252,9 @@ LUCETREE_API lucetree_status lucetree_verify_attn_shared_workspace(int B, int N,
  * anything, NaN included, and a tree node that is not finite changes only the rows
  * of nodes that see it (with V, all of such a row and its lse become NaN, and
  * NONFINITE is raised).  Committed V that is not finite likewise changes only the
- * rows that see it, those of its sequence or, in a common page, of its group.  A row that sees no key (no
+ * rows that see it, those of its sequence or, in a common page, of its group: all of
+ * such a row and its lse become NaN, whatever the groups are.  V that is finite but
+ * becomes fp16 (bf16 V with an fp32 output) counts as not finite from 65536 on.  A row that sees no key (no
  * committed one, and its mask lacks the node itself, which raises BAD_NODE) gives
  * zeros and lse = -infinity.  The page table's entries and the plan have to agree:
  * a table that has changed needs a new plan.  Errors as lucetree_verify_attn, plus

@@ -212,9 +212,15 @@ __global__ void __launch_bounds__(kMergeThreads, kCtasPerSm) merge_kernel(const 
             o[y] *= inv;
             finite = finite && isfinite(o[y]);
         }
+        finite = __all_sync(0xffffffffu, finite);
+        if (!finite) {  // (all of the row and its lse, as in the attention's epilogue)
+            l = __int_as_float(0x7FFFFFFF);
+#pragma unroll
+            for (int y = 0; y < kV; ++y) o[y] = l;
+        }
         const size_t row = (size_t)(sp.node0 + r / d.G) * d.Hq + sp.g * d.G + r % d.G;
         store_row<kV>(reinterpret_cast<TO*>(W.out) + row * D + lane * kV, o);
-        if (!finite) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
+        if (!finite && lane == 0) atomicOr(a.status, LUCETREE_DEV_NONFINITE);
         if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }

@@ -1037,7 +1037,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
-                bar_sync(1, kSoftmaxThreads);  // the piece's O and values in shared memory are no longer read
+                // (the barrier also says that the piece's O and values in shared memory are no longer read)
+                if (bar_sync_or(1, kSoftmaxThreads, mine && zero != zero)) {
+                    // All of such a row and its lse are NaN, as where the second pass notes its sequence:
+                    // which of the two happens depends on what else is in the block.
+                    ms->xchg[half][row] = zero;
+                    bar_sync(1, kSoftmaxThreads);
+                    const float both = zero + ms->xchg[half ^ 1][row];
+                    if (mine && both != both) {
+                        if (half == 0 && !whole) W.ws[partial_rows(d) * (D + 1) + my_row] = both;
+                        if (half == 0 && whole && a.lse) a.lse[my_row] = both;
+                        if (whole) {
+                            const int bytes = out16 ? 2 : 4;
+                            uint4* const to = reinterpret_cast<uint4*>(reinterpret_cast<char*>(W.out) +
+                                                                       ((size_t)my_row * D + half * (D / 2)) * bytes);
+                            const uint32_t nan = 0x7FFFFFFFu;  // (as two 16-bit numbers too)
+#pragma unroll 1
+                            for (int c = 0; c < D / 2 * bytes / 16; ++c) to[c] = make_uint4(nan, nan, nan, nan);
+                        }
+                    }
+                }
                 if (any && half == 0 && row < kBadWords) ms->vbad[cur.serial % kBadSets][row] = 0;
             }
             if (bad) set_abort(ms, a.status);

@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from tests.shared_cases import TYPES
+from tests.shared_cases import PAGE, TYPES
 from tests.test_gpu_attention_shared import P_STEP, _lt, make, near, reference
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +74,34 @@ def test_closely_following_calls_match_the_formula(cuda_dev):
         out, lse, status = Call(s).run()
         assert status == 0
         near(out, lse, reference(s, p_step=P_STEP[torch.float32]))
+
+
+BROKEN = [([(10, [700, 650, 800, 641])], 3, 8, 2, 128, "bf16"), ([(10, [700, 650, 641, 720])], 12, 8, 2, 256, "bf16"),
+          ([(10, [3700, 650, 641, 720])], 2, 6, 2, 128, "f16"), ([(200, [13000, 12900, 12950, 12800])], 1, 24, 4, 256, "bf16")]
+
+
+@pytest.mark.parametrize("case", BROKEN, ids=str)
+@pytest.mark.parametrize("out", ["f32", "same"])
+def test_values_that_are_not_finite_whatever_the_groups(cuda_dev, case, out):
+    """One committed V in a sequence's own page, or in a common one: all dims and the lse of the rows that see it are
+    NaN, and the others' within their bounds, with the batch as one group, as groups of one, and in between."""
+    LT = _lt()
+    s = make(*case, seed=41)
+    B, N, Hq, D = s["q"].shape
+    G, t = Hq // s["k_tree"].shape[2], torch.float32 if out == "f32" else s["q"].dtype
+    ref = reference(s, p_step=P_STEP[t])
+    values = [float("nan"), float("-inf")] + ([65536.0] if case[5] == "bf16" and t == torch.float32 else [])
+    places = [(1, int(s["ctx_len"][1]) - 1, 0), (B - 1, 64, D - 1)]  # own, common
+    for start in ([0, B], list(range(B + 1)), [0, 2, B], [0, 1, B], [0, B - 1, B]):
+        for b, pos, dim in places:
+            for value in values:
+                x = dict(s, v_pool=s["v_pool"].clone())
+                page = int(s["page_table"][b, pos // PAGE])
+                x["v_pool"][page, 1, pos % PAGE, dim] = value
+                got, lse, status = Call(x, t, start).run()
+                assert status == LT.DEV_NONFINITE
+                good = torch.ones(B, N, Hq, dtype=torch.bool)
+                seen = torch.tensor([page in s["page_table"][c, :-(-int(s["ctx_len"][c]) // PAGE)].tolist() for c in range(B)])
+                good[seen, :, G:2 * G] = False
+                near(got, lse, ref, good)
+                assert bool(torch.isnan(got[~good]).all()) and bool(torch.isnan(lse[~good]).all())
