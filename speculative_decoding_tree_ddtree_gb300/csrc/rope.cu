@@ -4,10 +4,10 @@
 //
 // A pair (x, y) of rotated dims at position p becomes m (x cos a - y sin a,
 // x sin a + y cos a), a = p f_i.  A step is f_i / 2 pi in units of 2^-64 turns, so
-// p * step mod 2^64 is the angle's fraction of a turn, taken to 2^-32 of it, for any
-// position (in fp32, p f_i is off by 2^-24 p f_i: 0.008 at p = 131,072), and what is left
-// of it after the nearest quarter turn is an integer too.  The cosine and sine are off by
-// less than a step of fp32 (turn), which decides how many of the keys that are stored as
+// p * step mod 2^64 is the angle's fraction of a turn for any position (in fp32, p f_i
+// is off by 2^-24 p f_i: 0.008 at p = 131,072), and what is left of it after the nearest
+// quarter turn is an integer too.  The cosine and sine are off by less than a step of
+// their own in fp32 (turn), which decides how many of the keys that are stored as
 // codes land on the other side of a border: of 16.8 million E4M3 codes 13 differ from those
 // of 64 bits (18 with cosines that are rounded from 64 bits and no fused products; 31 with
 // sincospi of the fraction in fp32, which took 1 % less time).
@@ -86,14 +86,17 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
     return make_uint4(pack2(f[0], f[1], T()), pack2(f[2], f[3], T()), pack2(f[4], f[5], T()), pack2(f[6], f[7], T()));
 }
 
-// Cosine and sine of `part` 2^-64 turns, times m.  After the nearest quarter turn |x| <= pi / 4, and the Taylor series
-// to x^9 and x^10 are off by less than 2^-28; the leading terms (2 pi r, and 1 - (2 pi r)^2 / 2) are kept as sums of
-// two floats: cosines are off by 0.58 steps at most, sines by 0.91 (two million angles, on the CPU).
+// Cosine and sine of `part` 2^-64 turns, times m.  After the nearest quarter turn |x| <= pi / 4, 31 bits of it from
+// its first one on (a slow pair's may lie in the lowest) in two floats, and the Taylor series to x^9 and x^10 are off by less than 2^-28;
+// the leading terms (2 pi r, and 1 - (2 pi r)^2 / 2) are kept as sums of two floats: cosines and sines are off by 0.81 of
+// their own steps at most, down to angles of 2^-64 of a turn (eight million angles, on the CPU).
 __device__ __forceinline__ void turn(uint64_t part, float m, float& c, float& s) {
     const uint32_t q = (uint32_t)((part + (1ull << 61)) >> 62);
-    const int rest = (int)((uint32_t)(part >> 32) - (q << 30));  // 2^-32 turns, [-2^29, 2^29]
-    const float top = (float)rest;
-    const float r = top * 0x1p-32f, rl = (float)(rest - (int)top) * 0x1p-32f;  // turns, in two parts
+    const long long rest = (long long)(part - ((uint64_t)q << 62));  // 2^-64 turns, [-2^61, 2^61]
+    const int up = __clzll(rest ^ (rest >> 63)) - 1;  // its top 31 bits and sign (64-bit conversions take longer)
+    const int bits = (int)((rest << up) >> 32);
+    const float unit = __int_as_float((127 - 32 - up) << 23), top = (float)bits;
+    const float r = top * unit, rl = (float)(bits - (int)top) * unit;  // turns, in two parts
     // (products whose rounding is made good are kept from being fused into a sum)
     const float t = __fmul_rn(r, r), tl = fmaf(2.f * r, rl, fmaf(r, r, -t));
     // sin: (2 pi)^k / k!
