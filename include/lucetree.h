@@ -502,8 +502,9 @@ typedef struct lucetree_rope_config {
     double factor;         /* s >= 1: stretch (not read with NONE) */
     double orig_ctx;       /* BANDS, YARN: the trained context C */
     double low, high;      /* BANDS, YARN: turns over C, 0 < low < high */
-    double magnitude;      /* YARN: factor of the rotated dims, 0 = 0.1 ln(s) + 1; others: not read (1) */
-    const double* factors; /* [r / 2] (host) divisors of the angles, > 0, after the scaling; or NULL */
+    double magnitude;      /* YARN: factor of the rotated dims, a finite float, 0 = 0.1 ln(s) + 1; others: not read (1) */
+    const double* factors; /* [r / 2] (host) divisors of the angles, > 0 with a finite reciprocal, after the
+                              scaling; or NULL */
 } lucetree_rope_config;
 
 /*

@@ -578,9 +578,10 @@ extern "C" lucetree_status lucetree_rope_steps(const lucetree_rope_config* c, ui
                    !isfinite(c->high)))
         return LUCETREE_ERR_INVALID_ARG;
     const bool yarn = c->scaling == LUCETREE_ROPE_YARN;
-    if (yarn && (!(c->magnitude >= 0.0) || !isfinite(c->magnitude))) return LUCETREE_ERR_INVALID_ARG;
+    if (yarn && (!(c->magnitude >= 0.0) || !isfinite((float)c->magnitude))) return LUCETREE_ERR_INVALID_ARG;
+    // (no angle is above 1 before its division, so that all of them stay finite)
     for (int i = 0; c->factors && i < r / 2; ++i)
-        if (!(c->factors[i] > 0.0) || !isfinite(c->factors[i])) return LUCETREE_ERR_INVALID_ARG;
+        if (!(c->factors[i] > 0.0) || !isfinite(c->factors[i]) || !isfinite(1.0 / c->factors[i])) return LUCETREE_ERR_INVALID_ARG;
     const double two_pi = 6.283185307179586476925286766559;
     const double s = scaled ? c->factor : 1.0;
     const double base = c->scaling == LUCETREE_ROPE_NTK ? c->base * pow(s, (double)r / (r - 2)) : c->base;
