@@ -510,9 +510,9 @@ typedef struct lucetree_rope_config {
 /*
  * The angle per position of each rotated pair i in [0, r / 2), f_i, as
  * steps[i] = frac(f_i / 2 pi) 2^64 (HOST output; the caller copies it to the
- * device once and keeps it), and the factor of the rotated dims.  An integer
- * times a step, modulo 2^64, is the angle's fraction of a turn, so an angle is as
- * exact at position 10^6 as at 1.  With f = base^(-2 i / r):
+ * device once and keeps it), rounded to the nearest, and the factor of the rotated
+ * dims.  An integer times a step, modulo 2^64, is the angle's fraction of a turn: at
+ * position p it is off by at most |p| 2^-65 turns.  With f = base^(-2 i / r):
  *   NONE    f
  *   LINEAR  f / s
  *   NTK     f for the base base s^(r / (r - 2)); r > 2

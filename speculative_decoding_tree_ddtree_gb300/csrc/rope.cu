@@ -564,55 +564,6 @@ bool stride_ok(long long stride, long long elems) {
 
 using namespace lucetree;
 
-extern "C" lucetree_status lucetree_rope_steps(const lucetree_rope_config* c, uint64_t* steps, float* magnitude) {
-    if (!c || !steps || !magnitude) return LUCETREE_ERR_INVALID_ARG;
-    const int r = c->rot_dims;
-    if (r < 2 || r > 1024 || r % 2 != 0 || c->scaling < LUCETREE_ROPE_NONE || c->scaling > LUCETREE_ROPE_YARN)
-        return LUCETREE_ERR_INVALID_ARG;
-    if (!(c->base > 1.0) || !isfinite(c->base)) return LUCETREE_ERR_INVALID_ARG;
-    const bool scaled = c->scaling != LUCETREE_ROPE_NONE;
-    if (scaled && (!(c->factor >= 1.0) || !isfinite(c->factor))) return LUCETREE_ERR_INVALID_ARG;
-    if (c->scaling == LUCETREE_ROPE_NTK && r <= 2) return LUCETREE_ERR_INVALID_ARG;
-    const bool banded = c->scaling == LUCETREE_ROPE_BANDS || c->scaling == LUCETREE_ROPE_YARN;
-    if (banded && (!(c->orig_ctx > 0.0) || !isfinite(c->orig_ctx) || !(c->low > 0.0) || !(c->high > c->low) ||
-                   !isfinite(c->high)))
-        return LUCETREE_ERR_INVALID_ARG;
-    const bool yarn = c->scaling == LUCETREE_ROPE_YARN;
-    if (yarn && (!(c->magnitude >= 0.0) || !isfinite((float)c->magnitude))) return LUCETREE_ERR_INVALID_ARG;
-    // (no angle is above 1 before its division, so that all of them stay finite)
-    for (int i = 0; c->factors && i < r / 2; ++i)
-        if (!(c->factors[i] > 0.0) || !isfinite(c->factors[i]) || !isfinite(1.0 / c->factors[i])) return LUCETREE_ERR_INVALID_ARG;
-    const double two_pi = 6.283185307179586476925286766559;
-    const double s = scaled ? c->factor : 1.0;
-    const double base = c->scaling == LUCETREE_ROPE_NTK ? c->base * pow(s, (double)r / (r - 2)) : c->base;
-    auto clamp01 = [](double x) { return x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x; };
-    double lo = 0.0, hi = 0.0;
-    if (yarn) {
-        auto dim = [&](double turns) { return r * log(c->orig_ctx / (two_pi * turns)) / (2.0 * log(base)); };
-        lo = fmax(floor(dim(c->high)), 0.0);
-        hi = fmin(ceil(dim(c->low)), r - 1.0);
-    }
-    for (int i = 0; i < r / 2; ++i) {
-        double f = pow(base, -2.0 * i / r);
-        if (c->scaling == LUCETREE_ROPE_LINEAR) f /= s;
-        if (c->scaling == LUCETREE_ROPE_BANDS) {
-            const double w = clamp01((c->orig_ctx * f / two_pi - c->low) / (c->high - c->low));
-            f = w * f + (1.0 - w) * f / s;
-        }
-        if (yarn) {
-            const double w = clamp01((i - lo) / fmax(hi - lo, 0.001));
-            f = w * f / s + (1.0 - w) * f;
-        }
-        if (c->factors) f /= c->factors[i];
-        double turns = f / two_pi;
-        turns -= floor(turns);
-        const double x = nearbyint(ldexp(turns, 64));
-        steps[i] = x >= 18446744073709551616.0 ? 0 : (uint64_t)x;  // (a whole turn is none)
-    }
-    *magnitude = yarn ? (float)(c->magnitude > 0.0 ? c->magnitude : 0.1 * log(s) + 1.0) : 1.f;
-    return LUCETREE_OK;
-}
-
 extern "C" lucetree_status lucetree_rope(const lucetree_rope_args* a, void* stream) {
     if (!a) return LUCETREE_ERR_INVALID_ARG;
     if (a->dtype != LUCETREE_F16 && a->dtype != LUCETREE_BF16) return LUCETREE_ERR_UNSUPPORTED;
