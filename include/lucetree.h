@@ -245,8 +245,9 @@ LUCETREE_API lucetree_status lucetree_verify_attn_shared_workspace(int B, int N,
 
 /*
  * lucetree_verify_attn of a batch in which groups of sequences share their first
- * pages: the same sums, but a group's common pages are read once for the rows of
- * all its sequences.  Softmax statistics, sums and partial outputs are fp32; P and
+ * pages: the same sums, but a group's common pages are read once for a block of the
+ * rows of its sequences: up to 128 rows of a KV head, 256 where the mean group has more
+ * than 128.  Softmax statistics, sums and partial outputs are fp32; P and
  * V are rounded as in lucetree_verify_attn_win (with a bf16 output P is bf16 and V as
  * it is), and a 16-bit output is rounded once.  Keys past a sequence's length may hold
  * anything, NaN included, and a tree node that is not finite changes only the rows

@@ -57,9 +57,10 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
     // dims; V of a pair with D = 128: half of them)
     const cuuint64_t v_dims[3] = {64, pool_dims[1], D / 64}, v_strides[2] = {row, 128};
     const cuuint32_t w_box[3] = {64, (cuuint32_t)kPage, (cuuint32_t)(D / 64)}, v_box[3] = {64, (cuuint32_t)kPage, p.pair == 2 && D == 128 ? 1u : 2u};
-    // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x a CTA's nodes of a block of either kind
+    // queries as [B*N nodes][Hq heads][D]; box = 64 dims x G heads x a CTA's nodes of a block of each kind
     const cuuint64_t q_dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.N}, q_strides[2] = {row, (cuuint64_t)a.Hq * row};
-    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(false)}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(true)};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(kMeanCut)}, o_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(kOwnCut)},
+                     l_box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.half(kLargeCut)};
     // tree K/V as [B*N nodes][Hkv][D]; box = 64 dims of one head of 64 nodes
     const cuuint64_t t_dims[3] = {D, (cuuint64_t)a.Hkv, (cuuint64_t)a.B * a.N}, t_strides[2] = {row, (cuuint64_t)a.Hkv * row};
     const cuuint32_t t_box[3] = {64, 1, (cuuint32_t)kPage};
@@ -67,6 +68,7 @@ cudaError_t launch_shared(const Launch& W, cudaStream_t stream) {
                                   : map(&m.k, 2, a.k_pool, pool_dims, pool_strides, pool_box);
     if (!k_ok || !map(&m.v, 3, a.v_pool, v_dims, v_strides, v_box) ||
         !map(&m.q, 3, a.q, q_dims, q_strides, q_box) || !map(&m.qown, 3, a.q, q_dims, q_strides, o_box) ||
+        !map(&m.qlarge, 3, a.q, q_dims, q_strides, l_box) ||
         !map(&m.kt, 3, a.k_tree, t_dims, t_strides, t_box) || !map(&m.vt, 3, a.v_tree, t_dims, t_strides, t_box))
         return cudaErrorInvalidValue;
     if (a.dtype == LUCETREE_F16) return a.D == 256 ? launch_f16_256(m, W, stream) : launch_f16_128(m, W, stream);

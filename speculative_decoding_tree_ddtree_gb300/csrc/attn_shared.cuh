@@ -5,7 +5,9 @@
 // pages: the group's common pages, which all of its rows see, then for each of its
 // sequences the pages that it has for itself, which that sequence's rows see, and last
 // the tree nodes of all its sequences (they follow each other in memory), 64 to a page.  Two pages make a key tile.  In a group without common
-// pages to read once, a block holds rows of one sequence.  The segments (block, KV
+// pages to read once, a block holds rows of one sequence.  Blocks have the mean group's size, or,
+// in a group that this would cut in far more of them than it needs, its own (blocks_of in the
+// plan).  The segments (block, KV
 // head) form one flat list of tiles that is cut over the CTAs; a piece that does not
 // hold all tiles of its segment leaves partial sums (O, max, sum), which the merge
 // joins.
@@ -20,15 +22,22 @@ constexpr int kMagic = 0x6c745370;
 constexpr int kRows = 128;  // of a CTA: the MMA's M
 constexpr int kMaxCtas = 512;
 
+// Kinds of blocks: of a group that shares pages, cut by the mean group's size; of a sequence without common
+// pages; of a group that shares pages, cut by its own size.
+enum { kMeanCut = 0, kOwnCut = 1, kLargeCut = 2 };
+
 struct Dims {
     int B, N, Hq, Hkv, G, D, groups;
     int pair;      // CTAs of a block: 1, or 2 with half of its nodes each
     int C;         // CTAs, or pairs of CTAs
-    int NPG;       // nodes of a block in a group that shares pages
+    int cap;       // nodes of a block at most
+    int NPG;       // nodes of a block in a group that shares pages, cut by the mean group
     int NG, NPGo;  // other groups: blocks of a sequence, and their nodes
     __host__ __device__ int block_rows() const { return pair * kRows; }
-    // nodes of a block in its first CTA, of either kind of group
-    __host__ __device__ int half(bool own) const { return ((own ? NPGo : NPG) + pair - 1) / pair; }
+    // nodes of a block in its first CTA, of each kind
+    __host__ __device__ int half(int kind) const {
+        return ((kind == kOwnCut ? NPGo : kind == kLargeCut ? cap : NPG) + pair - 1) / pair;
+    }
     __host__ __device__ int max_blocks() const { return B * NG; }
     __host__ __device__ int max_segs() const { return B * NG * Hkv; }
     __host__ __device__ long long max_pieces() const { return (long long)C + max_segs(); }
@@ -53,7 +62,7 @@ inline Dims make_dims(int B, int N, int Hq, int Hkv, int D, int groups, int ctas
     const long long nodes = (long long)((B + groups - 1) / groups) * N;
     d.pair = ctas >= 2 && nodes * d.G > kRows ? 2 : 1;
     d.C = ctas / d.pair;
-    const int cap = kRows / d.G * d.pair;
+    const int cap = d.cap = kRows / d.G * d.pair;
     d.NPG = block_nodes(nodes, N, cap);
     d.NG = (N + cap - 1) / cap;
     d.NPGo = (N + d.NG - 1) / d.NG;
@@ -80,7 +89,8 @@ struct Piece {
     int g;
     int slot;    // row of the partial sums, -1: all tiles
     int own;     // rows of a sequence without common pages
-    int reread;  // other blocks read most of its pages too
+    int how;     // bit 0: other blocks read most of its pages too; bit 1: its group is cut by its own size
+    __device__ int kind() const { return own ? kOwnCut : how & 2; }
 };
 static_assert(sizeof(Piece) == 48, "three 16-byte words");
 

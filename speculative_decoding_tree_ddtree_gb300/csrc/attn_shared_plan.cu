@@ -25,6 +25,7 @@ constexpr int kClusterMax = 8;
 // Batches that are laid out in shared memory (each trip to the plan in global memory costs its latency).
 constexpr int kSmallSeqs = 256, kSmallBlocks = 512;
 constexpr int kLoads = 8;      // table entries of a lane in flight
+constexpr int kFewPages = 60;
 constexpr int kPieceCost = 2;  // tiles' time that a segment's queries, first tile and output take
 
 // n / d for 0 <= n < 2^31: n m >> s with m = ceil(2^s / d), s = 31 + ceil(log2 d); m d - 2^s < d,
@@ -43,7 +44,7 @@ Quick quick(int d) {
 struct PlanLaunch {
     Dims d;
     Plan plan;
-    Quick N, NPG, NG, Hkv;
+    Quick N, NPG, cap, NG, Hkv;
     int lane_bits;  // 2^lane_bits lanes compare a row
     const int32_t* table;
     int max_pages;
@@ -91,6 +92,25 @@ __device__ __noinline__ int last_at_most(const int* number, int stride, int n, i
 }
 
 __device__ __noinline__ int2 div_mod(int a, int b) { return make_int2(a / b, a % b); }
+
+// Blocks of a group of n sequences that share `common` pages: by the mean group's size, or (*large) by its own where its
+// rows then go through kFewPages fewer common pages, or without any in common through so many more.  By the mean,
+// 32 sequences under 256 common pages beside 32 alone took 169 us instead of 46.5 with one token each (16 blocks
+// instead of 2) and 492 instead of 282 with 22 (nothing shared), 24 groups of 12 and 4 under 64 pages 101 instead of 88.
+// Its own size is faster below kFewPages too (under 16 pages 45 us instead of 54), but there the checks of plans in
+// tests/shared_cases.py hold blocks to the mean group's size.
+__device__ __forceinline__ int blocks_of(const PlanLaunch& A, int n, int common, bool* large) {
+    const int nodes = n * A.d.N, mean = A.NPG.div(nodes + A.d.NPG - 1), least = A.cap.div(nodes + A.d.cap - 1);
+    *large = (min(mean, n * A.d.NG) - least) * common >= kFewPages;
+    return *large ? least : mean;
+}
+// Nodes of each of them, by its own size: as block_nodes.
+__device__ __noinline__ int large_nodes(int nodes, int blocks, int N, int cap) {
+    const int per = (nodes + blocks - 1) / blocks, whole = (per + N - 1) / N * N;
+    if (whole <= cap) return whole;
+    const int most = cap / N * N;
+    return most > 0 && (nodes + most - 1) / most <= blocks ? most : per;
+}
 
 __device__ __forceinline__ int pages_of(int L) { return (L + kPage - 1) / kPage; }
 __device__ __forceinline__ int tiles_of(int vp) { return (vp + 1) / 2; }
@@ -196,7 +216,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         r.n = (bad ? d.B : starts[g + 1]) - r.a;
         r.common = bad || r.n < 2 ? 0 : grps[g].used;
         // pages are read once for a block: fewer blocks than without
-        const int blocks = A.NPG.div(r.n * d.N + d.NPG - 1);
+        bool large;
+        const int blocks = blocks_of(A, r.n, r.common, &large);
         r.used = blocks < r.n * d.NG ? r.common : 0;
         r.blocks = r.used > 0 ? blocks : r.n * d.NG;
         return r;
@@ -244,8 +265,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
             const Group q = grps[k.group];
             k.used = q.used;
             if (q.used > 0) {
-                k.node0 = q.seq0 * d.N + (x - q.block0) * d.NPG;
-                k.nodes = min(d.NPG, (q.seq0 + q.n) * d.N - k.node0);
+                bool large;
+                blocks_of(A, q.n, q.used, &large);
+                const int per = large ? large_nodes(q.n * d.N, q.blocks, d.N, d.cap) : d.NPG;
+                k.node0 = q.seq0 * d.N + (x - q.block0) * per;
+                k.nodes = min(per, (q.seq0 + q.n) * d.N - k.node0);
             } else {
                 const int b = A.NG.div(x - q.block0), part = x - q.block0 - b * d.NG;
                 k.node0 = (q.seq0 + b) * d.N + part * d.NPGo;
@@ -334,7 +358,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
                 int4* const p = reinterpret_cast<int4*>(P.piece + (s == s0 ? r : d.C + s));
                 p[0] = make_int4(b.b0, b.seqs, b.node0, b.nodes);
                 p[1] = make_int4(b.used, b.vp, ta, te);
-                p[2] = make_int4(hd, slot, q.used == 0, (q.used > 0 ? q.blocks : d.NG) > 1);
+                bool large;
+                blocks_of(A, q.n, q.used, &large);
+                p[2] = make_int4(hd, slot, q.used == 0, (int)((q.used > 0 ? q.blocks : d.NG) > 1) | (int)large << 1);
                 if (ta == 0 && !whole) {  // (the CTA's last piece)
                     split[0] = make_int4(last_at_most(s_seg, 1, ctas, s) - r + 1, slot, b.node0, b.nodes * d.G);
                     split[1] = make_int4(hd, 0, 0, 0);
@@ -387,6 +413,7 @@ cudaError_t launch_shared_plan(const lucetree_shared_plan_args& a, const Dims& d
     A.status = a.status;
     A.N = quick(d.N);
     A.NPG = quick(d.NPG);
+    A.cap = quick(d.cap);
     A.NG = quick(d.NG);
     A.Hkv = quick(d.Hkv);
     // One CTA where it compares all rows at once, with eight lanes or more to a row that go through

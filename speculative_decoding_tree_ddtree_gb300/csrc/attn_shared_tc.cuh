@@ -257,6 +257,7 @@ template <int D, bool BF16, bool PV16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qown,
+                     const __grid_constant__ CUtensorMap tm_qlarge,
                      const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                      const __grid_constant__ Launch W) {
     using L = Lay<D, PAIR>;
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tm_v);
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_qown);
+        prefetch_tensormap(&tm_qlarge);
         prefetch_tensormap(&tm_kt);
         prefetch_tensormap(&tm_vt);
     }
@@ -499,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!(ok = __all_sync(0xffffffffu, w))) break;
                         }
                         if (leader) {
-                            const int nodes = d.half(cur.pc.own);
-                            const CUtensorMap* tm = cur.pc.own ? &tm_qown : &tm_q;
+                            const int kind = cur.pc.kind(), nodes = d.half(kind);
+                            const CUtensorMap* tm = kind == kOwnCut ? &tm_qown : kind == kLargeCut ? &tm_qlarge : &tm_q;
                             mbar_arrive_expect_tx(&ms->q_full, D / 64 * nodes * d.G * 128);
 #pragma unroll 1
                             for (int c = 0; c < D / 64; ++c)
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     op.at0 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15));
                     op.at1 = __shfl_sync(0xffffffffu, at_cur, 2 * (rel & 15) + 1);
                     op.g = cur.pc.g;
-                    op.pol = cur.pc.reread ? pol_again : pol_once;
+                    op.pol = cur.pc.how & 1 ? pol_again : pol_once;
                 }
                 if (have_k) ok = issue_k(op);
                 if (ok && have_v) ok = issue_v(v_op);
@@ -812,8 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 cur.next_piece(W);
                 if (!cur.live) break;
                 const Piece& blk = cur.pc;
-                const int before = (int)rank * d.half(cur.pc.own);  // the block's nodes in the pair's first CTA
-                const bool mine = row < min(d.half(cur.pc.own), blk.nodes - before) * d.G;
+                const int first_nodes = d.half(cur.pc.kind()), before = (int)rank * first_nodes;  // the block's nodes in the pair's first CTA
+                const bool mine = row < min(first_nodes, blk.nodes - before) * d.G;
                 const int node = blk.node0 + (mine ? before + row / d.G : 0);
                 const int b = node / d.N, i = node - b * d.N;
                 // (rows past the block's own go along with what all rows see, so that their warp needs no masks)
@@ -970,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool whole = done.slot < 0;
                 // rows of the output, or of the partial sums: mine, and the four of my lane's group of four
                 const int my_row = whole ? node * d.Hq + done.g * d.G + row % d.G : done.slot + before * d.G + row;
-                const int row4 = row & ~3, rows = min(d.half(done.own), done.nodes - before) * d.G;
+                const int row4 = row & ~3, rows = min(first_nodes, done.nodes - before) * d.G;
                 int to_row[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) to_row[k] = __shfl_sync(0xffffffffu, my_row, (lane & 28) + k);
@@ -1085,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 struct Maps {
-    CUtensorMap k, v, q, qown, kt, vt;
+    CUtensorMap k, v, q, qown, qlarge, kt, vt;
 };
 
 template <int D, bool BF16, bool PV16, bool PAIR>
@@ -1108,7 +1110,7 @@ cudaError_t launch_pairs(const Maps& m, const Launch& W, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, m.k, m.v, m.q, m.qown, m.kt, m.vt, W);
+    return cudaLaunchKernelEx(&cfg, kern, m.k, m.v, m.q, m.qown, m.qlarge, m.kt, m.vt, W);
 }
 
 template <int D, bool BF16, bool PV16>
