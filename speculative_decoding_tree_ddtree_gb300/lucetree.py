@@ -1175,7 +1175,7 @@ def lucetree_reorder_states(state_in, src, state_out, status, stream=None):
     _check(load().lucetree_reorder_states(args, _raw_stream(stream, dev)))
 
 
-# ---------------------------------------------------------------- failure path self-test
+# ---------------------------------------------------------------- rotary positions, appending to the cache
 
 def lucetree_rope_steps(rot_dims: int, base: float, scaling: int = LUCETREE_ROPE_NONE, factor: float = 1.0,
                         orig_ctx: float = 0.0, low: float = 0.0, high: float = 0.0, magnitude: float = 0.0,
@@ -1259,6 +1259,8 @@ def lucetree_append_kv(k, v, start, page_table, ctx_len_in, ctx_len_out, k_pool,
         0 if q_out is None else _arg(q_out, "q_out", kind, dev, T, Hq, D), _arg(status, "status", _K_W32, dev))
     _check(load().lucetree_append_kv(args, _raw_stream(stream, dev)))
 
+
+# ---------------------------------------------------------------- failure path self-test
 
 def lucetree_selftest_wait_timeout(status, limit_cycles: int, waited_cycles=None, stream=None):
     """One block waits on a barrier nothing arrives on; after ~limit_cycles SM

@@ -88,3 +88,35 @@ def test_attention_of_uneven_groups(cuda_dev, i, out):
     got, lse, status = Call(s, t).run()
     assert status == 0
     near(got, lse, reference(s, p_step=P_STEP[t]))
+
+
+def test_a_captured_step_whose_groups_change(cuda_dev):
+    """Plan and attention captured with even groups, replayed with one large group: which cut is taken is decided on the
+    device."""
+    even = make([(10, [700, 650, 800, 641]) for _ in range(10)], 1, 24, 4, 128, "bf16", seed=3)
+    large = make(fork(30, 31, 9), 1, 24, 4, 128, "bf16", seed=4)
+    B, G = 40, 10
+    assert large["q"].shape == even["q"].shape and large["group_start"].numel() == even["group_start"].numel() == G + 1
+    wide = max(s["page_table"].shape[1] for s in (even, large))
+    pages = max(s["k_pool"].shape[0] for s in (even, large))
+    for s in (even, large):
+        table = torch.full((B, wide), -1, dtype=torch.int32)
+        table[:, :s["page_table"].shape[1]] = s["page_table"]
+        s["page_table"] = table
+        for k in ("k_pool", "v_pool"):
+            s[k] = torch.cat([s[k], torch.full((pages - s[k].shape[0], *s[k].shape[1:]), float("nan"), dtype=s[k].dtype)])
+    c = Call(even)
+    c.run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.make_plan()
+        c.attend()
+    for s in (large, even, large):
+        for k, v in s.items():
+            c.d[k].copy_(v)
+        c.out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(c.status.item()) == 0 and c.shared.tolist() == ([30] + [0] * 9 if s is large else [10] * 10)
+        near(c.out.cpu(), c.lse.cpu(), reference(s, p_step=P_STEP[torch.float32]))
+        assert int(c.plan.cpu().numpy().view(np.int32)[10]) == (11 if s is large else 10)  # blocks
