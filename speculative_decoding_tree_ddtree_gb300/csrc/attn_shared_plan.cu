@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         }
     }
     if (gridDim.x > 1) {
+        __syncwarp();  // (rows of a warp end at different turns; the cluster's barrier wants whole warps)
         tc::cluster_sync();
         if (!lead) return;
 #pragma unroll 1

@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!fits) start.tiles = 0;
     if (start.tiles == 0) {  // uniform across the CTA: nothing to do but give TMEM back
         if (!fits && threadIdx.x == 0) atomicOr(a.status, LUCETREE_DEV_BAD_ROW);
+        __syncwarp();
         if constexpr (PAIR) cluster_sync();
         teardown();
         return;
