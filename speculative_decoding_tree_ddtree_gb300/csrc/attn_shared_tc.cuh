@@ -29,8 +29,8 @@
 //     (exact from 2^-17 to below 65536).
 //
 // Measured with 24 query and 4 KV heads of 256 dims, bf16 in and out, the merge included: 96
-// sequences at budget 22 under 16,384 tokens 460 to 474 us (1.79 to 1.85 PFLOP/s); 16 such sequences
-// 99; one token each of 192 60, of 96 42, of 8 23 (67 MB of keys and values, 10 us at HBM's rate;
+// sequences at budget 22 under 16,384 tokens 457 to 460 us (1.85 PFLOP/s; 500 to 520 in long runs, where
+// the clock gives way); 16 such sequences 98; one token each of 192 60, of 96 41, of 8 21 (67 MB of keys and values, 10 us at HBM's rate;
 // four tiles in most CTAs where the mean is 3.4 are 1.8 of the rest, the others the chain of plan,
 // page table and first tile, the last tile and the merge).  With one CTA a tile of 128 KB takes 2.9 us
 // where every page is read once (24 groups of 8 beams: 86 us), which is HBM's rate.

@@ -19,9 +19,10 @@
 // its 8 pairs), the next two heads' vectors in flight.  The first ones are asked for
 // before the positions are known, so that a single token waits for three loads in a row
 // (start, page, row) and not for four.  Measured with 24 query and 4 KV heads of 256
-// dims in bf16: 24,576 prompt tokens into the cache 132 to 137 us (5.9 to 6.1 TB/s, 88 to
-// 91 % of a copy's rate), 6,144 into E4M3 / int8 pools 37 us (5.1 TB/s), 704 tree nodes
-// 7.4 us (3.2 TB/s; the launch and the chain of loads are 2 us of it: 8 nodes take 2.1).
+// dims in bf16: 24,576 prompt tokens into the cache 130 to 136 us (5.9 to 6.2 TB/s, 88 to
+// 93 % of a copy's rate), 6,144 into E4M3 / int8 pools 38 us (4.9 TB/s), 704 tree nodes
+// 6.7 us a call back to back, 7.5 in a replayed graph over 280 MB of inputs (3.4, 3.1 TB/s; the
+// launch and the chain of loads are 2 us of it: 8 nodes take 2.1).
 #include <math.h>
 
 #include "e4m3.cuh"
